@@ -231,6 +231,145 @@ ATTN_API int attn_fwd_fp8(const void* q8, const float* sq, const void* k8, const
                           int N, int d, int causal, float scale, void* stream);
 
 /*
+ * A paged key-value cache (the paged cache of CS336 Lecture 5 notes, section 6.3).  K and V are each
+ * num_pages pages of H_kv heads of page_size rows of d elements; row r of page p and K/V head h
+ * starts at element p * page_stride + (h * page_size + r) * d.  A token's place is its slot,
+ * page * page_size + row.  Passed by address; the struct itself is host memory, read during the call.
+ *   k, v             : device pointers, 16-byte aligned; bf16, or E4M3 codes
+ *   k_scale, v_scale : E4M3 only (else ignored): fp32 [num_pages, H_kv, page_size], contiguous,
+ *                      16-byte aligned: the value of an element is its code x its row's scale
+ *   page_stride      : elements from one page to the next, of k and of v (>= H_kv * page_size * d;
+ *                      a multiple of 16 bytes), so k and v may be interleaved page by page
+ *   page_size        : 16, 32, 64, 128 or 256
+ *   dtype            : ATTN_CACHE_BF16 or ATTN_CACHE_E4M3
+ * A malformed cache is ATTN_ERR_SHAPE (sizes, strides), ATTN_ERR_NULL, ATTN_ERR_ALIGN or
+ * ATTN_ERR_UNSUPPORTED (dtype, page_size).
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t page_stride;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t dtype;
+} attn_kv_cache;
+
+#define ATTN_CACHE_BF16 0
+#define ATTN_CACHE_E4M3 1
+
+/*
+ * Pages, slots and positions of the new tokens of B requests, from their lengths.  Request s holds
+ * seq_lens[s] tokens and gets new tokens cu_new[s] .. cu_new[s+1]-1 of a packed batch of T; the
+ * pages it lacks come from free_pages in order, request by request, starting at entry *free_head:
+ *   had_s = ceil(len_s / P), need_s = ceil((len_s + new_s) / P) - had_s,
+ *   page j of request s = block_table[s][j] for j < had_s, else
+ *                         free_pages[*free_head + sum_{r<s} need_r + j - had_s];
+ *   a token at position i of its request has slot page(i / P) * P + i % P.
+ *   seq_lens int32[B]; cu_new int32[B+1] (0 to T); block_table int32[B, max_pages], whose new
+ *   entries are written; free_pages int32[n_free]; free_head int32[1]
+ *   slots int64[T], positions int32[T], seq_lens_out int32[B] (len + new), free_head_out int32[1]
+ *   (*free_head + sum of need): outputs.  seq_lens_out and free_head_out must not be seq_lens and
+ *   free_head (ATTN_ERR_UNSUPPORTED): every CTA reads the old values.  The call can be repeated
+ *   with the same inputs.
+ *   max_pages : row length of block_table; page_size : 1 to 65536; B <= 16384 (ATTN_ERR_SHAPE)
+ * A token whose page would lie past max_pages, or past the free list, gets slot -1 (and its table
+ * entry, if there is one, -1) and the status word reports kind 4; cu_new that is not a
+ * non-decreasing prefix sum from 0 to T reports kind 2, is clamped into [0, T], and leaves tokens
+ * that belong to no request with slot -1 and position 0.  A negative length counts as 0.
+ * One launch.  T == 0 copies the lengths and the head; B == 0 does nothing.  Pointers of 4-byte
+ * elements must be 4-byte aligned, slots 8-byte.  Returns an attn_status.
+ */
+ATTN_API int attn_kv_slots(const int32_t* seq_lens, const int32_t* cu_new, int32_t* block_table,
+                           const int32_t* free_pages, const int32_t* free_head, int64_t* slots,
+                           int32_t* positions, int32_t* seq_lens_out, int32_t* free_head_out,
+                           int B, int T, int max_pages, int n_free, int page_size, void* stream);
+
+/*
+ * The step before attention: from the rows a projection wrote, token by token, to q, k, v head by
+ * head, normed and rotated, and into a paged cache; one pass over the data.  A token's row holds H
+ * query heads, H_kv key heads and H_kv value heads of d elements.  For a query or key head x:
+ *   n = x * w / sqrt(mean(x^2) + eps)          (n = x where w is NULL)
+ *   (y_a, y_b) = rope_scale * (n_a cos t - n_b sin t, n_b cos t + n_a sin t),
+ *   t = position * inv_freq[i] for pair i of the first `rot` elements: elements i and i + rot/2, or
+ *   2i and 2i + 1 if interleaved; elements from rot on stay n.  Value heads are copied.
+ *   qkv       : bf16 [B, N, ld] rows, ld >= (H + 2 H_kv) d elements from one token to the next, a
+ *               multiple of 8
+ *   wq, wk    : bf16 [d] weights of the norms, each may be NULL (no norm); eps >= 0
+ *   inv_freq  : float64 [rot/2], radians a position (any scaling for long contexts is in it);
+ *               rot : a multiple of 16 up to d, 0 for no rotation (inv_freq may then be NULL)
+ *   positions : int32 [B, N] (NULL only with rot 0).  The angle is reduced modulo a turn in 64-bit
+ *               fixed point, so far positions keep fp32 accuracy
+ *   q         : bf16 [B, H, N, d];  k, v : bf16 [B, H_kv, N, d], both or neither NULL.  With B = 1
+ *               these are the packed layout [H, T, d] of attn_fwd; with N = 1 one new token of
+ *               each of B requests, as attn_fwd_paged takes it.  q may be NULL.
+ *   cache     : NULL, or the cache that token t's K and V rows go into at slots[t] (int64 [B, N];
+ *               negative: not stored).  E4M3 rows: scale = amax / 448 (1 if that is below fp32's
+ *               normal range, as for a zero row), code = E4M3 round-to-nearest-even of the fp32
+ *               y / scale.  A slot past the cache is not stored and the status word reports kind 5;
+ *               two tokens with one slot leave either's row there, never part of both within 16
+ *               bytes.
+ * Norm and rotation are fp32, rounded once on the way out.  Outputs must not overlap qkv.
+ * One launch.  Tensors 16-byte aligned (inv_freq and slots 8, positions 4).  Returns an attn_status
+ * (rot, ld, eps, rope_scale out of range: ATTN_ERR_SHAPE for sizes, ATTN_ERR_SCALE for the floats).
+ */
+ATTN_API int attn_qkv_rope(const void* qkv, int64_t ld, const void* wq, const void* wk, float eps,
+                           const double* inv_freq, int rot, int interleaved, float rope_scale,
+                           const int32_t* positions, void* q, void* k, void* v,
+                           const attn_kv_cache* cache, const int64_t* slots, int B, int N, int H,
+                           int H_kv, int d, void* stream);
+
+/*
+ * Backward of attn_qkv_rope without a cache.  With g = rope_scale * R(t)^T dy, r = 1/sqrt(mean(x^2)
+ * + eps) and u = g w:  dx = r (u - x r^2 mean(u x)),  dw = sum over rows of g x r  (dx = g without a
+ * norm);  dv is copied.
+ *   dq bf16 [B, H, N, d]; dk, dv bf16 [B, H_kv, N, d]: gradients of q, k, v (as attn_bwd writes them)
+ *   dqkv bf16 [B, N, ld_out] : gradient of qkv; columns past (H + 2 H_kv) d are left as they were
+ *   dwq, dwk fp32 [d] : written where wq, wk are given (ignored where they are NULL)
+ *   workspace : attn_qkv_rope_bwd_workspace_bytes(B, N, H, H_kv, d) bytes, 256-byte aligned, needed
+ *               only with a norm (NULL is fine without)
+ * Sums over rows are taken in a fixed order (no atomics): equal inputs give equal bits.
+ * B * N == 0 writes nothing.  Other arguments and errors as attn_qkv_rope.
+ */
+ATTN_API int attn_qkv_rope_bwd(const void* dq, const void* dk, const void* dv, const void* qkv,
+                               int64_t ld, const void* wq, const void* wk, float eps,
+                               const double* inv_freq, int rot, int interleaved, float rope_scale,
+                               const int32_t* positions, void* dqkv, int64_t ld_out, float* dwq,
+                               float* dwk, int B, int N, int H, int H_kv, int d, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Workspace bytes attn_qkv_rope_bwd needs (0 for invalid sizes). */
+ATTN_API size_t attn_qkv_rope_bwd_workspace_bytes(int B, int N, int H, int H_kv, int d);
+
+/*
+ * Attention of one new token of each of B requests over a paged cache: for request s and query head
+ * h, O = softmax(scale q K^T) V over the first seq_lens[s] rows of the pages block_table[s][0], [1],
+ * ... of K/V head h / (H / H_kv), and the log-sum-exp.  (The new token's own K and V are in the
+ * cache already, and counted.)
+ *   q, o : bf16 [B, H, d] (= [B, H, 1, d]);  lse : fp32 [B, H]
+ *   block_table : int32 [B, max_pages]; only the entries that seq_lens needs are read, and a row past
+ *     seq_lens is never used, whatever it holds.  seq_lens : int32 [B], clamped to 0 ..
+ *     max_pages * page_size.  A request of length 0 gets O = 0 and lse = -inf.
+ *   workspace : attn_fwd_paged_workspace_bytes(B, H, H_kv, d) bytes (it does not depend on the
+ *     lengths), 256-byte aligned; calls whose work may overlap on the GPU need one each.
+ * The rows of all requests are cut into equal shares, one a CTA, whatever the lengths are, and a second
+ * launch joins the parts of a request that fell to several CTAs by the block merge of
+ * attn_fwd_splitkv.  Everything that depends on lengths is decided on the GPU: a captured call can be
+ * replayed with other lengths, tables and contents.  Equal inputs give equal bits.
+ * A table entry that is needed and names no page of the cache is read as a page of zeros, and the
+ * status word reports kind 5.
+ * H_kv must divide H (ATTN_ERR_SHAPE).  Returns an attn_status.
+ */
+ATTN_API int attn_fwd_paged(const void* q, const attn_kv_cache* cache, const int32_t* block_table,
+                            const int32_t* seq_lens, void* o, float* lse, int B, int H, int H_kv,
+                            int d, int max_pages, float scale, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Workspace bytes attn_fwd_paged needs (0 for invalid sizes). */
+ATTN_API size_t attn_fwd_paged_workspace_bytes(int B, int H, int H_kv, int d);
+
+/*
  * Unfused comparison path (the "standard attention" of the pages: S written to HBM, read back for
  * the softmax, P written to HBM, read back for P V; CS336 GPU/attention notes, "Attention 为什么
  * 容易 memory-bound"; CS336 Lecture 5 notes, section 6.1).  Three kernel launches on `stream`:
@@ -284,7 +423,8 @@ ATTN_API int attn_fwd_unfused_noalloc(const void* q, const void* k, const void* 
  * packed-batch call was not a non-decreasing prefix sum from 0 to N; the kernel computed on its
  * offsets clamped into [0, N] and read or wrote nothing outside the tensors) or 3 (a kernel's
  * shared-memory layout did not fit the dynamic shared memory it was given at a 1024-byte boundary;
- * that kernel wrote nothing and its outputs are not valid).  The first problem
+ * that kernel wrote nothing and its outputs are not valid) or 4 (attn_kv_slots had no page for some
+ * token) or 5 (a slot or a block-table entry named no page of the cache).  The first problem
  * recorded is kept.  Synchronises `stream`, then clears the status.  Returns ATTN_ERR_LAUNCH (< 0)
  * if the status cannot be read.
  */

@@ -5,7 +5,8 @@ torch tensors into its C entry points.  Importing this package does not load the
 the first call does, and fails loudly if the library is missing.
 """
 __all__ = ["attn_fwd", "attn_bwd", "bwd_workspace_bytes", "attn_fwd_splitkv", "quantize_fp8", "attn_fwd_fp8", "splitkv_workspace_bytes", "attn_fwd_unfused",
-           "unfused_workspace_bytes", "last_device_error"]
+           "unfused_workspace_bytes", "last_device_error", "KVCache", "kv_cache", "kv_slots",
+           "rope_inv_freq", "qkv_rope", "qkv_rope_bwd", "attn_fwd_paged", "paged_workspace_bytes"]
 
 
 def __getattr__(name):

@@ -7,12 +7,15 @@ missing or the GPU is not an sm_103 part, calls raise.
 Layouts (same as the C ABI in ``include/attn_gb300.h``):
   dense  q, k, v, o: [B, H, N, d] bf16 contiguous; lse [B, H, N] fp32
   packed q, k, v, o: [H, T, d] bf16 contiguous + cu_seqlens int32 [n+1]; lse [H, T] fp32
+  paged  K, V caches: [num_pages, H_kv, page_size, d] bf16 or E4M3 (see KVCache)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
+from typing import Any, NamedTuple
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libattn_gb300.so")
 
@@ -24,6 +27,7 @@ STATUS = {
 
 # exported C symbols and their ctypes signatures (kept in step with include/attn_gb300.h)
 _P, _I, _F, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_L = ctypes.c_int64
 SIGNATURES = {
     "attn_fwd": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P]),
     "attn_fwd_gqa": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P]),
@@ -39,6 +43,14 @@ SIGNATURES = {
     "attn_bwd_workspace_bytes": (_S, [_I, _I, _I, _I]),
     "attn_quantize_fp8": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P]),
     "attn_fwd_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P]),
+    "attn_kv_slots": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "attn_qkv_rope": (_I, [_P, _L, _P, _P, _F, _P, _I, _I, _F, _P, _P, _P, _P, _P, _P, _I, _I, _I,
+                           _I, _I, _P]),
+    "attn_qkv_rope_bwd": (_I, [_P, _P, _P, _P, _L, _P, _P, _F, _P, _I, _I, _F, _P, _P, _L, _P, _P,
+                               _I, _I, _I, _I, _I, _P, _S, _P]),
+    "attn_qkv_rope_bwd_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
+    "attn_fwd_paged": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _S, _P]),
+    "attn_fwd_paged_workspace_bytes": (_S, [_I, _I, _I, _I]),
     "attn_fwd_unfused": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _S, _P]),
     "attn_fwd_unfused_workspace_bytes": (_S, [_I, _I, _I, _I]),
     "attn_fwd_unfused_noalloc": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P]),
@@ -275,6 +287,278 @@ def attn_fwd_fp8(q8, sq, k8, sk, vt8, sv, causal: bool = False, scale: float | N
                                 B, H, N, d, int(bool(causal)), float(scale),
                                 _stream_handle(stream, q8.device))
     _check("attn_fwd_fp8", rc)
+    return out, lse
+
+
+# ------------------------------------------------------------------------------- generation
+class KVCache(NamedTuple):
+    """A paged key-value cache: k, v [num_pages, H_kv, page_size, d], bf16, or E4M3 codes
+    (torch.float8_e4m3fn or uint8) with k_scale, v_scale fp32 [num_pages, H_kv, page_size].  The stride
+    from page to page is free (k and v may be the two halves of one tensor of pages); inside a
+    page the rows are contiguous."""
+    k: Any
+    v: Any
+    k_scale: Any = None
+    v_scale: Any = None
+
+
+class _CacheStruct(ctypes.Structure):  # attn_kv_cache in the header
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("page_stride", _L),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+def kv_cache(num_pages: int, H_kv: int, page_size: int, d: int, dtype=None, device="cuda") -> KVCache:
+    """An empty cache (zeros): bf16, or E4M3 with dtype torch.float8_e4m3fn."""
+    import torch
+    dtype = torch.bfloat16 if dtype is None else dtype
+    if dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8):
+        raise ValueError("a cache is bf16 or float8_e4m3fn")
+    shape = (num_pages, H_kv, page_size, d)
+    kind = torch.uint8 if dtype == torch.float8_e4m3fn else dtype
+    k, v = (torch.zeros(shape, dtype=kind, device=device).view(dtype) for _ in range(2))
+    if dtype == torch.bfloat16:
+        return KVCache(k, v)
+    return KVCache(k, v, *(torch.zeros(shape[:3], dtype=torch.float32, device=device)
+                           for _ in range(2)))
+
+
+def _cache_struct(cache, H_kv, d, device):
+    import torch
+    k, v = cache.k, cache.v
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != device or \
+            v.device != device:
+        raise ValueError("cache k and v must be [num_pages, H_kv, page_size, d] tensors of one type "
+                         "on q's device")
+    n, h, page, dd = k.shape
+    if h != H_kv or dd != d:
+        raise ValueError("the cache's heads or head dim differ from the inputs'")
+    stride = k.stride()
+    inner = (page * d, d, 1)
+    if v.stride() != stride or any(s != w and e != 1 for s, w, e in zip(stride[1:], inner, (h, page, d))):
+        raise ValueError("cache pages must be contiguous, with one page stride for k and v")
+    page_stride = stride[0] if n > 1 else h * page * d
+    ks = vs = None
+    if k.dtype == torch.bfloat16:
+        dtype = 0
+    elif k.dtype in (torch.float8_e4m3fn, torch.uint8):
+        dtype = 1
+        for t in (cache.k_scale, cache.v_scale):
+            if t is None or t.dtype != torch.float32 or t.shape != k.shape[:3] or \
+                    not t.is_contiguous() or t.device != device:
+                raise ValueError("an E4M3 cache needs contiguous fp32 k_scale and v_scale "
+                                 "[num_pages, H_kv, page_size]")
+        ks, vs = cache.k_scale.data_ptr(), cache.v_scale.data_ptr()
+    else:
+        raise ValueError("a cache is bf16, float8_e4m3fn or uint8 codes")
+    return _CacheStruct(k.data_ptr(), v.data_ptr(), ks, vs, page_stride, n, page, dtype)
+
+
+@contextlib.contextmanager
+def _launching(device, stream):
+    """The device made current, and torch's allocations made on the launching stream (so that a
+    buffer released after the call is not handed out before the work is done); yields the handle."""
+    import torch
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+def _ints(t, dtype, name, device, shape=None):
+    if t.dtype != dtype or not t.is_contiguous() or t.device != device or \
+            (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on the inputs' device"
+                         + (f" of shape {tuple(shape)}" if shape is not None else ""))
+    return t.data_ptr()
+
+
+def kv_slots(seq_lens, cu_new, T: int, block_table, free_pages, free_head, page_size: int,
+             stream=None):
+    """Pages, slots and positions of T new tokens (see attn_kv_slots in the header).  seq_lens
+    int32 [B], cu_new int32 [B + 1], block_table int32 [B, max_pages] (new entries are written),
+    free_pages int32 [n], free_head int32 [1].  Returns (slots int64 [T], positions int32 [T],
+    block_table, new seq_lens, new free_head); the old seq_lens and free_head are left alone."""
+    import torch
+    dev = seq_lens.device
+    if dev.type != "cuda" or seq_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("seq_lens [B], block_table [B, max_pages] and free_pages [n] must be CUDA tensors")
+    B, i32 = seq_lens.shape[0], torch.int32
+    args = (_ints(seq_lens, i32, "seq_lens", dev), _ints(cu_new, i32, "cu_new", dev, (B + 1,)),
+            _ints(block_table, i32, "block_table", dev, (B, block_table.shape[1])),
+            _ints(free_pages, i32, "free_pages", dev), _ints(free_head, i32, "free_head", dev, (1,)))
+    with _launching(dev, stream) as st:
+        slots = torch.empty(T, dtype=torch.int64, device=dev)
+        out = torch.empty(T + B + 1, dtype=i32, device=dev)
+        positions, lens, head = out[:T], out[T:T + B], out[T + B:]
+        if B == 0:
+            head.copy_(free_head)
+        rc = lib().attn_kv_slots(*args, slots.data_ptr(), positions.data_ptr(), lens.data_ptr(),
+                                 head.data_ptr(), B, int(T), block_table.shape[1],
+                                 free_pages.shape[0], int(page_size), st)
+    _check("attn_kv_slots", rc)
+    return slots, positions, block_table, lens, head
+
+
+def rope_inv_freq(rot: int, base: float = 10000.0, factor: float = 1.0, original_len: int = 0,
+                  low: float = 1.0, high: float = 4.0, device="cuda"):
+    """Rotation frequencies base^(-2i/rot), float64 [rot/2], radians a position.  factor > 1
+    stretches them for a longer context: all of them divided by it, or, with original_len, only those
+    that turn fewer than ``low`` times over original_len positions, none of those that turn
+    more than ``high`` times, and a linear blend between."""
+    import torch
+    f = float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64) / max(rot, 1))
+    if factor != 1.0:
+        if original_len:
+            turns = original_len * f / (2.0 * math.pi)
+            keep = ((turns - low) / (high - low)).clamp(0.0, 1.0)
+            f = f * (keep + (1.0 - keep) / factor)
+        else:
+            f = f / factor
+    return f.to(device)
+
+
+def _rope_args(qkv, H, H_kv, positions, inv_freq, wq, wk):
+    """Checks and the leading arguments: (B, N, d, row stride, shape prefix, inv_freq pointer, rot,
+    positions pointer, wq pointer, wk pointer)."""
+    import torch
+    if qkv.dtype != torch.bfloat16 or not qkv.is_cuda or qkv.dim() not in (2, 3):
+        raise ValueError("qkv must be a bf16 CUDA tensor [B, N, (H + 2 H_kv) d] or [T, (H + 2 H_kv) d]")
+    heads, width = H + 2 * H_kv, qkv.shape[-1]
+    if H <= 0 or H_kv <= 0 or H % H_kv != 0 or width % heads != 0:
+        raise ValueError("qkv's rows must hold H + 2 H_kv heads, H a multiple of H_kv")
+    B, N = (1, qkv.shape[0]) if qkv.dim() == 2 else qkv.shape[:2]
+    d, dev = width // heads, qkv.device
+    ld = width
+    if B * N > 1:
+        ld = qkv.stride(-2) if N > 1 else qkv.stride(0)
+        if (width > 1 and qkv.stride(-1) != 1) or (B > 1 and N > 1 and qkv.stride(0) != N * ld):
+            raise ValueError("qkv's rows must be contiguous and evenly spaced")
+    elif B * N == 1 and qkv.stride(-1) != 1:
+        raise ValueError("qkv's rows must be contiguous and evenly spaced")
+    rot = 0
+    fp = pp = None
+    if inv_freq is not None:
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be one-dimensional")
+        rot = 2 * inv_freq.shape[0]
+        fp = _ints(inv_freq, torch.float64, "inv_freq", dev)
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        pp = _ints(positions, torch.int32, "positions", dev, qkv.shape[:-1])
+    w = [None if t is None else _ints(t, torch.bfloat16, "wq and wk", dev, (d,)) for t in (wq, wk)]
+    return B, N, d, ld, fp, rot, pp, w[0], w[1]
+
+
+def qkv_rope(qkv, H: int, H_kv: int, positions=None, inv_freq=None, interleaved: bool = False,
+             wq=None, wk=None, eps: float = 1e-6, rope_scale: float = 1.0, cache=None, slots=None,
+             with_kv: bool = True, stream=None):
+    """q, k, v of a projection's rows: RMS norm of each query and key head where wq, wk (bf16 [d])
+    are given, rotation of the first 2 len(inv_freq) elements by positions (int32, shaped like the
+    rows), head-major layout.  qkv [B, N, (H + 2 H_kv) d] gives q [B, H, N, d] and k, v
+    [B, H_kv, N, d] (attn_fwd dense; attn_fwd_paged for N = 1); qkv [T, ...] gives the packed
+    [H, T, d].  With ``cache`` the K and V rows also go to ``slots`` (int64, shaped like the rows;
+    negative: not stored).  with_kv=False returns None for k and v."""
+    import torch
+    B, N, d, ld, fp, rot, pp, pq, pk = _rope_args(qkv, H, H_kv, positions, inv_freq, wq, wk)
+    dev = qkv.device
+    cs = sp = None
+    if cache is not None:
+        if slots is None:
+            raise ValueError("a cache needs slots")
+        cs = _cache_struct(cache, H_kv, d, dev)
+        sp = _ints(slots, torch.int64, "slots", dev, qkv.shape[:-1] if slots.dim() > 1 else (B * N,))
+    lead = () if qkv.dim() == 2 else (B,)
+    with _launching(dev, stream) as st:
+        q = torch.empty((*lead, H, N, d), dtype=torch.bfloat16, device=dev)
+        k = v = None
+        if with_kv:
+            k = torch.empty((*lead, H_kv, N, d), dtype=torch.bfloat16, device=dev)
+            v = torch.empty_like(k)
+        rc = lib().attn_qkv_rope(qkv.data_ptr(), ld, pq, pk, eps, fp, rot, int(bool(interleaved)),
+                                 rope_scale, pp, q.data_ptr(), k.data_ptr() if with_kv else None,
+                                 v.data_ptr() if with_kv else None,
+                                 ctypes.byref(cs) if cs is not None else None, sp, B, N, H, H_kv, d,
+                                 st)
+    _check("attn_qkv_rope", rc)
+    return q, k, v
+
+
+def qkv_rope_bwd(dq, dk, dv, qkv, positions=None, inv_freq=None, interleaved: bool = False, wq=None,
+                 wk=None, eps: float = 1e-6, rope_scale: float = 1.0, workspace=None, stream=None):
+    """Backward of qkv_rope: the gradient of qkv's rows (contiguous, qkv's shape) from dq [B, H, N, d]
+    (or [H, T, d]) and dk, dv, and fp32 gradients of wq and wk (None where not given)."""
+    import torch
+    H, H_kv = dq.shape[-3], dk.shape[-3]
+    B, N, d, ld, fp, rot, pp, pq, pk = _rope_args(qkv, H, H_kv, positions, inv_freq, wq, wk)
+    dev = qkv.device
+    lead = () if qkv.dim() == 2 else (B,)
+    gp = [_ints(t, torch.bfloat16, name, dev, (*lead, h, N, d))
+          for t, name, h in ((dq, "dq", H), (dk, "dk", H_kv), (dv, "dv", H_kv))]
+    norm = wq is not None or wk is not None
+    need = int(lib().attn_qkv_rope_bwd_workspace_bytes(B, N, H, H_kv, d)) if norm else 0
+    with _launching(dev, stream) as st:
+        dqkv = torch.empty(qkv.shape, dtype=torch.bfloat16, device=dev)
+        if need and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
+            if workspace is not None else (None, 0)
+        make = torch.empty if B * N else torch.zeros
+        dw = [None if w is None else make(d, dtype=torch.float32, device=dev) for w in (wq, wk)]
+        rc = lib().attn_qkv_rope_bwd(*gp, qkv.data_ptr(), ld, pq, pk, eps, fp, rot,
+                                     int(bool(interleaved)), rope_scale, pp, dqkv.data_ptr(),
+                                     (H + 2 * H_kv) * d,
+                                     *(None if w is None else w.data_ptr() for w in dw), B, N, H,
+                                     H_kv, d, *ws, st)
+    _check("attn_qkv_rope_bwd", rc)
+    return dqkv, dw[0], dw[1]
+
+
+def paged_workspace_bytes(B: int, H: int, H_kv: int, d: int) -> int:
+    return int(lib().attn_fwd_paged_workspace_bytes(B, H, H_kv, d))
+
+
+def attn_fwd_paged(q, cache, block_table, seq_lens, scale: float | None = None, workspace=None,
+                   out=None, lse=None, stream=None):
+    """Attention of one new token of each request over a paged cache: q [B, H, 1, d] (or [B, H, d]),
+    block_table int32 [B, max_pages], seq_lens int32 [B] (rows in the cache, the new token's own
+    among them).  Returns (O bf16 like q, LSE fp32 [B, H, 1] or [B, H])."""
+    import torch
+    dev = q.device
+    if q.dtype != torch.bfloat16 or not q.is_cuda or not q.is_contiguous() or \
+            not (q.dim() == 3 or (q.dim() == 4 and q.shape[2] == 1)):
+        raise ValueError("q must be a contiguous bf16 CUDA tensor [B, H, 1, d] or [B, H, d]")
+    B, H, d = q.shape[0], q.shape[1], q.shape[-1]
+    if cache.k.dim() != 4 or cache.k.shape[1] == 0 or H % cache.k.shape[1] != 0:
+        raise ValueError("the number of K/V heads must divide the number of query heads")
+    H_kv = cache.k.shape[1]
+    cs = _cache_struct(cache, H_kv, d, dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    tp = _ints(block_table, torch.int32, "block_table", dev, (B, block_table.shape[1]))
+    lp = _ints(seq_lens, torch.int32, "seq_lens", dev, (B,))
+    for t, dt, shape, name in ((out, torch.bfloat16, q.shape, "out"),
+                               (lse, torch.float32, q.shape[:-1], "lse")):
+        if t is not None:
+            _ints(t, dt, name, dev, shape)
+    with _launching(dev, stream) as st:
+        if workspace is None:
+            workspace = torch.empty(max(paged_workspace_bytes(B, H, H_kv, d), 1), dtype=torch.uint8,
+                                    device=dev)
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+        rc = lib().attn_fwd_paged(q.data_ptr(), ctypes.byref(cs), tp, lp, out.data_ptr(),
+                                  lse.data_ptr(), B, H, H_kv, d, block_table.shape[1],
+                                  scale if scale is not None else 1.0 / math.sqrt(d),
+                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                  st)
+    _check("attn_fwd_paged", rc)
     return out, lse
 
 

@@ -11,6 +11,7 @@
 #include "attn_host.h"
 #include "attn_bwd.h"
 #include "attn_fp8.h"
+#include "attn_gen.h"
 #include "attn_params.h"
 
 namespace attn {
@@ -78,6 +79,24 @@ int encode_u8_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t r
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+// A paged cache [pages][heads][page_size][d] with its own stride from page to page, box 128 bytes
+// (64 for one-byte rows of 64) x box_rows, swizzled as wide as the box.
+int encode_cache_map(CUtensorMap* map, const void* base, bool e4m3, uint64_t d, uint64_t page_size,
+                     uint64_t heads, uint64_t pages, uint64_t page_stride, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return CUDA_ERROR_NOT_FOUND;
+  const uint64_t size = e4m3 ? 1 : 2;
+  const uint64_t row = d * size;
+  const cuuint64_t dims[4] = {d, page_size, heads, pages};
+  const cuuint64_t strides[3] = {row, row * page_size, page_stride * size};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>((row < 128 ? row : 128) / size), box_rows, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 

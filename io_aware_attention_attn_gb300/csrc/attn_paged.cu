@@ -1,0 +1,699 @@
+// attn_paged.cu -- attention of one new token per request over a paged key-value cache.
+//
+// For each (request s, K/V head, group of up to 32 of its query rows) -- a unit -- with K, V the
+// request's rows:  S = scale Q K^T,  O = softmax(S) V,  read once in tiles of 64 keys.
+//
+// What bounds it: reading K and V.  A key costs 4 d bytes (bf16) and 4 d operations a query row, so at
+// up to 32 rows the tensor work is far below what the copy takes and the kernel is built around the
+// copies: a producer warp fills a ring of tiles by TMA (one box per page part), four consumer
+// warps each take 16 of a tile's 64 keys and never wait for one another inside a unit.
+//
+// Products: with few query rows the keys go on the 16-row side of the warp product,
+// S^T[keys x rows] = K Q^T and O^T[d x rows] += V^T P^T, rows in groups of 8 -- half the products and
+// half the registers of the other orientation at up to 8 rows.  (A tcgen05 product has 64 or 128
+// rows at least, its result sits in tensor memory, and each tile would pay a
+// commit, a load and two hand-offs between warps; a warp product leaves everything in registers.)
+// P^T needs the score tile transposed between the products: two movmatrix per 8 rows.
+//
+// Softmax: each warp keeps a reference maximum m of its own keys per row (log2 units) that trails
+// the true one by at most 8, so P <= 256; the maximum is looked for across lanes only when some
+// score passes m + 8.  Row sums stay per lane until a unit ends.
+//
+// E4M3 cache: codes become f16 on the way from shared memory to the product (exact); q becomes f16
+// after a power-of-two scaling of its row (exact down to 2^-22 of the row's largest element); a
+// key's K scale multiplies its scores, its V scale its P, divided by the largest V scale the warp has
+// seen so that P V operands stay in f16's range.
+//
+// Work split: the tiles of all units in order (request, head, row group) are cut into equal runs, one a
+// CTA.  A unit inside one run is finished by its CTA; the parts of a unit that spans several runs go to
+// the workspace, at most two a CTA, and paged_join_kernel merges them.  The CTA that holds a
+// unit's end but not its start leaves the merge's description.
+#include "attn_gen.cuh"
+#include "attn_gen.h"
+#include "sm103_ptx.cuh"
+
+#include <atomic>
+#include <cmath>
+
+namespace attn {
+namespace {
+
+constexpr int kWarps = 4;                        // consumer warps
+constexpr int kThreads = (kWarps + 1) * 32;      // and one producer warp
+constexpr float kTrail = 8.f;                    // how far m may trail (log2 units)
+enum : int { kRoleProducer = 7, kRoleConsumer = 8 };
+
+template <int D, bool E4M3, int NT>
+struct PagedSmem {
+  static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
+  static constexpr int kBlk = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a row in one box
+  static constexpr int kBlks = kRowBytes / kBlk;                  // boxes side by side
+  static constexpr int kSide = kPagedTile * kRowBytes;            // K or V of a tile
+  static constexpr int kStage = 2 * kSide;
+  static constexpr int kCtas = NT <= 2 ? 2 : 1;                   // per SM
+  static constexpr int kRing = (kCtas == 2 ? 98304 : 196608);
+  static constexpr int kStages = kRing / kStage < 8 ? kRing / kStage : 8;
+  static constexpr int kScales = kStages * kStage;                // [stage][2][64] fp32
+  static constexpr int kMerge = kScales + (E4M3 ? kStages * 2 * kPagedTile * 4 : 0);
+  static constexpr int kMergeLd = D + 4;                          // spreads rows over the banks
+  static constexpr int kStat = kMerge + 2 * 8 * kMergeLd * 4;     // [2][warp][8 rows][2]
+  static constexpr int kBar = kStat + 2 * kWarps * 8 * 2 * 4;
+  static constexpr int kMisc = kBar + 2 * kStages * 8;
+  static constexpr int kBytes = kMisc + 32;
+  static constexpr int kDyn = kBytes + 1024;
+  static_assert(kCtas * (kDyn + 1024) <= 233472, "paged ring exceeds shared memory");
+};
+
+// The unit and tile a CTA is at.
+struct Walk {
+  int s, h, rg, t, n, len;  // request, K/V head, row group, tile, tiles of the request, its length
+};
+
+__device__ __forceinline__ int req_len(const PagedParams& p, int s) {
+  const int most = p.max_pages << p.page_shift;
+  return min(max(p.seq_lens[s], 0), most);
+}
+// A request of length 0 has one empty tile, so that its O and lse are written.
+__device__ __forceinline__ int req_tiles(int len) {
+  return max((len + kPagedTile - 1) / kPagedTile, 1);
+}
+__device__ __forceinline__ void next_unit(const PagedParams& p, Walk& w) {
+  w.t = 0;
+  if (++w.rg < p.n_rg) return;
+  w.rg = 0;
+  if (++w.h < p.H_kv) return;
+  w.h = 0;
+  if (++w.s < p.B) {
+    w.len = req_len(p, w.s);
+    w.n = req_tiles(w.len);
+  }
+}
+// Walk at tile `at` of the whole order (a warp's lanes together); returns the first tile of its unit.
+__device__ long long find(const PagedParams& p, long long at, Walk& w) {
+  const int lane = threadIdx.x & 31, per = p.H_kv * p.n_rg;
+  long long before = 0;
+  for (int s0 = 0; s0 < p.B; s0 += 32) {
+    const int s = s0 + lane;
+    const int len = s < p.B ? req_len(p, s) : 0;
+    const int n = s < p.B ? req_tiles(len) : 0;
+    long long scan = static_cast<long long>(n) * per;
+    #pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, scan, off);
+      if (lane >= off) scan += up;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, before + scan > at);
+    if (past) {
+      const int k = __ffs(past) - 1;
+      const long long own = scan - static_cast<long long>(n) * per;
+      before += __shfl_sync(0xffffffffu, own, k);
+      w.s = s0 + k;
+      w.n = __shfl_sync(0xffffffffu, n, k);
+      w.len = __shfl_sync(0xffffffffu, len, k);
+      const long long in = at - before;
+      const int u = static_cast<int>(in / w.n);
+      w.t = static_cast<int>(in - static_cast<long long>(u) * w.n);
+      w.h = u / p.n_rg;
+      w.rg = u - w.h * p.n_rg;
+      return at - w.t;
+    }
+    before += __shfl_sync(0xffffffffu, scan, 31);
+  }
+  w = Walk{p.B, 0, 0, 0, 1, 0};
+  return at;
+}
+
+template <int D, bool E4M3, int NT>
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
+paged_kernel(const __grid_constant__ PagedParams p) {
+  using L = PagedSmem<D, E4M3, NT>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (base - smem_u32(smem_raw));
+  int* misc = reinterpret_cast<int*>(sm + L::kMisc);  // [0] abort [2..3] total tiles (64-bit)
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto full = [&](int st) { return base + L::kBar + st * 8; };
+  auto empty = [&](int st) { return base + L::kBar + (L::kStages + st) * 8; };
+  if (tid == 0) {
+    misc[0] = 0;
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), kWarps);
+    }
+    fence_barrier_init();
+  }
+  // tiles of all units
+  long long mine = 0;
+  for (int s = tid; s < p.B; s += kThreads) mine += req_tiles(req_len(p, s));
+  #pragma unroll
+  for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
+  long long* sums = reinterpret_cast<long long*>(sm + L::kMerge);
+  if (lane == 0) sums[warp] = mine;
+  __syncthreads();
+  long long total = 0;
+  for (int i = 0; i <= kWarps; ++i) total += sums[i];
+  total *= p.H_kv * p.n_rg;
+  __syncthreads();
+  const long long G = min(static_cast<long long>(gridDim.x), total);
+  const long long i = blockIdx.x;
+  pdl_launch_dependents();
+  if (i >= G) {
+    if (tid == 0) p.joins[i] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  const long long w0 = i * total / G, w1 = (i + 1) * total / G;
+  Walk w;
+  const long long unit0 = find(p, w0, w);
+  const WaitCtx ctx{misc, p.status};
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------------------------ producer
+    if (lane == 0) {
+      // the unit that ends here and began in an earlier CTA, and where its parts are
+      int4 join = make_int4(-1, 0, 0, 0);
+      if (unit0 < w0 && unit0 + w.n <= w1) {
+        const long long i0 = ((unit0 + 1) * G - 1) / total;
+        join = make_int4((w.s * p.H_kv + w.h) * p.n_rg + w.rg, static_cast<int>(i0),
+                         i0 * total / G < unit0 ? 1 : 0, 0);
+      }
+      p.joins[i] = join;
+      tma_prefetch_desc(&p.tm_k);
+      tma_prefetch_desc(&p.tm_v);
+    }
+    const uint64_t policy = l2_policy_evict_first();
+    const int box_shift = 31 - __clz(p.box_rows);
+    const int parts_tile = kPagedTile >> box_shift;
+    const int ops = parts_tile * 2 * L::kBlks;
+    int entries = 0, entry_base = -1, entry_s = -1;  // lane's entry of the 32 looked up last
+    bool ok = true;
+    long long it = 0;
+    for (long long g = w0; g < w1 && ok; ++g, ++it) {
+      const int st = static_cast<int>(it % L::kStages);
+      const int rows = min(kPagedTile, w.len - w.t * kPagedTile);
+      const int parts = rows > 0 ? (rows + p.box_rows - 1) >> box_shift : 0;
+      const int page0 = (w.t * kPagedTile) >> p.page_shift;
+      if (parts > 0 && (entry_s != w.s || page0 < entry_base || page0 + parts_tile > entry_base + 32)) {
+        entry_s = w.s;
+        entry_base = page0;
+        const int e = page0 + lane;
+        const int have = (w.len + (1 << p.page_shift) - 1) >> p.page_shift;
+        entries = e < have ? p.table[static_cast<size_t>(w.s) * p.max_pages + e] : 0;
+        if (e < have && static_cast<unsigned>(entries) >= static_cast<unsigned>(p.num_pages)) {
+          atomicCAS(p.status, 0, kStatusBadPage);
+          entries = -1;
+        }
+      }
+      if (it >= L::kStages)
+        ok = mbar_wait_warp(empty(st), static_cast<uint32_t>((it / L::kStages - 1) & 1), ctx,
+                            kRoleProducer, 1);
+      if (!ok) break;
+      // lane -> (part, block, K or V); every lane takes part in the look-up of its page
+      const uint32_t stage = base + st * L::kStage;
+      const int per_part = 2 * L::kBlks;
+      int bad_parts = 0;
+      for (int q = 0; q < parts; ++q) {
+        const int pg = __shfl_sync(0xffffffffu, entries,
+                                   ((w.t * kPagedTile + q * p.box_rows) >> p.page_shift) - entry_base);
+        if (E4M3 && pg < 0) {
+          ++bad_parts;  // no scales to copy: zeros
+          for (int r = lane; r < 2 * p.box_rows; r += 32) {
+            const int side = r >> box_shift, row = r & (p.box_rows - 1);
+            reinterpret_cast<float*>(sm + L::kScales)[(st * 2 + side) * kPagedTile +
+                                                      q * p.box_rows + row] = 0.f;
+          }
+          fence_proxy_async_smem();
+        }
+      }
+      __syncwarp();
+      if (lane == 0) {
+        uint32_t bytes = static_cast<uint32_t>(parts) * p.box_rows * 2 * L::kRowBytes;
+        if (E4M3) bytes += static_cast<uint32_t>(parts - bad_parts) * p.box_rows * 8;
+        mbar_arrive_expect_tx(full(st), bytes);
+      }
+      __syncwarp();
+      {
+        const int q = lane / per_part, o = lane % per_part;
+        const int side = o / L::kBlks, blk = o % L::kBlks;
+        const int row0 = w.t * kPagedTile + q * p.box_rows;
+        const int at = (row0 >> p.page_shift) - entry_base;
+        const int pg = __shfl_sync(0xffffffffu, entries, at & 31);
+        if (lane < ops && q < parts) {
+          const uint32_t dst = stage + side * L::kSide + blk * (kPagedTile * L::kBlk) +
+                               q * p.box_rows * L::kBlk;
+          const int y = row0 & ((1 << p.page_shift) - 1);
+          tma_load_4d_hint(dst, side ? &p.tm_v : &p.tm_k, full(st), blk * (L::kBlk / (E4M3 ? 1 : 2)),
+                           y, w.h, pg >= 0 ? pg : p.num_pages, policy);
+          if (E4M3 && blk == 0 && pg >= 0) {
+            const float* src = (side ? p.vs : p.ks) +
+                               (((static_cast<int64_t>(pg) * p.H_kv + w.h) << p.page_shift) + y);
+            bulk_load_1d(base + L::kScales + ((st * 2 + side) * kPagedTile + q * p.box_rows) * 4, src,
+                         p.box_rows * 4, full(st));
+          }
+        }
+      }
+      if (++w.t == w.n) next_unit(p, w);
+    }
+    if (!ok) {  // copies in flight land before the CTA's shared memory goes
+      const long long from = it > L::kStages ? it - L::kStages : 0;
+      for (long long k = from; k < it; ++k)
+        mbar_wait_drain(full(static_cast<int>(k % L::kStages)),
+                        static_cast<uint32_t>((k / L::kStages) & 1));
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------------------------- consumers
+  const int g = lane >> 2, q4 = lane & 3;
+  constexpr int kSteps = D / 16;      // k16 steps of S, m16 tiles of O^T
+  bool dead = false;                  // a wait gave up: go through the motions, compute nothing
+  long long it = 0, cur = w0;
+  int merges = 0, seg = 0;
+  float* merge = reinterpret_cast<float*>(sm + L::kMerge);
+  float* stat = reinterpret_cast<float*>(sm + L::kStat);
+  while (cur < w1) {
+    const long long left = w1 - cur;
+    const int t_end = static_cast<int>(min(static_cast<long long>(w.n), w.t + left));
+    const int t_begin = w.t;
+    const int row0 = w.rg * p.rg_rows, rows = min(p.rg_rows, p.group - row0);
+    const __nv_bfloat16* qg =
+        p.q + (static_cast<int64_t>(w.s) * p.H + static_cast<int64_t>(w.h) * p.group + row0) * D;
+    // B operand of K Q^T: lane (g, q4) holds, of query row g, the elements its k positions stand for
+    uint32_t qf[NT][kSteps][2];
+    float mul[NT][2];  // rows 2 q4, 2 q4 + 1: score factor (log2 units)
+    #pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g;
+      #pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        qf[nt][k][0] = qf[nt][k][1] = 0u;
+        if (r < rows) {
+          const __nv_bfloat16* src = qg + r * D + 16 * k;
+          if (E4M3) {  // codes 4 q4 .. 4 q4 + 3 of a key arrive in one register
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + 4 * q4));
+            qf[nt][k][0] = v.x;
+            qf[nt][k][1] = v.y;
+          } else {
+            qf[nt][k][0] = __ldg(reinterpret_cast<const uint32_t*>(src + 2 * q4));
+            qf[nt][k][1] = __ldg(reinterpret_cast<const uint32_t*>(src + 2 * q4 + 8));
+          }
+        }
+      }
+      if (E4M3) {
+        float amax = 0.f;
+        #pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+          #pragma unroll
+          for (int j = 0; j < 2; ++j)
+            amax = fmaxf(amax, fmaxf(fabsf(bf16lo_to_f32(qf[nt][k][j])),
+                                     fabsf(bf16hi_to_f32(qf[nt][k][j]))));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // largest element to 2^8 .. 2^9: its exponent field, kept where both factors are normal
+        const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23), 16), 254) - 8;
+        const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^(127 - e)
+        const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);          // 2^(e - 127)
+        #pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+          #pragma unroll
+          for (int j = 0; j < 2; ++j)
+            qf[nt][k][j] = pack_f16x2(bf16lo_to_f32(qf[nt][k][j]) * down,
+                                      bf16hi_to_f32(qf[nt][k][j]) * down);
+        mul[nt][0] = p.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * q4) * 4);
+        mul[nt][1] = p.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * q4 + 1) * 4);
+      } else {
+        mul[nt][0] = mul[nt][1] = p.scale_log2;
+      }
+    }
+    float acc[NT][kSteps][4], m[NT][2], l[NT][2];
+    float vref = 0.f, vinv = 0.f;
+    #pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+      #pragma unroll
+      for (int k = 0; k < kSteps; ++k)
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) acc[nt][k][j] = 0.f;
+    }
+
+    for (int t = t_begin; t < t_end; ++t, ++it) {
+      const int st = static_cast<int>(it % L::kStages);
+      if (!dead && !mbar_wait_warp(full(st), static_cast<uint32_t>((it / L::kStages) & 1), ctx,
+                                   kRoleConsumer, 2))
+        dead = true;
+      const int live = w.len - t * kPagedTile - warp * 16;  // of this warp's 16 keys
+      if (!dead && live > 0) {
+        const uint32_t kst = base + st * L::kStage, vst = kst + L::kSide;
+        float s[NT][4];
+        #pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+        if (!E4M3) {
+          const int key = warp * 16 + (lane & 15);
+          #pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            const int chunk = (k & 3) * 2 + (lane >> 4);
+            uint32_t a[4];
+            ldsm4(kst + (k >> 2) * (kPagedTile * 128) + key * 128 + ((chunk ^ (key & 7)) << 4), a);
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816<false>(s[nt], a[0], a[1], a[2], a[3], qf[nt][k][0], qf[nt][k][1]);
+          }
+        } else {
+          const int key = warp * 16 + (lane & 15);
+          #pragma unroll
+          for (int k = 0; k < kSteps; k += 2) {
+            const int chunk = k + (lane >> 4);
+            const int sw = L::kBlk == 128 ? chunk ^ (key & 7) : chunk ^ ((key >> 1) & 3);
+            uint32_t a[4];
+            ldsm4(kst + key * L::kBlk + (sw << 4), a);
+            #pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t lo0 = e4m3x2_to_f16x2(a[2 * j]), hi0 = e4m3x2_to_f16x2(a[2 * j] >> 16);
+              const uint32_t lo1 = e4m3x2_to_f16x2(a[2 * j + 1]),
+                             hi1 = e4m3x2_to_f16x2(a[2 * j + 1] >> 16);
+              #pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816<true>(s[nt], lo0, lo1, hi0, hi1, qf[nt][k + j][0], qf[nt][k + j][1]);
+            }
+          }
+        }
+        // lane (g, q4): s[0], s[1] = key g, rows 2 q4, 2 q4 + 1;  s[2], s[3] = key g + 8
+        const bool in0 = g < live, in1 = g + 8 < live;
+        float sk0 = 1.f, sk1 = 1.f, sv0 = 1.f, sv1 = 1.f;
+        if (E4M3) {
+          const float* sc =
+              reinterpret_cast<const float*>(sm + L::kScales) + st * 2 * kPagedTile + warp * 16;
+          sk0 = sc[g];
+          sk1 = sc[g + 8];
+          sv0 = in0 ? sc[kPagedTile + g] : 0.f;
+          sv1 = in1 ? sc[kPagedTile + g + 8] : 0.f;
+        }
+        bool grow = E4M3 && (sv0 > vref || sv1 > vref);
+        #pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          s[nt][0] = in0 ? s[nt][0] * (mul[nt][0] * sk0) : -INFINITY;
+          s[nt][1] = in0 ? s[nt][1] * (mul[nt][1] * sk0) : -INFINITY;
+          s[nt][2] = in1 ? s[nt][2] * (mul[nt][0] * sk1) : -INFINITY;
+          s[nt][3] = in1 ? s[nt][3] * (mul[nt][1] * sk1) : -INFINITY;
+          grow |= fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + kTrail ||
+                  fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + kTrail;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+          float vscale = 1.f;
+          if (E4M3) {
+            float vm = fmaxf(vref, fmaxf(sv0, sv1));
+            #pragma unroll
+            for (int off = 4; off < 32; off <<= 1)
+              vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, off));
+            vscale = vm > 0.f ? vref / vm : 1.f;
+            vref = vm;
+            vinv = vm > 0.f ? 1.f / vm : 0.f;
+          }
+          #pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float c[2];
+            #pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float top = fmaxf(m[nt][j], fmaxf(s[nt][j], s[nt][j + 2]));
+              #pragma unroll
+              for (int off = 4; off < 32; off <<= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+              c[j] = top == -INFINITY ? 1.f : ex2_approx(m[nt][j] - top);
+              m[nt][j] = top;
+              l[nt][j] *= c[j];
+              c[j] *= vscale;
+            }
+            #pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+              acc[nt][k][0] *= c[0];
+              acc[nt][k][1] *= c[1];
+              acc[nt][k][2] *= c[0];
+              acc[nt][k][3] *= c[1];
+            }
+          }
+        }
+        uint32_t pf[NT][2];
+        #pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float r0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+          const float r1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+          const float p0 = ex2_approx(s[nt][0] - r0), p1 = ex2_approx(s[nt][1] - r1);
+          const float p2 = ex2_approx(s[nt][2] - r0), p3 = ex2_approx(s[nt][3] - r1);
+          l[nt][0] += p0 + p2;
+          l[nt][1] += p1 + p3;
+          if (E4M3) {
+            const float f0 = sv0 * vinv, f1 = sv1 * vinv;
+            pf[nt][0] = transpose8x8(pack_f16x2(p0 * f0, p1 * f0));
+            pf[nt][1] = transpose8x8(pack_f16x2(p2 * f1, p3 * f1));
+          } else {
+            pf[nt][0] = transpose8x8(pack_bf16x2(p0, p1));
+            pf[nt][1] = transpose8x8(pack_bf16x2(p2, p3));
+          }
+        }
+        // V rows past the request's end may hold anything: taken as zero
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if (live < 16) {
+          keep0 = (2 * q4 < live ? 0xffffu : 0u) | (2 * q4 + 1 < live ? 0xffff0000u : 0u);
+          keep1 = (2 * q4 + 8 < live ? 0xffffu : 0u) | (2 * q4 + 9 < live ? 0xffff0000u : 0u);
+        }
+        if (!E4M3) {
+          const int key = warp * 16 + ((lane >> 4) << 3) + (lane & 7);
+          #pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            const int chunk = (k & 3) * 2 + ((lane >> 3) & 1);
+            uint32_t a[4];
+            ldsm4_t(vst + (k >> 2) * (kPagedTile * 128) + key * 128 + ((chunk ^ (key & 7)) << 4), a);
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816<false>(acc[nt][k], a[0] & keep0, a[1] & keep0, a[2] & keep1, a[3] & keep1,
+                              pf[nt][0], pf[nt][1]);
+          }
+        } else {
+          const int key = warp * 16 + (lane & 15);
+          #pragma unroll
+          for (int k = 0; k < kSteps; k += 2) {
+            const int chunk = k + (lane >> 4);
+            const int sw = L::kBlk == 128 ? chunk ^ (key & 7) : chunk ^ ((key >> 1) & 3);
+            uint32_t a[4];
+            ldsm4_t(vst + key * L::kBlk + (sw << 4), a);
+            // a register: key pair x columns 2g, 2g + 1; split into the column's key pairs
+            #pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t x0 = __byte_perm(a[2 * j], 0, 0x3120);
+              const uint32_t x1 = __byte_perm(a[2 * j + 1], 0, 0x3120);
+              const uint32_t v0 = e4m3x2_to_f16x2(x0) & keep0, v1 = e4m3x2_to_f16x2(x0 >> 16) & keep0;
+              const uint32_t v2 = e4m3x2_to_f16x2(x1) & keep1, v3 = e4m3x2_to_f16x2(x1 >> 16) & keep1;
+              #pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816<true>(acc[nt][k + j], v0, v1, v2, v3, pf[nt][0], pf[nt][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(st));
+    }
+
+    // ---- end of the unit (or of this CTA's part of it): the four warps' results become one
+    const bool whole = t_begin == 0 && t_end == w.n;
+    const int slot = static_cast<int>(2 * i) + (seg > 0 ? 1 : 0);
+    #pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float* st2 = stat + (merges & 1) * kWarps * 16;
+      ++merges;
+      #pragma unroll
+      for (int j = 0; j < 2; ++j)
+        #pragma unroll
+        for (int off = 4; off < 32; off <<= 1)
+          l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], off);
+      if (g == 0) {
+        #pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          st2[(warp * 8 + 2 * q4 + j) * 2] = m[nt][j];
+          st2[(warp * 8 + 2 * q4 + j) * 2 + 1] = l[nt][j];
+        }
+      }
+      named_barrier_sync(1, kWarps * 32);
+      #pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float top = -INFINITY;
+        #pragma unroll
+        for (int x = 0; x < kWarps; ++x) top = fmaxf(top, st2[(x * 8 + 2 * q4 + j) * 2]);
+        // m = -inf: no finite score, so acc and l are 0 (or NaN, which stays)
+        const float c = (m[nt][j] == -INFINITY ? 1.f : ex2_approx(m[nt][j] - top)) *
+                        (E4M3 ? vref : 1.f);
+        #pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          acc[nt][k][j] *= c;
+          acc[nt][k][j + 2] *= c;
+        }
+      }
+      // element (row, column) of this lane's j-th accumulator of tile k
+      auto cell = [&](int k, int j) {
+        const int row = 2 * q4 + (j & 1);
+        const int col = E4M3 ? 16 * k + 2 * g + (j >> 1) : 16 * k + g + 8 * (j >> 1);
+        return row * L::kMergeLd + col;
+      };
+      float* mine2 = merge + (warp & 1) * 8 * L::kMergeLd;
+      if (warp >= 2) {
+        #pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+          #pragma unroll
+          for (int j = 0; j < 4; ++j) mine2[cell(k, j)] = acc[nt][k][j];
+      }
+      named_barrier_sync(1, kWarps * 32);
+      if (warp < 2) {
+        #pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+          #pragma unroll
+          for (int j = 0; j < 4; ++j) mine2[cell(k, j)] += acc[nt][k][j];
+      }
+      named_barrier_sync(1, kWarps * 32);
+      for (int e = tid; e < 8 * (D / 4); e += kWarps * 32) {
+        const int r = e / (D / 4), c4 = e % (D / 4);
+        const int row = nt * 8 + r;
+        if (row >= rows) continue;
+        float top = -INFINITY, sum = 0.f;
+        #pragma unroll
+        for (int x = 0; x < kWarps; ++x) top = fmaxf(top, st2[(x * 8 + r) * 2]);
+        #pragma unroll
+        for (int x = 0; x < kWarps; ++x) {
+          const float mx = st2[(x * 8 + r) * 2];
+          sum += (mx == -INFINITY ? 1.f : ex2_approx(mx - top)) * st2[(x * 8 + r) * 2 + 1];
+        }
+        const float4 a = *reinterpret_cast<const float4*>(merge + r * L::kMergeLd + 4 * c4);
+        const float4 b =
+            *reinterpret_cast<const float4*>(merge + (8 + r) * L::kMergeLd + 4 * c4);
+        float4 v = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+        if (whole) {
+          const float inv = w.len > 0 ? 1.f / sum : 0.f;
+          const int64_t at = static_cast<int64_t>(w.s) * p.H +
+                             static_cast<int64_t>(w.h) * p.group + row0 + row;
+          *reinterpret_cast<uint2*>(p.o + at * D + 4 * c4) =
+              make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+          if (c4 == 0)
+            p.lse[at] = sum > 0.f || sum != sum ? (top + log2f(sum)) * 0.69314718055994530942f
+                                                : -INFINITY;
+        } else {
+          const int64_t at = static_cast<int64_t>(slot) * p.rg_rows + row;
+          *reinterpret_cast<float4*>(p.part_o + at * D + 4 * c4) = v;
+          if (c4 == 0)
+            *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(top, sum);
+        }
+      }
+    }
+    cur += t_end - t_begin;
+    ++seg;
+    next_unit(p, w);
+  }
+}
+
+// Merge of the parts of the unit that CTA blockIdx.x ended: part of CTA i0 (its last), then the
+// first of each CTA up to blockIdx.x.  M = max m_j, weights 2^(m_j - M).  Four warps take every
+// fourth part each; a lane holds d/32 columns.
+template <int D>
+__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedParams p) {
+  constexpr int kPer = D / 32;
+  __shared__ float s_o[4][D], s_l[4];
+  pdl_wait();
+  const int4 join = p.joins[blockIdx.x];
+  if (join.x < 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i0 = join.y, n = static_cast<int>(blockIdx.x) - i0 + 1;
+  const int rg = join.x % p.n_rg, sh = join.x / p.n_rg;
+  const int row0 = rg * p.rg_rows, rows = min(p.rg_rows, p.group - row0);
+  auto part = [&](int j) { return 2 * (i0 + j) + (j == 0 ? join.z : 0); };
+  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+    float M = -INFINITY;
+    for (int j = lane; j < n; j += 32)
+      M = fmaxf(M, p.part_ml[(static_cast<int64_t>(part(j)) * p.rg_rows + row) * 2]);
+    #pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float acc[kPer], le = 0.f;
+    #pragma unroll
+    for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
+    #pragma unroll 4
+    for (int j = warp; j < n; j += 4) {
+      const int64_t at = static_cast<int64_t>(part(j)) * p.rg_rows + row;
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+      const float wt = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - M);  // 0 or NaN parts
+      le += wt * ml.y;
+      const float* src = p.part_o + at * D + lane * kPer;
+      if constexpr (kPer == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        acc[0] = fmaf(wt, x.x, acc[0]);
+        acc[1] = fmaf(wt, x.y, acc[1]);
+        acc[2] = fmaf(wt, x.z, acc[2]);
+        acc[3] = fmaf(wt, x.w, acc[3]);
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        acc[0] = fmaf(wt, x.x, acc[0]);
+        acc[1] = fmaf(wt, x.y, acc[1]);
+      }
+    }
+    #pragma unroll
+    for (int c = 0; c < kPer; ++c) s_o[warp][lane * kPer + c] = acc[c];
+    if (lane == 0) s_l[warp] = le;
+    __syncthreads();
+    const float total = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+    const int64_t out = static_cast<int64_t>(sh / p.H_kv) * p.H +
+                        static_cast<int64_t>(sh % p.H_kv) * p.group + row0 + row;
+    const int c = threadIdx.x;
+    if (c < D)
+      p.o[out * D + c] =
+          __float2bfloat16((s_o[0][c] + s_o[1][c] + s_o[2][c] + s_o[3][c]) * (1.f / total));
+    if (c == 0)
+      p.lse[out] = total > 0.f || total != total ? (M + log2f(total)) * 0.69314718055994530942f
+                                                 : -INFINITY;
+    __syncthreads();
+  }
+}
+
+template <int D, bool E4M3, int NT>
+cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
+  using L = PagedSmem<D, E4M3, NT>;
+  auto* kernel = paged_kernel<D, E4M3, NT>;
+  static std::atomic<uint64_t> attr_done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDyn);
+    if (e != cudaSuccess) return e;
+    attr_done.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  const int most = L::kCtas * (kPagedMaxCtas / 2);
+  if (ctas > most) ctas = most;
+  kernel<<<ctas, kThreads, L::kDyn, stream>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(p.rg_rows < 8 ? p.rg_rows : 8));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p)) != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_rows(const PagedParams& p, int ctas, cudaStream_t stream) {
+  if (p.rg_rows <= 8) return launch<D, E4M3, 1>(p, ctas, stream);
+  if (p.rg_rows <= 16) return launch<D, E4M3, 2>(p, ctas, stream);
+  return launch<D, E4M3, 4>(p, ctas, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_fwd_paged(const PagedParams& p, int d, bool e4m3, long long max_units,
+                             cudaStream_t stream) {
+  const int ctas = static_cast<int>(max_units < kPagedMaxCtas ? max_units : kPagedMaxCtas);
+  if (d == 64) return e4m3 ? launch_rows<64, true>(p, ctas, stream) : launch_rows<64, false>(p, ctas, stream);
+  return e4m3 ? launch_rows<128, true>(p, ctas, stream) : launch_rows<128, false>(p, ctas, stream);
+}
+
+}  // namespace attn
