@@ -11,11 +11,12 @@ Layouts (same as the C ABI in ``include/attn_gb300.h``):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
 from typing import Any, NamedTuple
+
+import torch
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libattn_gb300.so")
 
@@ -302,15 +303,8 @@ class KVCache(NamedTuple):
     v_scale: Any = None
 
 
-class _CacheStruct(ctypes.Structure):  # attn_kv_cache in the header
-    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("page_stride", _L),
-                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
-                ("dtype", ctypes.c_int32)]
-
-
 def kv_cache(num_pages: int, H_kv: int, page_size: int, d: int, dtype=None, device="cuda") -> KVCache:
     """An empty cache (zeros): bf16, or E4M3 with dtype torch.float8_e4m3fn."""
-    import torch
     dtype = torch.bfloat16 if dtype is None else dtype
     if dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8):
         raise ValueError("a cache is bf16 or float8_e4m3fn")
@@ -323,58 +317,30 @@ def kv_cache(num_pages: int, H_kv: int, page_size: int, d: int, dtype=None, devi
                            for _ in range(2)))
 
 
-def _cache_struct(cache, H_kv, d, device):
-    import torch
-    k, v = cache.k, cache.v
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != device or \
-            v.device != device:
-        raise ValueError("cache k and v must be [num_pages, H_kv, page_size, d] tensors of one type "
-                         "on q's device")
-    n, h, page, dd = k.shape
-    if h != H_kv or dd != d:
-        raise ValueError("the cache's heads or head dim differ from the inputs'")
-    stride = k.stride()
-    inner = (page * d, d, 1)
-    if v.stride() != stride or any(s != w and e != 1 for s, w, e in zip(stride[1:], inner, (h, page, d))):
-        raise ValueError("cache pages must be contiguous, with one page stride for k and v")
-    page_stride = stride[0] if n > 1 else h * page * d
-    ks = vs = None
-    if k.dtype == torch.bfloat16:
-        dtype = 0
-    elif k.dtype in (torch.float8_e4m3fn, torch.uint8):
-        dtype = 1
-        for t in (cache.k_scale, cache.v_scale):
-            if t is None or t.dtype != torch.float32 or t.shape != k.shape[:3] or \
-                    not t.is_contiguous() or t.device != device:
-                raise ValueError("an E4M3 cache needs contiguous fp32 k_scale and v_scale "
-                                 "[num_pages, H_kv, page_size]")
-        ks, vs = cache.k_scale.data_ptr(), cache.v_scale.data_ptr()
-    else:
-        raise ValueError("a cache is bf16, float8_e4m3fn or uint8 codes")
-    return _CacheStruct(k.data_ptr(), v.data_ptr(), ks, vs, page_stride, n, page, dtype)
+_native_module = None
 
 
-@contextlib.contextmanager
-def _launching(device, stream):
-    """The device made current, and torch's allocations made on the launching stream (so that a
-    buffer released after the call is not handed out before the work is done); yields the handle."""
-    import torch
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-        else:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+def _native():
+    """The marshalling module of the generation path (csrc/py_binding.cpp), loaded once.  Its
+    functions check the tensors, allocate the outputs and call the C entry point on the current stream of
+    the tensors' device; in Python and ctypes that took several times as long as these kernels."""
+    global _native_module
+    if _native_module is None:
+        lib()
+        from . import _attn_binding
+        _attn_binding.set_error(AttnError)
+        _native_module = _attn_binding
+    return _native_module
 
 
-def _ints(t, dtype, name, device, shape=None):
-    if t.dtype != dtype or not t.is_contiguous() or t.device != device or \
-            (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on the inputs' device"
-                         + (f" of shape {tuple(shape)}" if shape is not None else ""))
-    return t.data_ptr()
+def _on(stream, device):
+    """Makes ``stream`` (a torch stream or a cudaStream_t) current: torch's allocations of the call
+    are then made on it, and a buffer released after the call is not handed out before its work is
+    done."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
+            torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def kv_slots(seq_lens, cu_new, T: int, block_table, free_pages, free_head, page_size: int,
@@ -383,25 +349,10 @@ def kv_slots(seq_lens, cu_new, T: int, block_table, free_pages, free_head, page_
     int32 [B], cu_new int32 [B + 1], block_table int32 [B, max_pages] (new entries are written),
     free_pages int32 [n], free_head int32 [1].  Returns (slots int64 [T], positions int32 [T],
     block_table, new seq_lens, new free_head); the old seq_lens and free_head are left alone."""
-    import torch
-    dev = seq_lens.device
-    if dev.type != "cuda" or seq_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
-        raise ValueError("seq_lens [B], block_table [B, max_pages] and free_pages [n] must be CUDA tensors")
-    B, i32 = seq_lens.shape[0], torch.int32
-    args = (_ints(seq_lens, i32, "seq_lens", dev), _ints(cu_new, i32, "cu_new", dev, (B + 1,)),
-            _ints(block_table, i32, "block_table", dev, (B, block_table.shape[1])),
-            _ints(free_pages, i32, "free_pages", dev), _ints(free_head, i32, "free_head", dev, (1,)))
-    with _launching(dev, stream) as st:
-        slots = torch.empty(T, dtype=torch.int64, device=dev)
-        out = torch.empty(T + B + 1, dtype=i32, device=dev)
-        positions, lens, head = out[:T], out[T:T + B], out[T + B:]
-        if B == 0:
-            head.copy_(free_head)
-        rc = lib().attn_kv_slots(*args, slots.data_ptr(), positions.data_ptr(), lens.data_ptr(),
-                                 head.data_ptr(), B, int(T), block_table.shape[1],
-                                 free_pages.shape[0], int(page_size), st)
-    _check("attn_kv_slots", rc)
-    return slots, positions, block_table, lens, head
+    if stream is not None:
+        with _on(stream, seq_lens.device):
+            return kv_slots(seq_lens, cu_new, T, block_table, free_pages, free_head, page_size)
+    return _native().kv_slots(seq_lens, cu_new, T, block_table, free_pages, free_head, page_size)
 
 
 def rope_inv_freq(rot: int, base: float = 10000.0, factor: float = 1.0, original_len: int = 0,
@@ -410,7 +361,6 @@ def rope_inv_freq(rot: int, base: float = 10000.0, factor: float = 1.0, original
     stretches them for a longer context: all of them divided by it, or, with original_len, only those
     that turn fewer than ``low`` times over original_len positions, none of those that turn
     more than ``high`` times, and a linear blend between."""
-    import torch
     f = float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64) / max(rot, 1))
     if factor != 1.0:
         if original_len:
@@ -422,36 +372,7 @@ def rope_inv_freq(rot: int, base: float = 10000.0, factor: float = 1.0, original
     return f.to(device)
 
 
-def _rope_args(qkv, H, H_kv, positions, inv_freq, wq, wk):
-    """Checks and the leading arguments: (B, N, d, row stride, shape prefix, inv_freq pointer, rot,
-    positions pointer, wq pointer, wk pointer)."""
-    import torch
-    if qkv.dtype != torch.bfloat16 or not qkv.is_cuda or qkv.dim() not in (2, 3):
-        raise ValueError("qkv must be a bf16 CUDA tensor [B, N, (H + 2 H_kv) d] or [T, (H + 2 H_kv) d]")
-    heads, width = H + 2 * H_kv, qkv.shape[-1]
-    if H <= 0 or H_kv <= 0 or H % H_kv != 0 or width % heads != 0:
-        raise ValueError("qkv's rows must hold H + 2 H_kv heads, H a multiple of H_kv")
-    B, N = (1, qkv.shape[0]) if qkv.dim() == 2 else qkv.shape[:2]
-    d, dev = width // heads, qkv.device
-    ld = width
-    if B * N > 1:
-        ld = qkv.stride(-2) if N > 1 else qkv.stride(0)
-        if (width > 1 and qkv.stride(-1) != 1) or (B > 1 and N > 1 and qkv.stride(0) != N * ld):
-            raise ValueError("qkv's rows must be contiguous and evenly spaced")
-    elif B * N == 1 and qkv.stride(-1) != 1:
-        raise ValueError("qkv's rows must be contiguous and evenly spaced")
-    rot = 0
-    fp = pp = None
-    if inv_freq is not None:
-        if inv_freq.dim() != 1:
-            raise ValueError("inv_freq must be one-dimensional")
-        rot = 2 * inv_freq.shape[0]
-        fp = _ints(inv_freq, torch.float64, "inv_freq", dev)
-        if positions is None:
-            raise ValueError("a rotation needs positions")
-        pp = _ints(positions, torch.int32, "positions", dev, qkv.shape[:-1])
-    w = [None if t is None else _ints(t, torch.bfloat16, "wq and wk", dev, (d,)) for t in (wq, wk)]
-    return B, N, d, ld, fp, rot, pp, w[0], w[1]
+_NO_CACHE = KVCache(None, None)
 
 
 def qkv_rope(qkv, H: int, H_kv: int, positions=None, inv_freq=None, interleaved: bool = False,
@@ -463,59 +384,24 @@ def qkv_rope(qkv, H: int, H_kv: int, positions=None, inv_freq=None, interleaved:
     [B, H_kv, N, d] (attn_fwd dense; attn_fwd_paged for N = 1); qkv [T, ...] gives the packed
     [H, T, d].  With ``cache`` the K and V rows also go to ``slots`` (int64, shaped like the rows;
     negative: not stored).  with_kv=False returns None for k and v."""
-    import torch
-    B, N, d, ld, fp, rot, pp, pq, pk = _rope_args(qkv, H, H_kv, positions, inv_freq, wq, wk)
-    dev = qkv.device
-    cs = sp = None
-    if cache is not None:
-        if slots is None:
-            raise ValueError("a cache needs slots")
-        cs = _cache_struct(cache, H_kv, d, dev)
-        sp = _ints(slots, torch.int64, "slots", dev, qkv.shape[:-1] if slots.dim() > 1 else (B * N,))
-    lead = () if qkv.dim() == 2 else (B,)
-    with _launching(dev, stream) as st:
-        q = torch.empty((*lead, H, N, d), dtype=torch.bfloat16, device=dev)
-        k = v = None
-        if with_kv:
-            k = torch.empty((*lead, H_kv, N, d), dtype=torch.bfloat16, device=dev)
-            v = torch.empty_like(k)
-        rc = lib().attn_qkv_rope(qkv.data_ptr(), ld, pq, pk, eps, fp, rot, int(bool(interleaved)),
-                                 rope_scale, pp, q.data_ptr(), k.data_ptr() if with_kv else None,
-                                 v.data_ptr() if with_kv else None,
-                                 ctypes.byref(cs) if cs is not None else None, sp, B, N, H, H_kv, d,
-                                 st)
-    _check("attn_qkv_rope", rc)
-    return q, k, v
+    if stream is not None:
+        with _on(stream, qkv.device):
+            return qkv_rope(qkv, H, H_kv, positions, inv_freq, interleaved, wq, wk, eps,
+                            rope_scale, cache, slots, with_kv)
+    return _native().qkv_rope(qkv, H, H_kv, positions, inv_freq, interleaved, wq, wk, eps, rope_scale,
+                              *(cache or _NO_CACHE), slots, with_kv)
 
 
 def qkv_rope_bwd(dq, dk, dv, qkv, positions=None, inv_freq=None, interleaved: bool = False, wq=None,
                  wk=None, eps: float = 1e-6, rope_scale: float = 1.0, workspace=None, stream=None):
     """Backward of qkv_rope: the gradient of qkv's rows (contiguous, qkv's shape) from dq [B, H, N, d]
     (or [H, T, d]) and dk, dv, and fp32 gradients of wq and wk (None where not given)."""
-    import torch
-    H, H_kv = dq.shape[-3], dk.shape[-3]
-    B, N, d, ld, fp, rot, pp, pq, pk = _rope_args(qkv, H, H_kv, positions, inv_freq, wq, wk)
-    dev = qkv.device
-    lead = () if qkv.dim() == 2 else (B,)
-    gp = [_ints(t, torch.bfloat16, name, dev, (*lead, h, N, d))
-          for t, name, h in ((dq, "dq", H), (dk, "dk", H_kv), (dv, "dv", H_kv))]
-    norm = wq is not None or wk is not None
-    need = int(lib().attn_qkv_rope_bwd_workspace_bytes(B, N, H, H_kv, d)) if norm else 0
-    with _launching(dev, stream) as st:
-        dqkv = torch.empty(qkv.shape, dtype=torch.bfloat16, device=dev)
-        if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
-            if workspace is not None else (None, 0)
-        make = torch.empty if B * N else torch.zeros
-        dw = [None if w is None else make(d, dtype=torch.float32, device=dev) for w in (wq, wk)]
-        rc = lib().attn_qkv_rope_bwd(*gp, qkv.data_ptr(), ld, pq, pk, eps, fp, rot,
-                                     int(bool(interleaved)), rope_scale, pp, dqkv.data_ptr(),
-                                     (H + 2 * H_kv) * d,
-                                     *(None if w is None else w.data_ptr() for w in dw), B, N, H,
-                                     H_kv, d, *ws, st)
-    _check("attn_qkv_rope_bwd", rc)
-    return dqkv, dw[0], dw[1]
+    if stream is not None:
+        with _on(stream, qkv.device):
+            return qkv_rope_bwd(dq, dk, dv, qkv, positions, inv_freq, interleaved, wq, wk, eps,
+                                rope_scale, workspace)
+    return _native().qkv_rope_bwd(dq, dk, dv, qkv, positions, inv_freq, interleaved, wq, wk, eps,
+                                  rope_scale, workspace)
 
 
 def paged_workspace_bytes(B: int, H: int, H_kv: int, d: int) -> int:
@@ -527,39 +413,10 @@ def attn_fwd_paged(q, cache, block_table, seq_lens, scale: float | None = None, 
     """Attention of one new token of each request over a paged cache: q [B, H, 1, d] (or [B, H, d]),
     block_table int32 [B, max_pages], seq_lens int32 [B] (rows in the cache, the new token's own
     among them).  Returns (O bf16 like q, LSE fp32 [B, H, 1] or [B, H])."""
-    import torch
-    dev = q.device
-    if q.dtype != torch.bfloat16 or not q.is_cuda or not q.is_contiguous() or \
-            not (q.dim() == 3 or (q.dim() == 4 and q.shape[2] == 1)):
-        raise ValueError("q must be a contiguous bf16 CUDA tensor [B, H, 1, d] or [B, H, d]")
-    B, H, d = q.shape[0], q.shape[1], q.shape[-1]
-    if cache.k.dim() != 4 or cache.k.shape[1] == 0 or H % cache.k.shape[1] != 0:
-        raise ValueError("the number of K/V heads must divide the number of query heads")
-    H_kv = cache.k.shape[1]
-    cs = _cache_struct(cache, H_kv, d, dev)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    tp = _ints(block_table, torch.int32, "block_table", dev, (B, block_table.shape[1]))
-    lp = _ints(seq_lens, torch.int32, "seq_lens", dev, (B,))
-    for t, dt, shape, name in ((out, torch.bfloat16, q.shape, "out"),
-                               (lse, torch.float32, q.shape[:-1], "lse")):
-        if t is not None:
-            _ints(t, dt, name, dev, shape)
-    with _launching(dev, stream) as st:
-        if workspace is None:
-            workspace = torch.empty(max(paged_workspace_bytes(B, H, H_kv, d), 1), dtype=torch.uint8,
-                                    device=dev)
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
-        rc = lib().attn_fwd_paged(q.data_ptr(), ctypes.byref(cs), tp, lp, out.data_ptr(),
-                                  lse.data_ptr(), B, H, H_kv, d, block_table.shape[1],
-                                  scale if scale is not None else 1.0 / math.sqrt(d),
-                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                  st)
-    _check("attn_fwd_paged", rc)
-    return out, lse
+    if stream is not None:
+        with _on(stream, q.device):
+            return attn_fwd_paged(q, cache, block_table, seq_lens, scale, workspace, out, lse)
+    return _native().attn_fwd_paged(q, *cache, block_table, seq_lens, scale, workspace, out, lse)
 
 
 def unfused_workspace_bytes(B: int, H: int, N: int, d: int) -> int:

@@ -2,7 +2,8 @@
 
 Each ``csrc/*.cu`` translation unit is compiled to an object in ``_build/`` in parallel, then
 linked into a shared library next to this file.  CUDA's runtime is linked statically, so the
-library only needs the NVIDIA driver at run time.
+library only needs the NVIDIA driver at run time.  ``csrc/py_binding.cpp`` (marshalling of torch
+tensors) is compiled alongside with the host compiler and linked against the library and torch.
 
 Usage: ``python -m io_aware_attention_attn_gb300.build [--verbose-ptxas] [--force]``.
 """
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libattn_gb300.so")
+BINDING = os.path.join(PKG, "_attn_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -46,7 +49,8 @@ def _newest_input_mtime() -> float:
 
 
 def up_to_date() -> bool:
-    return os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input_mtime()
+    newest = _newest_input_mtime()
+    return all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING))
 
 
 def _compile(src: str, verbose_ptxas: bool) -> str:
@@ -62,20 +66,49 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _run(cmd, what: str):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_binding() -> str:
+    import torch
+    obj = os.path.join(BUILD, "py_binding.o")
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    dirs = [INCLUDE, inc, os.path.join(inc, "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], cuda]
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *(f for d in dirs for f in ("-isystem" if d is not INCLUDE else "-I", d)),
+          "-c", os.path.join(CSRC, "py_binding.cpp"), "-o", obj], "compiling py_binding.cpp")
+    return obj
+
+
+def _link_binding(obj: str):
+    import torch
+    tlib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", PKG, "-l:libattn_gb300.so",
+          "-L", tlib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+          "-Wl,-rpath,$ORIGIN"], "linking the binding")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     """Compile and link the library if any input changed; returns its path."""
     if not force and not verbose_ptxas and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
     tmp = LIB + ".tmp"
-    r = subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], capture_output=True,
-                       text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-Xlinker", "-soname=libattn_gb300.so"], "link")
     os.replace(tmp, LIB)
+    _link_binding(binding.result())
     return LIB
 
 

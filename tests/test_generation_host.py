@@ -18,11 +18,18 @@ def lib():
     return attn.lib()
 
 
+class CacheStruct(ctypes.Structure):  # attn_kv_cache in the header
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
 def cache(**kw):
     a = dict(k=A, v=A, k_scale=None, v_scale=None, page_stride=2 * 64 * 128, num_pages=9, page_size=64,
              dtype=0)
     a.update(kw)
-    return attn._CacheStruct(*a.values())
+    return CacheStruct(*a.values())
 
 
 def paged(lib, c=None, **kw):
@@ -134,38 +141,45 @@ def test_slots_checks(lib, kw, code):
     assert slots(lib, **kw) == code
 
 
-def test_binding_refuses_host_tensors():
+def test_binding_refuses(lib):
     c = attn.kv_cache(2, 2, 16, 64, device="cpu")
     x = torch.zeros(2, 8, 1, 64, dtype=torch.bfloat16)
     i = torch.zeros(2, 1, dtype=torch.int32)
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match="CUDA"):
         attn.attn_fwd_paged(x, c, i, i[:, 0])
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match="CUDA"):
         attn.qkv_rope(torch.zeros(3, 12 * 64, dtype=torch.bfloat16), 8, 2)
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match="CUDA"):
+        attn.qkv_rope_bwd(x, x[:, :2], x[:, :2], torch.zeros(2, 1, 12 * 64, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="CUDA"):
         attn.kv_slots(i[:, 0], i[:, 0], 0, i, i[:, 0], i[:1, 0], 16)
+    with pytest.raises(TypeError):
+        attn.kv_slots([0], i[:, 0], 0, i, i[:, 0], i[:1, 0], 16)
+    with pytest.raises(ValueError, match="32 bits"):
+        attn.kv_slots(i[:, 0], i[:, 0], 1 << 40, i, i[:, 0], i[:1, 0], 16)
 
 
-def test_cache_layouts():
-    def struct(c, H_kv=2, d=64):
-        return attn._cache_struct(c, H_kv, d, torch.device("cpu"))
+def test_cache_layouts(lib):
+    def layout(c, H_kv=2, d=64):
+        return attn._native().cache_layout(*c, H_kv, d)
 
     c = attn.kv_cache(5, 2, 16, 64, device="cpu")
-    s = struct(c)
-    assert (s.page_stride, s.num_pages, s.page_size, s.dtype) == (2 * 16 * 64, 5, 16, 0)
+    assert layout(c) == (2 * 16 * 64, 5, 16, 0)
     both = torch.zeros(5, 2, 2, 16, 64, dtype=torch.bfloat16)  # K and V page by page
-    s = struct(attn.KVCache(both[:, 0], both[:, 1]))
-    assert s.page_stride == 2 * 2 * 16 * 64 and s.v - s.k == 2 * 16 * 64 * 2
+    assert layout(attn.KVCache(both[:, 0], both[:, 1])) == (2 * 2 * 16 * 64, 5, 16, 0)
+    one = torch.zeros(3, 16, 1, 64, dtype=torch.bfloat16).transpose(1, 2)  # one head: its stride is free
+    assert layout(attn.KVCache(one, one), 1) == (16 * 64, 3, 16, 0)
     e = attn.kv_cache(5, 2, 16, 64, torch.float8_e4m3fn, "cpu")
-    assert struct(e).dtype == 1 and struct(attn.KVCache(e.k.view(torch.uint8), e.v.view(torch.uint8),
-                                                        e.k_scale, e.v_scale)).dtype == 1
+    assert layout(e) == (2 * 16 * 64, 5, 16, 1)
+    assert layout(attn.KVCache(e.k.view(torch.uint8), e.v.view(torch.uint8), e.k_scale, e.v_scale))[3] == 1
     for bad in (attn.KVCache(c.k.transpose(1, 2), c.v.transpose(1, 2)), attn.KVCache(c.k, c.v[:4]),
                 attn.KVCache(e.k, e.v), attn.KVCache(e.k, e.v, e.k_scale, e.v_scale[:4]),
-                attn.KVCache(c.k.float(), c.v.float()), attn.KVCache(c.k, both[:, 1])):
+                attn.KVCache(c.k.float(), c.v.float()), attn.KVCache(c.k, both[:, 1]),
+                attn.KVCache(both[:, 0, :, ::2], both[:, 1, :, ::2])):
         with pytest.raises(ValueError):
-            struct(bad)
+            layout(bad)
     with pytest.raises(ValueError):
-        struct(c, H_kv=1)
+        layout(c, H_kv=1)
 
 
 def test_inv_freq():
