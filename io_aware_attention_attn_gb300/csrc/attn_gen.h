@@ -65,10 +65,10 @@ struct RopeParams {
   float* dwk;
   float* partial;             // [CTAs][2][d] sums of one CTA's rows
   int N, H, H_kv, tokens;
-  int tok_cta, head_cta;      // tokens and heads of one CTA
+  int parts;                  // warps that share a token
 };
 constexpr int kRopeThreads = 256;
-constexpr int kRopeBwdMaxCtas = 608;  // 4 on each of 152 SMs
+constexpr int kRopeBwdCtas = 304;  // at most: 2 on each of 152 SMs
 cudaError_t launch_qkv_rope(RopeParams& p, int d, bool interleaved, int cache_kind,
                             cudaStream_t stream);
 cudaError_t launch_qkv_rope_bwd(RopeParams& p, int d, bool interleaved, cudaStream_t stream);

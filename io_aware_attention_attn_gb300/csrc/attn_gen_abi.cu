@@ -143,7 +143,7 @@ extern "C" int attn_qkv_rope(const void* qkv, int64_t ld, const void* wq, const 
 
 extern "C" size_t attn_qkv_rope_bwd_workspace_bytes(int B, int N, int H, int H_kv, int d) {
   if (B <= 0 || N <= 0 || H <= 0 || H_kv <= 0 || (d != 64 && d != 128)) return 0;
-  return static_cast<size_t>(kRopeBwdMaxCtas) * 2 * d * 4;
+  return static_cast<size_t>(kRopeBwdCtas) * 2 * d * 4;
 }
 
 extern "C" int attn_qkv_rope_bwd(const void* dq, const void* dk, const void* dv, const void* qkv,

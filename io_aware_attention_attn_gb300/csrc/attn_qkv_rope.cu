@@ -1,18 +1,25 @@
 // attn_qkv_rope.cu -- the step before attention and its backward: RMS norm of each query and key
 // head, rotation by position, token-major rows to head-major tensors, rows into a paged cache.
 //
+// What bounds it: memory, one read and one write of every row; then, below it, instructions, so the
+// arithmetic is packed and nothing is computed twice.
+//
 // A head's row of d elements is held by d/16 lanes with 16 elements each, as two 16-byte chunks
 // chosen so that every pair (a, b) of the rotation lies in one lane: chunks l and l + rot/16 when
 // element i turns with i + rot/2, any two when 2i turns with 2i + 1.  The mean of squares is then
-// the only value that crosses lanes.  A CTA takes a few tokens and all (or, when there are few
-// tokens, some) of their heads; cos and sin are computed once per token and pair into shared
-// memory and shared by the heads.
+// the only value that crosses lanes.  A warp-wide load covers 4 rows (d = 128) or 8 (d = 64).
+//
+// A warp takes a token (or, when there are few tokens, a share of a token's rows) and works alone: it
+// puts the token's coefficients into its own shared memory, 64 pairs of them at d = 128, two a lane,
+// and streams the token's heads through them, loads a batch ahead.  In the forward the norm's
+// weight is folded in: with r the inverse root mean square,
+//   (y_a, y_b) = r (x_a, x_b) * (w_a c, w_b c) + r (x_b, x_a) * (-w_b s, w_a s),
+// three packed operations a pair.
 //
 // Angles: t = position * inv_freq modulo one turn, in 64-bit fixed point (a turn is 2^64), so the
 // product wraps exactly and a position of 2^20 costs no accuracy; the top 32 bits go to sincospi.
-// A float64 frequency leaves position * 2^-53 relative error at most.
-//
-// What bounds it: memory, one read and one write of every row.
+// The frequency is brought to fixed point by an integer product, not in float64, which this GPU
+// computes at 1/64 of its fp32 rate.
 #include "attn_gen.h"
 #include "sm103_ptx.cuh"
 
@@ -21,94 +28,88 @@
 namespace attn {
 namespace {
 
-constexpr int kBatch = 4;  // rows a thread loads before it uses the first
+constexpr int kWarps = kRopeThreads / 32;
 
-// cos and sin (times rope_scale) of the CTA's tokens, [token][rot/2] each.
-__device__ __forceinline__ void fill_angles(const RopeParams& p, int t0, int nt, float* s_cos,
-                                            float* s_sin) {
-  const int nf = p.rot >> 1;
-  for (int i = threadIdx.x; i < nt * nf; i += kRopeThreads) {
-    const int tok = i / nf, f = i - tok * nf;
-    double turns = p.inv_freq[f] * 0.15915494309189533577;  // 1 / (2 pi)
-    turns -= rint(turns);
-    const uint64_t step = static_cast<uint64_t>(__double2ll_rn(turns * 18446744073709551616.0));
-    const uint64_t phase =
-        static_cast<uint64_t>(static_cast<int64_t>(p.positions[t0 + tok])) * step;
-    const int half_turns = static_cast<int>(phase >> 32);  // 2^31 is half a turn
-    float s, c;
-    sincospif(static_cast<float>(half_turns) * 0x1p-31f, &s, &c);
-    s_cos[i] = c * p.rope_scale;
-    s_sin[i] = s * p.rope_scale;
-  }
+// inv_freq (radians a position) in turns a position, modulo 1, times 2^64.
+__device__ __forceinline__ uint64_t turn_step(double f) {
+  const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(f));
+  const int e = static_cast<int>((bits >> 52) & 0x7FF) - 1023;  // |f| = m * 2^(e - 63)
+  const uint64_t m = ((bits << 11) & 0x7FFFFFFFFFFFFFFFull) | 0x8000000000000000ull;
+  const uint64_t p = __umul64hi(m, 0xA2F9836E4E44152Aull);      // round(2^66 / (2 pi))
+  const int sh = e - 1;                                         // |f| / (2 pi) = p * 2^(e - 65)
+  uint64_t step = sh >= 64 || sh <= -64 ? 0 : sh >= 0 ? p << sh : p >> -sh;
+  return bits >> 63 ? 0 - step : step;
+}
+// cos and sin (times scale) of pair `f` of a token.
+__device__ __forceinline__ void angle(const RopeParams& p, int position, int f, float& c, float& s) {
+  const uint64_t phase =
+      static_cast<uint64_t>(static_cast<int64_t>(position)) * turn_step(__ldg(p.inv_freq + f));
+  sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, &s, &c);  // 2^31: half a turn
+  c *= p.rope_scale;
+  s *= p.rope_scale;
 }
 
-// The two 16-byte chunks of a lane, and the first pair of each that turns (-1: none).
+// A lane's 16 elements as 8 pairs.  Half layout: pair i is element i of chunk a and of chunk b.
+// Interleaved: pairs 0..3 are chunk a's neighbours, 4..7 chunk b's.
 template <int D, bool INTER>
-struct Chunks {
-  int a, b, fa, fb;
-  __device__ __forceinline__ Chunks(int l, int rot) {
-    constexpr int kLanes = D / 16;
+struct Lane {
+  static constexpr int kLanes = D / 16;
+  int a, b;        // chunks
+  bool ta, tb;     // whether a chunk's pairs turn
+  __device__ __forceinline__ Lane(int l, int rot) {
     if (INTER) {
       a = l;
       b = l + kLanes;
-      fa = 8 * a < rot ? 4 * a : -1;
-      fb = 8 * b < rot ? 4 * b : -1;
+      ta = 8 * a < rot;
+      tb = 8 * b < rot;
     } else {
       const int half = rot >> 4;
       a = l < half ? l : 2 * half + 2 * (l - half);
       b = l < half ? l + half : a + 1;
-      fa = fb = l < half ? 8 * l : -1;
+      ta = tb = l < half;
     }
+  }
+  // elements and frequency of pair i
+  __device__ __forceinline__ int first(int i) const {
+    return INTER ? (i < 4 ? 8 * a + 2 * i : 8 * b + 2 * (i - 4)) : 8 * a + i;
+  }
+  __device__ __forceinline__ int second(int i) const { return INTER ? first(i) + 1 : 8 * b + i; }
+  __device__ __forceinline__ int freq(int i) const { return INTER ? first(i) >> 1 : 8 * a + i; }
+  __device__ __forceinline__ bool turns(int i) const { return i < 4 ? ta : tb; }
+  // 16 bf16 values to pairs and back
+  static __device__ __forceinline__ void unpack(const uint4& va, const uint4& vb, float (&x)[8][2]) {
+    const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (INTER) {
+        x[i][0] = bf16lo_to_f32(wa[i]);
+        x[i][1] = bf16hi_to_f32(wa[i]);
+        x[4 + i][0] = bf16lo_to_f32(wb[i]);
+        x[4 + i][1] = bf16hi_to_f32(wb[i]);
+      } else {
+        x[2 * i][0] = bf16lo_to_f32(wa[i]);
+        x[2 * i + 1][0] = bf16hi_to_f32(wa[i]);
+        x[2 * i][1] = bf16lo_to_f32(wb[i]);
+        x[2 * i + 1][1] = bf16hi_to_f32(wb[i]);
+      }
+    }
+  }
+  static __device__ __forceinline__ void pack(const float (&x)[8][2], uint4& va, uint4& vb) {
+    uint32_t wa[4], wb[4];
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (INTER) {
+        wa[i] = pack_bf16x2(x[i][0], x[i][1]);
+        wb[i] = pack_bf16x2(x[4 + i][0], x[4 + i][1]);
+      } else {
+        wa[i] = pack_bf16x2(x[2 * i][0], x[2 * i + 1][0]);
+        wb[i] = pack_bf16x2(x[2 * i][1], x[2 * i + 1][1]);
+      }
+    }
+    va = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+    vb = make_uint4(wb[0], wb[1], wb[2], wb[3]);
   }
 };
-
-__device__ __forceinline__ void unpack8(const uint4& w, float* f) {
-  f[0] = bf16lo_to_f32(w.x); f[1] = bf16hi_to_f32(w.x);
-  f[2] = bf16lo_to_f32(w.y); f[3] = bf16hi_to_f32(w.y);
-  f[4] = bf16lo_to_f32(w.z); f[5] = bf16hi_to_f32(w.z);
-  f[6] = bf16lo_to_f32(w.w); f[7] = bf16hi_to_f32(w.w);
-}
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
-}
-
-// Turns a lane's 16 elements by its token's angles (SIGN = -1: back).
-template <int D, bool INTER, int SIGN>
-__device__ __forceinline__ void turn(float* f, const Chunks<D, INTER>& ch, const float* cs,
-                                     const float* sn) {
-  if (INTER) {
-    #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int f0 = h ? ch.fb : ch.fa;
-      if (f0 < 0) continue;
-      const float4 c4 = *reinterpret_cast<const float4*>(cs + f0);
-      const float4 s4 = *reinterpret_cast<const float4*>(sn + f0);
-      const float c[4] = {c4.x, c4.y, c4.z, c4.w};
-      const float s[4] = {s4.x, s4.y, s4.z, s4.w};
-      #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x = f[8 * h + 2 * i], y = f[8 * h + 2 * i + 1];
-        f[8 * h + 2 * i] = x * c[i] - SIGN * y * s[i];
-        f[8 * h + 2 * i + 1] = y * c[i] + SIGN * x * s[i];
-      }
-    }
-  } else if (ch.fa >= 0) {
-    #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 c4 = *reinterpret_cast<const float4*>(cs + ch.fa + 4 * h);
-      const float4 s4 = *reinterpret_cast<const float4*>(sn + ch.fa + 4 * h);
-      const float c[4] = {c4.x, c4.y, c4.z, c4.w};
-      const float s[4] = {s4.x, s4.y, s4.z, s4.w};
-      #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x = f[4 * h + i], y = f[8 + 4 * h + i];
-        f[4 * h + i] = x * c[i] - SIGN * y * s[i];
-        f[8 + 4 * h + i] = y * c[i] + SIGN * x * s[i];
-      }
-    }
-  }
-}
 
 template <int D>
 __device__ __forceinline__ float row_sum(float v) {
@@ -118,218 +119,321 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 // A row's E4M3 codes and scale into the cache.
-template <int D>
-__device__ __forceinline__ void store_codes(const float* f, uint8_t* row, float* scale, int ca,
+template <int D, bool INTER>
+__device__ __forceinline__ void store_codes(const float (&x)[8][2], uint8_t* row, float* scale, int ca,
                                             int cb, bool write, bool first_lane) {
   float amax = 0.f;
   #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
+  for (int i = 0; i < 8; ++i) amax = fmax3(amax, fabsf(x[i][0]), fabsf(x[i][1]));
   #pragma unroll
   for (int off = D / 32; off > 0; off >>= 1)
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
   float sc = __fdiv_rn(amax, 448.f);
   if (!(sc >= 0x1p-126f)) sc = 1.f;
   if (!write) return;
-  uint32_t w[4];
+  uint32_t wa[2], wb[2];
+  auto codes = [&](float a, float b, float c, float e) {
+    return static_cast<uint32_t>(pack_e4m3x2(__fdiv_rn(a, sc), __fdiv_rn(b, sc))) |
+           static_cast<uint32_t>(pack_e4m3x2(__fdiv_rn(c, sc), __fdiv_rn(e, sc))) << 16;
+  };
   #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = static_cast<uint32_t>(pack_e4m3x2(__fdiv_rn(f[4 * i], sc), __fdiv_rn(f[4 * i + 1], sc))) |
-           static_cast<uint32_t>(pack_e4m3x2(__fdiv_rn(f[4 * i + 2], sc),
-                                             __fdiv_rn(f[4 * i + 3], sc))) << 16;
-  *reinterpret_cast<uint2*>(row + 8 * ca) = make_uint2(w[0], w[1]);
-  *reinterpret_cast<uint2*>(row + 8 * cb) = make_uint2(w[2], w[3]);
+  for (int i = 0; i < 2; ++i) {
+    if (INTER) {
+      wa[i] = codes(x[2 * i][0], x[2 * i][1], x[2 * i + 1][0], x[2 * i + 1][1]);
+      wb[i] = codes(x[4 + 2 * i][0], x[4 + 2 * i][1], x[5 + 2 * i][0], x[5 + 2 * i][1]);
+    } else {
+      wa[i] = codes(x[4 * i][0], x[4 * i + 1][0], x[4 * i + 2][0], x[4 * i + 3][0]);
+      wb[i] = codes(x[4 * i][1], x[4 * i + 1][1], x[4 * i + 2][1], x[4 * i + 3][1]);
+    }
+  }
+  *reinterpret_cast<uint2*>(row + 8 * ca) = make_uint2(wa[0], wa[1]);
+  *reinterpret_cast<uint2*>(row + 8 * cb) = make_uint2(wb[0], wb[1]);
   if (first_lane) *scale = sc;
 }
 
+// The rows a warp-wide load covers: group gi of a token, 0 .. nq - 1 query heads, then key, then
+// value heads.
+template <int RW>
+struct Groups {
+  int nq, nk, all;
+  __device__ __forceinline__ Groups(int H, int H_kv)
+      : nq((H + RW - 1) / RW), nk((H_kv + RW - 1) / RW), all(nq + 2 * nk) {}
+  // 0 query, 1 key, 2 value; `h`: this lane's head of that kind
+  __device__ __forceinline__ int kind(int gi, int sub, int& h) const {
+    const int k = gi < nq ? 0 : gi < nq + nk ? 1 : 2;
+    h = (gi - (k == 0 ? 0 : k == 1 ? nq : nq + nk)) * RW + sub;
+    return k;
+  }
+};
+
+constexpr int kBatch = 4;  // groups a warp loads before it uses the first
+
 template <int D, bool INTER, int CACHE>
 __global__ void __launch_bounds__(kRopeThreads) qkv_rope_kernel(RopeParams p) {
-  extern __shared__ __align__(16) float s_angles[];
-  constexpr int kLanes = D / 16, kRows = kRopeThreads / kLanes;
-  const int l = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
-  const Chunks<D, INTER> ch(l, p.rot);
-  const int heads = p.H + 2 * p.H_kv;
-  const int t0 = blockIdx.x * p.tok_cta, nt = min(p.tok_cta, p.tokens - t0);
-  const int h0 = blockIdx.y * p.head_cta, nh = min(p.head_cta, heads - h0);
-  const int rows = nt * nh, nf = p.rot >> 1;
-  float* s_cos = s_angles;
-  float* s_sin = s_angles + p.tok_cta * nf;
+  using L = Lane<D, INTER>;
+  constexpr int kLanes = D / 16, kRw = 32 / kLanes;
+  __shared__ float4 s_coef[kWarps][2][D / 2];  // [query, key][pair i of lane l at i * kLanes + l]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int l = lane % kLanes, sub = lane / kLanes;
+  const int t = blockIdx.x * (kWarps / p.parts) + warp / p.parts;
+  if (t >= p.tokens) return;
+  const int part = warp % p.parts;
+  const L ln(l, p.rot);
+  const Groups<kRw> gr(p.H, p.H_kv);
+  const int b = t / p.N, n = t - b * p.N;
+  const uint4* row = reinterpret_cast<const uint4*>(p.qkv + static_cast<int64_t>(t) * p.ld);
   uint4 xa[kBatch], xb[kBatch];
-  auto load = [&](int base) {
+  auto load = [&](int g0) {
     #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int r = base + u * kRows + grp;
-      if (r < rows) {
-        const int tok = r / nh;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.qkv + static_cast<int64_t>(t0 + tok) * p.ld + (h0 + r - tok * nh) * D);
-        xa[u] = __ldcs(src + ch.a);
-        xb[u] = __ldcs(src + ch.b);
-      } else {
-        xa[u] = xb[u] = make_uint4(0u, 0u, 0u, 0u);
+      int h;
+      const int kind = gr.kind(g0 + u * p.parts, sub, h);
+      xa[u] = xb[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (g0 + u * p.parts < gr.all && h < (kind ? p.H_kv : p.H)) {
+        const int hh = h + (kind == 0 ? 0 : kind == 1 ? p.H : p.H + p.H_kv);
+        xa[u] = __ldcs(row + hh * (D / 8) + ln.a);
+        xb[u] = __ldcs(row + hh * (D / 8) + ln.b);
       }
     }
   };
-  load(0);
-  fill_angles(p, t0, nt, s_cos, s_sin);
-  __syncthreads();
-  for (int base = 0; base < rows; base += kBatch * kRows) {
-    if (base > 0) load(base);
+  load(part);
+  {
+    const int position = p.rot ? p.positions[t] : 0;
+    #pragma unroll
+    for (int j = lane; j < D / 2; j += 32) {
+      const int i = j / kLanes, lj = j % kLanes;
+      const L o(lj, p.rot);
+      float c = 1.f, s = 0.f;
+      if (o.turns(i)) angle(p, position, o.freq(i), c, s);
+      #pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const __nv_bfloat16* w = k ? p.wk : p.wq;
+        const float wa = w ? __bfloat162float(w[o.first(i)]) : 1.f;
+        const float wb = w ? __bfloat162float(w[o.second(i)]) : 1.f;
+        s_coef[warp][k][j] = make_float4(wa * c, wb * c, -(wb * s), wa * s);
+      }
+    }
+    __syncwarp();
+  }
+  const int64_t step = static_cast<int64_t>(p.N) * D;
+  const int64_t tq = (static_cast<int64_t>(b) * p.H * p.N + n) * D;
+  const int64_t tk = (static_cast<int64_t>(b) * p.H_kv * p.N + n) * D;
+  int64_t slot = -1, page = 0;
+  if (CACHE != kCacheNone) {
+    slot = p.slots[t];
+    page = slot >> p.page_shift;
+    if (slot >= 0 && page >= p.num_pages) {
+      if (lane == 0) atomicCAS(p.status, 0, kStatusBadPage);
+      slot = -1;
+    }
+  }
+  for (int g0 = part; g0 < gr.all; g0 += kBatch * p.parts) {
+    if (g0 != part) load(g0);
     #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      if (base + u * kRows >= rows) break;  // the same for all threads
-      const int r = base + u * kRows + grp;
-      const bool live = r < rows;
-      const int tok = live ? r / nh : 0;
-      const int hh = live ? h0 + r - tok * nh : 0;
-      const bool is_q = hh < p.H, is_v = hh >= p.H + p.H_kv;
-      const int h = is_q ? hh : is_v ? hh - p.H - p.H_kv : hh - p.H;
-      float f[16];
-      unpack8(xa[u], f);
-      unpack8(xb[u], f + 8);
-      const __nv_bfloat16* w = is_q ? p.wq : is_v ? nullptr : p.wk;
-      float ss = 0.f;
-      #pragma unroll
-      for (int i = 0; i < 16; ++i) ss = fmaf(f[i], f[i], ss);
-      ss = row_sum<D>(ss);
-      if (w) {
-        const float rn = rsqrtf(ss * (1.f / D) + p.eps);
-        float wf[16];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(w) + ch.a), wf);
-        unpack8(__ldg(reinterpret_cast<const uint4*>(w) + ch.b), wf + 8);
+      if (g0 + u * p.parts >= gr.all) break;
+      int h;
+      const int kind = gr.kind(g0 + u * p.parts, sub, h);
+      const bool live = h < (kind ? p.H_kv : p.H);
+      uint4 oa = xa[u], ob = xb[u];
+      float x[8][2];
+      if (kind < 2) {
+        L::unpack(xa[u], xb[u], x);
+        if (kind ? p.wk != nullptr : p.wq != nullptr) {
+          float s0 = 0.f, s1 = 0.f;
+          #pragma unroll
+          for (int i = 0; i < 8; ++i)
+            ffma2(s0, s1, x[i][0], x[i][1], x[i][0], x[i][1], s0, s1);
+          const float r = rsqrtf(row_sum<D>(s0 + s1) * (1.f / D) + p.eps);
+          #pragma unroll
+          for (int i = 0; i < 8; ++i) fmul2(x[i][0], x[i][1], x[i][0], x[i][1], r, r);
+        }
+        const float4* co = s_coef[warp][kind] + l;
         #pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = f[i] * rn * wf[i];
+        for (int i = 0; i < 8; ++i) {
+          const float4 c = co[i * kLanes];
+          float y0, y1;
+          fmul2(y0, y1, x[i][0], x[i][1], c.x, c.y);
+          if (ln.turns(i)) ffma2(y0, y1, x[i][1], x[i][0], c.z, c.w, y0, y1);
+          x[i][0] = y0;
+          x[i][1] = y1;
+        }
+        L::pack(x, oa, ob);
+      } else if (CACHE == kCacheE4m3) {
+        L::unpack(xa[u], xb[u], x);
       }
-      if (!is_v) turn<D, INTER, 1>(f, ch, s_cos + tok * nf, s_sin + tok * nf);
-      const int t = t0 + tok;
-      const uint4 oa = pack8(f), ob = pack8(f + 8);
-      __nv_bfloat16* out = is_q ? p.q : is_v ? p.v : p.k;
+      __nv_bfloat16* out = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
       if (live && out) {
-        const int b = t / p.N, n = t - b * p.N;
-        uint4* dst = reinterpret_cast<uint4*>(
-            out + ((static_cast<int64_t>(b) * (is_q ? p.H : p.H_kv) + h) * p.N + n) * D);
-        dst[ch.a] = oa;
-        dst[ch.b] = ob;
+        uint4* dst = reinterpret_cast<uint4*>(out + (kind ? tk : tq) + h * step);
+        dst[ln.a] = oa;
+        dst[ln.b] = ob;
       }
-      if (CACHE != kCacheNone) {
-        const int64_t slot = live && !is_q ? p.slots[t] : -1;
-        const int64_t page = slot >> p.page_shift;
-        const bool write = slot >= 0 && page < p.num_pages;
-        if (slot >= 0 && !write) atomicCAS(p.status, 0, kStatusBadPage);
-        const int64_t row =
+      if (CACHE != kCacheNone && kind > 0) {
+        const bool write = live && slot >= 0;
+        const int64_t at_row =
             (static_cast<int64_t>(h) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
-        uint8_t* base8 = is_v ? p.vc : p.kc;
-        const int64_t at = page * p.page_stride + row * D;
+        const int64_t at = page * p.page_stride + at_row * D;
+        uint8_t* base = kind == 2 ? p.vc : p.kc;
         if (CACHE == kCacheBf16) {
           if (write) {
-            uint4* dst = reinterpret_cast<uint4*>(base8 + 2 * at);
-            dst[ch.a] = oa;
-            dst[ch.b] = ob;
+            uint4* dst = reinterpret_cast<uint4*>(base + 2 * at);
+            dst[ln.a] = oa;
+            dst[ln.b] = ob;
           }
         } else {
-          store_codes<D>(f, base8 + (write ? at : 0),
-                         (is_v ? p.vs : p.ks) +
-                             (write ? ((page * p.H_kv) << p.page_shift) + row : 0),
-                         ch.a, ch.b, write, l == 0);
+          float* scales = kind == 2 ? p.vs : p.ks;
+          store_codes<D, INTER>(x, base + (write ? at : 0),
+                                scales + (write ? ((page * p.H_kv) << p.page_shift) + at_row : 0),
+                                ln.a, ln.b, write, l == 0);
         }
       }
     }
   }
 }
 
-// Gradients of the rows, and each CTA's share of the weights' gradients.
+// Gradients of the rows, and each CTA's share of the weights' gradients.  With t = x r, g the
+// gradient turned back and u = g w:  dx = r (u - t mean(u t)),  dw += g t.
+constexpr int kBatchBwd = 2;
+
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) qkv_rope_bwd_kernel(RopeParams p) {
-  extern __shared__ __align__(16) float s_angles[];
-  constexpr int kLanes = D / 16, kRows = kRopeThreads / kLanes, kWarps = kRopeThreads / 32;
-  __shared__ __align__(16) float s_dw[kWarps][D];
-  const int l = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
-  const Chunks<D, INTER> ch(l, p.rot);
-  const int heads = p.H + 2 * p.H_kv, nf = p.rot >> 1;
-  float* s_cos = s_angles;
-  float* s_sin = s_angles + p.tok_cta * nf;
-  float dwq[16], dwk[16];
+__global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParams p) {
+  using L = Lane<D, INTER>;
+  constexpr int kLanes = D / 16, kRw = 32 / kLanes;
+  __shared__ __align__(16) float s_dw[kWarps][D];     // the weights' sums, at the end
+  __shared__ float2 s_cs[kWarps][D / 2];              // cos, sin of pair i of lane l
+  __shared__ float2 s_w[2][D / 2];                    // the weights, likewise
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int l = lane % kLanes, sub = lane / kLanes;
+  const L ln(l, p.rot);
+  const Groups<kRw> gr(p.H, p.H_kv);
+  for (int j = threadIdx.x; j < D; j += kRopeThreads) {
+    const int k = j / (D / 2), jj = j % (D / 2);
+    const L o(jj % kLanes, p.rot);
+    const __nv_bfloat16* w = k ? p.wk : p.wq;
+    s_w[k][jj] = w ? make_float2(__bfloat162float(w[o.first(jj / kLanes)]),
+                                 __bfloat162float(w[o.second(jj / kLanes)]))
+                   : make_float2(1.f, 1.f);
+  }
+  __syncthreads();
+  float dw[2][8][2];
   #pragma unroll
-  for (int i = 0; i < 16; ++i) dwq[i] = dwk[i] = 0.f;
-  const int groups = (p.tokens + p.tok_cta - 1) / p.tok_cta;
-  for (int g = blockIdx.x; g < groups; g += gridDim.x) {
-    const int t0 = g * p.tok_cta, nt = min(p.tok_cta, p.tokens - t0);
-    const int rows = nt * heads;
-    __syncthreads();
-    fill_angles(p, t0, nt, s_cos, s_sin);
-    __syncthreads();
-    for (int base = 0; base < rows; base += kRows) {
-      const int r = base + grp;
-      const bool live = r < rows;
-      const int tok = live ? r / heads : 0;
-      const int hh = live ? r - tok * heads : 0;
-      const bool is_q = hh < p.H, is_v = hh >= p.H + p.H_kv;
-      const int h = is_q ? hh : is_v ? hh - p.H - p.H_kv : hh - p.H;
-      const int t = t0 + tok, b = t / p.N, n = t - b * p.N;
-      const __nv_bfloat16* w = is_q ? p.wq : is_v ? nullptr : p.wk;
-      const __nv_bfloat16* dy = is_q ? p.dq : is_v ? p.dv : p.dk;
-      float gr[16], x[16];
+  for (int k = 0; k < 2; ++k)
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) dw[k][i][0] = dw[k][i][1] = 0.f;
+  const int64_t step = static_cast<int64_t>(p.N) * D;
+  const int64_t tasks = static_cast<int64_t>(p.tokens) * p.parts;
+  for (int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + warp; task < tasks;
+       task += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const int t = static_cast<int>(task / p.parts), part = static_cast<int>(task - static_cast<int64_t>(t) * p.parts);
+    const int b = t / p.N, n = t - b * p.N;
+    const uint4* row = reinterpret_cast<const uint4*>(p.qkv + static_cast<int64_t>(t) * p.ld);
+    uint4* out = reinterpret_cast<uint4*>(p.dqkv + static_cast<int64_t>(t) * p.ld_out);
+    const int64_t tq = (static_cast<int64_t>(b) * p.H * p.N + n) * D;
+    const int64_t tk = (static_cast<int64_t>(b) * p.H_kv * p.N + n) * D;
+    uint4 ga[kBatchBwd], gb[kBatchBwd], xa[kBatchBwd], xb[kBatchBwd];
+    auto load = [&](int g0) {
       #pragma unroll
-      for (int i = 0; i < 16; ++i) gr[i] = x[i] = 0.f;
-      if (live) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            dy + ((static_cast<int64_t>(b) * (is_q ? p.H : p.H_kv) + h) * p.N + n) * D);
-        unpack8(__ldcs(src + ch.a), gr);
-        unpack8(__ldcs(src + ch.b), gr + 8);
-        if (w) {
-          const uint4* xs = reinterpret_cast<const uint4*>(p.qkv + static_cast<int64_t>(t) * p.ld +
-                                                           hh * D);
-          unpack8(__ldcs(xs + ch.a), x);
-          unpack8(__ldcs(xs + ch.b), x + 8);
+      for (int u = 0; u < kBatchBwd; ++u) {
+        int h;
+        const int kind = gr.kind(g0 + u * p.parts, sub, h);
+        ga[u] = gb[u] = xa[u] = xb[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (g0 + u * p.parts < gr.all && h < (kind ? p.H_kv : p.H)) {
+          const __nv_bfloat16* dy = kind == 0 ? p.dq : kind == 1 ? p.dk : p.dv;
+          const uint4* src = reinterpret_cast<const uint4*>(dy + (kind ? tk : tq) + h * step);
+          ga[u] = __ldcs(src + ln.a);
+          gb[u] = __ldcs(src + ln.b);
+          if (kind == 0 ? p.wq != nullptr : kind == 1 && p.wk != nullptr) {
+            const int hh = h + (kind ? p.H : 0);
+            xa[u] = __ldcs(row + hh * (D / 8) + ln.a);
+            xb[u] = __ldcs(row + hh * (D / 8) + ln.b);
+          }
         }
       }
-      if (!is_v) turn<D, INTER, -1>(gr, ch, s_cos + tok * nf, s_sin + tok * nf);
-      float wf[16], ss = 0.f, dot = 0.f;
-      if (w) {
-        unpack8(__ldg(reinterpret_cast<const uint4*>(w) + ch.a), wf);
-        unpack8(__ldg(reinterpret_cast<const uint4*>(w) + ch.b), wf + 8);
-        #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          ss = fmaf(x[i], x[i], ss);
-          dot = fmaf(gr[i] * wf[i], x[i], dot);
+    };
+    load(part);
+    __syncwarp();
+    const int position = p.rot ? p.positions[t] : 0;
+    #pragma unroll
+    for (int j = lane; j < D / 2; j += 32) {
+      const L o(j % kLanes, p.rot);
+      float c = 1.f, s = 0.f;
+      if (o.turns(j / kLanes)) angle(p, position, o.freq(j / kLanes), c, s);
+      s_cs[warp][j] = make_float2(c, s);
+    }
+    __syncwarp();
+    for (int g0 = part; g0 < gr.all; g0 += kBatchBwd * p.parts) {
+      if (g0 != part) load(g0);
+      #pragma unroll
+      for (int u = 0; u < kBatchBwd; ++u) {
+        if (g0 + u * p.parts >= gr.all) break;
+        int h;
+        const int kind = gr.kind(g0 + u * p.parts, sub, h);
+        const bool live = h < (kind ? p.H_kv : p.H);
+        uint4 oa = ga[u], ob = gb[u];
+        if (kind < 2) {
+          float g[8][2];
+          L::unpack(ga[u], gb[u], g);
+          #pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (!ln.turns(i)) continue;
+            const float2 cs = s_cs[warp][i * kLanes + l];
+            float y0, y1;
+            fmul2(y0, y1, g[i][1], g[i][0], cs.y, -cs.y);
+            ffma2(g[i][0], g[i][1], g[i][0], g[i][1], cs.x, cs.x, y0, y1);
+          }
+          if (kind ? p.wk != nullptr : p.wq != nullptr) {
+            float x[8][2];
+            L::unpack(xa[u], xb[u], x);
+            float s0 = 0.f, s1 = 0.f, d0 = 0.f, d1 = 0.f;
+            #pragma unroll
+            for (int i = 0; i < 8; ++i)
+              ffma2(s0, s1, x[i][0], x[i][1], x[i][0], x[i][1], s0, s1);
+            const float r = rsqrtf(row_sum<D>(s0 + s1) * (1.f / D) + p.eps);
+            auto weigh = [&](float (&acc)[8][2]) {
+              #pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 w = s_w[kind][i * kLanes + l];
+                fmul2(x[i][0], x[i][1], x[i][0], x[i][1], r, r);
+                ffma2(acc[i][0], acc[i][1], g[i][0], g[i][1], x[i][0], x[i][1], acc[i][0], acc[i][1]);
+                fmul2(g[i][0], g[i][1], g[i][0], g[i][1], w.x, w.y);
+                ffma2(d0, d1, g[i][0], g[i][1], x[i][0], x[i][1], d0, d1);
+              }
+            };
+            if (kind) weigh(dw[1]); else weigh(dw[0]);
+            const float mean = row_sum<D>(d0 + d1) * (-1.f / D);
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              ffma2(g[i][0], g[i][1], x[i][0], x[i][1], mean, mean, g[i][0], g[i][1]);
+              fmul2(g[i][0], g[i][1], g[i][0], g[i][1], r, r);
+            }
+          }
+          L::pack(g, oa, ob);
         }
-      }
-      ss = row_sum<D>(ss);
-      dot = row_sum<D>(dot);
-      if (w) {
-        const float rn = rsqrtf(ss * (1.f / D) + p.eps);
-        const float back = rn * rn * dot * (1.f / D);
-        #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float gx = gr[i] * x[i] * rn;
-          if (is_q) dwq[i] += gx; else dwk[i] += gx;
-          gr[i] = rn * (gr[i] * wf[i] - x[i] * back);
+        if (live) {
+          const int hh = h + (kind == 0 ? 0 : kind == 1 ? p.H : p.H + p.H_kv);
+          out[hh * (D / 8) + ln.a] = oa;
+          out[hh * (D / 8) + ln.b] = ob;
         }
-      }
-      if (live) {
-        uint4* dst =
-            reinterpret_cast<uint4*>(p.dqkv + static_cast<int64_t>(t) * p.ld_out + hh * D);
-        dst[ch.a] = pack8(gr);
-        dst[ch.b] = pack8(gr + 8);
       }
     }
   }
   if (!p.partial) return;
-  // the CTA's sums: over the warp's row groups by shuffles, over the warps in order
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // the CTA's sums: over the rows of a warp's groups by shuffles, over the warps in order
   #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    float* acc = which ? dwk : dwq;
+  for (int k = 0; k < 2; ++k) {
     #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 8; ++i)
       #pragma unroll
-      for (int off = 16; off >= kLanes; off >>= 1)
-        acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
+      for (int j = 0; j < 2; ++j)
+        #pragma unroll
+        for (int off = 16; off >= kLanes; off >>= 1)
+          dw[k][i][j] += __shfl_xor_sync(0xffffffffu, dw[k][i][j], off);
     __syncthreads();
-    if (lane < kLanes) {
+    if (sub == 0) {
       #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        s_dw[warp][8 * ch.a + i] = acc[i];
-        s_dw[warp][8 * ch.b + i] = acc[8 + i];
+        s_dw[warp][ln.first(i)] = dw[k][i][0];
+        s_dw[warp][ln.second(i)] = dw[k][i][1];
       }
     }
     __syncthreads();
@@ -337,12 +441,12 @@ __global__ void __launch_bounds__(kRopeThreads) qkv_rope_bwd_kernel(RopeParams p
       float v = 0.f;
       #pragma unroll
       for (int wi = 0; wi < kWarps; ++wi) v += s_dw[wi][threadIdx.x];
-      p.partial[(static_cast<size_t>(blockIdx.x) * 2 + which) * D + threadIdx.x] = v;
+      p.partial[(static_cast<size_t>(blockIdx.x) * 2 + k) * D + threadIdx.x] = v;
     }
   }
 }
 
-// dwq (block 0) and dwk (block 1): the CTAs' shares, 8 runs of CTAs summed side by side, then joined
+// dwq (block 0) and dwk (block 1): the CTAs' shares, runs of CTAs summed side by side, then joined
 // in order.
 __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__ partial, int ctas,
                                                        int d, float* dwq, float* dwk) {
@@ -363,43 +467,44 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__
 }
 
 template <int D, bool INTER>
-cudaError_t launch_fwd(const RopeParams& p, int kind, dim3 grid, int smem, cudaStream_t st) {
-  if (kind == kCacheNone) qkv_rope_kernel<D, INTER, kCacheNone><<<grid, kRopeThreads, smem, st>>>(p);
-  else if (kind == kCacheBf16)
-    qkv_rope_kernel<D, INTER, kCacheBf16><<<grid, kRopeThreads, smem, st>>>(p);
-  else qkv_rope_kernel<D, INTER, kCacheE4m3><<<grid, kRopeThreads, smem, st>>>(p);
+cudaError_t launch_fwd(const RopeParams& p, int kind, int ctas, cudaStream_t st) {
+  if (kind == kCacheNone) qkv_rope_kernel<D, INTER, kCacheNone><<<ctas, kRopeThreads, 0, st>>>(p);
+  else if (kind == kCacheBf16) qkv_rope_kernel<D, INTER, kCacheBf16><<<ctas, kRopeThreads, 0, st>>>(p);
+  else qkv_rope_kernel<D, INTER, kCacheE4m3><<<ctas, kRopeThreads, 0, st>>>(p);
   return cudaGetLastError();
+}
+
+// Warps of one token: one while the tokens alone fill the GPU (two CTAs of 8 warps on each of 152
+// SMs); else more, so that each has fewer rows one after another.
+int parts_of(int tokens) {
+  int parts = 1;
+  while (parts < kWarps && static_cast<int64_t>(tokens) * parts < 2 * kWarps * 152) parts *= 2;
+  return parts;
 }
 
 }  // namespace
 
 cudaError_t launch_qkv_rope(RopeParams& p, int d, bool interleaved, int kind, cudaStream_t st) {
-  const int heads = p.H + 2 * p.H_kv, rows_cta = kRopeThreads / (d / 16);
-  // Enough tokens for four CTAs of four tokens on every SM: four tokens a CTA share the angles'
-  // work and a CTA's rows of one head are neighbours.  Fewer: one row a thread, for latency.
-  const bool many = p.tokens >= 4 * 4 * 152;
-  p.tok_cta = many ? 4 : 1;
-  p.head_cta = many ? heads : rows_cta;
-  const dim3 grid((p.tokens + p.tok_cta - 1) / p.tok_cta, (heads + p.head_cta - 1) / p.head_cta);
-  const int smem = p.tok_cta * p.rot * 4;
+  p.parts = parts_of(p.tokens);
+  const int tok_cta = kWarps / p.parts;
+  const int ctas = (p.tokens + tok_cta - 1) / tok_cta;
   if (d == 64)
-    return interleaved ? launch_fwd<64, true>(p, kind, grid, smem, st)
-                       : launch_fwd<64, false>(p, kind, grid, smem, st);
-  return interleaved ? launch_fwd<128, true>(p, kind, grid, smem, st)
-                     : launch_fwd<128, false>(p, kind, grid, smem, st);
+    return interleaved ? launch_fwd<64, true>(p, kind, ctas, st)
+                       : launch_fwd<64, false>(p, kind, ctas, st);
+  return interleaved ? launch_fwd<128, true>(p, kind, ctas, st)
+                     : launch_fwd<128, false>(p, kind, ctas, st);
 }
 
 cudaError_t launch_qkv_rope_bwd(RopeParams& p, int d, bool interleaved, cudaStream_t st) {
-  p.tok_cta = 4;
-  const int groups = (p.tokens + p.tok_cta - 1) / p.tok_cta;
-  const int ctas = groups < kRopeBwdMaxCtas ? groups : kRopeBwdMaxCtas;
-  const int smem = p.tok_cta * p.rot * 4;
+  p.parts = parts_of(p.tokens);
+  const int64_t want = (static_cast<int64_t>(p.tokens) * p.parts + kWarps - 1) / kWarps;
+  const int ctas = static_cast<int>(want < kRopeBwdCtas ? want : kRopeBwdCtas);
   if (d == 64) {
-    if (interleaved) qkv_rope_bwd_kernel<64, true><<<ctas, kRopeThreads, smem, st>>>(p);
-    else qkv_rope_bwd_kernel<64, false><<<ctas, kRopeThreads, smem, st>>>(p);
+    if (interleaved) qkv_rope_bwd_kernel<64, true><<<ctas, kRopeThreads, 0, st>>>(p);
+    else qkv_rope_bwd_kernel<64, false><<<ctas, kRopeThreads, 0, st>>>(p);
   } else {
-    if (interleaved) qkv_rope_bwd_kernel<128, true><<<ctas, kRopeThreads, smem, st>>>(p);
-    else qkv_rope_bwd_kernel<128, false><<<ctas, kRopeThreads, smem, st>>>(p);
+    if (interleaved) qkv_rope_bwd_kernel<128, true><<<ctas, kRopeThreads, 0, st>>>(p);
+    else qkv_rope_bwd_kernel<128, false><<<ctas, kRopeThreads, 0, st>>>(p);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.partial) return e;

@@ -118,7 +118,7 @@ def test_rope_bwd_checks(lib, kw, code):
 
 def test_rope_bwd_workspace(lib):
     f = lib.attn_qkv_rope_bwd_workspace_bytes
-    assert f(2, 5, 8, 2, 128) == 608 * 2 * 128 * 4 and f(1, 1, 1, 1, 64) == 608 * 2 * 64 * 4
+    assert f(2, 5, 8, 2, 128) == 304 * 2 * 128 * 4 and f(1, 1, 1, 1, 64) == 304 * 2 * 64 * 4
     assert f(1, 1, 1, 1, 96) == f(0, 1, 1, 1, 64) == f(1, 1, 0, 1, 64) == 0
 
 
