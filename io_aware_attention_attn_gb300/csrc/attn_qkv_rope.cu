@@ -14,7 +14,7 @@
 // and streams the token's heads through them, loads a batch ahead.  In the forward the norm's
 // weight is folded in: with r the inverse root mean square,
 //   (y_a, y_b) = r (x_a, x_b) * (w_a c, w_b c) + r (x_b, x_a) * (-w_b s, w_a s),
-// three packed operations a pair.
+// three packed operations on two values each.
 //
 // Angles: t = position * inv_freq modulo one turn, in 64-bit fixed point (a turn is 2^64), so the
 // product wraps exactly and a position of 2^20 costs no accuracy; the top 32 bits go to sincospi.
@@ -49,8 +49,9 @@ __device__ __forceinline__ void angle(const RopeParams& p, int position, int f, 
   s *= p.rope_scale;
 }
 
-// A lane's 16 elements as 8 pairs.  Half layout: pair i is element i of chunk a and of chunk b.
-// Interleaved: pairs 0..3 are chunk a's neighbours, 4..7 chunk b's.
+// A lane's 16 elements as 8 pairs (a_i, b_i).  Half layout: element i of chunk a and of chunk b.
+// Interleaved: pairs 0..3 are chunk a's neighbours, 4..7 chunk b's.  The a's and the b's are two
+// arrays, so that packed operations run along i in both layouts.
 template <int D, bool INTER>
 struct Lane {
   static constexpr int kLanes = D / 16;
@@ -77,33 +78,35 @@ struct Lane {
   __device__ __forceinline__ int freq(int i) const { return INTER ? first(i) >> 1 : 8 * a + i; }
   __device__ __forceinline__ bool turns(int i) const { return i < 4 ? ta : tb; }
   // 16 bf16 values to pairs and back
-  static __device__ __forceinline__ void unpack(const uint4& va, const uint4& vb, float (&x)[8][2]) {
+  static __device__ __forceinline__ void unpack(const uint4& va, const uint4& vb, float (&xa)[8],
+                                                float (&xb)[8]) {
     const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
     #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (INTER) {
-        x[i][0] = bf16lo_to_f32(wa[i]);
-        x[i][1] = bf16hi_to_f32(wa[i]);
-        x[4 + i][0] = bf16lo_to_f32(wb[i]);
-        x[4 + i][1] = bf16hi_to_f32(wb[i]);
+        xa[i] = bf16lo_to_f32(wa[i]);
+        xb[i] = bf16hi_to_f32(wa[i]);
+        xa[4 + i] = bf16lo_to_f32(wb[i]);
+        xb[4 + i] = bf16hi_to_f32(wb[i]);
       } else {
-        x[2 * i][0] = bf16lo_to_f32(wa[i]);
-        x[2 * i + 1][0] = bf16hi_to_f32(wa[i]);
-        x[2 * i][1] = bf16lo_to_f32(wb[i]);
-        x[2 * i + 1][1] = bf16hi_to_f32(wb[i]);
+        xa[2 * i] = bf16lo_to_f32(wa[i]);
+        xa[2 * i + 1] = bf16hi_to_f32(wa[i]);
+        xb[2 * i] = bf16lo_to_f32(wb[i]);
+        xb[2 * i + 1] = bf16hi_to_f32(wb[i]);
       }
     }
   }
-  static __device__ __forceinline__ void pack(const float (&x)[8][2], uint4& va, uint4& vb) {
+  static __device__ __forceinline__ void pack(const float (&xa)[8], const float (&xb)[8], uint4& va,
+                                              uint4& vb) {
     uint32_t wa[4], wb[4];
     #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (INTER) {
-        wa[i] = pack_bf16x2(x[i][0], x[i][1]);
-        wb[i] = pack_bf16x2(x[4 + i][0], x[4 + i][1]);
+        wa[i] = pack_bf16x2(xa[i], xb[i]);
+        wb[i] = pack_bf16x2(xa[4 + i], xb[4 + i]);
       } else {
-        wa[i] = pack_bf16x2(x[2 * i][0], x[2 * i + 1][0]);
-        wb[i] = pack_bf16x2(x[2 * i][1], x[2 * i + 1][1]);
+        wa[i] = pack_bf16x2(xa[2 * i], xa[2 * i + 1]);
+        wb[i] = pack_bf16x2(xb[2 * i], xb[2 * i + 1]);
       }
     }
     va = make_uint4(wa[0], wa[1], wa[2], wa[3]);
@@ -117,14 +120,24 @@ __device__ __forceinline__ float row_sum(float v) {
   for (int off = D / 32; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
   return v;
 }
+__device__ __forceinline__ float sum_squares(const float (&xa)[8], const float (&xb)[8]) {
+  float s0 = 0.f, s1 = 0.f;
+  #pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    ffma2(s0, s1, xa[i], xa[i + 1], xa[i], xa[i + 1], s0, s1);
+    ffma2(s0, s1, xb[i], xb[i + 1], xb[i], xb[i + 1], s0, s1);
+  }
+  return s0 + s1;
+}
 
 // A row's E4M3 codes and scale into the cache.
 template <int D, bool INTER>
-__device__ __forceinline__ void store_codes(const float (&x)[8][2], uint8_t* row, float* scale, int ca,
-                                            int cb, bool write, bool first_lane) {
+__device__ __forceinline__ void store_codes(const float (&xa)[8], const float (&xb)[8], uint8_t* row,
+                                            float* scale, int ca, int cb, bool write,
+                                            bool first_lane) {
   float amax = 0.f;
   #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmax3(amax, fabsf(x[i][0]), fabsf(x[i][1]));
+  for (int i = 0; i < 8; ++i) amax = fmax3(amax, fabsf(xa[i]), fabsf(xb[i]));
   #pragma unroll
   for (int off = D / 32; off > 0; off >>= 1)
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
@@ -139,11 +152,11 @@ __device__ __forceinline__ void store_codes(const float (&x)[8][2], uint8_t* row
   #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if (INTER) {
-      wa[i] = codes(x[2 * i][0], x[2 * i][1], x[2 * i + 1][0], x[2 * i + 1][1]);
-      wb[i] = codes(x[4 + 2 * i][0], x[4 + 2 * i][1], x[5 + 2 * i][0], x[5 + 2 * i][1]);
+      wa[i] = codes(xa[2 * i], xb[2 * i], xa[2 * i + 1], xb[2 * i + 1]);
+      wb[i] = codes(xa[4 + 2 * i], xb[4 + 2 * i], xa[5 + 2 * i], xb[5 + 2 * i]);
     } else {
-      wa[i] = codes(x[4 * i][0], x[4 * i + 1][0], x[4 * i + 2][0], x[4 * i + 3][0]);
-      wb[i] = codes(x[4 * i][1], x[4 * i + 1][1], x[4 * i + 2][1], x[4 * i + 3][1]);
+      wa[i] = codes(xa[4 * i], xa[4 * i + 1], xa[4 * i + 2], xa[4 * i + 3]);
+      wb[i] = codes(xb[4 * i], xb[4 * i + 1], xb[4 * i + 2], xb[4 * i + 3]);
     }
   }
   *reinterpret_cast<uint2*>(row + 8 * ca) = make_uint2(wa[0], wa[1]);
@@ -151,48 +164,37 @@ __device__ __forceinline__ void store_codes(const float (&x)[8][2], uint8_t* row
   if (first_lane) *scale = sc;
 }
 
-// The rows a warp-wide load covers: group gi of a token, 0 .. nq - 1 query heads, then key, then
-// value heads.
-template <int RW>
-struct Groups {
-  int nq, nk, all;
-  __device__ __forceinline__ Groups(int H, int H_kv)
-      : nq((H + RW - 1) / RW), nk((H_kv + RW - 1) / RW), all(nq + 2 * nk) {}
-  // 0 query, 1 key, 2 value; `h`: this lane's head of that kind
-  __device__ __forceinline__ int kind(int gi, int sub, int& h) const {
-    const int k = gi < nq ? 0 : gi < nq + nk ? 1 : 2;
-    h = (gi - (k == 0 ? 0 : k == 1 ? nq : nq + nk)) * RW + sub;
-    return k;
-  }
-};
-
-constexpr int kBatch = 4;  // groups a warp loads before it uses the first
+// A warp-wide load covers kRw consecutive heads of the row (group g: heads g kRw ..), query, key and
+// value heads alike; a group may hold heads of two kinds.  Two groups are computed while the next
+// two are on their way.
+constexpr int kBatch = 2;
 
 template <int D, bool INTER, int CACHE>
-__global__ void __launch_bounds__(kRopeThreads) qkv_rope_kernel(RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, CACHE == kCacheE4m3 ? 2 : 3) qkv_rope_kernel(RopeParams p) {
   using L = Lane<D, INTER>;
   constexpr int kLanes = D / 16, kRw = 32 / kLanes;
-  __shared__ float4 s_coef[kWarps][2][D / 2];  // [query, key][pair i of lane l at i * kLanes + l]
+  // per warp and kind (query, key): of pairs 2m, 2m + 1 of lane l, at m * kLanes + l,
+  // (w_a c, w_a c, w_b c, w_b c) and (-w_b s, -w_b s, w_a s, w_a s)
+  __shared__ float4 s_coef[kWarps][2][2][D / 4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % kLanes, sub = lane / kLanes;
   const int t = blockIdx.x * (kWarps / p.parts) + warp / p.parts;
   if (t >= p.tokens) return;
   const int part = warp % p.parts;
   const L ln(l, p.rot);
-  const Groups<kRw> gr(p.H, p.H_kv);
+  const int heads = p.H + 2 * p.H_kv, groups = (heads + kRw - 1) / kRw;
   const int b = t / p.N, n = t - b * p.N;
   const uint4* row = reinterpret_cast<const uint4*>(p.qkv + static_cast<int64_t>(t) * p.ld);
-  uint4 xa[kBatch], xb[kBatch];
+  const uint4 *row_a = row + ln.a, *row_b = row + ln.b;
+  uint4 na[kBatch], nb[kBatch];
   auto load = [&](int g0) {
     #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      int h;
-      const int kind = gr.kind(g0 + u * p.parts, sub, h);
-      xa[u] = xb[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (g0 + u * p.parts < gr.all && h < (kind ? p.H_kv : p.H)) {
-        const int hh = h + (kind == 0 ? 0 : kind == 1 ? p.H : p.H + p.H_kv);
-        xa[u] = __ldcs(row + hh * (D / 8) + ln.a);
-        xb[u] = __ldcs(row + hh * (D / 8) + ln.b);
+      const int hh = (g0 + u * p.parts) * kRw + sub;
+      na[u] = nb[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (hh < heads) {
+        na[u] = __ldcs(row_a + hh * (D / 8));
+        nb[u] = __ldcs(row_b + hh * (D / 8));
       }
     }
   };
@@ -201,8 +203,8 @@ __global__ void __launch_bounds__(kRopeThreads) qkv_rope_kernel(RopeParams p) {
     const int position = p.rot ? p.positions[t] : 0;
     #pragma unroll
     for (int j = lane; j < D / 2; j += 32) {
-      const int i = j / kLanes, lj = j % kLanes;
-      const L o(lj, p.rot);
+      const int i = j / kLanes;
+      const L o(j % kLanes, p.rot);
       float c = 1.f, s = 0.f;
       if (o.turns(i)) angle(p, position, o.freq(i), c, s);
       #pragma unroll
@@ -210,7 +212,13 @@ __global__ void __launch_bounds__(kRopeThreads) qkv_rope_kernel(RopeParams p) {
         const __nv_bfloat16* w = k ? p.wk : p.wq;
         const float wa = w ? __bfloat162float(w[o.first(i)]) : 1.f;
         const float wb = w ? __bfloat162float(w[o.second(i)]) : 1.f;
-        s_coef[warp][k][j] = make_float4(wa * c, wb * c, -(wb * s), wa * s);
+        const int at = (i >> 1) * kLanes + j % kLanes;
+        float* cc = reinterpret_cast<float*>(&s_coef[warp][k][0][at]) + (i & 1);
+        float* cs = reinterpret_cast<float*>(&s_coef[warp][k][1][at]) + (i & 1);
+        cc[0] = wa * c;
+        cc[2] = wb * c;
+        cs[0] = -(wb * s);
+        cs[2] = wa * s;
       }
     }
     __syncwarp();
@@ -227,62 +235,78 @@ __global__ void __launch_bounds__(kRopeThreads) qkv_rope_kernel(RopeParams p) {
       slot = -1;
     }
   }
-  for (int g0 = part; g0 < gr.all; g0 += kBatch * p.parts) {
-    if (g0 != part) load(g0);
+  for (int g0 = part; g0 < groups; g0 += kBatch * p.parts) {
+    uint4 oa[kBatch], ob[kBatch];
     #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      if (g0 + u * p.parts >= gr.all) break;
-      int h;
-      const int kind = gr.kind(g0 + u * p.parts, sub, h);
-      const bool live = h < (kind ? p.H_kv : p.H);
-      uint4 oa = xa[u], ob = xb[u];
-      float x[8][2];
-      if (kind < 2) {
-        L::unpack(xa[u], xb[u], x);
-        if (kind ? p.wk != nullptr : p.wq != nullptr) {
-          float s0 = 0.f, s1 = 0.f;
+      oa[u] = na[u];
+      ob[u] = nb[u];
+    }
+    if (g0 + kBatch * p.parts < groups) load(g0 + kBatch * p.parts);
+    #pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int g = g0 + u * p.parts;
+      if (g >= groups) break;
+      const int hh = g * kRw + sub;
+      const bool live = hh < heads, is_q = hh < p.H, is_v = hh >= p.H + p.H_kv;
+      float xa[8], xb[8];
+      if (g * kRw < p.H + p.H_kv) {  // not all value heads
+        L::unpack(oa[u], ob[u], xa, xb);
+        const bool normed = is_q ? p.wq != nullptr : !is_v && p.wk != nullptr;
+        if (p.wq || p.wk) {
+          float r = rsqrtf(row_sum<D>(sum_squares(xa, xb)) * (1.f / D) + p.eps);
+          r = normed ? r : 1.f;
           #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            ffma2(s0, s1, x[i][0], x[i][1], x[i][0], x[i][1], s0, s1);
-          const float r = rsqrtf(row_sum<D>(s0 + s1) * (1.f / D) + p.eps);
+          for (int i = 0; i < 8; i += 2) {
+            fmul2(xa[i], xa[i + 1], xa[i], xa[i + 1], r, r);
+            fmul2(xb[i], xb[i + 1], xb[i], xb[i + 1], r, r);
+          }
+        }
+        if (!is_v) {
+          const float4* cc = &s_coef[warp][is_q ? 0 : 1][0][l];
           #pragma unroll
-          for (int i = 0; i < 8; ++i) fmul2(x[i][0], x[i][1], x[i][0], x[i][1], r, r);
+          for (int i = 0; i < 8; i += 2) {
+            const float4 c = cc[(i >> 1) * kLanes];
+            float ya0, ya1, yb0, yb1;
+            fmul2(ya0, ya1, xa[i], xa[i + 1], c.x, c.y);
+            fmul2(yb0, yb1, xb[i], xb[i + 1], c.z, c.w);
+            if (ln.turns(i)) {
+              const float4 s = cc[D / 4 + (i >> 1) * kLanes];
+              ffma2(ya0, ya1, xb[i], xb[i + 1], s.x, s.y, ya0, ya1);
+              ffma2(yb0, yb1, xa[i], xa[i + 1], s.z, s.w, yb0, yb1);
+            }
+            xa[i] = ya0;
+            xa[i + 1] = ya1;
+            xb[i] = yb0;
+            xb[i + 1] = yb1;
+          }
+          L::pack(xa, xb, oa[u], ob[u]);
         }
-        const float4* co = s_coef[warp][kind] + l;
-        #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 c = co[i * kLanes];
-          float y0, y1;
-          fmul2(y0, y1, x[i][0], x[i][1], c.x, c.y);
-          if (ln.turns(i)) ffma2(y0, y1, x[i][1], x[i][0], c.z, c.w, y0, y1);
-          x[i][0] = y0;
-          x[i][1] = y1;
-        }
-        L::pack(x, oa, ob);
       } else if (CACHE == kCacheE4m3) {
-        L::unpack(xa[u], xb[u], x);
+        L::unpack(oa[u], ob[u], xa, xb);
       }
-      __nv_bfloat16* out = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+      const int h = hh - (is_q ? 0 : is_v ? p.H + p.H_kv : p.H);
+      __nv_bfloat16* out = is_q ? p.q : is_v ? p.v : p.k;
       if (live && out) {
-        uint4* dst = reinterpret_cast<uint4*>(out + (kind ? tk : tq) + h * step);
-        dst[ln.a] = oa;
-        dst[ln.b] = ob;
+        uint4* dst = reinterpret_cast<uint4*>(out + (is_q ? tq : tk) + h * step);
+        dst[ln.a] = oa[u];
+        dst[ln.b] = ob[u];
       }
-      if (CACHE != kCacheNone && kind > 0) {
-        const bool write = live && slot >= 0;
+      if (CACHE != kCacheNone && g * kRw + kRw > p.H) {
+        const bool write = live && !is_q && slot >= 0;
         const int64_t at_row =
             (static_cast<int64_t>(h) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
         const int64_t at = page * p.page_stride + at_row * D;
-        uint8_t* base = kind == 2 ? p.vc : p.kc;
+        uint8_t* base = is_v ? p.vc : p.kc;
         if (CACHE == kCacheBf16) {
           if (write) {
             uint4* dst = reinterpret_cast<uint4*>(base + 2 * at);
-            dst[ln.a] = oa;
-            dst[ln.b] = ob;
+            dst[ln.a] = oa[u];
+            dst[ln.b] = ob[u];
           }
         } else {
-          float* scales = kind == 2 ? p.vs : p.ks;
-          store_codes<D, INTER>(x, base + (write ? at : 0),
+          float* scales = is_v ? p.vs : p.ks;
+          store_codes<D, INTER>(xa, xb, base + (write ? at : 0),
                                 scales + (write ? ((page * p.H_kv) << p.page_shift) + at_row : 0),
                                 ln.a, ln.b, write, l == 0);
         }
@@ -293,59 +317,57 @@ __global__ void __launch_bounds__(kRopeThreads) qkv_rope_kernel(RopeParams p) {
 
 // Gradients of the rows, and each CTA's share of the weights' gradients.  With t = x r, g the
 // gradient turned back and u = g w:  dx = r (u - t mean(u t)),  dw += g t.
-constexpr int kBatchBwd = 2;
-
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParams p) {
   using L = Lane<D, INTER>;
   constexpr int kLanes = D / 16, kRw = 32 / kLanes;
   __shared__ __align__(16) float s_dw[kWarps][D];     // the weights' sums, at the end
-  __shared__ float2 s_cs[kWarps][D / 2];              // cos, sin of pair i of lane l
-  __shared__ float2 s_w[2][D / 2];                    // the weights, likewise
+  // of pairs 2m, 2m + 1 of lane l, at m * kLanes + l: (c, c, s, s), per warp
+  __shared__ float4 s_cs[kWarps][D / 4];
+  __shared__ float4 s_w[2][D / 4];                    // (w_a, w_a, w_b, w_b), likewise
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % kLanes, sub = lane / kLanes;
   const L ln(l, p.rot);
-  const Groups<kRw> gr(p.H, p.H_kv);
   for (int j = threadIdx.x; j < D; j += kRopeThreads) {
-    const int k = j / (D / 2), jj = j % (D / 2);
+    const int k = j / (D / 2), jj = j % (D / 2), i = jj / kLanes;
     const L o(jj % kLanes, p.rot);
     const __nv_bfloat16* w = k ? p.wk : p.wq;
-    s_w[k][jj] = w ? make_float2(__bfloat162float(w[o.first(jj / kLanes)]),
-                                 __bfloat162float(w[o.second(jj / kLanes)]))
-                   : make_float2(1.f, 1.f);
+    float* f = reinterpret_cast<float*>(&s_w[k][(i >> 1) * kLanes + jj % kLanes]) + (i & 1);
+    f[0] = w ? __bfloat162float(w[o.first(i)]) : 1.f;
+    f[2] = w ? __bfloat162float(w[o.second(i)]) : 1.f;
   }
   __syncthreads();
-  float dw[2][8][2];
+  float dqa[8], dqb[8], dka[8], dkb[8];
   #pragma unroll
-  for (int k = 0; k < 2; ++k)
-    #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[k][i][0] = dw[k][i][1] = 0.f;
+  for (int i = 0; i < 8; ++i) dqa[i] = dqb[i] = dka[i] = dkb[i] = 0.f;
+  const int heads = p.H + 2 * p.H_kv, groups = (heads + kRw - 1) / kRw;
   const int64_t step = static_cast<int64_t>(p.N) * D;
   const int64_t tasks = static_cast<int64_t>(p.tokens) * p.parts;
   for (int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + warp; task < tasks;
        task += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int t = static_cast<int>(task / p.parts), part = static_cast<int>(task - static_cast<int64_t>(t) * p.parts);
+    const int t = static_cast<int>(task / p.parts);
+    const int part = static_cast<int>(task - static_cast<int64_t>(t) * p.parts);
     const int b = t / p.N, n = t - b * p.N;
     const uint4* row = reinterpret_cast<const uint4*>(p.qkv + static_cast<int64_t>(t) * p.ld);
     uint4* out = reinterpret_cast<uint4*>(p.dqkv + static_cast<int64_t>(t) * p.ld_out);
     const int64_t tq = (static_cast<int64_t>(b) * p.H * p.N + n) * D;
     const int64_t tk = (static_cast<int64_t>(b) * p.H_kv * p.N + n) * D;
-    uint4 ga[kBatchBwd], gb[kBatchBwd], xa[kBatchBwd], xb[kBatchBwd];
+    uint4 ga[kBatch], gb[kBatch], ya[kBatch], yb[kBatch];
     auto load = [&](int g0) {
       #pragma unroll
-      for (int u = 0; u < kBatchBwd; ++u) {
-        int h;
-        const int kind = gr.kind(g0 + u * p.parts, sub, h);
-        ga[u] = gb[u] = xa[u] = xb[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (g0 + u * p.parts < gr.all && h < (kind ? p.H_kv : p.H)) {
-          const __nv_bfloat16* dy = kind == 0 ? p.dq : kind == 1 ? p.dk : p.dv;
-          const uint4* src = reinterpret_cast<const uint4*>(dy + (kind ? tk : tq) + h * step);
+      for (int u = 0; u < kBatch; ++u) {
+        const int hh = (g0 + u * p.parts) * kRw + sub;
+        ga[u] = gb[u] = ya[u] = yb[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (hh < heads) {
+          const bool is_q = hh < p.H, is_v = hh >= p.H + p.H_kv;
+          const int h = hh - (is_q ? 0 : is_v ? p.H + p.H_kv : p.H);
+          const uint4* src = reinterpret_cast<const uint4*>((is_q ? p.dq : is_v ? p.dv : p.dk) +
+                                                            (is_q ? tq : tk) + h * step);
           ga[u] = __ldcs(src + ln.a);
           gb[u] = __ldcs(src + ln.b);
-          if (kind == 0 ? p.wq != nullptr : kind == 1 && p.wk != nullptr) {
-            const int hh = h + (kind ? p.H : 0);
-            xa[u] = __ldcs(row + hh * (D / 8) + ln.a);
-            xb[u] = __ldcs(row + hh * (D / 8) + ln.b);
+          if (is_q ? p.wq != nullptr : !is_v && p.wk != nullptr) {
+            ya[u] = __ldcs(row + hh * (D / 8) + ln.a);
+            yb[u] = __ldcs(row + hh * (D / 8) + ln.b);
           }
         }
       }
@@ -355,62 +377,105 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
     const int position = p.rot ? p.positions[t] : 0;
     #pragma unroll
     for (int j = lane; j < D / 2; j += 32) {
+      const int i = j / kLanes;
       const L o(j % kLanes, p.rot);
       float c = 1.f, s = 0.f;
-      if (o.turns(j / kLanes)) angle(p, position, o.freq(j / kLanes), c, s);
-      s_cs[warp][j] = make_float2(c, s);
+      if (o.turns(i)) angle(p, position, o.freq(i), c, s);
+      float* f = reinterpret_cast<float*>(&s_cs[warp][(i >> 1) * kLanes + j % kLanes]) + (i & 1);
+      f[0] = c;
+      f[2] = s;
     }
     __syncwarp();
-    for (int g0 = part; g0 < gr.all; g0 += kBatchBwd * p.parts) {
+    for (int g0 = part; g0 < groups; g0 += kBatch * p.parts) {
       if (g0 != part) load(g0);
       #pragma unroll
-      for (int u = 0; u < kBatchBwd; ++u) {
-        if (g0 + u * p.parts >= gr.all) break;
-        int h;
-        const int kind = gr.kind(g0 + u * p.parts, sub, h);
-        const bool live = h < (kind ? p.H_kv : p.H);
+      for (int u = 0; u < kBatch; ++u) {
+        const int g = g0 + u * p.parts;
+        if (g >= groups) break;
+        const int hh = g * kRw + sub;
+        const bool is_q = hh < p.H, is_v = hh >= p.H + p.H_kv;
         uint4 oa = ga[u], ob = gb[u];
-        if (kind < 2) {
-          float g[8][2];
-          L::unpack(ga[u], gb[u], g);
-          #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (!ln.turns(i)) continue;
-            const float2 cs = s_cs[warp][i * kLanes + l];
-            float y0, y1;
-            fmul2(y0, y1, g[i][1], g[i][0], cs.y, -cs.y);
-            ffma2(g[i][0], g[i][1], g[i][0], g[i][1], cs.x, cs.x, y0, y1);
-          }
-          if (kind ? p.wk != nullptr : p.wq != nullptr) {
-            float x[8][2];
-            L::unpack(xa[u], xb[u], x);
-            float s0 = 0.f, s1 = 0.f, d0 = 0.f, d1 = 0.f;
+        if (g * kRw < p.H + p.H_kv) {  // not all value heads
+          float fa[8], fb[8];
+          L::unpack(ga[u], gb[u], fa, fb);
+          if (!is_v) {
+            const float4* cs = &s_cs[warp][l];
             #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              ffma2(s0, s1, x[i][0], x[i][1], x[i][0], x[i][1], s0, s1);
-            const float r = rsqrtf(row_sum<D>(s0 + s1) * (1.f / D) + p.eps);
-            auto weigh = [&](float (&acc)[8][2]) {
-              #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float2 w = s_w[kind][i * kLanes + l];
-                fmul2(x[i][0], x[i][1], x[i][0], x[i][1], r, r);
-                ffma2(acc[i][0], acc[i][1], g[i][0], g[i][1], x[i][0], x[i][1], acc[i][0], acc[i][1]);
-                fmul2(g[i][0], g[i][1], g[i][0], g[i][1], w.x, w.y);
-                ffma2(d0, d1, g[i][0], g[i][1], x[i][0], x[i][1], d0, d1);
-              }
-            };
-            if (kind) weigh(dw[1]); else weigh(dw[0]);
-            const float mean = row_sum<D>(d0 + d1) * (-1.f / D);
-            #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              ffma2(g[i][0], g[i][1], x[i][0], x[i][1], mean, mean, g[i][0], g[i][1]);
-              fmul2(g[i][0], g[i][1], g[i][0], g[i][1], r, r);
+            for (int i = 0; i < 8; i += 2) {
+              if (!ln.turns(i)) continue;
+              const float4 c = cs[(i >> 1) * kLanes];
+              float ta0, ta1, tb0, tb1;
+              fmul2(ta0, ta1, fb[i], fb[i + 1], c.z, c.w);
+              fmul2(tb0, tb1, fa[i], fa[i + 1], -c.z, -c.w);
+              ffma2(fa[i], fa[i + 1], fa[i], fa[i + 1], c.x, c.y, ta0, ta1);
+              ffma2(fb[i], fb[i + 1], fb[i], fb[i + 1], c.x, c.y, tb0, tb1);
             }
           }
-          L::pack(g, oa, ob);
+          if (p.wq || p.wk) {
+            const bool normed = is_q ? p.wq != nullptr : !is_v && p.wk != nullptr;
+            float xa[8], xb[8];
+            L::unpack(ya[u], yb[u], xa, xb);
+            float r = rsqrtf(row_sum<D>(sum_squares(xa, xb)) * (1.f / D) + p.eps);
+            r = normed ? r : 1.f;  // without a norm x was not read and is 0
+            const bool all_q = g * kRw + kRw <= p.H, all_k = g * kRw >= p.H && (g + 1) * kRw <= p.H + p.H_kv;
+            const float4* wt = &s_w[is_q ? 0 : 1][l];
+            float d0 = 0.f, d1 = 0.f;
+            #pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              fmul2(xa[i], xa[i + 1], xa[i], xa[i + 1], r, r);
+              fmul2(xb[i], xb[i + 1], xb[i], xb[i + 1], r, r);
+            }
+            if (all_q) {
+              #pragma unroll
+              for (int i = 0; i < 8; i += 2) {
+                ffma2(dqa[i], dqa[i + 1], fa[i], fa[i + 1], xa[i], xa[i + 1], dqa[i], dqa[i + 1]);
+                ffma2(dqb[i], dqb[i + 1], fb[i], fb[i + 1], xb[i], xb[i + 1], dqb[i], dqb[i + 1]);
+              }
+            } else if (all_k) {
+              #pragma unroll
+              for (int i = 0; i < 8; i += 2) {
+                ffma2(dka[i], dka[i + 1], fa[i], fa[i + 1], xa[i], xa[i + 1], dka[i], dka[i + 1]);
+                ffma2(dkb[i], dkb[i + 1], fb[i], fb[i + 1], xb[i], xb[i + 1], dkb[i], dkb[i + 1]);
+              }
+            } else {  // heads of two kinds, or none past the row's end (zeros)
+              #pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if (is_q) {
+                  dqa[i] = fmaf(fa[i], xa[i], dqa[i]);
+                  dqb[i] = fmaf(fb[i], xb[i], dqb[i]);
+                } else if (!is_v) {
+                  dka[i] = fmaf(fa[i], xa[i], dka[i]);
+                  dkb[i] = fmaf(fb[i], xb[i], dkb[i]);
+                }
+              }
+            }
+            if (!is_v) {
+              #pragma unroll
+              for (int i = 0; i < 8; i += 2) {
+                const float4 w = wt[(i >> 1) * kLanes];
+                fmul2(fa[i], fa[i + 1], fa[i], fa[i + 1], w.x, w.y);
+                fmul2(fb[i], fb[i + 1], fb[i], fb[i + 1], w.z, w.w);
+              }
+            }
+            #pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              ffma2(d0, d1, fa[i], fa[i + 1], xa[i], xa[i + 1], d0, d1);
+              ffma2(d0, d1, fb[i], fb[i + 1], xb[i], xb[i + 1], d0, d1);
+            }
+            const float mean = row_sum<D>(d0 + d1) * (-1.f / D);
+            if (normed) {
+              #pragma unroll
+              for (int i = 0; i < 8; i += 2) {
+                ffma2(fa[i], fa[i + 1], xa[i], xa[i + 1], mean, mean, fa[i], fa[i + 1]);
+                ffma2(fb[i], fb[i + 1], xb[i], xb[i + 1], mean, mean, fb[i], fb[i + 1]);
+                fmul2(fa[i], fa[i + 1], fa[i], fa[i + 1], r, r);
+                fmul2(fb[i], fb[i + 1], fb[i], fb[i + 1], r, r);
+              }
+            }
+          }
+          if (!is_v) L::pack(fa, fb, oa, ob);
         }
-        if (live) {
-          const int hh = h + (kind == 0 ? 0 : kind == 1 ? p.H : p.H + p.H_kv);
+        if (hh < heads) {
           out[hh * (D / 8) + ln.a] = oa;
           out[hh * (D / 8) + ln.b] = ob;
         }
@@ -421,19 +486,21 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
   // the CTA's sums: over the rows of a warp's groups by shuffles, over the warps in order
   #pragma unroll
   for (int k = 0; k < 2; ++k) {
+    float* va = k ? dka : dqa;
+    float* vb = k ? dkb : dqb;
     #pragma unroll
     for (int i = 0; i < 8; ++i)
       #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        #pragma unroll
-        for (int off = 16; off >= kLanes; off >>= 1)
-          dw[k][i][j] += __shfl_xor_sync(0xffffffffu, dw[k][i][j], off);
+      for (int off = 16; off >= kLanes; off >>= 1) {
+        va[i] += __shfl_xor_sync(0xffffffffu, va[i], off);
+        vb[i] += __shfl_xor_sync(0xffffffffu, vb[i], off);
+      }
     __syncthreads();
     if (sub == 0) {
       #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        s_dw[warp][ln.first(i)] = dw[k][i][0];
-        s_dw[warp][ln.second(i)] = dw[k][i][1];
+        s_dw[warp][ln.first(i)] = va[i];
+        s_dw[warp][ln.second(i)] = vb[i];
       }
     }
     __syncthreads();
