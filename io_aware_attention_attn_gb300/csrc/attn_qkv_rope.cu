@@ -20,9 +20,11 @@
 // product wraps exactly and a position of 2^20 costs no accuracy; the top 32 bits go to sincospi.
 // The frequency is brought to fixed point by an integer product, not in float64, which this GPU
 // computes at 1/64 of its fp32 rate.
+#include "attn_gen.cuh"
 #include "attn_gen.h"
 #include "sm103_ptx.cuh"
 
+#include <atomic>
 #include <cmath>
 
 namespace attn {
@@ -40,10 +42,10 @@ __device__ __forceinline__ uint64_t turn_step(double f) {
   uint64_t step = sh >= 64 || sh <= -64 ? 0 : sh >= 0 ? p << sh : p >> -sh;
   return bits >> 63 ? 0 - step : step;
 }
-// cos and sin (times scale) of pair `f` of a token.
-__device__ __forceinline__ void angle(const RopeParams& p, int position, int f, float& c, float& s) {
-  const uint64_t phase =
-      static_cast<uint64_t>(static_cast<int64_t>(position)) * turn_step(__ldg(p.inv_freq + f));
+// cos and sin (times scale) of a position's angle.
+__device__ __forceinline__ void angle(const RopeParams& p, int position, uint64_t step, float& c,
+                                      float& s) {
+  const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(position)) * step;
   sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, &s, &c);  // 2^31: half a turn
   c *= p.rope_scale;
   s *= p.rope_scale;
@@ -206,7 +208,7 @@ __global__ void __launch_bounds__(kRopeThreads, CACHE == kCacheE4m3 ? 2 : 3) qkv
       const int i = j / kLanes;
       const L o(j % kLanes, p.rot);
       float c = 1.f, s = 0.f;
-      if (o.turns(i)) angle(p, position, o.freq(i), c, s);
+      if (o.turns(i)) angle(p, position, turn_step(__ldg(p.inv_freq + o.freq(i))), c, s);
       #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const __nv_bfloat16* w = k ? p.wk : p.wq;
@@ -317,10 +319,26 @@ __global__ void __launch_bounds__(kRopeThreads, CACHE == kCacheE4m3 ? 2 : 3) qkv
 
 // Gradients of the rows, and each CTA's share of the weights' gradients.  With t = x r, g the
 // gradient turned back and u = g w:  dx = r (u - t mean(u t)),  dw += g t.
+// A warp walks (token, share of its groups) tasks.  Its rows come through a ring in shared memory, each
+// lane copying and reading its own chunks, so that kDepth - 1 groups are in flight without holding
+// registers, across tokens too (two groups in registers, per token: 69 us where this takes less;
+// see the launcher for figures).
+constexpr int kDepth = 4;
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParams p) {
   using L = Lane<D, INTER>;
-  constexpr int kLanes = D / 16, kRw = 32 / kLanes;
+  constexpr int kLanes = D / 16, kRw = 32 / kLanes, kPairs = D / 64;  // pairs a lane has angles of
+  extern __shared__ uint4 s_ring[];                   // [warp][kDepth][dy a, dy b, x a, x b][lane]
   __shared__ __align__(16) float s_dw[kWarps][D];     // the weights' sums, at the end
   // of pairs 2m, 2m + 1 of lane l, at m * kLanes + l: (c, c, s, s), per warp
   __shared__ float4 s_cs[kWarps][D / 4];
@@ -328,6 +346,52 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % kLanes, sub = lane / kLanes;
   const L ln(l, p.rot);
+  pdl_launch_dependents();
+  const int heads = p.H + 2 * p.H_kv, groups = (heads + kRw - 1) / kRw;
+  const int64_t step = static_cast<int64_t>(p.N) * D;
+  const int tasks = p.tokens * p.parts, stride = gridDim.x * kWarps;
+  uint4* ring = s_ring + warp * (kDepth * 4 * 32) + lane;
+  const uint32_t ring32 = smem_u32(ring);
+  // what is copied next: group i_g of task i_task; past the last task: empty commits
+  int i_task = blockIdx.x * kWarps + warp, i_g = i_task % p.parts, i_slot = 0;
+  const uint4 *i_row = nullptr, *i_q = nullptr, *i_k = nullptr, *i_v = nullptr;
+  auto aim = [&] {
+    if (i_task >= tasks) return;
+    const int t = i_task / p.parts, b = t / p.N, n = t - b * p.N;
+    const int64_t tk = (static_cast<int64_t>(b) * p.H_kv * p.N + n) * D;
+    i_row = reinterpret_cast<const uint4*>(p.qkv + static_cast<int64_t>(t) * p.ld);
+    i_q = reinterpret_cast<const uint4*>(p.dq + (static_cast<int64_t>(b) * p.H * p.N + n) * D);
+    i_k = reinterpret_cast<const uint4*>(p.dk + tk);
+    i_v = reinterpret_cast<const uint4*>(p.dv + tk);
+  };
+  auto issue = [&] {
+    if (i_task < tasks) {
+      const int hh = i_g * kRw + sub;
+      if (hh < heads) {
+        const bool is_q = hh < p.H, is_v = hh >= p.H + p.H_kv;
+        const int h = hh - (is_q ? 0 : is_v ? p.H + p.H_kv : p.H);
+        const uint4* src = (is_q ? i_q : is_v ? i_v : i_k) + h * (step / 8);
+        const uint32_t dst = ring32 + i_slot * (4 * 32 * 16);
+        copy16(dst, src + ln.a);
+        copy16(dst + 32 * 16, src + ln.b);
+        if (is_q ? p.wq != nullptr : !is_v && p.wk != nullptr) {
+          copy16(dst + 64 * 16, i_row + hh * (D / 8) + ln.a);
+          copy16(dst + 96 * 16, i_row + hh * (D / 8) + ln.b);
+        }
+      }
+      i_slot = i_slot + 1 == kDepth ? 0 : i_slot + 1;
+      if ((i_g += p.parts) >= groups) {
+        i_task += stride;
+        i_g = i_task % p.parts;
+        aim();
+      }
+    }
+    copy_commit();
+  };
+  aim();
+  #pragma unroll
+  for (int i = 0; i < kDepth - 1; ++i) issue();
+
   for (int j = threadIdx.x; j < D; j += kRopeThreads) {
     const int k = j / (D / 2), jj = j % (D / 2), i = jj / kLanes;
     const L o(jj % kLanes, p.rot);
@@ -336,149 +400,121 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
     f[0] = w ? __bfloat162float(w[o.first(i)]) : 1.f;
     f[2] = w ? __bfloat162float(w[o.second(i)]) : 1.f;
   }
+  uint64_t turn[kPairs];
+  #pragma unroll
+  for (int k = 0; k < kPairs; ++k) {
+    const int j = lane + 32 * k;
+    const L o(j % kLanes, p.rot);
+    turn[k] = o.turns(j / kLanes) ? turn_step(__ldg(p.inv_freq + o.freq(j / kLanes))) : 0;
+  }
   __syncthreads();
   float dqa[8], dqb[8], dka[8], dkb[8];
   #pragma unroll
   for (int i = 0; i < 8; ++i) dqa[i] = dqb[i] = dka[i] = dkb[i] = 0.f;
-  const int heads = p.H + 2 * p.H_kv, groups = (heads + kRw - 1) / kRw;
-  const int64_t step = static_cast<int64_t>(p.N) * D;
-  const int64_t tasks = static_cast<int64_t>(p.tokens) * p.parts;
-  for (int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + warp; task < tasks;
-       task += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int t = static_cast<int>(task / p.parts);
-    const int part = static_cast<int>(task - static_cast<int64_t>(t) * p.parts);
-    const int b = t / p.N, n = t - b * p.N;
-    const uint4* row = reinterpret_cast<const uint4*>(p.qkv + static_cast<int64_t>(t) * p.ld);
+  int slot = 0;
+  const int first = blockIdx.x * kWarps + warp;
+  int next_pos = p.rot && first < tasks ? p.positions[first / p.parts] : 0;
+  for (int task = first; task < tasks; task += stride) {
+    const int t = task / p.parts, part = task - t * p.parts;
     uint4* out = reinterpret_cast<uint4*>(p.dqkv + static_cast<int64_t>(t) * p.ld_out);
-    const int64_t tq = (static_cast<int64_t>(b) * p.H * p.N + n) * D;
-    const int64_t tk = (static_cast<int64_t>(b) * p.H_kv * p.N + n) * D;
-    uint4 ga[kBatch], gb[kBatch], ya[kBatch], yb[kBatch];
-    auto load = [&](int g0) {
-      #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int hh = (g0 + u * p.parts) * kRw + sub;
-        ga[u] = gb[u] = ya[u] = yb[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (hh < heads) {
-          const bool is_q = hh < p.H, is_v = hh >= p.H + p.H_kv;
-          const int h = hh - (is_q ? 0 : is_v ? p.H + p.H_kv : p.H);
-          const uint4* src = reinterpret_cast<const uint4*>((is_q ? p.dq : is_v ? p.dv : p.dk) +
-                                                            (is_q ? tq : tk) + h * step);
-          ga[u] = __ldcs(src + ln.a);
-          gb[u] = __ldcs(src + ln.b);
-          if (is_q ? p.wq != nullptr : !is_v && p.wk != nullptr) {
-            ya[u] = __ldcs(row + hh * (D / 8) + ln.a);
-            yb[u] = __ldcs(row + hh * (D / 8) + ln.b);
-          }
-        }
-      }
-    };
-    load(part);
+    const int position = next_pos;
+    if (p.rot && task + stride < tasks) next_pos = p.positions[(task + stride) / p.parts];
     __syncwarp();
-    const int position = p.rot ? p.positions[t] : 0;
     #pragma unroll
-    for (int j = lane; j < D / 2; j += 32) {
-      const int i = j / kLanes;
-      const L o(j % kLanes, p.rot);
-      float c = 1.f, s = 0.f;
-      if (o.turns(i)) angle(p, position, o.freq(i), c, s);
+    for (int k = 0; k < kPairs; ++k) {
+      const int j = lane + 32 * k, i = j / kLanes;
+      float c, s;
+      angle(p, position, turn[k], c, s);
       float* f = reinterpret_cast<float*>(&s_cs[warp][(i >> 1) * kLanes + j % kLanes]) + (i & 1);
       f[0] = c;
       f[2] = s;
     }
     __syncwarp();
-    for (int g0 = part; g0 < groups; g0 += kBatch * p.parts) {
-      if (g0 != part) load(g0);
-      #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int g = g0 + u * p.parts;
-        if (g >= groups) break;
-        const int hh = g * kRw + sub;
-        const bool is_q = hh < p.H, is_v = hh >= p.H + p.H_kv;
-        uint4 oa = ga[u], ob = gb[u];
-        if (g * kRw < p.H + p.H_kv) {  // not all value heads
-          float fa[8], fb[8];
-          L::unpack(ga[u], gb[u], fa, fb);
-          if (!is_v) {
-            const float4* cs = &s_cs[warp][l];
+    for (int g = part; g < groups; g += p.parts) {
+      issue();
+      copy_wait<kDepth - 1>();
+      const uint4* in = ring + slot * (4 * 32);
+      slot = slot + 1 == kDepth ? 0 : slot + 1;
+      const int hh = g * kRw + sub;
+      const bool is_q = hh < p.H, is_v = hh >= p.H + p.H_kv;
+      uint4 oa = in[0], ob = in[32];
+      if (g * kRw < p.H + p.H_kv) {  // not all value heads
+        float fa[8], fb[8];
+        L::unpack(oa, ob, fa, fb);
+        if (!is_v) {
+          const float4* cs = &s_cs[warp][l];
+          #pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            if (!ln.turns(i)) continue;
+            const float4 c = cs[(i >> 1) * kLanes];
+            float ta0, ta1, tb0, tb1;
+            fmul2(ta0, ta1, fb[i], fb[i + 1], c.z, c.w);
+            fmul2(tb0, tb1, fa[i], fa[i + 1], -c.z, -c.w);
+            ffma2(fa[i], fa[i + 1], fa[i], fa[i + 1], c.x, c.y, ta0, ta1);
+            ffma2(fb[i], fb[i + 1], fb[i], fb[i + 1], c.x, c.y, tb0, tb1);
+          }
+        }
+        const bool normed = is_q ? p.wq != nullptr : !is_v && p.wk != nullptr;
+        if (p.wq || p.wk) {
+          float xa[8], xb[8];
+          uint4 va = make_uint4(0u, 0u, 0u, 0u), vb = va;
+          if (normed) {
+            va = in[64];
+            vb = in[96];
+          }
+          L::unpack(va, vb, xa, xb);
+          const float r = rsqrtf(row_sum<D>(sum_squares(xa, xb)) * (1.f / D) + p.eps);
+          #pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            fmul2(xa[i], xa[i + 1], xa[i], xa[i + 1], r, r);
+            fmul2(xb[i], xb[i + 1], xb[i], xb[i + 1], r, r);
+          }
+          if (g * kRw + kRw <= p.H) {
             #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-              if (!ln.turns(i)) continue;
-              const float4 c = cs[(i >> 1) * kLanes];
-              float ta0, ta1, tb0, tb1;
-              fmul2(ta0, ta1, fb[i], fb[i + 1], c.z, c.w);
-              fmul2(tb0, tb1, fa[i], fa[i + 1], -c.z, -c.w);
-              ffma2(fa[i], fa[i + 1], fa[i], fa[i + 1], c.x, c.y, ta0, ta1);
-              ffma2(fb[i], fb[i + 1], fb[i], fb[i + 1], c.x, c.y, tb0, tb1);
+              ffma2(dqa[i], dqa[i + 1], fa[i], fa[i + 1], xa[i], xa[i + 1], dqa[i], dqa[i + 1]);
+              ffma2(dqb[i], dqb[i + 1], fb[i], fb[i + 1], xb[i], xb[i + 1], dqb[i], dqb[i + 1]);
+            }
+          } else {  // key heads, or heads of two kinds
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (is_q) {
+                dqa[i] = fmaf(fa[i], xa[i], dqa[i]);
+                dqb[i] = fmaf(fb[i], xb[i], dqb[i]);
+              } else if (!is_v) {
+                dka[i] = fmaf(fa[i], xa[i], dka[i]);
+                dkb[i] = fmaf(fb[i], xb[i], dkb[i]);
+              }
             }
           }
-          if (p.wq || p.wk) {
-            const bool normed = is_q ? p.wq != nullptr : !is_v && p.wk != nullptr;
-            float xa[8], xb[8];
-            L::unpack(ya[u], yb[u], xa, xb);
-            float r = rsqrtf(row_sum<D>(sum_squares(xa, xb)) * (1.f / D) + p.eps);
-            r = normed ? r : 1.f;  // without a norm x was not read and is 0
-            const bool all_q = g * kRw + kRw <= p.H, all_k = g * kRw >= p.H && (g + 1) * kRw <= p.H + p.H_kv;
+          float d0 = 0.f, d1 = 0.f;
+          if (normed) {
             const float4* wt = &s_w[is_q ? 0 : 1][l];
-            float d0 = 0.f, d1 = 0.f;
             #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-              fmul2(xa[i], xa[i + 1], xa[i], xa[i + 1], r, r);
-              fmul2(xb[i], xb[i + 1], xb[i], xb[i + 1], r, r);
-            }
-            if (all_q) {
-              #pragma unroll
-              for (int i = 0; i < 8; i += 2) {
-                ffma2(dqa[i], dqa[i + 1], fa[i], fa[i + 1], xa[i], xa[i + 1], dqa[i], dqa[i + 1]);
-                ffma2(dqb[i], dqb[i + 1], fb[i], fb[i + 1], xb[i], xb[i + 1], dqb[i], dqb[i + 1]);
-              }
-            } else if (all_k) {
-              #pragma unroll
-              for (int i = 0; i < 8; i += 2) {
-                ffma2(dka[i], dka[i + 1], fa[i], fa[i + 1], xa[i], xa[i + 1], dka[i], dka[i + 1]);
-                ffma2(dkb[i], dkb[i + 1], fb[i], fb[i + 1], xb[i], xb[i + 1], dkb[i], dkb[i + 1]);
-              }
-            } else {  // heads of two kinds, or none past the row's end (zeros)
-              #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                if (is_q) {
-                  dqa[i] = fmaf(fa[i], xa[i], dqa[i]);
-                  dqb[i] = fmaf(fb[i], xb[i], dqb[i]);
-                } else if (!is_v) {
-                  dka[i] = fmaf(fa[i], xa[i], dka[i]);
-                  dkb[i] = fmaf(fb[i], xb[i], dkb[i]);
-                }
-              }
-            }
-            if (!is_v) {
-              #pragma unroll
-              for (int i = 0; i < 8; i += 2) {
-                const float4 w = wt[(i >> 1) * kLanes];
-                fmul2(fa[i], fa[i + 1], fa[i], fa[i + 1], w.x, w.y);
-                fmul2(fb[i], fb[i + 1], fb[i], fb[i + 1], w.z, w.w);
-              }
-            }
-            #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
+              const float4 w = wt[(i >> 1) * kLanes];
+              fmul2(fa[i], fa[i + 1], fa[i], fa[i + 1], w.x, w.y);
+              fmul2(fb[i], fb[i + 1], fb[i], fb[i + 1], w.z, w.w);
               ffma2(d0, d1, fa[i], fa[i + 1], xa[i], xa[i + 1], d0, d1);
               ffma2(d0, d1, fb[i], fb[i + 1], xb[i], xb[i + 1], d0, d1);
             }
-            const float mean = row_sum<D>(d0 + d1) * (-1.f / D);
-            if (normed) {
-              #pragma unroll
-              for (int i = 0; i < 8; i += 2) {
-                ffma2(fa[i], fa[i + 1], xa[i], xa[i + 1], mean, mean, fa[i], fa[i + 1]);
-                ffma2(fb[i], fb[i + 1], xb[i], xb[i + 1], mean, mean, fb[i], fb[i + 1]);
-                fmul2(fa[i], fa[i + 1], fa[i], fa[i + 1], r, r);
-                fmul2(fb[i], fb[i + 1], fb[i], fb[i + 1], r, r);
-              }
+          }
+          const float mean = row_sum<D>(d0 + d1) * (-1.f / D);
+          if (normed) {
+            #pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              ffma2(fa[i], fa[i + 1], xa[i], xa[i + 1], mean, mean, fa[i], fa[i + 1]);
+              ffma2(fb[i], fb[i + 1], xb[i], xb[i + 1], mean, mean, fb[i], fb[i + 1]);
+              fmul2(fa[i], fa[i + 1], fa[i], fa[i + 1], r, r);
+              fmul2(fb[i], fb[i + 1], fb[i], fb[i + 1], r, r);
             }
           }
-          if (!is_v) L::pack(fa, fb, oa, ob);
         }
-        if (hh < heads) {
-          out[hh * (D / 8) + ln.a] = oa;
-          out[hh * (D / 8) + ln.b] = ob;
-        }
+        if (!is_v) L::pack(fa, fb, oa, ob);
+      }
+      if (hh < heads) {
+        out[hh * (D / 8) + ln.a] = oa;
+        out[hh * (D / 8) + ln.b] = ob;
       }
     }
   }
@@ -519,6 +555,7 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__
                                                        int d, float* dwq, float* dwk) {
   __shared__ float s_sum[1024];
   float* out = blockIdx.x ? dwk : dwq;
+  pdl_wait();
   if (!out) return;
   const int runs = 1024 / d, c = threadIdx.x % d, run = threadIdx.x / d;
   float v = 0.f;
@@ -562,21 +599,43 @@ cudaError_t launch_qkv_rope(RopeParams& p, int d, bool interleaved, int kind, cu
                      : launch_fwd<128, false>(p, kind, ctas, st);
 }
 
+template <int D, bool INTER>
+cudaError_t launch_bwd(const RopeParams& p, int ctas, cudaStream_t st) {
+  constexpr int kSmem = kWarps * kDepth * 4 * 32 * 16;
+  auto* kernel = qkv_rope_bwd_kernel<D, INTER>;
+  static std::atomic<uint64_t> attr_done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    attr_done.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  kernel<<<ctas, kRopeThreads, kSmem, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess || !p.partial) return e;
+  // the sums of the CTAs' shares: set up while the rows' kernel still runs
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const float* partial = p.partial;
+  e = cudaLaunchKernelEx(&cfg, rope_dw_kernel, partial, ctas, static_cast<int>(D), p.dwq, p.dwk);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 cudaError_t launch_qkv_rope_bwd(RopeParams& p, int d, bool interleaved, cudaStream_t st) {
   p.parts = parts_of(p.tokens);
   const int64_t want = (static_cast<int64_t>(p.tokens) * p.parts + kWarps - 1) / kWarps;
   const int ctas = static_cast<int>(want < kRopeBwdCtas ? want : kRopeBwdCtas);
-  if (d == 64) {
-    if (interleaved) qkv_rope_bwd_kernel<64, true><<<ctas, kRopeThreads, 0, st>>>(p);
-    else qkv_rope_bwd_kernel<64, false><<<ctas, kRopeThreads, 0, st>>>(p);
-  } else {
-    if (interleaved) qkv_rope_bwd_kernel<128, true><<<ctas, kRopeThreads, 0, st>>>(p);
-    else qkv_rope_bwd_kernel<128, false><<<ctas, kRopeThreads, 0, st>>>(p);
-  }
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !p.partial) return e;
-  rope_dw_kernel<<<2, 1024, 0, st>>>(p.partial, ctas, d, p.dwq, p.dwk);
-  return cudaGetLastError();
+  if (d == 64) return interleaved ? launch_bwd<64, true>(p, ctas, st) : launch_bwd<64, false>(p, ctas, st);
+  return interleaved ? launch_bwd<128, true>(p, ctas, st) : launch_bwd<128, false>(p, ctas, st);
 }
 
 }  // namespace attn
