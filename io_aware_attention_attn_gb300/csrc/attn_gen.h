@@ -75,7 +75,7 @@ cudaError_t launch_qkv_rope_bwd(RopeParams& p, int d, bool interleaved, cudaStre
 
 // -------------------------------------------------------------------- attention over a paged cache
 constexpr int kPagedTile = 64;         // keys of a tile
-constexpr int kPagedMaxCtas = 304;     // 2 on each of 152 SMs
+constexpr int kPagedMaxCtas = 456;     // 3 on each of 152 SMs
 constexpr int kPagedMaxRows = 32;      // query rows (heads of one K/V head) of a unit
 
 struct PagedParams {

@@ -8,6 +8,7 @@
 // another, one launch is enough, and the only entries of the table that are read are old ones while
 // the only ones written are new ones (by the token that is first in its page).
 // What bounds it: latency.  It moves 12 bytes a token and 20 a request.
+#include "attn_gen.cuh"
 #include "attn_gen.h"
 #include "sm103_ptx.cuh"
 
@@ -24,6 +25,7 @@ __global__ void __launch_bounds__(kSlotThreads) kv_slots_kernel(SlotsParams p) {
   __shared__ int s_warp[kSlotThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = false;
+  pdl_wait();
   for (int s = tid; s <= p.B; s += kSlotThreads) {
     const int c = p.cu_new[s];
     s_cu[s] = min(max(c, 0), p.T);
@@ -123,8 +125,7 @@ cudaError_t launch_kv_slots(const SlotsParams& p, cudaStream_t stream) {
   }
   const long long want = (static_cast<long long>(p.T) + kSlotThreads - 1) / kSlotThreads;
   const int ctas = static_cast<int>(want < 1 ? 1 : want > 608 ? 608 : want);
-  kv_slots_kernel<<<ctas, kSlotThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(kv_slots_kernel, dim3(static_cast<unsigned>(ctas)), kSlotThreads, smem, stream, p);
 }
 
 }  // namespace attn

@@ -38,35 +38,47 @@
 namespace attn {
 namespace {
 
-constexpr int kWarps = 4;                        // consumer warps
-constexpr int kThreads = (kWarps + 1) * 32;      // and one producer warp
+constexpr int kSlices = 4;                       // key slices of 16 in a tile, a warp each
 constexpr float kTrail = 8.f;                    // how far m may trail (log2 units)
 enum : int { kRoleProducer = 7, kRoleConsumer = 8 };
 
-template <int D, bool E4M3, int NT>
-struct PagedSmem {
+// NT: groups of 8 query rows a warp holds; RW: row slices, each with four warps of its own.
+template <int D, bool E4M3, int NT, int RW>
+struct PagedCfg {
+  static constexpr int kWarps = kSlices * RW;                     // consumers; one producer more
+  static constexpr int kThreads = (kWarps + 1) * 32;
+  // CTAs an SM holds.  Where a tile is 32 KB two are enough for the copies to run at full rate; a
+  // tile of half that or less has to be through a warp's chain of dependent steps in half the
+  // time, so three share it (e4m3, d = 128, 64-row pages: 94 us with two against DRAM's 82).
+  static constexpr int kCtas = RW == 2 ? 1 : D == 128 && (!E4M3 || NT == 2) ? 2 : 3;
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
   static constexpr int kBlk = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a row in one box
   static constexpr int kBlks = kRowBytes / kBlk;                  // boxes side by side
   static constexpr int kSide = kPagedTile * kRowBytes;            // K or V of a tile
   static constexpr int kStage = 2 * kSide;
-  static constexpr int kCtas = NT <= 2 ? 2 : 1;                   // per SM
-  static constexpr int kRing = (kCtas == 2 ? 98304 : 196608);
-  static constexpr int kStages = kRing / kStage < 8 ? kRing / kStage : 8;
-  static constexpr int kScales = kStages * kStage;                // [stage][2][64] fp32
-  static constexpr int kMerge = kScales + (E4M3 ? kStages * 2 * kPagedTile * 4 : 0);
   static constexpr int kMergeLd = D + 4;                          // spreads rows over the banks
-  static constexpr int kStat = kMerge + 2 * 8 * kMergeLd * 4;     // [2][warp][8 rows][2]
-  static constexpr int kBar = kStat + 2 * kWarps * 8 * 2 * 4;
+  static constexpr int kMergeBytes = 2 * 8 * kMergeLd * 4;        // of one row slice
+  static constexpr int kStatBytes = 2 * kSlices * 8 * 2 * 4;      // [2][slice][8 rows][2], likewise
+  // tiles in the ring: what shared memory holds beside the rest (each CTA's 1 KB of the system's and
+  // 1 KB for alignment), 8 at most
+  static constexpr int kScaleBytes = E4M3 ? 2 * kPagedTile * 4 : 0;
+  static constexpr int kFit = (233472 / kCtas - 2048 - RW * (kMergeBytes + kStatBytes) - 32) /
+                              (kStage + kScaleBytes + 16);
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  static constexpr int kScales = kStages * kStage;                // [stage][2][64] fp32
+  static constexpr int kMerge = kScales + kStages * kScaleBytes;
+  static constexpr int kStat = kMerge + RW * kMergeBytes;
+  static constexpr int kBar = kStat + RW * kStatBytes;
   static constexpr int kMisc = kBar + 2 * kStages * 8;
   static constexpr int kBytes = kMisc + 32;
   static constexpr int kDyn = kBytes + 1024;
-  static_assert(kCtas * (kDyn + 1024) <= 233472, "paged ring exceeds shared memory");
+  static_assert(kStages >= 2 && kCtas * (kDyn + 1024) <= 233472, "paged ring exceeds shared memory");
 };
 
 // The unit and tile a CTA is at.
 struct Walk {
   int s, h, rg, t, n, len;  // request, K/V head, row group, tile, tiles of the request, its length
+  int ahead;                // the next request's length, asked for when this one began
 };
 
 __device__ __forceinline__ int req_len(const PagedParams& p, int s) {
@@ -83,10 +95,10 @@ __device__ __forceinline__ void next_unit(const PagedParams& p, Walk& w) {
   w.rg = 0;
   if (++w.h < p.H_kv) return;
   w.h = 0;
-  if (++w.s < p.B) {
-    w.len = req_len(p, w.s);
-    w.n = req_tiles(w.len);
-  }
+  ++w.s;
+  w.len = w.ahead;
+  w.n = req_tiles(w.len);
+  w.ahead = w.s + 1 < p.B ? req_len(p, w.s + 1) : 0;
 }
 // Walk at tile `at` of the whole order (a warp's lanes together); returns the first tile of its unit.
 __device__ long long find(const PagedParams& p, long long at, Walk& w) {
@@ -115,58 +127,120 @@ __device__ long long find(const PagedParams& p, long long at, Walk& w) {
       w.t = static_cast<int>(in - static_cast<long long>(u) * w.n);
       w.h = u / p.n_rg;
       w.rg = u - w.h * p.n_rg;
+      w.ahead = w.s + 1 < p.B ? req_len(p, w.s + 1) : 0;
       return at - w.t;
     }
     before += __shfl_sync(0xffffffffu, scan, 31);
   }
-  w = Walk{p.B, 0, 0, 0, 1, 0};
+  w = Walk{p.B, 0, 0, 0, 1, 0, 0};
   return at;
 }
 
+// This lane's share of the B operand of K Q^T (query row g of each group of 8, the elements that its
+// positions along d stand for), and the factors of scores (log2 units) of rows 2 q4, 2 q4 + 1.
 template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
+__device__ __forceinline__ void load_q(const PagedParams& p, const Walk& w, int row_slice,
+                                       uint32_t (&qf)[NT][D / 16][2], float (&mul)[NT][2]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
+  const int row0 = w.rg * p.rg_rows, rows = min(p.rg_rows, p.group - row0);
+  const __nv_bfloat16* q =
+      p.q + (static_cast<int64_t>(w.s) * p.H + static_cast<int64_t>(w.h) * p.group + row0) * D;
+  #pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = (row_slice * NT + nt) * 8 + g;
+    #pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      qf[nt][k][0] = qf[nt][k][1] = 0u;
+      if (r < rows) {
+        const __nv_bfloat16* src = q + r * D + 16 * k;
+        if (E4M3) {  // codes 4 q4 .. 4 q4 + 3 of a key arrive in one register
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + 4 * q4));
+          qf[nt][k][0] = v.x;
+          qf[nt][k][1] = v.y;
+        } else {
+          qf[nt][k][0] = __ldg(reinterpret_cast<const uint32_t*>(src + 2 * q4));
+          qf[nt][k][1] = __ldg(reinterpret_cast<const uint32_t*>(src + 2 * q4 + 8));
+        }
+      }
+    }
+    if (E4M3) {
+      float amax = 0.f;
+      #pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        #pragma unroll
+        for (int j = 0; j < 2; ++j)
+          amax = fmax3(amax, fabsf(bf16lo_to_f32(qf[nt][k][j])), fabsf(bf16hi_to_f32(qf[nt][k][j])));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // largest element to 2^8 .. 2^9: its exponent field, kept where both factors are normal
+      const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23), 16), 254) - 8;
+      const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^(127 - e)
+      const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);          // 2^(e - 127)
+      #pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        #pragma unroll
+        for (int j = 0; j < 2; ++j)
+          qf[nt][k][j] = pack_f16x2(bf16lo_to_f32(qf[nt][k][j]) * down,
+                                    bf16hi_to_f32(qf[nt][k][j]) * down);
+      mul[nt][0] = p.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * q4) * 4);
+      mul[nt][1] = p.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * q4 + 1) * 4);
+    } else {
+      mul[nt][0] = mul[nt][1] = p.scale_log2;
+    }
+  }
+}
+
+template <int D, bool E4M3, int NT, int RW>
+__global__ void __launch_bounds__((kSlices * RW + 1) * 32, PagedCfg<D, E4M3, NT, RW>::kCtas)
 paged_kernel(const __grid_constant__ PagedParams p) {
-  using L = PagedSmem<D, E4M3, NT>;
+  using L = PagedCfg<D, E4M3, NT, RW>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - smem_u32(smem_raw));
-  int* misc = reinterpret_cast<int*>(sm + L::kMisc);  // [0] abort [2..3] total tiles (64-bit)
+  int* misc = reinterpret_cast<int*>(sm + L::kMisc);  // [0] abort
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto full = [&](int st) { return base + L::kBar + st * 8; };
   auto empty = [&](int st) { return base + L::kBar + (L::kStages + st) * 8; };
   if (tid == 0) {
     misc[0] = 0;
     for (int i = 0; i < L::kStages; ++i) {
-      mbar_init(full(i), 1);
-      mbar_init(empty(i), kWarps);
+      mbar_init(full(i), E4M3 ? 33 : 1);  // E4M3: each producer lane's scale copies too
+      mbar_init(empty(i), L::kWarps);
     }
     fence_barrier_init();
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
   }
-  // tiles of all units
-  long long mine = 0;
-  for (int s = tid; s < p.B; s += kThreads) mine += req_tiles(req_len(p, s));
-  #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
-  long long* sums = reinterpret_cast<long long*>(sm + L::kMerge);
-  if (lane == 0) sums[warp] = mine;
-  __syncthreads();
+  pdl_wait();
+  // tiles of all units: each warp for itself when one look at the lengths is enough
   long long total = 0;
-  for (int i = 0; i <= kWarps; ++i) total += sums[i];
-  total *= p.H_kv * p.n_rg;
+  const int few = p.B <= 32;
+  for (int s = few ? lane : tid; s < p.B; s += L::kThreads) total += req_tiles(req_len(p, s));
+  #pragma unroll
+  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  long long* sums = reinterpret_cast<long long*>(sm + L::kMerge);
+  if (!few && lane == 0) sums[warp] = total;
   __syncthreads();
+  if (!few) {
+    total = 0;
+    for (int i = 0; i <= L::kWarps; ++i) total += sums[i];
+    __syncthreads();
+  }
+  total *= p.H_kv * p.n_rg;
   const long long G = min(static_cast<long long>(gridDim.x), total);
-  const long long i = blockIdx.x;
+  const long long cta = blockIdx.x;
   pdl_launch_dependents();
-  if (i >= G) {
-    if (tid == 0) p.joins[i] = make_int4(-1, 0, 0, 0);
+  if (cta >= G) {
+    if (tid == 0) p.joins[cta] = make_int4(-1, 0, 0, 0);
     return;
   }
-  const long long w0 = i * total / G, w1 = (i + 1) * total / G;
+  const long long w0 = cta * total / G, w1 = (cta + 1) * total / G;
+  const int n_tiles = static_cast<int>(w1 - w0);
   Walk w;
   const long long unit0 = find(p, w0, w);
   const WaitCtx ctx{misc, p.status};
 
-  if (warp == kWarps) {
+  if (warp == L::kWarps) {
     // ------------------------------------------------------------------------------ producer
     if (lane == 0) {
       // the unit that ends here and began in an earlier CTA, and where its parts are
@@ -176,19 +250,16 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         join = make_int4((w.s * p.H_kv + w.h) * p.n_rg + w.rg, static_cast<int>(i0),
                          i0 * total / G < unit0 ? 1 : 0, 0);
       }
-      p.joins[i] = join;
-      tma_prefetch_desc(&p.tm_k);
-      tma_prefetch_desc(&p.tm_v);
+      p.joins[cta] = join;
     }
     const uint64_t policy = l2_policy_evict_first();
     const int box_shift = 31 - __clz(p.box_rows);
     const int parts_tile = kPagedTile >> box_shift;
-    const int ops = parts_tile * 2 * L::kBlks;
     int entries = 0, entry_base = -1, entry_s = -1;  // lane's entry of the 32 looked up last
     bool ok = true;
-    long long it = 0;
-    for (long long g = w0; g < w1 && ok; ++g, ++it) {
-      const int st = static_cast<int>(it % L::kStages);
+    int it = 0, st = 0;
+    uint32_t phase = 1;  // of the empty barrier waited for, from the second round on
+    for (; it < n_tiles; ++it) {
       const int rows = min(kPagedTile, w.len - w.t * kPagedTile);
       const int parts = rows > 0 ? (rows + p.box_rows - 1) >> box_shift : 0;
       const int page0 = (w.t * kPagedTile) >> p.page_shift;
@@ -204,126 +275,69 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         }
       }
       if (it >= L::kStages)
-        ok = mbar_wait_warp(empty(st), static_cast<uint32_t>((it / L::kStages - 1) & 1), ctx,
-                            kRoleProducer, 1);
+        ok = mbar_wait_warp(empty(st), phase, ctx, kRoleProducer, 1);
       if (!ok) break;
-      // lane -> (part, block, K or V); every lane takes part in the look-up of its page
       const uint32_t stage = base + st * L::kStage;
-      const int per_part = 2 * L::kBlks;
-      int bad_parts = 0;
-      for (int q = 0; q < parts; ++q) {
-        const int pg = __shfl_sync(0xffffffffu, entries,
-                                   ((w.t * kPagedTile + q * p.box_rows) >> p.page_shift) - entry_base);
-        if (E4M3 && pg < 0) {
-          ++bad_parts;  // no scales to copy: zeros
-          for (int r = lane; r < 2 * p.box_rows; r += 32) {
-            const int side = r >> box_shift, row = r & (p.box_rows - 1);
-            reinterpret_cast<float*>(sm + L::kScales)[(st * 2 + side) * kPagedTile +
-                                                      q * p.box_rows + row] = 0.f;
-          }
-          fence_proxy_async_smem();
+      if (E4M3) {  // lane: the scales of rows 4 r4 .. 4 r4 + 3 of K or V; zeros of a page that is none
+        const int side = lane >> 4, row = (lane & 15) * 4;
+        const int at = ((w.t * kPagedTile + row) >> p.page_shift) - entry_base;
+        const int pg = __shfl_sync(0xffffffffu, entries, at & 31);
+        if ((row >> box_shift) < parts) {
+          const uint32_t dst = base + L::kScales + ((st * 2 + side) * kPagedTile + row) * 4;
+          if (pg >= 0)
+            copy16(dst, (side ? p.vs : p.ks) + (((static_cast<int64_t>(pg) * p.H_kv + w.h) << p.page_shift) +
+                                                ((w.t * kPagedTile + row) & ((1 << p.page_shift) - 1))));
+          else
+            st_shared_v4(dst, 0u, 0u, 0u, 0u);
         }
+        copy_arrive(full(st));
+        __syncwarp();
       }
+      if (lane == 0)
+        mbar_arrive_expect_tx(full(st), static_cast<uint32_t>(parts) * p.box_rows * 2 * L::kRowBytes);
       __syncwarp();
-      if (lane == 0) {
-        uint32_t bytes = static_cast<uint32_t>(parts) * p.box_rows * 2 * L::kRowBytes;
-        if (E4M3) bytes += static_cast<uint32_t>(parts - bad_parts) * p.box_rows * 8;
-        mbar_arrive_expect_tx(full(st), bytes);
-      }
-      __syncwarp();
-      {
-        const int q = lane / per_part, o = lane % per_part;
+      {  // lane -> (part, block, K or V); every lane takes part in the look-up of its page
+        constexpr int kPerPart = 2 * L::kBlks;
+        const int q = lane / kPerPart, o = lane % kPerPart;
         const int side = o / L::kBlks, blk = o % L::kBlks;
         const int row0 = w.t * kPagedTile + q * p.box_rows;
         const int at = (row0 >> p.page_shift) - entry_base;
         const int pg = __shfl_sync(0xffffffffu, entries, at & 31);
-        if (lane < ops && q < parts) {
-          const uint32_t dst = stage + side * L::kSide + blk * (kPagedTile * L::kBlk) +
-                               q * p.box_rows * L::kBlk;
-          const int y = row0 & ((1 << p.page_shift) - 1);
-          tma_load_4d_hint(dst, side ? &p.tm_v : &p.tm_k, full(st), blk * (L::kBlk / (E4M3 ? 1 : 2)),
-                           y, w.h, pg >= 0 ? pg : p.num_pages, policy);
-          if (E4M3 && blk == 0 && pg >= 0) {
-            const float* src = (side ? p.vs : p.ks) +
-                               (((static_cast<int64_t>(pg) * p.H_kv + w.h) << p.page_shift) + y);
-            bulk_load_1d(base + L::kScales + ((st * 2 + side) * kPagedTile + q * p.box_rows) * 4, src,
-                         p.box_rows * 4, full(st));
-          }
-        }
+        if (q < parts)
+          tma_load_4d_hint(stage + side * L::kSide + blk * (kPagedTile * L::kBlk) +
+                               q * p.box_rows * L::kBlk,
+                           side ? &p.tm_v : &p.tm_k, full(st), blk * (L::kBlk / (E4M3 ? 1 : 2)),
+                           row0 & ((1 << p.page_shift) - 1), w.h, pg >= 0 ? pg : p.num_pages, policy);
+      }
+      if (++st == L::kStages) {
+        st = 0;
+        phase ^= 1;
       }
       if (++w.t == w.n) next_unit(p, w);
     }
     if (!ok) {  // copies in flight land before the CTA's shared memory goes
-      const long long from = it > L::kStages ? it - L::kStages : 0;
-      for (long long k = from; k < it; ++k)
-        mbar_wait_drain(full(static_cast<int>(k % L::kStages)),
-                        static_cast<uint32_t>((k / L::kStages) & 1));
+      if (E4M3) copy_wait<0>();
+      for (int k = it > L::kStages ? it - L::kStages : 0; k < it; ++k)
+        mbar_wait_drain(full(k % L::kStages), static_cast<uint32_t>((k / L::kStages) & 1));
     }
     return;
   }
 
   // -------------------------------------------------------------------------------- consumers
   const int g = lane >> 2, q4 = lane & 3;
+  const int slice = warp % kSlices, row_slice = RW == 1 ? 0 : warp / kSlices;
   constexpr int kSteps = D / 16;      // k16 steps of S, m16 tiles of O^T
   bool dead = false;                  // a wait gave up: go through the motions, compute nothing
-  long long it = 0, cur = w0;
-  int merges = 0, seg = 0;
-  float* merge = reinterpret_cast<float*>(sm + L::kMerge);
-  float* stat = reinterpret_cast<float*>(sm + L::kStat);
-  while (cur < w1) {
-    const long long left = w1 - cur;
-    const int t_end = static_cast<int>(min(static_cast<long long>(w.n), w.t + left));
-    const int t_begin = w.t;
-    const int row0 = w.rg * p.rg_rows, rows = min(p.rg_rows, p.group - row0);
-    const __nv_bfloat16* qg =
-        p.q + (static_cast<int64_t>(w.s) * p.H + static_cast<int64_t>(w.h) * p.group + row0) * D;
-    // B operand of K Q^T: lane (g, q4) holds, of query row g, the elements its k positions stand for
-    uint32_t qf[NT][kSteps][2];
-    float mul[NT][2];  // rows 2 q4, 2 q4 + 1: score factor (log2 units)
-    #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = nt * 8 + g;
-      #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        qf[nt][k][0] = qf[nt][k][1] = 0u;
-        if (r < rows) {
-          const __nv_bfloat16* src = qg + r * D + 16 * k;
-          if (E4M3) {  // codes 4 q4 .. 4 q4 + 3 of a key arrive in one register
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + 4 * q4));
-            qf[nt][k][0] = v.x;
-            qf[nt][k][1] = v.y;
-          } else {
-            qf[nt][k][0] = __ldg(reinterpret_cast<const uint32_t*>(src + 2 * q4));
-            qf[nt][k][1] = __ldg(reinterpret_cast<const uint32_t*>(src + 2 * q4 + 8));
-          }
-        }
-      }
-      if (E4M3) {
-        float amax = 0.f;
-        #pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-          #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            amax = fmaxf(amax, fmaxf(fabsf(bf16lo_to_f32(qf[nt][k][j])),
-                                     fabsf(bf16hi_to_f32(qf[nt][k][j]))));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // largest element to 2^8 .. 2^9: its exponent field, kept where both factors are normal
-        const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23), 16), 254) - 8;
-        const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^(127 - e)
-        const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);          // 2^(e - 127)
-        #pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-          #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            qf[nt][k][j] = pack_f16x2(bf16lo_to_f32(qf[nt][k][j]) * down,
-                                      bf16hi_to_f32(qf[nt][k][j]) * down);
-        mul[nt][0] = p.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * q4) * 4);
-        mul[nt][1] = p.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * q4 + 1) * 4);
-      } else {
-        mul[nt][0] = mul[nt][1] = p.scale_log2;
-      }
-    }
+  int left = n_tiles, st = 0, merges = 0;
+  uint32_t phase = 0;
+  bool first = true;                  // the CTA's first unit
+  float* merge = reinterpret_cast<float*>(sm + L::kMerge + row_slice * L::kMergeBytes);
+  float* stat = reinterpret_cast<float*>(sm + L::kStat) + row_slice * 2 * kSlices * 16;
+  uint32_t qf[NT][kSteps][2];
+  float mul[NT][2];
+  load_q<D, E4M3, NT>(p, w, row_slice, qf, mul);
+  while (left > 0) {
+    const int t_begin = w.t, t_end = min(w.n, w.t + left);
     float acc[NT][kSteps][4], m[NT][2], l[NT][2];
     float vref = 0.f, vinv = 0.f;
     #pragma unroll
@@ -336,19 +350,16 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         for (int j = 0; j < 4; ++j) acc[nt][k][j] = 0.f;
     }
 
-    for (int t = t_begin; t < t_end; ++t, ++it) {
-      const int st = static_cast<int>(it % L::kStages);
-      if (!dead && !mbar_wait_warp(full(st), static_cast<uint32_t>((it / L::kStages) & 1), ctx,
-                                   kRoleConsumer, 2))
-        dead = true;
-      const int live = w.len - t * kPagedTile - warp * 16;  // of this warp's 16 keys
+    for (int t = t_begin; t < t_end; ++t) {
+      if (!dead && !mbar_wait_warp(full(st), phase, ctx, kRoleConsumer, 2)) dead = true;
+      const int live = w.len - t * kPagedTile - slice * 16;  // of this warp's 16 keys
       if (!dead && live > 0) {
         const uint32_t kst = base + st * L::kStage, vst = kst + L::kSide;
         float s[NT][4];
         #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
         if (!E4M3) {
-          const int key = warp * 16 + (lane & 15);
+          const int key = slice * 16 + (lane & 15);
           #pragma unroll
           for (int k = 0; k < kSteps; ++k) {
             const int chunk = (k & 3) * 2 + (lane >> 4);
@@ -359,7 +370,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
               mma16816<false>(s[nt], a[0], a[1], a[2], a[3], qf[nt][k][0], qf[nt][k][1]);
           }
         } else {
-          const int key = warp * 16 + (lane & 15);
+          const int key = slice * 16 + (lane & 15);
           #pragma unroll
           for (int k = 0; k < kSteps; k += 2) {
             const int chunk = k + (lane >> 4);
@@ -382,7 +393,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         float sk0 = 1.f, sk1 = 1.f, sv0 = 1.f, sv1 = 1.f;
         if (E4M3) {
           const float* sc =
-              reinterpret_cast<const float*>(sm + L::kScales) + st * 2 * kPagedTile + warp * 16;
+              reinterpret_cast<const float*>(sm + L::kScales) + st * 2 * kPagedTile + slice * 16;
           sk0 = sc[g];
           sk1 = sc[g + 8];
           sv0 = in0 ? sc[kPagedTile + g] : 0.f;
@@ -457,7 +468,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
           keep1 = (2 * q4 + 8 < live ? 0xffffu : 0u) | (2 * q4 + 9 < live ? 0xffff0000u : 0u);
         }
         if (!E4M3) {
-          const int key = warp * 16 + ((lane >> 4) << 3) + (lane & 7);
+          const int key = slice * 16 + ((lane >> 4) << 3) + (lane & 7);
           #pragma unroll
           for (int k = 0; k < kSteps; ++k) {
             const int chunk = (k & 3) * 2 + ((lane >> 3) & 1);
@@ -469,7 +480,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
                               pf[nt][0], pf[nt][1]);
           }
         } else {
-          const int key = warp * 16 + (lane & 15);
+          const int key = slice * 16 + (lane & 15);
           #pragma unroll
           for (int k = 0; k < kSteps; k += 2) {
             const int chunk = k + (lane >> 4);
@@ -492,14 +503,28 @@ paged_kernel(const __grid_constant__ PagedParams p) {
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(st));
+      if (++st == L::kStages) {
+        st = 0;
+        phase ^= 1;
+      }
     }
+    left -= t_end - t_begin;
 
-    // ---- end of the unit (or of this CTA's part of it): the four warps' results become one
+    // ---- end of the unit (or of this CTA's part of it): the four warps' results become one, while
+    // the next unit's query rows are on their way
     const bool whole = t_begin == 0 && t_end == w.n;
-    const int slot = static_cast<int>(2 * i) + (seg > 0 ? 1 : 0);
+    const int len = w.len;
+    const int part = 2 * static_cast<int>(cta) + (first ? 0 : 1);
+    first = false;
+    const int row0 = w.rg * p.rg_rows, rows = min(p.rg_rows, p.group - row0);
+    const int64_t out0 = static_cast<int64_t>(w.s) * p.H + static_cast<int64_t>(w.h) * p.group + row0;
+    if (left > 0) {
+      next_unit(p, w);
+      load_q<D, E4M3, NT>(p, w, row_slice, qf, mul);
+    }
     #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float* st2 = stat + (merges & 1) * kWarps * 16;
+      float* st2 = stat + (merges & 1) * kSlices * 16;
       ++merges;
       #pragma unroll
       for (int j = 0; j < 2; ++j)
@@ -509,16 +534,16 @@ paged_kernel(const __grid_constant__ PagedParams p) {
       if (g == 0) {
         #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          st2[(warp * 8 + 2 * q4 + j) * 2] = m[nt][j];
-          st2[(warp * 8 + 2 * q4 + j) * 2 + 1] = l[nt][j];
+          st2[(slice * 8 + 2 * q4 + j) * 2] = m[nt][j];
+          st2[(slice * 8 + 2 * q4 + j) * 2 + 1] = l[nt][j];
         }
       }
-      named_barrier_sync(1, kWarps * 32);
+      named_barrier_sync(1 + row_slice, kSlices * 32);
       #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float top = -INFINITY;
         #pragma unroll
-        for (int x = 0; x < kWarps; ++x) top = fmaxf(top, st2[(x * 8 + 2 * q4 + j) * 2]);
+        for (int x = 0; x < kSlices; ++x) top = fmaxf(top, st2[(x * 8 + 2 * q4 + j) * 2]);
         // m = -inf: no finite score, so acc and l are 0 (or NaN, which stays)
         const float c = (m[nt][j] == -INFINITY ? 1.f : ex2_approx(m[nt][j] - top)) *
                         (E4M3 ? vref : 1.f);
@@ -534,30 +559,30 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         const int col = E4M3 ? 16 * k + 2 * g + (j >> 1) : 16 * k + g + 8 * (j >> 1);
         return row * L::kMergeLd + col;
       };
-      float* mine2 = merge + (warp & 1) * 8 * L::kMergeLd;
-      if (warp >= 2) {
+      float* mine = merge + (slice & 1) * 8 * L::kMergeLd;
+      if (slice >= 2) {
         #pragma unroll
         for (int k = 0; k < kSteps; ++k)
           #pragma unroll
-          for (int j = 0; j < 4; ++j) mine2[cell(k, j)] = acc[nt][k][j];
+          for (int j = 0; j < 4; ++j) mine[cell(k, j)] = acc[nt][k][j];
       }
-      named_barrier_sync(1, kWarps * 32);
-      if (warp < 2) {
+      named_barrier_sync(1 + row_slice, kSlices * 32);
+      if (slice < 2) {
         #pragma unroll
         for (int k = 0; k < kSteps; ++k)
           #pragma unroll
-          for (int j = 0; j < 4; ++j) mine2[cell(k, j)] += acc[nt][k][j];
+          for (int j = 0; j < 4; ++j) mine[cell(k, j)] += acc[nt][k][j];
       }
-      named_barrier_sync(1, kWarps * 32);
-      for (int e = tid; e < 8 * (D / 4); e += kWarps * 32) {
+      named_barrier_sync(1 + row_slice, kSlices * 32);
+      for (int e = slice * 32 + lane; e < 8 * (D / 4); e += kSlices * 32) {
         const int r = e / (D / 4), c4 = e % (D / 4);
-        const int row = nt * 8 + r;
+        const int row = (row_slice * NT + nt) * 8 + r;
         if (row >= rows) continue;
         float top = -INFINITY, sum = 0.f;
         #pragma unroll
-        for (int x = 0; x < kWarps; ++x) top = fmaxf(top, st2[(x * 8 + r) * 2]);
+        for (int x = 0; x < kSlices; ++x) top = fmaxf(top, st2[(x * 8 + r) * 2]);
         #pragma unroll
-        for (int x = 0; x < kWarps; ++x) {
+        for (int x = 0; x < kSlices; ++x) {
           const float mx = st2[(x * 8 + r) * 2];
           sum += (mx == -INFINITY ? 1.f : ex2_approx(mx - top)) * st2[(x * 8 + r) * 2 + 1];
         }
@@ -566,25 +591,21 @@ paged_kernel(const __grid_constant__ PagedParams p) {
             *reinterpret_cast<const float4*>(merge + (8 + r) * L::kMergeLd + 4 * c4);
         float4 v = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
         if (whole) {
-          const float inv = w.len > 0 ? 1.f / sum : 0.f;
-          const int64_t at = static_cast<int64_t>(w.s) * p.H +
-                             static_cast<int64_t>(w.h) * p.group + row0 + row;
+          const float inv = len > 0 ? 1.f / sum : 0.f;
+          const int64_t at = out0 + row;
           *reinterpret_cast<uint2*>(p.o + at * D + 4 * c4) =
               make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
           if (c4 == 0)
             p.lse[at] = sum > 0.f || sum != sum ? (top + log2f(sum)) * 0.69314718055994530942f
                                                 : -INFINITY;
         } else {
-          const int64_t at = static_cast<int64_t>(slot) * p.rg_rows + row;
+          const int64_t at = static_cast<int64_t>(part) * p.rg_rows + row;
           *reinterpret_cast<float4*>(p.part_o + at * D + 4 * c4) = v;
           if (c4 == 0)
             *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(top, sum);
         }
       }
     }
-    cur += t_end - t_begin;
-    ++seg;
-    next_unit(p, w);
   }
 }
 
@@ -649,10 +670,10 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   }
 }
 
-template <int D, bool E4M3, int NT>
+template <int D, bool E4M3, int NT, int RW>
 cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
-  using L = PagedSmem<D, E4M3, NT>;
-  auto* kernel = paged_kernel<D, E4M3, NT>;
+  using L = PagedCfg<D, E4M3, NT, RW>;
+  auto* kernel = paged_kernel<D, E4M3, NT, RW>;
   static std::atomic<uint64_t> attr_done{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -663,28 +684,22 @@ cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit, std::memory_order_acq_rel);
   }
-  const int most = L::kCtas * (kPagedMaxCtas / 2);
+  const int most = L::kCtas * 152;
+  static_assert(L::kCtas * 152 <= kPagedMaxCtas, "the workspace holds the parts of fewer CTAs");
   if (ctas > most) ctas = most;
-  kernel<<<ctas, kThreads, L::kDyn, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(p.rg_rows < 8 ? p.rg_rows : 8));
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p)) != cudaSuccess) return e;
-  return cudaGetLastError();
+  e = launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), L::kThreads, L::kDyn, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(paged_join_kernel<D>,
+                          dim3(static_cast<unsigned>(ctas),
+                               static_cast<unsigned>(p.rg_rows < 8 ? p.rg_rows : 8)),
+                          128, 0, stream, p);
 }
 
 template <int D, bool E4M3>
 cudaError_t launch_rows(const PagedParams& p, int ctas, cudaStream_t stream) {
-  if (p.rg_rows <= 8) return launch<D, E4M3, 1>(p, ctas, stream);
-  if (p.rg_rows <= 16) return launch<D, E4M3, 2>(p, ctas, stream);
-  return launch<D, E4M3, 4>(p, ctas, stream);
+  if (p.rg_rows <= 8) return launch<D, E4M3, 1, 1>(p, ctas, stream);
+  if (p.rg_rows <= 16) return launch<D, E4M3, 2, 1>(p, ctas, stream);
+  return launch<D, E4M3, 2, 2>(p, ctas, stream);
 }
 
 }  // namespace

@@ -180,9 +180,9 @@ __global__ void __launch_bounds__(kRopeThreads, CACHE == kCacheE4m3 ? 2 : 3) qkv
   __shared__ float4 s_coef[kWarps][2][2][D / 4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % kLanes, sub = lane / kLanes;
-  const int t = blockIdx.x * (kWarps / p.parts) + warp / p.parts;
+  const int task = blockIdx.x * kWarps + warp, t = task / p.parts, part = task - t * p.parts;
+  pdl_wait();
   if (t >= p.tokens) return;
-  const int part = warp % p.parts;
   const L ln(l, p.rot);
   const int heads = p.H + 2 * p.H_kv, groups = (heads + kRw - 1) / kRw;
   const int b = t / p.N, n = t - b * p.N;
@@ -325,15 +325,6 @@ __global__ void __launch_bounds__(kRopeThreads, CACHE == kCacheE4m3 ? 2 : 3) qkv
 // see the launcher for figures).
 constexpr int kDepth = 4;
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParams p) {
   using L = Lane<D, INTER>;
@@ -346,6 +337,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % kLanes, sub = lane / kLanes;
   const L ln(l, p.rot);
+  pdl_wait();
   pdl_launch_dependents();
   const int heads = p.H + 2 * p.H_kv, groups = (heads + kRw - 1) / kRw;
   const int64_t step = static_cast<int64_t>(p.N) * D;
@@ -572,32 +564,49 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__
 
 template <int D, bool INTER>
 cudaError_t launch_fwd(const RopeParams& p, int kind, int ctas, cudaStream_t st) {
-  if (kind == kCacheNone) qkv_rope_kernel<D, INTER, kCacheNone><<<ctas, kRopeThreads, 0, st>>>(p);
-  else if (kind == kCacheBf16) qkv_rope_kernel<D, INTER, kCacheBf16><<<ctas, kRopeThreads, 0, st>>>(p);
-  else qkv_rope_kernel<D, INTER, kCacheE4m3><<<ctas, kRopeThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  const dim3 grid(static_cast<unsigned>(ctas));
+  if (kind == kCacheNone)
+    return launch_dependent(qkv_rope_kernel<D, INTER, kCacheNone>, grid, kRopeThreads, 0, st, p);
+  if (kind == kCacheBf16)
+    return launch_dependent(qkv_rope_kernel<D, INTER, kCacheBf16>, grid, kRopeThreads, 0, st, p);
+  return launch_dependent(qkv_rope_kernel<D, INTER, kCacheE4m3>, grid, kRopeThreads, 0, st, p);
 }
 
-// Warps of one token: one while the tokens alone fill the GPU (two CTAs of 8 warps on each of 152
-// SMs); else more, so that each has fewer rows one after another.
-int parts_of(int tokens) {
-  int parts = 1;
-  while (parts < kWarps && static_cast<int64_t>(tokens) * parts < 2 * kWarps * 152) parts *= 2;
-  return parts;
+// Warps that share a token: the count of 1, 2, 4 .. 32 that minimises rounds of `resident` warps times
+// a warp's work in groups of rows, its own share and `fixed` for the token's angles (the smaller on
+// ties).  Many tokens: few, so that the angles are not computed again; few tokens: as many as have rows.
+int parts_of(int tokens, int groups, int resident, int fixed) {
+  int best = 1;
+  int64_t best_cost = -1;
+  for (int parts = 1; parts <= 32 && parts < 2 * groups; parts *= 2) {
+    const int64_t rounds = (static_cast<int64_t>(tokens) * parts + resident - 1) / resident;
+    const int64_t cost = rounds * ((groups + parts - 1) / parts + fixed);
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
+      best = parts;
+    }
+  }
+  return best;
+}
+int groups_of(const RopeParams& p, int d) {
+  const int rows = 32 / (d / 16);
+  return (p.H + 2 * p.H_kv + rows - 1) / rows;
 }
 
 }  // namespace
 
 cudaError_t launch_qkv_rope(RopeParams& p, int d, bool interleaved, int kind, cudaStream_t st) {
-  p.parts = parts_of(p.tokens);
-  const int tok_cta = kWarps / p.parts;
-  const int ctas = (p.tokens + tok_cta - 1) / tok_cta;
+  // three CTAs an SM; the angles and coefficients of a token take about as long as two groups
+  p.parts = parts_of(p.tokens, groups_of(p, d), 3 * 152 * kWarps, 2);
+  const int ctas = static_cast<int>((static_cast<int64_t>(p.tokens) * p.parts + kWarps - 1) / kWarps);
   if (d == 64)
     return interleaved ? launch_fwd<64, true>(p, kind, ctas, st)
                        : launch_fwd<64, false>(p, kind, ctas, st);
   return interleaved ? launch_fwd<128, true>(p, kind, ctas, st)
                      : launch_fwd<128, false>(p, kind, ctas, st);
 }
+
+namespace {
 
 template <int D, bool INTER>
 cudaError_t launch_bwd(const RopeParams& p, int ctas, cudaStream_t st) {
@@ -613,25 +622,17 @@ cudaError_t launch_bwd(const RopeParams& p, int ctas, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit, std::memory_order_acq_rel);
   }
-  kernel<<<ctas, kRopeThreads, kSmem, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess || !p.partial) return e;
+  e = launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), kRopeThreads, kSmem, st, p);
+  if (e != cudaSuccess || !p.partial) return e;
   // the sums of the CTAs' shares: set up while the rows' kernel still runs
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const float* partial = p.partial;
-  e = cudaLaunchKernelEx(&cfg, rope_dw_kernel, partial, ctas, static_cast<int>(D), p.dwq, p.dwk);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_dependent(rope_dw_kernel, dim3(2), 1024, 0, st, p.partial, ctas, D, p.dwq, p.dwk);
 }
 
+}  // namespace
+
 cudaError_t launch_qkv_rope_bwd(RopeParams& p, int d, bool interleaved, cudaStream_t st) {
-  p.parts = parts_of(p.tokens);
+  // the angles of a token take about as long as one group
+  p.parts = parts_of(p.tokens, groups_of(p, d), kRopeBwdCtas * kWarps, 1);
   const int64_t want = (static_cast<int64_t>(p.tokens) * p.parts + kWarps - 1) / kWarps;
   const int ctas = static_cast<int>(want < kRopeBwdCtas ? want : kRopeBwdCtas);
   if (d == 64) return interleaved ? launch_bwd<64, true>(p, ctas, st) : launch_bwd<64, false>(p, ctas, st);
