@@ -75,7 +75,8 @@ cudaError_t launch_qkv_rope_bwd(RopeParams& p, int d, bool interleaved, cudaStre
 
 // -------------------------------------------------------------------- attention over a paged cache
 constexpr int kPagedTile = 64;         // keys of a tile
-constexpr int kPagedMaxCtas = 456;     // 3 on each of 152 SMs
+constexpr int kPagedMaxCtas = 608;     // 4 on each of 152 SMs
+constexpr float kPagedTrail = 8.f;     // the same in log2 units
 constexpr int kPagedMaxRows = 32;      // query rows (heads of one K/V head) of a unit
 
 struct PagedParams {
@@ -94,7 +95,8 @@ struct PagedParams {
   int* status;
   int B, H, H_kv, group, n_rg, rg_rows;  // row groups of a K/V head and the rows of one
   int max_pages, num_pages, page_shift, box_rows;
-  float scale_log2;
+  float scale_log2;     // scale * log2(e)
+  float trail;          // how far a score may pass the reference maximum, before the scale
 };
 struct PagedLayout {
   size_t o_off, ml_off, join_off, total;

@@ -250,6 +250,7 @@ extern "C" int attn_fwd_paged(const void* q, const attn_kv_cache* cache, const i
   p.num_pages = cache->num_pages;
   p.page_shift = log2_of(cache->page_size);
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.trail = kPagedTrail / p.scale_log2;
   const int64_t all = units > INT_MAX / tiles ? INT_MAX : units * tiles;
   return launch_fwd_paged(p, d, e4m3, all, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? ATTN_OK

@@ -39,7 +39,6 @@ namespace attn {
 namespace {
 
 constexpr int kSlices = 4;                       // key slices of 16 in a tile, a warp each
-constexpr float kTrail = 8.f;                    // how far m may trail (log2 units)
 enum : int { kRoleProducer = 7, kRoleConsumer = 8 };
 
 // NT: groups of 8 query rows a warp holds; RW: row slices, each with four warps of its own.
@@ -50,7 +49,7 @@ struct PagedCfg {
   // CTAs an SM holds.  Where a tile is 32 KB two are enough for the copies to run at full rate; a
   // tile of half that or less has to be through a warp's chain of dependent steps in half the
   // time, so three share it (e4m3, d = 128, 64-row pages: 94 us with two against DRAM's 82).
-  static constexpr int kCtas = RW == 2 ? 1 : D == 128 && (!E4M3 || NT == 2) ? 2 : 3;
+  static constexpr int kCtas = RW * NT == 4 ? 1 : D == 64 ? 4 / RW : !E4M3 || NT == 2 ? 2 : 3;
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
   static constexpr int kBlk = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a row in one box
   static constexpr int kBlks = kRowBytes / kBlk;                  // boxes side by side
@@ -338,11 +337,14 @@ paged_kernel(const __grid_constant__ PagedParams p) {
   load_q<D, E4M3, NT>(p, w, row_slice, qf, mul);
   while (left > 0) {
     const int t_begin = w.t, t_end = min(w.n, w.t + left);
-    float acc[NT][kSteps][4], m[NT][2], l[NT][2];
+    // per row: nm = -m (0 while there is no m), and the score above which m is moved (-inf while
+    // there is none), in the units that scores have when they are compared
+    float acc[NT][kSteps][4], nm[NT][2], above[NT][2], l[NT][2];
     float vref = 0.f, vinv = 0.f;
     #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
+      nm[nt][0] = nm[nt][1] = 0.f;
+      above[nt][0] = above[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
       #pragma unroll
       for (int k = 0; k < kSteps; ++k)
@@ -390,29 +392,39 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         }
         // lane (g, q4): s[0], s[1] = key g, rows 2 q4, 2 q4 + 1;  s[2], s[3] = key g + 8
         const bool in0 = g < live, in1 = g + 8 < live;
-        float sk0 = 1.f, sk1 = 1.f, sv0 = 1.f, sv1 = 1.f;
+        float sv0 = 0.f, sv1 = 0.f;
+        bool grow = false;
         if (E4M3) {
           const float* sc =
               reinterpret_cast<const float*>(sm + L::kScales) + st * 2 * kPagedTile + slice * 16;
-          sk0 = sc[g];
-          sk1 = sc[g + 8];
+          const float sk0 = sc[g], sk1 = sc[g + 8];
           sv0 = in0 ? sc[kPagedTile + g] : 0.f;
           sv1 = in1 ? sc[kPagedTile + g + 8] : 0.f;
+          grow = sv0 > vref || sv1 > vref;
+          #pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            s[nt][0] *= mul[nt][0] * sk0;
+            s[nt][1] *= mul[nt][1] * sk0;
+            s[nt][2] *= mul[nt][0] * sk1;
+            s[nt][3] *= mul[nt][1] * sk1;
+          }
         }
-        bool grow = E4M3 && (sv0 > vref || sv1 > vref);
+        if (live < 16) {
+          #pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            s[nt][0] = in0 ? s[nt][0] : -INFINITY;
+            s[nt][1] = in0 ? s[nt][1] : -INFINITY;
+            s[nt][2] = in1 ? s[nt][2] : -INFINITY;
+            s[nt][3] = in1 ? s[nt][3] : -INFINITY;
+          }
+        }
         #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          s[nt][0] = in0 ? s[nt][0] * (mul[nt][0] * sk0) : -INFINITY;
-          s[nt][1] = in0 ? s[nt][1] * (mul[nt][1] * sk0) : -INFINITY;
-          s[nt][2] = in1 ? s[nt][2] * (mul[nt][0] * sk1) : -INFINITY;
-          s[nt][3] = in1 ? s[nt][3] * (mul[nt][1] * sk1) : -INFINITY;
-          grow |= fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + kTrail ||
-                  fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + kTrail;
-        }
+        for (int nt = 0; nt < NT; ++nt)
+          grow |= fmaxf(s[nt][0], s[nt][2]) > above[nt][0] || fmaxf(s[nt][1], s[nt][3]) > above[nt][1];
         if (__any_sync(0xffffffffu, grow)) {
           float vscale = 1.f;
           if (E4M3) {
-            float vm = fmaxf(vref, fmaxf(sv0, sv1));
+            float vm = fmax3(vref, sv0, sv1);
             #pragma unroll
             for (int off = 4; off < 32; off <<= 1)
               vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, off));
@@ -425,12 +437,18 @@ paged_kernel(const __grid_constant__ PagedParams p) {
             float c[2];
             #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float top = fmaxf(m[nt][j], fmaxf(s[nt][j], s[nt][j + 2]));
+              float top = fmaxf(s[nt][j], s[nt][j + 2]);
               #pragma unroll
               for (int off = 4; off < 32; off <<= 1)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-              c[j] = top == -INFINITY ? 1.f : ex2_approx(m[nt][j] - top);
-              m[nt][j] = top;
+              const float m = E4M3 ? top : top * p.scale_log2;
+              const bool none = above[nt][j] == -INFINITY;  // no m yet: acc and l are 0 (or NaN)
+              c[j] = 1.f;
+              if (top != -INFINITY && (none || m > -nm[nt][j])) {
+                c[j] = none ? 1.f : ex2_approx(-nm[nt][j] - m);
+                nm[nt][j] = -m;
+                above[nt][j] = top + (E4M3 ? kPagedTrail : p.trail);
+              }
               l[nt][j] *= c[j];
               c[j] *= vscale;
             }
@@ -446,10 +464,18 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         uint32_t pf[NT][2];
         #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float r0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-          const float r1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-          const float p0 = ex2_approx(s[nt][0] - r0), p1 = ex2_approx(s[nt][1] - r1);
-          const float p2 = ex2_approx(s[nt][2] - r0), p3 = ex2_approx(s[nt][3] - r1);
+          float p0, p1, p2, p3;
+          if (E4M3) {
+            p0 = ex2_approx(s[nt][0] + nm[nt][0]);
+            p1 = ex2_approx(s[nt][1] + nm[nt][1]);
+            p2 = ex2_approx(s[nt][2] + nm[nt][0]);
+            p3 = ex2_approx(s[nt][3] + nm[nt][1]);
+          } else {
+            p0 = ex2_approx(fmaf(s[nt][0], p.scale_log2, nm[nt][0]));
+            p1 = ex2_approx(fmaf(s[nt][1], p.scale_log2, nm[nt][1]));
+            p2 = ex2_approx(fmaf(s[nt][2], p.scale_log2, nm[nt][0]));
+            p3 = ex2_approx(fmaf(s[nt][3], p.scale_log2, nm[nt][1]));
+          }
           l[nt][0] += p0 + p2;
           l[nt][1] += p1 + p3;
           if (E4M3) {
@@ -462,11 +488,9 @@ paged_kernel(const __grid_constant__ PagedParams p) {
           }
         }
         // V rows past the request's end may hold anything: taken as zero
-        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-        if (live < 16) {
-          keep0 = (2 * q4 < live ? 0xffffu : 0u) | (2 * q4 + 1 < live ? 0xffff0000u : 0u);
-          keep1 = (2 * q4 + 8 < live ? 0xffffu : 0u) | (2 * q4 + 9 < live ? 0xffff0000u : 0u);
-        }
+        const bool tail = live < 16;
+        const uint32_t keep0 = (2 * q4 < live ? 0xffffu : 0u) | (2 * q4 + 1 < live ? 0xffff0000u : 0u);
+        const uint32_t keep1 = (2 * q4 + 8 < live ? 0xffffu : 0u) | (2 * q4 + 9 < live ? 0xffff0000u : 0u);
         if (!E4M3) {
           const int key = slice * 16 + ((lane >> 4) << 3) + (lane & 7);
           #pragma unroll
@@ -474,10 +498,15 @@ paged_kernel(const __grid_constant__ PagedParams p) {
             const int chunk = (k & 3) * 2 + ((lane >> 3) & 1);
             uint32_t a[4];
             ldsm4_t(vst + (k >> 2) * (kPagedTile * 128) + key * 128 + ((chunk ^ (key & 7)) << 4), a);
+            if (tail) {
+              a[0] &= keep0;
+              a[1] &= keep0;
+              a[2] &= keep1;
+              a[3] &= keep1;
+            }
             #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma16816<false>(acc[nt][k], a[0] & keep0, a[1] & keep0, a[2] & keep1, a[3] & keep1,
-                              pf[nt][0], pf[nt][1]);
+              mma16816<false>(acc[nt][k], a[0], a[1], a[2], a[3], pf[nt][0], pf[nt][1]);
           }
         } else {
           const int key = slice * 16 + (lane & 15);
@@ -492,8 +521,14 @@ paged_kernel(const __grid_constant__ PagedParams p) {
             for (int j = 0; j < 2; ++j) {
               const uint32_t x0 = __byte_perm(a[2 * j], 0, 0x3120);
               const uint32_t x1 = __byte_perm(a[2 * j + 1], 0, 0x3120);
-              const uint32_t v0 = e4m3x2_to_f16x2(x0) & keep0, v1 = e4m3x2_to_f16x2(x0 >> 16) & keep0;
-              const uint32_t v2 = e4m3x2_to_f16x2(x1) & keep1, v3 = e4m3x2_to_f16x2(x1 >> 16) & keep1;
+              uint32_t v0 = e4m3x2_to_f16x2(x0), v1 = e4m3x2_to_f16x2(x0 >> 16);
+              uint32_t v2 = e4m3x2_to_f16x2(x1), v3 = e4m3x2_to_f16x2(x1 >> 16);
+              if (tail) {
+                v0 &= keep0;
+                v1 &= keep0;
+                v2 &= keep1;
+                v3 &= keep1;
+              }
               #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 mma16816<true>(acc[nt][k + j], v0, v1, v2, v3, pf[nt][0], pf[nt][1]);
@@ -531,10 +566,13 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         #pragma unroll
         for (int off = 4; off < 32; off <<= 1)
           l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], off);
+      float m[2];
+      #pragma unroll
+      for (int j = 0; j < 2; ++j) m[j] = above[nt][j] == -INFINITY ? -INFINITY : -nm[nt][j];
       if (g == 0) {
         #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          st2[(slice * 8 + 2 * q4 + j) * 2] = m[nt][j];
+          st2[(slice * 8 + 2 * q4 + j) * 2] = m[j];
           st2[(slice * 8 + 2 * q4 + j) * 2 + 1] = l[nt][j];
         }
       }
@@ -545,7 +583,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         #pragma unroll
         for (int x = 0; x < kSlices; ++x) top = fmaxf(top, st2[(x * 8 + 2 * q4 + j) * 2]);
         // m = -inf: no finite score, so acc and l are 0 (or NaN, which stays)
-        const float c = (m[nt][j] == -INFINITY ? 1.f : ex2_approx(m[nt][j] - top)) *
+        const float c = (m[j] == -INFINITY ? 1.f : ex2_approx(m[j] - top)) *
                         (E4M3 ? vref : 1.f);
         #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
@@ -610,12 +648,17 @@ paged_kernel(const __grid_constant__ PagedParams p) {
 }
 
 // Merge of the parts of the unit that CTA blockIdx.x ended: part of CTA i0 (its last), then the
-// first of each CTA up to blockIdx.x.  M = max m_j, weights 2^(m_j - M).  Four warps take every
-// fourth part each; a lane holds d/32 columns.
+// first of each CTA up to blockIdx.x.  M = max m_j, weights 2^(m_j - M).  A row's parts are shared
+// out to 1, 2, 4 or 8 of the block's warps, by how many there are, and joined through shared
+// memory; a lane holds d/32 columns.  Latency bounds it (three dependent reads), so many rows go side by
+// side: 32 rows of 2 or 3 parts each, four rows one after another in a block, took 8 us.
+constexpr int kJoinWarps = 8;
+
 template <int D>
-__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __grid_constant__ PagedParams p) {
   constexpr int kPer = D / 32;
-  __shared__ float s_o[4][D], s_l[4];
+  __shared__ float s_o[kJoinWarps][D];
+  __shared__ float2 s_ml[kJoinWarps];
   pdl_wait();
   const int4 join = p.joins[blockIdx.x];
   if (join.x < 0) return;
@@ -623,50 +666,88 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   const int i0 = join.y, n = static_cast<int>(blockIdx.x) - i0 + 1;
   const int rg = join.x % p.n_rg, sh = join.x / p.n_rg;
   const int row0 = rg * p.rg_rows, rows = min(p.rg_rows, p.group - row0);
-  auto part = [&](int j) { return 2 * (i0 + j) + (j == 0 ? join.z : 0); };
-  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-    float M = -INFINITY;
-    for (int j = lane; j < n; j += 32)
-      M = fmaxf(M, p.part_ml[(static_cast<int64_t>(part(j)) * p.rg_rows + row) * 2]);
-    #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float acc[kPer], le = 0.f;
+  const int share = n <= 4 ? 1 : n <= 16 ? 2 : n <= 48 ? 4 : 8;  // warps of a row
+  const int side = kJoinWarps / share, sub = warp % share;
+  for (int r0 = blockIdx.y * side; r0 < rows; r0 += gridDim.y * side) {
+    const int row = r0 + warp / share;
+    float acc[kPer], m = -INFINITY, l = 0.f;
     #pragma unroll
     for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
-    #pragma unroll 4
-    for (int j = warp; j < n; j += 4) {
-      const int64_t at = static_cast<int64_t>(part(j)) * p.rg_rows + row;
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
-      const float wt = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - M);  // 0 or NaN parts
-      le += wt * ml.y;
-      const float* src = p.part_o + at * D + lane * kPer;
-      if constexpr (kPer == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        acc[0] = fmaf(wt, x.x, acc[0]);
-        acc[1] = fmaf(wt, x.y, acc[1]);
-        acc[2] = fmaf(wt, x.z, acc[2]);
-        acc[3] = fmaf(wt, x.w, acc[3]);
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        acc[0] = fmaf(wt, x.x, acc[0]);
-        acc[1] = fmaf(wt, x.y, acc[1]);
+    if (row < rows) {
+      // four parts at a time, against the largest maximum so far
+      for (int j0 = sub; j0 < n; j0 += 4 * share) {
+        float2 ml[4];
+        float x[4][kPer];
+        #pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int j = j0 + u * share;
+          ml[u] = make_float2(-INFINITY, 0.f);
+          #pragma unroll
+          for (int c = 0; c < kPer; ++c) x[u][c] = 0.f;
+          if (j < n) {
+            const int64_t at =
+                static_cast<int64_t>(2 * (i0 + j) + (j == 0 ? join.z : 0)) * p.rg_rows + row;
+            ml[u] = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+            const float* src = p.part_o + at * D + lane * kPer;
+            if constexpr (kPer == 4)
+              *reinterpret_cast<float4*>(x[u]) = *reinterpret_cast<const float4*>(src);
+            else
+              *reinterpret_cast<float2*>(x[u]) = *reinterpret_cast<const float2*>(src);
+          }
+        }
+        float top = m;
+        #pragma unroll
+        for (int u = 0; u < 4; ++u) top = fmaxf(top, ml[u].x);
+        // a maximum of -inf: nothing, or NaN, which stays
+        const float keep = m == -INFINITY ? 1.f : ex2_approx(m - top);
+        l *= keep;
+        #pragma unroll
+        for (int c = 0; c < kPer; ++c) acc[c] *= keep;
+        #pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float wt = ml[u].x == -INFINITY ? 1.f : ex2_approx(ml[u].x - top);
+          l = fmaf(wt, ml[u].y, l);
+          #pragma unroll
+          for (int c = 0; c < kPer; ++c) acc[c] = fmaf(wt, x[u][c], acc[c]);
+        }
+        m = top;
       }
     }
-    #pragma unroll
-    for (int c = 0; c < kPer; ++c) s_o[warp][lane * kPer + c] = acc[c];
-    if (lane == 0) s_l[warp] = le;
-    __syncthreads();
-    const float total = s_l[0] + s_l[1] + s_l[2] + s_l[3];
-    const int64_t out = static_cast<int64_t>(sh / p.H_kv) * p.H +
-                        static_cast<int64_t>(sh % p.H_kv) * p.group + row0 + row;
-    const int c = threadIdx.x;
-    if (c < D)
-      p.o[out * D + c] =
-          __float2bfloat16((s_o[0][c] + s_o[1][c] + s_o[2][c] + s_o[3][c]) * (1.f / total));
-    if (c == 0)
-      p.lse[out] = total > 0.f || total != total ? (M + log2f(total)) * 0.69314718055994530942f
-                                                 : -INFINITY;
-    __syncthreads();
+    if (share > 1) {  // the same for the whole block
+      #pragma unroll
+      for (int c = 0; c < kPer; ++c) s_o[warp][lane * kPer + c] = acc[c];
+      if (lane == 0) s_ml[warp] = make_float2(m, l);
+      __syncthreads();
+      if (sub == 0) {
+        float top = -INFINITY;
+        for (int u = 0; u < share; ++u) top = fmaxf(top, s_ml[warp + u].x);
+        m = top;
+        l = 0.f;
+        #pragma unroll
+        for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
+        for (int u = 0; u < share; ++u) {
+          const float2 ml = s_ml[warp + u];
+          const float wt = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - top);
+          l = fmaf(wt, ml.y, l);
+          #pragma unroll
+          for (int c = 0; c < kPer; ++c) acc[c] = fmaf(wt, s_o[warp + u][lane * kPer + c], acc[c]);
+        }
+      }
+      __syncthreads();
+    }
+    if (sub == 0 && row < rows) {
+      const int64_t out = static_cast<int64_t>(sh / p.H_kv) * p.H +
+                          static_cast<int64_t>(sh % p.H_kv) * p.group + row0 + row;
+      const float inv = 1.f / l;
+      __nv_bfloat16* dst = p.o + out * D + lane * kPer;
+      if constexpr (kPer == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                                                    pack_bf16x2(acc[2] * inv, acc[3] * inv));
+      else
+        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+      if (lane == 0)
+        p.lse[out] = l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+    }
   }
 }
 
@@ -692,13 +773,13 @@ cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
   return launch_dependent(paged_join_kernel<D>,
                           dim3(static_cast<unsigned>(ctas),
                                static_cast<unsigned>(p.rg_rows < 8 ? p.rg_rows : 8)),
-                          128, 0, stream, p);
+                          kJoinWarps * 32, 0, stream, p);
 }
 
 template <int D, bool E4M3>
 cudaError_t launch_rows(const PagedParams& p, int ctas, cudaStream_t stream) {
   if (p.rg_rows <= 8) return launch<D, E4M3, 1, 1>(p, ctas, stream);
-  if (p.rg_rows <= 16) return launch<D, E4M3, 2, 1>(p, ctas, stream);
+  if (p.rg_rows <= 16) return launch<D, E4M3, D == 64 ? 1 : 2, D == 64 ? 2 : 1>(p, ctas, stream);
   return launch<D, E4M3, 2, 2>(p, ctas, stream);
 }
 
