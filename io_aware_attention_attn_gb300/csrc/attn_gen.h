@@ -114,7 +114,7 @@ inline PagedLayout paged_layout(int group, int d) {
   L.total = L.join_off + up(kPagedMaxCtas * 16);
   return L;
 }
-cudaError_t launch_fwd_paged(const PagedParams& p, int d, bool e4m3, long long max_units,
+cudaError_t launch_fwd_paged(const PagedParams& p, int d, bool e4m3, int max_tiles,
                              cudaStream_t stream);
 
 // Encode the 4-D map of a paged cache's K or V (attn_abi.cu).  Returns a CUresult.

@@ -211,10 +211,8 @@ extern "C" int attn_fwd_paged(const void* q, const attn_kv_cache* cache, const i
   if (most > INT_MAX - kPagedTile) return ATTN_ERR_SHAPE;
   const int64_t units = static_cast<int64_t>(B) * H_kv * paged_row_groups(group);
   const int64_t tiles = most > 0 ? (most + kPagedTile - 1) / kPagedTile : 1;
-  // the kernel multiplies tile counts by CTA numbers in 64 bits, and numbers units in 32
-  if (units > INT_MAX || static_cast<int64_t>(B) * H > INT_MAX ||
-      units > LLONG_MAX / tiles / (2 * kPagedMaxCtas))
-    return ATTN_ERR_SHAPE;
+  // the kernel numbers tiles in 32 bits
+  if (static_cast<int64_t>(B) * H > INT_MAX || units > INT_MAX / tiles) return ATTN_ERR_SHAPE;
   const PagedLayout L = paged_layout(group, d);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total)
     return ATTN_ERR_WORKSPACE;
@@ -251,8 +249,7 @@ extern "C" int attn_fwd_paged(const void* q, const attn_kv_cache* cache, const i
   p.page_shift = log2_of(cache->page_size);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.trail = kPagedTrail / p.scale_log2;
-  const int64_t all = units > INT_MAX / tiles ? INT_MAX : units * tiles;
-  return launch_fwd_paged(p, d, e4m3, all, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_fwd_paged(p, d, e4m3, static_cast<int>(units * tiles), static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? ATTN_OK
              : ATTN_ERR_LAUNCH;
 }

@@ -100,33 +100,33 @@ __device__ __forceinline__ void next_unit(const PagedParams& p, Walk& w) {
   w.ahead = w.s + 1 < p.B ? req_len(p, w.s + 1) : 0;
 }
 // Walk at tile `at` of the whole order (a warp's lanes together); returns the first tile of its unit.
-__device__ long long find(const PagedParams& p, long long at, Walk& w) {
+__device__ int find(const PagedParams& p, int at, Walk& w) {
   const int lane = threadIdx.x & 31, per = p.H_kv * p.n_rg;
-  long long before = 0;
+  int before = 0;
   for (int s0 = 0; s0 < p.B; s0 += 32) {
     const int s = s0 + lane;
     const int len = s < p.B ? req_len(p, s) : 0;
     const int n = s < p.B ? req_tiles(len) : 0;
-    long long scan = static_cast<long long>(n) * per;
+    int scan = n * per;
     #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, scan, off);
+      const int up = __shfl_up_sync(0xffffffffu, scan, off);
       if (lane >= off) scan += up;
     }
     const uint32_t past = __ballot_sync(0xffffffffu, before + scan > at);
     if (past) {
       const int k = __ffs(past) - 1;
-      const long long own = scan - static_cast<long long>(n) * per;
-      before += __shfl_sync(0xffffffffu, own, k);
+      before += __shfl_sync(0xffffffffu, scan - n * per, k);
       w.s = s0 + k;
       w.n = __shfl_sync(0xffffffffu, n, k);
       w.len = __shfl_sync(0xffffffffu, len, k);
-      const long long in = at - before;
-      const int u = static_cast<int>(in / w.n);
-      w.t = static_cast<int>(in - static_cast<long long>(u) * w.n);
-      w.h = u / p.n_rg;
-      w.rg = u - w.h * p.n_rg;
-      w.ahead = w.s + 1 < p.B ? req_len(p, w.s + 1) : 0;
+      const uint32_t in = at - before;
+      const uint32_t u = in / static_cast<uint32_t>(w.n);
+      w.t = static_cast<int>(in - u * w.n);
+      w.h = p.n_rg == 1 ? u : u / p.n_rg;
+      w.rg = static_cast<int>(u) - w.h * p.n_rg;
+      w.ahead = k < 31 ? __shfl_sync(0xffffffffu, len, k + 1 & 31)
+                       : (w.s + 1 < p.B ? req_len(p, w.s + 1) : 0);
       return at - w.t;
     }
     before += __shfl_sync(0xffffffffu, scan, 31);
@@ -134,6 +134,18 @@ __device__ long long find(const PagedParams& p, long long at, Walk& w) {
   w = Walk{p.B, 0, 0, 0, 1, 0, 0};
   return at;
 }
+
+// CTA i's share of `total` tiles among G: starts at i * (total / G) plus one for each earlier CTA of the
+// first total % G, which take one tile more.
+struct Shares {
+  uint32_t q, r;
+  __device__ __forceinline__ Shares(uint32_t total, uint32_t G) : q(total / G), r(total - q * G) {}
+  __device__ __forceinline__ int start(uint32_t i) const { return static_cast<int>(i * q + min(i, r)); }
+  __device__ __forceinline__ int owner(uint32_t tile) const {
+    const uint32_t big = r * (q + 1);
+    return static_cast<int>(tile < big ? tile / (q + 1) : r + (tile - big) / q);
+  }
+};
 
 // This lane's share of the B operand of K Q^T (query row g of each group of 8, the elements that its
 // positions along d stand for), and the factors of scores (log2 units) of rows 2 q4, 2 q4 + 1.
@@ -211,32 +223,37 @@ paged_kernel(const __grid_constant__ PagedParams p) {
     tma_prefetch_desc(&p.tm_v);
   }
   pdl_wait();
-  // tiles of all units: each warp for itself when one look at the lengths is enough
-  long long total = 0;
-  const int few = p.B <= 32;
-  for (int s = few ? lane : tid; s < p.B; s += L::kThreads) total += req_tiles(req_len(p, s));
-  #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-  long long* sums = reinterpret_cast<long long*>(sm + L::kMerge);
-  if (!few && lane == 0) sums[warp] = total;
+  // tiles of all units (fewer than 2^31: the host's check): each warp for itself where eight loads a
+  // lane are enough
+  int tiles = 0;
+  const bool few = p.B <= 256;
+  if (few) {
+    #pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (32 * k + lane < p.B) tiles += req_tiles(req_len(p, 32 * k + lane));
+  } else {
+    for (int s = tid; s < p.B; s += L::kThreads) tiles += req_tiles(req_len(p, s));
+  }
+  tiles = __reduce_add_sync(0xffffffffu, tiles);
+  int* sums = reinterpret_cast<int*>(sm + L::kMerge);
+  if (!few && lane == 0) sums[warp] = tiles;
   __syncthreads();
   if (!few) {
-    total = 0;
-    for (int i = 0; i <= L::kWarps; ++i) total += sums[i];
+    tiles = 0;
+    for (int i = 0; i <= L::kWarps; ++i) tiles += sums[i];
     __syncthreads();
   }
-  total *= p.H_kv * p.n_rg;
-  const long long G = min(static_cast<long long>(gridDim.x), total);
-  const long long cta = blockIdx.x;
+  const int total = tiles * p.H_kv * p.n_rg;
+  const int cta = static_cast<int>(blockIdx.x), G = min(static_cast<int>(gridDim.x), total);
   pdl_launch_dependents();
   if (cta >= G) {
     if (tid == 0) p.joins[cta] = make_int4(-1, 0, 0, 0);
     return;
   }
-  const long long w0 = cta * total / G, w1 = (cta + 1) * total / G;
-  const int n_tiles = static_cast<int>(w1 - w0);
+  const Shares shares(static_cast<uint32_t>(total), static_cast<uint32_t>(G));
+  const int w0 = shares.start(cta), w1 = shares.start(cta + 1), n_tiles = w1 - w0;
   Walk w;
-  const long long unit0 = find(p, w0, w);
+  const int unit0 = find(p, w0, w);
   const WaitCtx ctx{misc, p.status};
 
   if (warp == L::kWarps) {
@@ -245,9 +262,8 @@ paged_kernel(const __grid_constant__ PagedParams p) {
       // the unit that ends here and began in an earlier CTA, and where its parts are
       int4 join = make_int4(-1, 0, 0, 0);
       if (unit0 < w0 && unit0 + w.n <= w1) {
-        const long long i0 = ((unit0 + 1) * G - 1) / total;
-        join = make_int4((w.s * p.H_kv + w.h) * p.n_rg + w.rg, static_cast<int>(i0),
-                         i0 * total / G < unit0 ? 1 : 0, 0);
+        const int i0 = shares.owner(unit0);
+        join = make_int4((w.s * p.H_kv + w.h) * p.n_rg + w.rg, i0, shares.start(i0) < unit0 ? 1 : 0, 0);
       }
       p.joins[cta] = join;
     }
@@ -549,7 +565,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
     // the next unit's query rows are on their way
     const bool whole = t_begin == 0 && t_end == w.n;
     const int len = w.len;
-    const int part = 2 * static_cast<int>(cta) + (first ? 0 : 1);
+    const int part = 2 * cta + (first ? 0 : 1);
     first = false;
     const int row0 = w.rg * p.rg_rows, rows = min(p.rg_rows, p.group - row0);
     const int64_t out0 = static_cast<int64_t>(w.s) * p.H + static_cast<int64_t>(w.h) * p.group + row0;
@@ -652,7 +668,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
 // out to 1, 2, 4 or 8 of the block's warps, by how many there are, and joined through shared
 // memory; a lane holds d/32 columns.  Latency bounds it (three dependent reads), so many rows go side by
 // side: 32 rows of 2 or 3 parts each, four rows one after another in a block, took 8 us.
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 8, kAtOnce = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __grid_constant__ PagedParams p) {
@@ -666,7 +682,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
   const int i0 = join.y, n = static_cast<int>(blockIdx.x) - i0 + 1;
   const int rg = join.x % p.n_rg, sh = join.x / p.n_rg;
   const int row0 = rg * p.rg_rows, rows = min(p.rg_rows, p.group - row0);
-  const int share = n <= 4 ? 1 : n <= 16 ? 2 : n <= 48 ? 4 : 8;  // warps of a row
+  const int share = n <= kAtOnce ? 1 : n <= 2 * kAtOnce ? 2 : n <= 4 * kAtOnce ? 4 : 8;  // warps of a row
   const int side = kJoinWarps / share, sub = warp % share;
   for (int r0 = blockIdx.y * side; r0 < rows; r0 += gridDim.y * side) {
     const int row = r0 + warp / share;
@@ -674,12 +690,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
     #pragma unroll
     for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
     if (row < rows) {
-      // four parts at a time, against the largest maximum so far
-      for (int j0 = sub; j0 < n; j0 += 4 * share) {
-        float2 ml[4];
-        float x[4][kPer];
+      // so many parts at a time, against the largest maximum so far
+      for (int j0 = sub; j0 < n; j0 += kAtOnce * share) {
+        float2 ml[kAtOnce];
+        float x[kAtOnce][kPer];
         #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kAtOnce; ++u) {
           const int j = j0 + u * share;
           ml[u] = make_float2(-INFINITY, 0.f);
           #pragma unroll
@@ -697,14 +713,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
         }
         float top = m;
         #pragma unroll
-        for (int u = 0; u < 4; ++u) top = fmaxf(top, ml[u].x);
+        for (int u = 0; u < kAtOnce; ++u) top = fmaxf(top, ml[u].x);
         // a maximum of -inf: nothing, or NaN, which stays
         const float keep = m == -INFINITY ? 1.f : ex2_approx(m - top);
         l *= keep;
         #pragma unroll
         for (int c = 0; c < kPer; ++c) acc[c] *= keep;
         #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kAtOnce; ++u) {
           const float wt = ml[u].x == -INFINITY ? 1.f : ex2_approx(ml[u].x - top);
           l = fmaf(wt, ml[u].y, l);
           #pragma unroll
@@ -785,9 +801,9 @@ cudaError_t launch_rows(const PagedParams& p, int ctas, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_fwd_paged(const PagedParams& p, int d, bool e4m3, long long max_units,
+cudaError_t launch_fwd_paged(const PagedParams& p, int d, bool e4m3, int max_tiles,
                              cudaStream_t stream) {
-  const int ctas = static_cast<int>(max_units < kPagedMaxCtas ? max_units : kPagedMaxCtas);
+  const int ctas = max_tiles < kPagedMaxCtas ? max_tiles : kPagedMaxCtas;
   if (d == 64) return e4m3 ? launch_rows<64, true>(p, ctas, stream) : launch_rows<64, false>(p, ctas, stream);
   return e4m3 ? launch_rows<128, true>(p, ctas, stream) : launch_rows<128, false>(p, ctas, stream);
 }
