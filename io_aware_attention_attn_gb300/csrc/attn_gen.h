@@ -91,10 +91,11 @@ struct PagedParams {
   const float* vs;
   float* part_o;        // [2 * CTAs][rows][d] unnormalised partial outputs
   float* part_ml;       // [2 * CTAs][rows][2] reference maximum (log2 units), row sum
-  int4* joins;          // [CTAs] the unit that CTA i ends and an earlier CTA began
+  int4* joins;          // units whose parts several CTAs hold: by unit, or by the CTA that ends them
   int* status;
   int B, H, H_kv, group, n_rg, rg_rows;  // row groups of a K/V head and the rows of one
   int max_pages, num_pages, page_shift, box_rows;
+  bool by_unit;
   float scale_log2;     // scale * log2(e)
   float trail;          // how far a score may pass the reference maximum, before the scale
 };

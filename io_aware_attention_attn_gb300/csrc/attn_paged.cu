@@ -247,7 +247,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
   const int cta = static_cast<int>(blockIdx.x), G = min(static_cast<int>(gridDim.x), total);
   pdl_launch_dependents();
   if (cta >= G) {
-    if (tid == 0) p.joins[cta] = make_int4(-1, 0, 0, 0);
+    if (tid == 0 && !p.by_unit) p.joins[cta] = make_int4(0, 0, 0, 0);
     return;
   }
   const Shares shares(static_cast<uint32_t>(total), static_cast<uint32_t>(G));
@@ -259,13 +259,16 @@ paged_kernel(const __grid_constant__ PagedParams p) {
   if (warp == L::kWarps) {
     // ------------------------------------------------------------------------------ producer
     if (lane == 0) {
-      // the unit that ends here and began in an earlier CTA, and where its parts are
-      int4 join = make_int4(-1, 0, 0, 0);
-      if (unit0 < w0 && unit0 + w.n <= w1) {
+      // the unit that ends here and began in an earlier CTA: its parts are that CTA's last and the first
+      // of each one since
+      const bool ends = unit0 < w0 && unit0 + w.n <= w1;
+      const int unit = (w.s * p.H_kv + w.h) * p.n_rg + w.rg;
+      int4 join = make_int4(0, 0, 0, 0);
+      if (ends) {
         const int i0 = shares.owner(unit0);
-        join = make_int4((w.s * p.H_kv + w.h) * p.n_rg + w.rg, i0, shares.start(i0) < unit0 ? 1 : 0, 0);
+        join = make_int4(cta - i0 + 1, unit, i0, shares.start(i0) < unit0 ? 1 : 0);
       }
-      p.joins[cta] = join;
+      if (ends || !p.by_unit) p.joins[p.by_unit ? unit : cta] = join;
     }
     const uint64_t policy = l2_policy_evict_first();
     const int box_shift = 31 - __clz(p.box_rows);
@@ -565,6 +568,8 @@ paged_kernel(const __grid_constant__ PagedParams p) {
     // the next unit's query rows are on their way
     const bool whole = t_begin == 0 && t_end == w.n;
     const int len = w.len;
+    if (whole && p.by_unit && tid == 0)
+      p.joins[(w.s * p.H_kv + w.h) * p.n_rg + w.rg] = make_int4(0, 0, 0, 0);
     const int part = 2 * cta + (first ? 0 : 1);
     first = false;
     const int row0 = w.rg * p.rg_rows, rows = min(p.rg_rows, p.group - row0);
@@ -663,8 +668,9 @@ paged_kernel(const __grid_constant__ PagedParams p) {
   }
 }
 
-// Merge of the parts of the unit that CTA blockIdx.x ended: part of CTA i0 (its last), then the
-// first of each CTA up to blockIdx.x.  M = max m_j, weights 2^(m_j - M).  A row's parts are shared
+// Merge of one unit's parts, as the CTA that ended it described them (joins[blockIdx.x]: parts, unit, the
+// CTA that began it and which of its two parts that is): that part, then the
+// first of each CTA that follows.  M = max m_j, weights 2^(m_j - M).  A row's parts are shared
 // out to 1, 2, 4 or 8 of the block's warps, by how many there are, and joined through shared
 // memory; a lane holds d/32 columns.  Latency bounds it (three dependent reads), so many rows go side by
 // side: 32 rows of 2 or 3 parts each, four rows one after another in a block, took 8 us.
@@ -677,10 +683,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
   __shared__ float2 s_ml[kJoinWarps];
   pdl_wait();
   const int4 join = p.joins[blockIdx.x];
-  if (join.x < 0) return;
+  if (join.x == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i0 = join.y, n = static_cast<int>(blockIdx.x) - i0 + 1;
-  const int rg = join.x % p.n_rg, sh = join.x / p.n_rg;
+  const int n = join.x, i0 = join.z, rg = join.y % p.n_rg, sh = join.y / p.n_rg;
   const int row0 = rg * p.rg_rows, rows = min(p.rg_rows, p.group - row0);
   const int share = n <= kAtOnce ? 1 : n <= 2 * kAtOnce ? 2 : n <= 4 * kAtOnce ? 4 : 8;  // warps of a row
   const int side = kJoinWarps / share, sub = warp % share;
@@ -702,7 +707,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
           for (int c = 0; c < kPer; ++c) x[u][c] = 0.f;
           if (j < n) {
             const int64_t at =
-                static_cast<int64_t>(2 * (i0 + j) + (j == 0 ? join.z : 0)) * p.rg_rows + row;
+                static_cast<int64_t>(2 * (i0 + j) + (j == 0 ? join.w : 0)) * p.rg_rows + row;
             ml[u] = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
             const float* src = p.part_o + at * D + lane * kPer;
             if constexpr (kPer == 4)
@@ -784,12 +789,19 @@ cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
   const int most = L::kCtas * 152;
   static_assert(L::kCtas * 152 <= kPagedMaxCtas, "the workspace holds the parts of fewer CTAs");
   if (ctas > most) ctas = most;
-  e = launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), L::kThreads, L::kDyn, stream, p);
+  // one join a unit where there are no more units than CTAs, with a block for each row while that is
+  // no more than a few blocks an SM; else one a CTA
+  const long long units = static_cast<long long>(p.B) * p.H_kv * p.n_rg;
+  PagedParams q = p;
+  q.by_unit = units <= ctas;
+  const int joins = q.by_unit ? static_cast<int>(units) : ctas;
+  const int side = q.by_unit && units < 128 ? 1024 / joins : 8;
+  e = launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), L::kThreads, L::kDyn, stream, q);
   if (e != cudaSuccess) return e;
   return launch_dependent(paged_join_kernel<D>,
-                          dim3(static_cast<unsigned>(ctas),
-                               static_cast<unsigned>(p.rg_rows < 8 ? p.rg_rows : 8)),
-                          kJoinWarps * 32, 0, stream, p);
+                          dim3(static_cast<unsigned>(joins),
+                               static_cast<unsigned>(p.rg_rows < side ? p.rg_rows : side)),
+                          kJoinWarps * 32, 0, stream, q);
 }
 
 template <int D, bool E4M3>
