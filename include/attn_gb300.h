@@ -359,8 +359,8 @@ ATTN_API size_t attn_qkv_rope_bwd_workspace_bytes(int B, int N, int H, int H_kv,
  * replayed with other lengths, tables and contents.  Equal inputs give equal bits.
  * A table entry that is needed and names no page of the cache is read as a page of zeros, and the
  * status word reports kind 5.
- * H_kv must divide H, and B * H_kv * ceil(H / H_kv / 32) * ceil(max_pages * page_size / 64), the tiles
- * that the table's shape allows, must be below 2^31 (ATTN_ERR_SHAPE).  Returns an attn_status.
+ * H_kv must divide H, and B * H_kv * ceil(H / H_kv / 32) * (ceil(max_pages * page_size / 64) + 2), by the
+ * tiles that the table's shape allows, must be below 2^31 (ATTN_ERR_SHAPE).  Returns an attn_status.
  */
 ATTN_API int attn_fwd_paged(const void* q, const attn_kv_cache* cache, const int32_t* block_table,
                             const int32_t* seq_lens, void* o, float* lse, int B, int H, int H_kv,

@@ -91,16 +91,17 @@ struct PagedParams {
   const float* vs;
   float* part_o;        // [2 * CTAs][rows][d] unnormalised partial outputs
   float* part_ml;       // [2 * CTAs][rows][2] reference maximum (log2 units), row sum
-  int4* joins;          // units whose parts several CTAs hold: by unit, or by the CTA that ends them
   int* status;
   int B, H, H_kv, group, n_rg, rg_rows;  // row groups of a K/V head and the rows of one
   int max_pages, num_pages, page_shift, box_rows;
-  bool by_unit;
+  int ctas;             // of the parts' kernel
+  int unit_cost;        // places that a unit takes beside its tiles
+  bool by_unit;         // one join a unit, else one a CTA
   float scale_log2;     // scale * log2(e)
   float trail;          // how far a score may pass the reference maximum, before the scale
 };
 struct PagedLayout {
-  size_t o_off, ml_off, join_off, total;
+  size_t o_off, ml_off, total;
 };
 inline int paged_row_groups(int group) {
   return (group + kPagedMaxRows - 1) / kPagedMaxRows;
@@ -111,8 +112,7 @@ inline PagedLayout paged_layout(int group, int d) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   PagedLayout L{};
   L.ml_off = up(2 * kPagedMaxCtas * rows * d * 4);
-  L.join_off = L.ml_off + up(2 * kPagedMaxCtas * rows * 2 * 4);
-  L.total = L.join_off + up(kPagedMaxCtas * 16);
+  L.total = L.ml_off + up(2 * kPagedMaxCtas * rows * 2 * 4);
   return L;
 }
 cudaError_t launch_fwd_paged(const PagedParams& p, int d, bool e4m3, int max_tiles,

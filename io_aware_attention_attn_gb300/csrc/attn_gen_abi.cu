@@ -211,8 +211,8 @@ extern "C" int attn_fwd_paged(const void* q, const attn_kv_cache* cache, const i
   if (most > INT_MAX - kPagedTile) return ATTN_ERR_SHAPE;
   const int64_t units = static_cast<int64_t>(B) * H_kv * paged_row_groups(group);
   const int64_t tiles = most > 0 ? (most + kPagedTile - 1) / kPagedTile : 1;
-  // the kernel numbers tiles in 32 bits
-  if (static_cast<int64_t>(B) * H > INT_MAX || units > INT_MAX / tiles) return ATTN_ERR_SHAPE;
+  // the kernel numbers tiles, and two places more a unit, in 32 bits
+  if (static_cast<int64_t>(B) * H > INT_MAX || units > INT_MAX / (tiles + 2)) return ATTN_ERR_SHAPE;
   const PagedLayout L = paged_layout(group, d);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total)
     return ATTN_ERR_WORKSPACE;
@@ -235,7 +235,6 @@ extern "C" int attn_fwd_paged(const void* q, const attn_kv_cache* cache, const i
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.part_o = reinterpret_cast<float*>(ws + L.o_off);
   p.part_ml = reinterpret_cast<float*>(ws + L.ml_off);
-  p.joins = reinterpret_cast<int4*>(ws + L.join_off);
   p.status = status_word();
   if (!p.status) return ATTN_ERR_LAUNCH;
   p.B = B;

@@ -24,10 +24,11 @@
 // key's K scale multiplies its scores, its V scale its P, divided by the largest V scale the warp has
 // seen so that P V operands stay in f16's range.
 //
-// Work split: the tiles of all units in order (request, head, row group) are cut into equal runs, one a
-// CTA.  A unit inside one run is finished by its CTA; the parts of a unit that spans several runs go to
-// the workspace, at most two a CTA, and paged_join_kernel merges them.  The CTA that holds a
-// unit's end but not its start leaves the merge's description.
+// Work split: the tiles of all units in order (request, head, row group), each unit with a few more for
+// what its end costs, are cut into equal shares, one a CTA.  A unit inside one share is finished by
+// its CTA; the parts of a unit that spans several go to the workspace, at most two a CTA, and
+// paged_join_kernel merges them.  It works out for itself which CTAs hold a unit's parts, from the
+// lengths, while it waits for them.
 #include "attn_gen.cuh"
 #include "attn_gen.h"
 #include "sm103_ptx.cuh"
@@ -56,8 +57,9 @@ struct PagedCfg {
   static constexpr int kSide = kPagedTile * kRowBytes;            // K or V of a tile
   static constexpr int kStage = 2 * kSide;
   static constexpr int kMergeLd = D + 4;                          // spreads rows over the banks
-  static constexpr int kMergeBytes = 2 * 8 * kMergeLd * 4;        // of one row slice
-  static constexpr int kStatBytes = 2 * kSlices * 8 * 2 * 4;      // [2][slice][8 rows][2], likewise
+  static constexpr int kMergeNt = kCtas == 1 ? NT : 1;            // row groups merged at once
+  static constexpr int kMergeBytes = kMergeNt * 2 * 8 * kMergeLd * 4;  // of one row slice
+  static constexpr int kStatBytes = 2 * kMergeNt * kSlices * 8 * 2 * 4;  // likewise, of two merges
   // tiles in the ring: what shared memory holds beside the rest (each CTA's 1 KB of the system's and
   // 1 KB for alignment), 8 at most
   static constexpr int kScaleBytes = E4M3 ? 2 * kPagedTile * 4 : 0;
@@ -99,14 +101,28 @@ __device__ __forceinline__ void next_unit(const PagedParams& p, Walk& w) {
   w.n = req_tiles(w.len);
   w.ahead = w.s + 1 < p.B ? req_len(p, w.s + 1) : 0;
 }
-// Walk at tile `at` of the whole order (a warp's lanes together); returns the first tile of its unit.
+// Places in the order of all units: a unit takes its tiles and `p.unit_cost` places more.
+__device__ __forceinline__ int req_places(const PagedParams& p, int s) {
+  return s < p.B ? req_tiles(req_len(p, s)) + p.unit_cost : 0;
+}
+// Places of all requests, by one warp.
+__device__ __forceinline__ int all_places(const PagedParams& p) {
+  int n = 0;
+  for (int s0 = threadIdx.x & 31; s0 < p.B; s0 += 256) {
+    #pragma unroll
+    for (int k = 0; k < 8; ++k) n += req_places(p, s0 + 32 * k);
+  }
+  return __reduce_add_sync(0xffffffffu, n) * (p.H_kv * p.n_rg);
+}
+// Walk at place `at` (a warp's lanes together; w.t past the tiles: in the places after them); returns
+// the first place of its unit.
 __device__ int find(const PagedParams& p, int at, Walk& w) {
   const int lane = threadIdx.x & 31, per = p.H_kv * p.n_rg;
   int before = 0;
   for (int s0 = 0; s0 < p.B; s0 += 32) {
     const int s = s0 + lane;
     const int len = s < p.B ? req_len(p, s) : 0;
-    const int n = s < p.B ? req_tiles(len) : 0;
+    const int n = s < p.B ? req_tiles(len) + p.unit_cost : 0;
     int scan = n * per;
     #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -117,16 +133,17 @@ __device__ int find(const PagedParams& p, int at, Walk& w) {
     if (past) {
       const int k = __ffs(past) - 1;
       before += __shfl_sync(0xffffffffu, scan - n * per, k);
+      const int places = __shfl_sync(0xffffffffu, n, k);
       w.s = s0 + k;
-      w.n = __shfl_sync(0xffffffffu, n, k);
+      w.n = places - p.unit_cost;
       w.len = __shfl_sync(0xffffffffu, len, k);
       const uint32_t in = at - before;
-      const uint32_t u = in / static_cast<uint32_t>(w.n);
-      w.t = static_cast<int>(in - u * w.n);
+      const uint32_t u = in / static_cast<uint32_t>(places);
+      w.t = static_cast<int>(in - u * places);
       w.h = p.n_rg == 1 ? u : u / p.n_rg;
       w.rg = static_cast<int>(u) - w.h * p.n_rg;
-      w.ahead = k < 31 ? __shfl_sync(0xffffffffu, len, k + 1 & 31)
-                       : (w.s + 1 < p.B ? req_len(p, w.s + 1) : 0);
+      const int after = __shfl_sync(0xffffffffu, len, (k + 1) & 31);
+      w.ahead = k < 31 ? after : w.s + 1 < p.B ? req_len(p, w.s + 1) : 0;
       return at - w.t;
     }
     before += __shfl_sync(0xffffffffu, scan, 31);
@@ -135,15 +152,15 @@ __device__ int find(const PagedParams& p, int at, Walk& w) {
   return at;
 }
 
-// CTA i's share of `total` tiles among G: starts at i * (total / G) plus one for each earlier CTA of the
-// first total % G, which take one tile more.
+// CTA i's share of `total` places among G: starts at i * (total / G) plus one for each earlier CTA of
+// the first total % G, which take one place more.
 struct Shares {
   uint32_t q, r;
   __device__ __forceinline__ Shares(uint32_t total, uint32_t G) : q(total / G), r(total - q * G) {}
   __device__ __forceinline__ int start(uint32_t i) const { return static_cast<int>(i * q + min(i, r)); }
-  __device__ __forceinline__ int owner(uint32_t tile) const {
+  __device__ __forceinline__ int owner(uint32_t place) const {
     const uint32_t big = r * (q + 1);
-    return static_cast<int>(tile < big ? tile / (q + 1) : r + (tile - big) / q);
+    return static_cast<int>(place < big ? place / (q + 1) : r + (place - big) / q);
   }
 };
 
@@ -223,53 +240,40 @@ paged_kernel(const __grid_constant__ PagedParams p) {
     tma_prefetch_desc(&p.tm_v);
   }
   pdl_wait();
-  // tiles of all units (fewer than 2^31: the host's check): each warp for itself where eight loads a
+  // places of all units (fewer than 2^31: the host's check): each warp for itself where eight loads a
   // lane are enough
-  int tiles = 0;
-  const bool few = p.B <= 256;
-  if (few) {
-    #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (32 * k + lane < p.B) tiles += req_tiles(req_len(p, 32 * k + lane));
+  int total = 0;
+  if (p.B <= 256) {
+    total = all_places(p);
+    __syncthreads();
   } else {
-    for (int s = tid; s < p.B; s += L::kThreads) tiles += req_tiles(req_len(p, s));
-  }
-  tiles = __reduce_add_sync(0xffffffffu, tiles);
-  int* sums = reinterpret_cast<int*>(sm + L::kMerge);
-  if (!few && lane == 0) sums[warp] = tiles;
-  __syncthreads();
-  if (!few) {
-    tiles = 0;
-    for (int i = 0; i <= L::kWarps; ++i) tiles += sums[i];
+    for (int s = tid; s < p.B; s += L::kThreads) total += req_places(p, s);
+    total = __reduce_add_sync(0xffffffffu, total);
+    int* sums = reinterpret_cast<int*>(sm + L::kMerge);
+    if (lane == 0) sums[warp] = total;
+    __syncthreads();
+    total = 0;
+    for (int i = 0; i <= L::kWarps; ++i) total += sums[i];
+    total *= p.H_kv * p.n_rg;
     __syncthreads();
   }
-  const int total = tiles * p.H_kv * p.n_rg;
-  const int cta = static_cast<int>(blockIdx.x), G = min(static_cast<int>(gridDim.x), total);
   pdl_launch_dependents();
-  if (cta >= G) {
-    if (tid == 0 && !p.by_unit) p.joins[cta] = make_int4(0, 0, 0, 0);
-    return;
-  }
+  const int cta = static_cast<int>(blockIdx.x), G = min(p.ctas, total);
+  if (cta >= G) return;
   const Shares shares(static_cast<uint32_t>(total), static_cast<uint32_t>(G));
-  const int w0 = shares.start(cta), w1 = shares.start(cta + 1), n_tiles = w1 - w0;
+  const int place0 = shares.start(cta);
   Walk w;
-  const int unit0 = find(p, w0, w);
+  const int unit0 = find(p, place0, w);
+  int left = shares.start(cta + 1) - place0;  // places of this CTA still to come
+  if (w.t >= w.n) {  // it starts behind a unit's last tile
+    left -= unit0 + w.n + p.unit_cost - place0;
+    if (left <= 0) return;
+    next_unit(p, w);
+  }
   const WaitCtx ctx{misc, p.status};
 
   if (warp == L::kWarps) {
     // ------------------------------------------------------------------------------ producer
-    if (lane == 0) {
-      // the unit that ends here and began in an earlier CTA: its parts are that CTA's last and the first
-      // of each one since
-      const bool ends = unit0 < w0 && unit0 + w.n <= w1;
-      const int unit = (w.s * p.H_kv + w.h) * p.n_rg + w.rg;
-      int4 join = make_int4(0, 0, 0, 0);
-      if (ends) {
-        const int i0 = shares.owner(unit0);
-        join = make_int4(cta - i0 + 1, unit, i0, shares.start(i0) < unit0 ? 1 : 0);
-      }
-      if (ends || !p.by_unit) p.joins[p.by_unit ? unit : cta] = join;
-    }
     const uint64_t policy = l2_policy_evict_first();
     const int box_shift = 31 - __clz(p.box_rows);
     const int parts_tile = kPagedTile >> box_shift;
@@ -277,7 +281,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
     bool ok = true;
     int it = 0, st = 0;
     uint32_t phase = 1;  // of the empty barrier waited for, from the second round on
-    for (; it < n_tiles; ++it) {
+    for (; left > 0; ++it) {
       const int rows = min(kPagedTile, w.len - w.t * kPagedTile);
       const int parts = rows > 0 ? (rows + p.box_rows - 1) >> box_shift : 0;
       const int page0 = (w.t * kPagedTile) >> p.page_shift;
@@ -331,7 +335,11 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         st = 0;
         phase ^= 1;
       }
-      if (++w.t == w.n) next_unit(p, w);
+      --left;
+      if (++w.t == w.n) {
+        left -= p.unit_cost;
+        if (left > 0) next_unit(p, w);
+      }
     }
     if (!ok) {  // copies in flight land before the CTA's shared memory goes
       if (E4M3) copy_wait<0>();
@@ -346,11 +354,11 @@ paged_kernel(const __grid_constant__ PagedParams p) {
   const int slice = warp % kSlices, row_slice = RW == 1 ? 0 : warp / kSlices;
   constexpr int kSteps = D / 16;      // k16 steps of S, m16 tiles of O^T
   bool dead = false;                  // a wait gave up: go through the motions, compute nothing
-  int left = n_tiles, st = 0, merges = 0;
+  int st = 0, merges = 0;
   uint32_t phase = 0;
   bool first = true;                  // the CTA's first unit
   float* merge = reinterpret_cast<float*>(sm + L::kMerge + row_slice * L::kMergeBytes);
-  float* stat = reinterpret_cast<float*>(sm + L::kStat) + row_slice * 2 * kSlices * 16;
+  float* stat = reinterpret_cast<float*>(sm + L::kStat + row_slice * L::kStatBytes);
   uint32_t qf[NT][kSteps][2];
   float mul[NT][2];
   load_q<D, E4M3, NT>(p, w, row_slice, qf, mul);
@@ -562,14 +570,12 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         phase ^= 1;
       }
     }
-    left -= t_end - t_begin;
+    left -= t_end - t_begin + (t_end == w.n ? p.unit_cost : 0);
 
     // ---- end of the unit (or of this CTA's part of it): the four warps' results become one, while
     // the next unit's query rows are on their way
     const bool whole = t_begin == 0 && t_end == w.n;
     const int len = w.len;
-    if (whole && p.by_unit && tid == 0)
-      p.joins[(w.s * p.H_kv + w.h) * p.n_rg + w.rg] = make_int4(0, 0, 0, 0);
     const int part = 2 * cta + (first ? 0 : 1);
     first = false;
     const int row0 = w.rg * p.rg_rows, rows = min(p.rg_rows, p.group - row0);
@@ -578,76 +584,98 @@ paged_kernel(const __grid_constant__ PagedParams p) {
       next_unit(p, w);
       load_q<D, E4M3, NT>(p, w, row_slice, qf, mul);
     }
+    // element (row, column) of this lane's j-th accumulator of tile k
+    auto cell = [&](int k, int j) {
+      const int row = 2 * q4 + (j & 1);
+      const int col = E4M3 ? 16 * k + 2 * g + (j >> 1) : 16 * k + g + 8 * (j >> 1);
+      return row * L::kMergeLd + col;
+    };
     #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float* st2 = stat + (merges & 1) * kSlices * 16;
+    for (int n0 = 0; n0 < NT; n0 += L::kMergeNt) {
+      float* st2 = stat + (merges & 1) * (L::kMergeNt * kSlices * 16);
       ++merges;
       #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        #pragma unroll
-        for (int off = 4; off < 32; off <<= 1)
-          l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], off);
-      float m[2];
-      #pragma unroll
-      for (int j = 0; j < 2; ++j) m[j] = above[nt][j] == -INFINITY ? -INFINITY : -nm[nt][j];
-      if (g == 0) {
+      for (int i = 0; i < L::kMergeNt; ++i) {
+        const int nt = n0 + i;
         #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          st2[(slice * 8 + 2 * q4 + j) * 2] = m[j];
-          st2[(slice * 8 + 2 * q4 + j) * 2 + 1] = l[nt][j];
+          #pragma unroll
+          for (int off = 4; off < 32; off <<= 1)
+            l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], off);
+          if (g == 0)
+            *reinterpret_cast<float2*>(st2 + ((i * kSlices + slice) * 8 + 2 * q4 + j) * 2) = make_float2(
+                above[nt][j] == -INFINITY ? -INFINITY : -nm[nt][j], l[nt][j]);
         }
       }
       named_barrier_sync(1 + row_slice, kSlices * 32);
       #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float top = -INFINITY;
+      for (int i = 0; i < L::kMergeNt; ++i) {
+        const int nt = n0 + i;
         #pragma unroll
-        for (int x = 0; x < kSlices; ++x) top = fmaxf(top, st2[(x * 8 + 2 * q4 + j) * 2]);
-        // m = -inf: no finite score, so acc and l are 0 (or NaN, which stays)
-        const float c = (m[j] == -INFINITY ? 1.f : ex2_approx(m[j] - top)) *
-                        (E4M3 ? vref : 1.f);
-        #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          acc[nt][k][j] *= c;
-          acc[nt][k][j + 2] *= c;
+        for (int j = 0; j < 2; ++j) {
+          float top = -INFINITY;
+          #pragma unroll
+          for (int x = 0; x < kSlices; ++x)
+            top = fmaxf(top, st2[((i * kSlices + x) * 8 + 2 * q4 + j) * 2]);
+          // no m: no finite score, so acc and l are 0 (or NaN, which stays)
+          const float c = (above[nt][j] == -INFINITY ? 1.f : ex2_approx(-nm[nt][j] - top)) *
+                          (E4M3 ? vref : 1.f);
+          #pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            acc[nt][k][j] *= c;
+            acc[nt][k][j + 2] *= c;
+          }
+        }
+        // slices 0 and 2 share a buffer, 1 and 3 the other: each writes the half of the columns
+        // that its partner then adds its own to
+        float* half = merge + (2 * i + (slice & 1)) * 8 * L::kMergeLd;
+        if (slice >= 2) {
+          #pragma unroll
+          for (int k = 0; k < kSteps / 2; ++k)
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) half[cell(k, j)] = acc[nt][k][j];
+        } else {
+          #pragma unroll
+          for (int k = kSteps / 2; k < kSteps; ++k)
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) half[cell(k, j)] = acc[nt][k][j];
         }
       }
-      // element (row, column) of this lane's j-th accumulator of tile k
-      auto cell = [&](int k, int j) {
-        const int row = 2 * q4 + (j & 1);
-        const int col = E4M3 ? 16 * k + 2 * g + (j >> 1) : 16 * k + g + 8 * (j >> 1);
-        return row * L::kMergeLd + col;
-      };
-      float* mine = merge + (slice & 1) * 8 * L::kMergeLd;
-      if (slice >= 2) {
-        #pragma unroll
-        for (int k = 0; k < kSteps; ++k)
+      named_barrier_sync(1 + row_slice, kSlices * 32);
+      #pragma unroll
+      for (int i = 0; i < L::kMergeNt; ++i) {
+        const int nt = n0 + i;
+        float* half = merge + (2 * i + (slice & 1)) * 8 * L::kMergeLd;
+        if (slice < 2) {
           #pragma unroll
-          for (int j = 0; j < 4; ++j) mine[cell(k, j)] = acc[nt][k][j];
+          for (int k = 0; k < kSteps / 2; ++k)
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) half[cell(k, j)] += acc[nt][k][j];
+        } else {
+          #pragma unroll
+          for (int k = kSteps / 2; k < kSteps; ++k)
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) half[cell(k, j)] += acc[nt][k][j];
+        }
       }
       named_barrier_sync(1 + row_slice, kSlices * 32);
-      if (slice < 2) {
-        #pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-          #pragma unroll
-          for (int j = 0; j < 4; ++j) mine[cell(k, j)] += acc[nt][k][j];
-      }
-      named_barrier_sync(1 + row_slice, kSlices * 32);
-      for (int e = slice * 32 + lane; e < 8 * (D / 4); e += kSlices * 32) {
-        const int r = e / (D / 4), c4 = e % (D / 4);
-        const int row = (row_slice * NT + nt) * 8 + r;
+      for (int e = slice * 32 + lane; e < L::kMergeNt * 8 * (D / 4); e += kSlices * 32) {
+        const int r = e / (D / 4), c4 = e % (D / 4), i = r / 8;
+        const int row = (row_slice * NT + n0) * 8 + r;
         if (row >= rows) continue;
         float top = -INFINITY, sum = 0.f;
-        #pragma unroll
-        for (int x = 0; x < kSlices; ++x) top = fmaxf(top, st2[(x * 8 + r) * 2]);
+        float2 ml[kSlices];
         #pragma unroll
         for (int x = 0; x < kSlices; ++x) {
-          const float mx = st2[(x * 8 + r) * 2];
-          sum += (mx == -INFINITY ? 1.f : ex2_approx(mx - top)) * st2[(x * 8 + r) * 2 + 1];
+          ml[x] = *reinterpret_cast<const float2*>(st2 + ((i * kSlices + x) * 8 + (r & 7)) * 2);
+          top = fmaxf(top, ml[x].x);
         }
-        const float4 a = *reinterpret_cast<const float4*>(merge + r * L::kMergeLd + 4 * c4);
-        const float4 b =
-            *reinterpret_cast<const float4*>(merge + (8 + r) * L::kMergeLd + 4 * c4);
+        #pragma unroll
+        for (int x = 0; x < kSlices; ++x)
+          sum += (ml[x].x == -INFINITY ? 1.f : ex2_approx(ml[x].x - top)) * ml[x].y;
+        const float* at0 = merge + (2 * i * 8 + (r & 7)) * L::kMergeLd + 4 * c4;
+        const float4 a = *reinterpret_cast<const float4*>(at0);
+        const float4 b = *reinterpret_cast<const float4*>(at0 + 8 * L::kMergeLd);
         float4 v = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
         if (whole) {
           const float inv = len > 0 ? 1.f / sum : 0.f;
@@ -668,26 +696,53 @@ paged_kernel(const __grid_constant__ PagedParams p) {
   }
 }
 
-// Merge of one unit's parts, as the CTA that ended it described them (joins[blockIdx.x]: parts, unit, the
-// CTA that began it and which of its two parts that is): that part, then the
-// first of each CTA that follows.  M = max m_j, weights 2^(m_j - M).  A row's parts are shared
-// out to 1, 2, 4 or 8 of the block's warps, by how many there are, and joined through shared
-// memory; a lane holds d/32 columns.  Latency bounds it (three dependent reads), so many rows go side by
-// side: 32 rows of 2 or 3 parts each, four rows one after another in a block, took 8 us.
-constexpr int kJoinWarps = 8, kAtOnce = 8;
+// Merge of one unit's parts: of the CTA that holds its first tile, then the first part of each that
+// follows, to the one that holds its last.  Block x is for unit x, or, when there are more units than
+// CTAs, for the unit that CTA x ends and an earlier one began.  M = max m_j, weights 2^(m_j - M).
+// A row's parts are shared out to 1, 2, 4 or 8 of the block's warps, by how many there are, and joined
+// through shared memory; a lane holds d/32 columns.  Latency bounds it, so who holds what is worked out
+// before the wait, many rows go side by side (32 rows of 2 or 3 parts each, four rows one after another
+// in a block, took 8 us), and the blocks are few and light enough to be there when the parts are.
+constexpr int kJoinWarps = 8, kAtOnce = 4;
+__host__ __device__ constexpr int join_share(int parts) {  // warps of a row
+  return parts <= kAtOnce ? 1 : parts <= 2 * kAtOnce ? 2 : parts <= 4 * kAtOnce ? 4 : 8;
+}
 
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __grid_constant__ PagedParams p) {
   constexpr int kPer = D / 32;
   __shared__ float s_o[kJoinWarps][D];
   __shared__ float2 s_ml[kJoinWarps];
-  pdl_wait();
-  const int4 join = p.joins[blockIdx.x];
-  if (join.x == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = join.x, i0 = join.z, rg = join.y % p.n_rg, sh = join.y / p.n_rg;
+  // (the lengths were complete before the first kernel began, and it let this one start only then)
+  const int total = all_places(p), G = min(p.ctas, total), x = static_cast<int>(blockIdx.x);
+  const Shares shares(static_cast<uint32_t>(total), static_cast<uint32_t>(G));
+  int unit, unit0, tiles;  // its number, first place and tiles
+  bool mine = true;
+  if (p.by_unit) {
+    const int per = p.H_kv * p.n_rg, s = x / per;
+    int before = 0;
+    for (int r = lane; r < s; r += 32) before += req_places(p, r);
+    const int places = req_places(p, s);
+    unit = x;
+    unit0 = __reduce_add_sync(0xffffffffu, before) * per + (x - s * per) * places;
+    tiles = places - p.unit_cost;
+  } else {
+    Walk w;
+    mine = x < G;
+    unit0 = find(p, mine ? shares.start(x) : 0, w);
+    unit = (w.s * p.H_kv + w.h) * p.n_rg + w.rg;
+    tiles = w.n;
+    mine = mine && w.t > 0 && w.t < w.n && shares.owner(unit0 + tiles - 1) == x;
+  }
+  const int i0 = shares.owner(unit0), n = shares.owner(unit0 + tiles - 1) - i0 + 1;
+  // the beginning CTA's second part, if it holds tiles of the unit before
+  const int second = shares.start(i0) < unit0 - p.unit_cost ? 1 : 0;
+  pdl_wait();  // by every block, so that the work after this one waits for the parts' kernel too
+  if (!mine || n == 1) return;
+  const int rg = unit % p.n_rg, sh = unit / p.n_rg;
   const int row0 = rg * p.rg_rows, rows = min(p.rg_rows, p.group - row0);
-  const int share = n <= kAtOnce ? 1 : n <= 2 * kAtOnce ? 2 : n <= 4 * kAtOnce ? 4 : 8;  // warps of a row
+  const int share = join_share(n);
   const int side = kJoinWarps / share, sub = warp % share;
   for (int r0 = blockIdx.y * side; r0 < rows; r0 += gridDim.y * side) {
     const int row = r0 + warp / share;
@@ -707,7 +762,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
           for (int c = 0; c < kPer; ++c) x[u][c] = 0.f;
           if (j < n) {
             const int64_t at =
-                static_cast<int64_t>(2 * (i0 + j) + (j == 0 ? join.w : 0)) * p.rg_rows + row;
+                static_cast<int64_t>(2 * (i0 + j) + (j == 0 ? second : 0)) * p.rg_rows + row;
             ml[u] = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
             const float* src = p.part_o + at * D + lane * kPer;
             if constexpr (kPer == 4)
@@ -789,18 +844,19 @@ cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
   const int most = L::kCtas * 152;
   static_assert(L::kCtas * 152 <= kPagedMaxCtas, "the workspace holds the parts of fewer CTAs");
   if (ctas > most) ctas = most;
-  // one join a unit where there are no more units than CTAs, with a block for each row while that is
-  // no more than a few blocks an SM; else one a CTA
+  // one join a unit where there are no more units than CTAs, else one a CTA
   const long long units = static_cast<long long>(p.B) * p.H_kv * p.n_rg;
   PagedParams q = p;
+  q.ctas = ctas;
+  q.unit_cost = NT * RW == 4 ? 2 : 1;
   q.by_unit = units <= ctas;
   const int joins = q.by_unit ? static_cast<int>(units) : ctas;
-  const int side = q.by_unit && units < 128 ? 1024 / joins : 8;
+  // blocks of a join: as many as its rows keep busy at the mean number of parts
+  const int blocks = (p.rg_rows * join_share(ctas / joins + 2) + kJoinWarps - 1) / kJoinWarps;
   e = launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), L::kThreads, L::kDyn, stream, q);
   if (e != cudaSuccess) return e;
   return launch_dependent(paged_join_kernel<D>,
-                          dim3(static_cast<unsigned>(joins),
-                               static_cast<unsigned>(p.rg_rows < side ? p.rg_rows : side)),
+                          dim3(static_cast<unsigned>(joins), static_cast<unsigned>(blocks)),
                           kJoinWarps * 32, 0, stream, q);
 }
 

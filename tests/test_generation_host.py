@@ -66,8 +66,8 @@ def test_cache_checks(lib, kw, code):
 
 def test_paged_workspace(lib):
     f = lib.attn_fwd_paged_workspace_bytes
-    def need(rows, d):  # partial outputs, maxima and sums, descriptions of joins, each up to 256 bytes
-        return sum(-(-n // 256) * 256 for n in (2 * 608 * rows * d * 4, 2 * 608 * rows * 8, 608 * 16))
+    def need(rows, d):  # partial outputs, maxima and sums, each up to 256 bytes
+        return sum(-(-n // 256) * 256 for n in (2 * 608 * rows * d * 4, 2 * 608 * rows * 8))
 
     assert f(2, 8, 2, 128) == need(4, 128)
     assert f(1, 40, 1, 64) == need(20, 64)  # two groups of 20 rows
