@@ -91,7 +91,7 @@ def _link_binding(obj: str):
     tlib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + ".tmp"
     _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", PKG, "-l:libattn_gb300.so",
-          "-L", tlib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+          "-L", tlib, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda",
           "-Wl,-rpath,$ORIGIN"], "linking the binding")
     os.replace(tmp, BINDING)
 

@@ -8,7 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -64,7 +64,7 @@ void* address(const at::Tensor& t, at::ScalarType type, at::IntArrayRef shape, a
 }
 
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+  return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
 
 PyObject* wrap(const at::Tensor& t) {
