@@ -9,9 +9,9 @@
 // element i turns with i + rot/2, any two when 2i turns with 2i + 1.  The mean of squares is then
 // the only value that crosses lanes.  A warp-wide load covers 4 rows (d = 128) or 8 (d = 64).
 //
-// A warp takes a token (or, when there are few tokens, a share of a token's rows) and works alone: it
-// puts the token's coefficients into its own shared memory, 64 pairs of them at d = 128, two a lane,
-// and streams the token's heads through them, loads a batch ahead.  In the forward the norm's
+// A warp takes a token, or two and more share a token's rows; they put the token's coefficients into
+// shared memory, 64 pairs of them at d = 128, and each streams its heads through them, loads a batch
+// ahead, without another wait for the others.  In the forward the norm's
 // weight is folded in: with r the inverse root mean square,
 //   (y_a, y_b) = r (x_a, x_b) * (w_a c, w_b c) + r (x_b, x_a) * (-w_b s, w_a s),
 // three packed operations on two values each.
@@ -177,12 +177,13 @@ __global__ void __launch_bounds__(kRopeThreads, CACHE == kCacheE4m3 ? 2 : 3) qkv
   constexpr int kLanes = D / 16, kRw = 32 / kLanes;
   // per warp and kind (query, key): of pairs 2m, 2m + 1 of lane l, at m * kLanes + l,
   // (w_a c, w_a c, w_b c, w_b c) and (-w_b s, -w_b s, w_a s, w_a s)
-  __shared__ float4 s_coef[kWarps][2][2][D / 4];
+  __shared__ float4 s_coef[kWarps][2][2][D / 4];  // by the first warp of those that share a token
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % kLanes, sub = lane / kLanes;
   const int task = blockIdx.x * kWarps + warp, t = task / p.parts, part = task - t * p.parts;
+  const int team = min(p.parts, kWarps), leader = warp / team * team;  // this token's warps in the CTA
   pdl_wait();
-  if (t >= p.tokens) return;
+  if (t >= p.tokens) return;  // a whole team: parts is a power of two
   const L ln(l, p.rot);
   const int heads = p.H + 2 * p.H_kv, groups = (heads + kRw - 1) / kRw;
   const int b = t / p.N, n = t - b * p.N;
@@ -203,8 +204,7 @@ __global__ void __launch_bounds__(kRopeThreads, CACHE == kCacheE4m3 ? 2 : 3) qkv
   load(part);
   {
     const int position = p.rot ? p.positions[t] : 0;
-    #pragma unroll
-    for (int j = lane; j < D / 2; j += 32) {
+    for (int j = (warp - leader) * 32 + lane; j < D / 2; j += 32 * team) {
       const int i = j / kLanes;
       const L o(j % kLanes, p.rot);
       float c = 1.f, s = 0.f;
@@ -215,15 +215,16 @@ __global__ void __launch_bounds__(kRopeThreads, CACHE == kCacheE4m3 ? 2 : 3) qkv
         const float wa = w ? __bfloat162float(w[o.first(i)]) : 1.f;
         const float wb = w ? __bfloat162float(w[o.second(i)]) : 1.f;
         const int at = (i >> 1) * kLanes + j % kLanes;
-        float* cc = reinterpret_cast<float*>(&s_coef[warp][k][0][at]) + (i & 1);
-        float* cs = reinterpret_cast<float*>(&s_coef[warp][k][1][at]) + (i & 1);
+        float* cc = reinterpret_cast<float*>(&s_coef[leader][k][0][at]) + (i & 1);
+        float* cs = reinterpret_cast<float*>(&s_coef[leader][k][1][at]) + (i & 1);
         cc[0] = wa * c;
         cc[2] = wb * c;
         cs[0] = -(wb * s);
         cs[2] = wa * s;
       }
     }
-    __syncwarp();
+    if (team == 1) __syncwarp();
+    else named_barrier_sync(1 + leader / team, team * 32);
   }
   const int64_t step = static_cast<int64_t>(p.N) * D;
   const int64_t tq = (static_cast<int64_t>(b) * p.H * p.N + n) * D;
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(kRopeThreads, CACHE == kCacheE4m3 ? 2 : 3) qkv
           }
         }
         if (!is_v) {
-          const float4* cc = &s_coef[warp][is_q ? 0 : 1][0][l];
+          const float4* cc = &s_coef[leader][is_q ? 0 : 1][0][l];
           #pragma unroll
           for (int i = 0; i < 8; i += 2) {
             const float4 c = cc[(i >> 1) * kLanes];
@@ -317,8 +318,8 @@ __global__ void __launch_bounds__(kRopeThreads, CACHE == kCacheE4m3 ? 2 : 3) qkv
   }
 }
 
-// Gradients of the rows, and each CTA's share of the weights' gradients.  With t = x r, g the
-// gradient turned back and u = g w:  dx = r (u - t mean(u t)),  dw += g t.
+// Gradients of the rows, and each CTA's share of the weights' gradients.  With h = r g, g the gradient
+// turned back, and u = h w:  dx = u - x r^2 mean(u x),  dw += h x.
 // A warp walks (token, share of its groups) tasks.  Its rows come through a ring in shared memory, each
 // lane copying and reading its own chunks, so that kDepth - 1 groups are in flight without holding
 // registers, across tokens too (two groups in registers, per token: 69 us where this takes less;
@@ -455,11 +456,12 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
             vb = in[96];
           }
           L::unpack(va, vb, xa, xb);
-          const float r = rsqrtf(row_sum<D>(sum_squares(xa, xb)) * (1.f / D) + p.eps);
+          float r = rsqrtf(row_sum<D>(sum_squares(xa, xb)) * (1.f / D) + p.eps);
+          r = normed ? r : 1.f;
           #pragma unroll
           for (int i = 0; i < 8; i += 2) {
-            fmul2(xa[i], xa[i + 1], xa[i], xa[i + 1], r, r);
-            fmul2(xb[i], xb[i + 1], xb[i], xb[i + 1], r, r);
+            fmul2(fa[i], fa[i + 1], fa[i], fa[i + 1], r, r);
+            fmul2(fb[i], fb[i + 1], fb[i], fb[i + 1], r, r);
           }
           if (g * kRw + kRw <= p.H) {
             #pragma unroll
@@ -491,14 +493,12 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
               ffma2(d0, d1, fb[i], fb[i + 1], xb[i], xb[i + 1], d0, d1);
             }
           }
-          const float mean = row_sum<D>(d0 + d1) * (-1.f / D);
+          const float back = row_sum<D>(d0 + d1) * (-1.f / D) * (r * r);
           if (normed) {
             #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-              ffma2(fa[i], fa[i + 1], xa[i], xa[i + 1], mean, mean, fa[i], fa[i + 1]);
-              ffma2(fb[i], fb[i + 1], xb[i], xb[i + 1], mean, mean, fb[i], fb[i + 1]);
-              fmul2(fa[i], fa[i + 1], fa[i], fa[i + 1], r, r);
-              fmul2(fb[i], fb[i + 1], fb[i], fb[i + 1], r, r);
+              ffma2(fa[i], fa[i + 1], xa[i], xa[i + 1], back, back, fa[i], fa[i + 1]);
+              ffma2(fb[i], fb[i + 1], xb[i], xb[i + 1], back, back, fb[i], fb[i + 1]);
             }
           }
         }
@@ -541,24 +541,40 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
   }
 }
 
-// dwq (block 0) and dwk (block 1): the CTAs' shares, runs of CTAs summed side by side, then joined
-// in order.
+// dwq (block 0) and dwk (block 1): the CTAs' shares, in runs of every 32nd or 64th CTA summed side by
+// side (four columns a thread, ten loads in flight at most), then joined in order.
+template <int D>
 __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__ partial, int ctas,
-                                                       int d, float* dwq, float* dwk) {
-  __shared__ float s_sum[1024];
+                                                       float* dwq, float* dwk) {
+  constexpr int kRuns = 1024 / (D / 4), kLoads = (kRopeBwdCtas + kRuns - 1) / kRuns;
+  __shared__ float4 s_sum[kRuns][D / 4];
   float* out = blockIdx.x ? dwk : dwq;
+  const int c4 = threadIdx.x % (D / 4), run = threadIdx.x / (D / 4);
   pdl_wait();
   if (!out) return;
-  const int runs = 1024 / d, c = threadIdx.x % d, run = threadIdx.x / d;
-  float v = 0.f;
-  #pragma unroll 8
-  for (int i = run; i < ctas; i += runs)
-    v += partial[(static_cast<size_t>(i) * 2 + blockIdx.x) * d + c];
-  s_sum[threadIdx.x] = v;
+  float4 x[kLoads];
+  #pragma unroll
+  for (int k = 0; k < kLoads; ++k) {
+    const int i = run + k * kRuns;
+    x[k] = i < ctas ? reinterpret_cast<const float4*>(partial)[(static_cast<size_t>(i) * 2 + blockIdx.x) * (D / 4) + c4]
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  float4 v = x[0];
+  #pragma unroll
+  for (int k = 1; k < kLoads; ++k) {
+    v.x += x[k].x;
+    v.y += x[k].y;
+    v.z += x[k].z;
+    v.w += x[k].w;
+  }
+  s_sum[run][c4] = v;
   __syncthreads();
-  if (run == 0) {
-    for (int i = 1; i < runs; ++i) v += s_sum[i * d + c];
-    out[c] = v;
+  if (threadIdx.x < D) {
+    const float* column = reinterpret_cast<const float*>(s_sum) + threadIdx.x;
+    float sum = 0.f;
+    #pragma unroll 16
+    for (int i = 0; i < kRuns; ++i) sum += column[i * D];
+    out[threadIdx.x] = sum;
   }
 }
 
@@ -572,13 +588,14 @@ cudaError_t launch_fwd(const RopeParams& p, int kind, int ctas, cudaStream_t st)
   return launch_dependent(qkv_rope_kernel<D, INTER, kCacheE4m3>, grid, kRopeThreads, 0, st, p);
 }
 
-// Warps that share a token: the count of 1, 2, 4 .. 32 that minimises rounds of `resident` warps times
-// a warp's work in groups of rows, its own share and `fixed` for the token's angles (the smaller on
-// ties).  Many tokens: few, so that the angles are not computed again; few tokens: as many as have rows.
-int parts_of(int tokens, int groups, int resident, int fixed) {
+// Warps that share a token: the count up to 32 (a power of two where they work as a team) that minimises
+// rounds of `resident` warps times a warp's work in groups of rows, its own share and `fixed` for the
+// token's angles (the smaller on ties).  Many tokens: few, so that the angles are not computed again;
+// few tokens: as many as have rows.
+int parts_of(int tokens, int groups, int resident, int fixed, bool team) {
   int best = 1;
   int64_t best_cost = -1;
-  for (int parts = 1; parts <= 32 && parts < 2 * groups; parts *= 2) {
+  for (int parts = 1; parts <= 32 && parts < 2 * groups; parts += team ? parts : 1) {
     const int64_t rounds = (static_cast<int64_t>(tokens) * parts + resident - 1) / resident;
     const int64_t cost = rounds * ((groups + parts - 1) / parts + fixed);
     if (best_cost < 0 || cost < best_cost) {
@@ -597,7 +614,7 @@ int groups_of(const RopeParams& p, int d) {
 
 cudaError_t launch_qkv_rope(RopeParams& p, int d, bool interleaved, int kind, cudaStream_t st) {
   // three CTAs an SM; the angles and coefficients of a token take about as long as two groups
-  p.parts = parts_of(p.tokens, groups_of(p, d), 3 * 152 * kWarps, 2);
+  p.parts = parts_of(p.tokens, groups_of(p, d), 3 * 152 * kWarps, 2, true);
   const int ctas = static_cast<int>((static_cast<int64_t>(p.tokens) * p.parts + kWarps - 1) / kWarps);
   if (d == 64)
     return interleaved ? launch_fwd<64, true>(p, kind, ctas, st)
@@ -625,14 +642,15 @@ cudaError_t launch_bwd(const RopeParams& p, int ctas, cudaStream_t st) {
   e = launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), kRopeThreads, kSmem, st, p);
   if (e != cudaSuccess || !p.partial) return e;
   // the sums of the CTAs' shares: set up while the rows' kernel still runs
-  return launch_dependent(rope_dw_kernel, dim3(2), 1024, 0, st, p.partial, ctas, D, p.dwq, p.dwk);
+  return launch_dependent(rope_dw_kernel<D>, dim3(2), 1024, 0, st,
+                          static_cast<const float*>(p.partial), ctas, p.dwq, p.dwk);
 }
 
 }  // namespace
 
 cudaError_t launch_qkv_rope_bwd(RopeParams& p, int d, bool interleaved, cudaStream_t st) {
   // the angles of a token take about as long as one group
-  p.parts = parts_of(p.tokens, groups_of(p, d), kRopeBwdCtas * kWarps, 1);
+  p.parts = parts_of(p.tokens, groups_of(p, d), kRopeBwdCtas * kWarps, 1, false);
   const int64_t want = (static_cast<int64_t>(p.tokens) * p.parts + kWarps - 1) / kWarps;
   const int ctas = static_cast<int>(want < kRopeBwdCtas ? want : kRopeBwdCtas);
   if (d == 64) return interleaved ? launch_bwd<64, true>(p, ctas, st) : launch_bwd<64, false>(p, ctas, st);
