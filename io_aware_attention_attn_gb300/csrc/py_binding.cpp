@@ -67,6 +67,16 @@ at::Tensor make(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
   return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
 
+// A contiguous tensor over part of `whole`'s memory, `at` bytes in (a multiple of the type's size): one
+// allocation for a call's small outputs, each 0.8 us of host time by itself.
+at::Tensor carve(const at::Tensor& whole, int64_t at, at::IntArrayRef shape, at::ScalarType type) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+      c10::Storage(whole.storage()), whole.key_set(), c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_storage_offset(at / static_cast<int64_t>(c10::elementSize(type)));
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+
 PyObject* wrap(const at::Tensor& t) {
   if (t.defined()) return THPVariable_Wrap(t);
   Py_RETURN_NONE;
@@ -168,8 +178,11 @@ PyObject* py_slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto* fp = static_cast<const int32_t*>(address(free, at::kInt, {spare}, dev, "free_pages"));
   const auto* hp = static_cast<const int32_t*>(address(head, at::kInt, {1}, dev, "free_head"));
   Launch on(dev);
-  at::Tensor slots = make({T}, at::kLong, dev), pos = make({T}, at::kInt, dev);
-  at::Tensor lens_out = make({B}, at::kInt, dev), head_out = make({1}, at::kInt, dev);
+  const int64_t t = T;
+  const at::Tensor all = make({12 * t + 4 * B + 4}, at::kByte, dev);
+  at::Tensor slots = carve(all, 0, {t}, at::kLong), pos = carve(all, 8 * t, {t}, at::kInt);
+  at::Tensor lens_out = carve(all, 12 * t, {B}, at::kInt);
+  at::Tensor head_out = carve(all, 12 * t + 4 * B, {1}, at::kInt);
   if (B == 0) head_out.copy_(head);
   check("attn_kv_slots",
         attn_kv_slots(lp, cp, tp, fp, hp, static_cast<int64_t*>(slots.data_ptr()),
@@ -290,10 +303,10 @@ PyObject* py_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (r.wq || r.wk) {
     const size_t need = attn_qkv_rope_bwd_workspace_bytes(B, N, r.H, r.H_kv, d);
     if (!ws.defined() && need) ws = make({static_cast<int64_t>(need)}, at::kByte, r.dev);
+    const at::Tensor both = r.B * r.N ? make({2 * r.d}, at::kFloat, r.dev)
+                                      : at::zeros({2 * r.d}, at::TensorOptions().dtype(at::kFloat).device(r.dev));
     for (int i = 0; i < 2; ++i)
-      if (i ? r.wk : r.wq)
-        dw[i] = r.B * r.N ? make({r.d}, at::kFloat, r.dev)
-                          : at::zeros({r.d}, at::TensorOptions().dtype(at::kFloat).device(r.dev));
+      if (i ? r.wk : r.wq) dw[i] = carve(both, 4 * i * r.d, {r.d}, at::kFloat);
   }
   auto ptr = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
   check("attn_qkv_rope_bwd",
