@@ -307,9 +307,8 @@ ATTN_API int attn_kv_slots(const int32_t* seq_lens, const int32_t* cu_new, int32
  *   cache     : NULL, or the cache that token t's K and V rows go into at slots[t] (int64 [B, N];
  *               negative: not stored).  E4M3 rows: scale = amax / 448 (1 if that is below fp32's
  *               normal range, as for a zero row), code = E4M3 round-to-nearest-even of the fp32
- *               y / scale.  A slot past the cache is not stored and the status word reports kind 5;
- *               two tokens with one slot leave either's row there, never part of both within 16
- *               bytes.
+ *               y / scale.  A slot past the cache is not stored and the status word reports kind 5.
+ *               What two tokens with one slot leave there is unspecified.
  * Norm and rotation are fp32, rounded once on the way out.  Outputs must not overlap qkv.
  * One launch.  Tensors 16-byte aligned (inv_freq and slots 8, positions 4).  Returns an attn_status
  * (rot, ld, eps, rope_scale out of range: ATTN_ERR_SHAPE for sizes, ATTN_ERR_SCALE for the floats).

@@ -457,7 +457,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
               vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, off));
             vscale = vm > 0.f ? vref / vm : 1.f;
             vref = vm;
-            vinv = vm > 0.f ? 1.f / vm : 0.f;
+            vinv = vm >= 0x1p-126f ? 1.f / vm : 0.f;  // below: its values are below fp32's range too
           }
           #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {

@@ -381,6 +381,9 @@ PAGED = [
     ([20000], 2, 1, 128, 64, 1.0),                # one unit over every CTA
     ([17] * 70, 8, 2, 64, 16, 1.0),               # more requests than a warp looks at together
     ([(37 * i) % 300 for i in range(150)], 4, 4, 64, 16, 1.0),
+    ([(61 * i) % 200 for i in range(320)], 4, 4, 128, 16, 1.0),   # more units than CTAs
+    ([3000, 2500] + [5] * 280 + [700], 20, 2, 64, 32, 1.0),       # long and short, two row slices
+    ([1500] + [0] * 40 + [900], 64, 2, 128, 64, 1.0),             # empty requests between, 32 rows
 ]
 
 
@@ -465,6 +468,31 @@ def test_paged_lengths_past_the_table_are_clamped():
     assert (o[0] == 0).all() and torch.isneginf(lse[0]).all()
     o, lse = attn.attn_fwd_paged(q, cache, table[:, :0].contiguous(), n)
     assert (o == 0).all() and torch.isneginf(lse).all()
+
+
+def test_paged_outputs_given_codes_as_bytes_and_one_page_of_any_stride():
+    q, cache, table, n, vals = paged_inputs(31, [9, 16], 6, 3, 64, 16, "e4m3")
+    out, lse = torch.full_like(q, 7.0), torch.full((2, 6, 1), 7.0, device="cuda")
+    raw = attn.KVCache(cache.k.view(torch.uint8), cache.v.view(torch.uint8), *cache[2:])
+    got = attn.attn_fwd_paged(q, raw, table, n, out=out, lse=lse)
+    assert got[0].data_ptr() == out.data_ptr() and got[1].data_ptr() == lse.data_ptr()
+    check_paged(out, lse, q, vals, table, [9, 16], 1 / 8, "e4m3", "paged outputs given")
+    q, cache, table, n, vals = paged_inputs(32, [16], 2, 1, 64, 16, "bf16", spare=0)
+    o, lse = attn.attn_fwd_paged(q, cache, table, n)
+    check_paged(o, lse, q, vals, table, [16], 1 / 8, "bf16", "paged one page")
+
+
+def test_rope_without_tokens():
+    f = attn.rope_inv_freq(64)
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    for shape, lead in (((0, 4 * 64), ()), ((2, 0, 4 * 64), (2,)), ((0, 3, 4 * 64), (0,))):
+        qkv = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+        pos = torch.empty(shape[:-1], dtype=torch.int32, device="cuda")
+        q, k, v = attn.qkv_rope(qkv, 2, 1, pos, f, wq=w, wk=w)
+        T = shape[-2]
+        assert q.shape == (*lead, 2, T, 64) and k.shape == v.shape == (*lead, 1, T, 64)
+        dx, dwq, dwk = attn.qkv_rope_bwd(q, k, v, qkv, pos, f, wq=w, wk=w)
+        assert dx.shape == qkv.shape and (dwq == 0).all() and (dwk == 0).all()
 
 
 def test_paged_workspace_stays_inside():
