@@ -76,6 +76,7 @@ cudaError_t launch_qkv_rope_bwd(RopeParams& p, int d, bool interleaved, cudaStre
 // -------------------------------------------------------------------- attention over a paged cache
 constexpr int kPagedTile = 64;         // keys of a tile
 constexpr int kPagedMaxCtas = 608;     // 4 on each of 152 SMs
+constexpr int kPagedMaxCost = 2;       // places that a unit takes beside its tiles, at most
 constexpr float kPagedTrail = 8.f;     // the same in log2 units
 constexpr int kPagedMaxRows = 32;      // query rows (heads of one K/V head) of a unit
 

@@ -211,8 +211,8 @@ extern "C" int attn_fwd_paged(const void* q, const attn_kv_cache* cache, const i
   if (most > INT_MAX - kPagedTile) return ATTN_ERR_SHAPE;
   const int64_t units = static_cast<int64_t>(B) * H_kv * paged_row_groups(group);
   const int64_t tiles = most > 0 ? (most + kPagedTile - 1) / kPagedTile : 1;
-  // the kernel numbers tiles, and two places more a unit, in 32 bits
-  if (static_cast<int64_t>(B) * H > INT_MAX || units > INT_MAX / (tiles + 2)) return ATTN_ERR_SHAPE;
+  // the kernel numbers tiles, and the places a unit takes beside them, in 32 bits
+  if (static_cast<int64_t>(B) * H > INT_MAX || units > INT_MAX / (tiles + kPagedMaxCost)) return ATTN_ERR_SHAPE;
   const PagedLayout L = paged_layout(group, d);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total)
     return ATTN_ERR_WORKSPACE;

@@ -49,15 +49,18 @@ struct PagedCfg {
   static constexpr int kThreads = (kWarps + 1) * 32;
   // CTAs an SM holds.  Where a tile is 32 KB two are enough for the copies to run at full rate; a
   // tile of half that or less has to be through a warp's chain of dependent steps in half the
-  // time, so three share it (e4m3, d = 128, 64-row pages: 94 us with two against DRAM's 82).
-  static constexpr int kCtas = RW * NT == 4 ? 1 : D == 64 ? 4 / RW : !E4M3 || NT == 2 ? 2 : 3;
+  // time, so three or four share it (e4m3, d = 128, 64-row pages: 94 us with two, 84 with three).
+  // Registers set the limit, by the five warps of a CTA on four sub-partitions.
+  static constexpr int kCtas = RW == 2 ? 1 : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2)
+                                                     : !E4M3 || NT == 2 ? 2 : 3;
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
   static constexpr int kBlk = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a row in one box
   static constexpr int kBlks = kRowBytes / kBlk;                  // boxes side by side
   static constexpr int kSide = kPagedTile * kRowBytes;            // K or V of a tile
   static constexpr int kStage = 2 * kSide;
   static constexpr int kMergeLd = D + 4;                          // spreads rows over the banks
-  static constexpr int kMergeNt = kCtas == 1 ? NT : 1;            // row groups merged at once
+  // row groups merged at once: all, but where that would cost the ring one of its three tiles
+  static constexpr int kMergeNt = kCtas == 2 && kStage == 32768 ? 1 : NT;
   static constexpr int kMergeBytes = kMergeNt * 2 * 8 * kMergeLd * 4;  // of one row slice
   static constexpr int kStatBytes = 2 * kMergeNt * kSlices * 8 * 2 * 4;  // likewise, of two merges
   // tiles in the ring: what shared memory holds beside the rest (each CTA's 1 KB of the system's and
@@ -848,7 +851,7 @@ cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
   const long long units = static_cast<long long>(p.B) * p.H_kv * p.n_rg;
   PagedParams q = p;
   q.ctas = ctas;
-  q.unit_cost = NT * RW == 4 ? 2 : 1;
+  q.unit_cost = NT * RW == 4 ? kPagedMaxCost : 1;
   q.by_unit = units <= ctas;
   const int joins = q.by_unit ? static_cast<int>(units) : ctas;
   // blocks of a join: as many as its rows keep busy at the mean number of parts
@@ -863,8 +866,14 @@ cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
 template <int D, bool E4M3>
 cudaError_t launch_rows(const PagedParams& p, int ctas, cudaStream_t stream) {
   if (p.rg_rows <= 8) return launch<D, E4M3, 1, 1>(p, ctas, stream);
-  if (p.rg_rows <= 16) return launch<D, E4M3, D == 64 ? 1 : 2, D == 64 ? 2 : 1>(p, ctas, stream);
-  return launch<D, E4M3, 2, 2>(p, ctas, stream);
+  if (p.rg_rows <= 16) return launch<D, E4M3, 2, 1>(p, ctas, stream);
+  // Up to 32 rows: two slices of warps, so that the accumulators fit, each reading the tile.  For codes
+  // that converts them twice, so at d = 64, where four groups of rows fit one warp, they take that
+  // (32 requests of 8192, 8 K/V heads: 117 us against 142); for bf16 the two are near (98 against
+  // 103 us) and the slices' fewer CTAs leave fewer parts to join (37 ragged requests: 17 us
+  // against 20).
+  if constexpr (D == 64 && E4M3) return launch<D, E4M3, 4, 1>(p, ctas, stream);
+  else return launch<D, E4M3, 2, 2>(p, ctas, stream);
 }
 
 }  // namespace
