@@ -26,6 +26,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 namespace attn {
 namespace {
@@ -334,6 +335,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
   __shared__ __align__(16) float s_dw[kWarps][D];     // the weights' sums, at the end
   // of pairs 2m, 2m + 1 of lane l, at m * kLanes + l: (c, c, s, s), per warp
   __shared__ float4 s_cs[kWarps][D / 4];
+  __shared__ float2 s_ns[kWarps][D / 4];              // (-s, -s), likewise
   __shared__ float4 s_w[2][D / 4];                    // (w_a, w_a, w_b, w_b), likewise
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % kLanes, sub = lane / kLanes;
@@ -360,17 +362,22 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
   auto issue = [&] {
     if (i_task < tasks) {
       const int hh = i_g * kRw + sub;
-      if (hh < heads) {
-        const bool is_q = hh < p.H, is_v = hh >= p.H + p.H_kv;
-        const int h = hh - (is_q ? 0 : is_v ? p.H + p.H_kv : p.H);
-        const uint4* src = (is_q ? i_q : is_v ? i_v : i_k) + h * (step / 8);
-        const uint32_t dst = ring32 + i_slot * (4 * 32 * 16);
+      const uint32_t dst = ring32 + i_slot * (4 * 32 * 16);
+      auto copy = [&](const uint4* src, bool normed) {
         copy16(dst, src + ln.a);
         copy16(dst + 32 * 16, src + ln.b);
-        if (is_q ? p.wq != nullptr : !is_v && p.wk != nullptr) {
+        if (normed) {
           copy16(dst + 64 * 16, i_row + hh * (D / 8) + ln.a);
           copy16(dst + 96 * 16, i_row + hh * (D / 8) + ln.b);
         }
+      };
+      if (i_g * kRw + kRw <= p.H) {
+        copy(i_q + hh * (step / 8), p.wq != nullptr);
+      } else if (hh < heads) {
+        const bool is_q = hh < p.H, is_v = hh >= p.H + p.H_kv;
+        const int h = hh - (is_q ? 0 : is_v ? p.H + p.H_kv : p.H);
+        copy((is_q ? i_q : is_v ? i_v : i_k) + h * (step / 8),
+             is_q ? p.wq != nullptr : !is_v && p.wk != nullptr);
       }
       i_slot = i_slot + 1 == kDepth ? 0 : i_slot + 1;
       if ((i_g += p.parts) >= groups) {
@@ -421,6 +428,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
       float* f = reinterpret_cast<float*>(&s_cs[warp][(i >> 1) * kLanes + j % kLanes]) + (i & 1);
       f[0] = c;
       f[2] = s;
+      reinterpret_cast<float*>(&s_ns[warp][(i >> 1) * kLanes + j % kLanes])[i & 1] = -s;
     }
     __syncwarp();
     for (int g = part; g < groups; g += p.parts) {
@@ -429,26 +437,33 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
       const uint4* in = ring + slot * (4 * 32);
       slot = slot + 1 == kDepth ? 0 : slot + 1;
       const int hh = g * kRw + sub;
-      const bool is_q = hh < p.H, is_v = hh >= p.H + p.H_kv;
       uint4 oa = in[0], ob = in[32];
-      if (g * kRw < p.H + p.H_kv) {  // not all value heads
+      // KIND: query heads, key heads, or heads of two kinds in one group
+      auto rows = [&](auto kind) {
+        constexpr int KIND = decltype(kind)::value;
+        const bool is_q = KIND == 0 || (KIND == 2 && hh < p.H);
+        const bool is_v = KIND == 2 && hh >= p.H + p.H_kv;
         float fa[8], fb[8];
         L::unpack(oa, ob, fa, fb);
-        if (!is_v) {
-          const float4* cs = &s_cs[warp][l];
+        auto back_turn = [&](int i) {
+          const float4 c = s_cs[warp][(i >> 1) * kLanes + l];
+          const float2 ns = s_ns[warp][(i >> 1) * kLanes + l];
+          float ta0, ta1, tb0, tb1;
+          fmul2(ta0, ta1, fb[i], fb[i + 1], c.z, c.w);
+          fmul2(tb0, tb1, fa[i], fa[i + 1], ns.x, ns.y);
+          ffma2(fa[i], fa[i + 1], fa[i], fa[i + 1], c.x, c.y, ta0, ta1);
+          ffma2(fb[i], fb[i + 1], fb[i], fb[i + 1], c.x, c.y, tb0, tb1);
+        };
+        if (ln.ta && !is_v) {
           #pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            if (!ln.turns(i)) continue;
-            const float4 c = cs[(i >> 1) * kLanes];
-            float ta0, ta1, tb0, tb1;
-            fmul2(ta0, ta1, fb[i], fb[i + 1], c.z, c.w);
-            fmul2(tb0, tb1, fa[i], fa[i + 1], -c.z, -c.w);
-            ffma2(fa[i], fa[i + 1], fa[i], fa[i + 1], c.x, c.y, ta0, ta1);
-            ffma2(fb[i], fb[i + 1], fb[i], fb[i + 1], c.x, c.y, tb0, tb1);
-          }
+          for (int i = 0; i < (INTER ? 4 : 8); i += 2) back_turn(i);
+        }
+        if (INTER && ln.tb && !is_v) {
+          #pragma unroll
+          for (int i = 4; i < 8; i += 2) back_turn(i);
         }
         const bool normed = is_q ? p.wq != nullptr : !is_v && p.wk != nullptr;
-        if (p.wq || p.wk) {
+        if (KIND == 2 ? p.wq != nullptr || p.wk != nullptr : normed) {
           float xa[8], xb[8];
           uint4 va = make_uint4(0u, 0u, 0u, 0u), vb = va;
           if (normed) {
@@ -463,13 +478,15 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
             fmul2(fa[i], fa[i + 1], fa[i], fa[i + 1], r, r);
             fmul2(fb[i], fb[i + 1], fb[i], fb[i + 1], r, r);
           }
-          if (g * kRw + kRw <= p.H) {
+          if constexpr (KIND < 2) {
+            float(&da)[8] = KIND == 0 ? dqa : dka;
+            float(&db)[8] = KIND == 0 ? dqb : dkb;
             #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-              ffma2(dqa[i], dqa[i + 1], fa[i], fa[i + 1], xa[i], xa[i + 1], dqa[i], dqa[i + 1]);
-              ffma2(dqb[i], dqb[i + 1], fb[i], fb[i + 1], xb[i], xb[i + 1], dqb[i], dqb[i + 1]);
+              ffma2(da[i], da[i + 1], fa[i], fa[i + 1], xa[i], xa[i + 1], da[i], da[i + 1]);
+              ffma2(db[i], db[i + 1], fb[i], fb[i + 1], xb[i], xb[i + 1], db[i], db[i + 1]);
             }
-          } else {  // key heads, or heads of two kinds
+          } else {
             #pragma unroll
             for (int i = 0; i < 8; ++i) {
               if (is_q) {
@@ -482,7 +499,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
             }
           }
           float d0 = 0.f, d1 = 0.f;
-          if (normed) {
+          if (KIND < 2 || normed) {
             const float4* wt = &s_w[is_q ? 0 : 1][l];
             #pragma unroll
             for (int i = 0; i < 8; i += 2) {
@@ -494,7 +511,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
             }
           }
           const float back = row_sum<D>(d0 + d1) * (-1.f / D) * (r * r);
-          if (normed) {
+          if (KIND < 2 || normed) {
             #pragma unroll
             for (int i = 0; i < 8; i += 2) {
               ffma2(fa[i], fa[i + 1], xa[i], xa[i + 1], back, back, fa[i], fa[i + 1]);
@@ -503,7 +520,11 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
           }
         }
         if (!is_v) L::pack(fa, fb, oa, ob);
-      }
+      };
+      const int h0 = g * kRw;
+      if (h0 + kRw <= p.H) rows(std::integral_constant<int, 0>());
+      else if (h0 >= p.H && h0 + kRw <= p.H + p.H_kv) rows(std::integral_constant<int, 1>());
+      else if (h0 < p.H + p.H_kv) rows(std::integral_constant<int, 2>());
       if (hh < heads) {
         out[hh * (D / 8) + ln.a] = oa;
         out[hh * (D / 8) + ln.b] = ob;
