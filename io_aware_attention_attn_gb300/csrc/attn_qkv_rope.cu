@@ -252,29 +252,32 @@ __global__ void __launch_bounds__(kRopeThreads, CACHE == kCacheE4m3 ? 2 : 3) qkv
       const int g = g0 + u * p.parts;
       if (g >= groups) break;
       const int hh = g * kRw + sub;
-      const bool live = hh < heads, is_q = hh < p.H, is_v = hh >= p.H + p.H_kv;
-      float xa[8], xb[8];
-      if (g * kRw < p.H + p.H_kv) {  // not all value heads
-        L::unpack(oa[u], ob[u], xa, xb);
-        const bool normed = is_q ? p.wq != nullptr : !is_v && p.wk != nullptr;
-        if (p.wq || p.wk) {
-          float r = rsqrtf(row_sum<D>(sum_squares(xa, xb)) * (1.f / D) + p.eps);
-          r = normed ? r : 1.f;
-          #pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            fmul2(xa[i], xa[i + 1], xa[i], xa[i + 1], r, r);
-            fmul2(xb[i], xb[i + 1], xb[i], xb[i + 1], r, r);
+      const bool live = hh < heads;
+      // KIND: query heads, key heads, value heads, or heads of two kinds in one group
+      auto rows = [&](auto kind) {
+        constexpr int KIND = decltype(kind)::value;
+        const bool is_q = KIND == 0 || (KIND == 3 && hh < p.H);
+        const bool is_v = KIND == 2 || (KIND == 3 && hh >= p.H + p.H_kv);
+        float xa[8], xb[8];
+        if (KIND != 2 || CACHE == kCacheE4m3) L::unpack(oa[u], ob[u], xa, xb);
+        if constexpr (KIND != 2) {
+          const bool normed = is_q ? p.wq != nullptr : !is_v && p.wk != nullptr;
+          if (KIND == 3 ? p.wq != nullptr || p.wk != nullptr : normed) {
+            float r = rsqrtf(row_sum<D>(sum_squares(xa, xb)) * (1.f / D) + p.eps);
+            if (KIND == 3) r = normed ? r : 1.f;
+            #pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              fmul2(xa[i], xa[i + 1], xa[i], xa[i + 1], r, r);
+              fmul2(xb[i], xb[i + 1], xb[i], xb[i + 1], r, r);
+            }
           }
-        }
-        if (!is_v) {
           const float4* cc = &s_coef[leader][is_q ? 0 : 1][0][l];
-          #pragma unroll
-          for (int i = 0; i < 8; i += 2) {
+          auto turn = [&](int i, bool turns) {
             const float4 c = cc[(i >> 1) * kLanes];
             float ya0, ya1, yb0, yb1;
             fmul2(ya0, ya1, xa[i], xa[i + 1], c.x, c.y);
             fmul2(yb0, yb1, xb[i], xb[i + 1], c.z, c.w);
-            if (ln.turns(i)) {
+            if (turns) {
               const float4 s = cc[D / 4 + (i >> 1) * kLanes];
               ffma2(ya0, ya1, xb[i], xb[i + 1], s.x, s.y, ya0, ya1);
               ffma2(yb0, yb1, xa[i], xa[i + 1], s.z, s.w, yb0, yb1);
@@ -283,38 +286,50 @@ __global__ void __launch_bounds__(kRopeThreads, CACHE == kCacheE4m3 ? 2 : 3) qkv
             xa[i + 1] = ya1;
             xb[i] = yb0;
             xb[i + 1] = yb1;
+          };
+          if (!is_v) {
+            if (p.rot == D) {
+              #pragma unroll
+              for (int i = 0; i < 8; i += 2) turn(i, true);
+            } else {
+              #pragma unroll
+              for (int i = 0; i < 8; i += 2) turn(i, ln.turns(i));
+            }
+            L::pack(xa, xb, oa[u], ob[u]);
           }
-          L::pack(xa, xb, oa[u], ob[u]);
         }
-      } else if (CACHE == kCacheE4m3) {
-        L::unpack(oa[u], ob[u], xa, xb);
-      }
-      const int h = hh - (is_q ? 0 : is_v ? p.H + p.H_kv : p.H);
-      __nv_bfloat16* out = is_q ? p.q : is_v ? p.v : p.k;
-      if (live && out) {
-        uint4* dst = reinterpret_cast<uint4*>(out + (is_q ? tq : tk) + h * step);
-        dst[ln.a] = oa[u];
-        dst[ln.b] = ob[u];
-      }
-      if (CACHE != kCacheNone && g * kRw + kRw > p.H) {
-        const bool write = live && !is_q && slot >= 0;
-        const int64_t at_row =
-            (static_cast<int64_t>(h) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
-        const int64_t at = page * p.page_stride + at_row * D;
-        uint8_t* base = is_v ? p.vc : p.kc;
-        if (CACHE == kCacheBf16) {
-          if (write) {
-            uint4* dst = reinterpret_cast<uint4*>(base + 2 * at);
-            dst[ln.a] = oa[u];
-            dst[ln.b] = ob[u];
+        const int h = hh - (is_q ? 0 : is_v ? p.H + p.H_kv : p.H);
+        __nv_bfloat16* out = is_q ? p.q : is_v ? p.v : p.k;
+        if (live && out) {
+          uint4* dst = reinterpret_cast<uint4*>(out + (is_q ? tq : tk) + h * step);
+          dst[ln.a] = oa[u];
+          dst[ln.b] = ob[u];
+        }
+        if constexpr (CACHE != kCacheNone && KIND != 0) {
+          const bool write = live && !is_q && slot >= 0;
+          const int64_t at_row =
+              (static_cast<int64_t>(h) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
+          const int64_t at = page * p.page_stride + at_row * D;
+          uint8_t* base = is_v ? p.vc : p.kc;
+          if constexpr (CACHE == kCacheBf16) {
+            if (write) {
+              uint4* dst = reinterpret_cast<uint4*>(base + 2 * at);
+              dst[ln.a] = oa[u];
+              dst[ln.b] = ob[u];
+            }
+          } else {
+            float* scales = is_v ? p.vs : p.ks;
+            store_codes<D, INTER>(xa, xb, base + (write ? at : 0),
+                                  scales + (write ? ((page * p.H_kv) << p.page_shift) + at_row : 0),
+                                  ln.a, ln.b, write, l == 0);
           }
-        } else {
-          float* scales = is_v ? p.vs : p.ks;
-          store_codes<D, INTER>(xa, xb, base + (write ? at : 0),
-                                scales + (write ? ((page * p.H_kv) << p.page_shift) + at_row : 0),
-                                ln.a, ln.b, write, l == 0);
         }
-      }
+      };
+      const int h0 = g * kRw, h1 = h0 + kRw;
+      if (h1 <= p.H) rows(std::integral_constant<int, 0>());
+      else if (h0 >= p.H && h1 <= p.H + p.H_kv) rows(std::integral_constant<int, 1>());
+      else if (h0 >= p.H + p.H_kv) rows(std::integral_constant<int, 2>());
+      else rows(std::integral_constant<int, 3>());
     }
   }
 }
