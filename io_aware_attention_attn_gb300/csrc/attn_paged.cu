@@ -168,7 +168,9 @@ struct Shares {
 };
 
 // This lane's share of the B operand of K Q^T (query row g of each group of 8, the elements that its
-// positions along d stand for), and the factors of scores (log2 units) of rows 2 q4, 2 q4 + 1.
+// positions along d stand for), and the factors of scores (log2 units) of rows 2 q4, 2 q4 + 1.  (Plain
+// loads, as everywhere here: the read-only path is for what no kernel writes while this one lives, and
+// this one may be set up while the kernel that writes q still runs.)
 template <int D, bool E4M3, int NT>
 __device__ __forceinline__ void load_q(const PagedParams& p, const Walk& w, int row_slice,
                                        uint32_t (&qf)[NT][D / 16][2], float (&mul)[NT][2]) {
@@ -185,12 +187,12 @@ __device__ __forceinline__ void load_q(const PagedParams& p, const Walk& w, int 
       if (r < rows) {
         const __nv_bfloat16* src = q + r * D + 16 * k;
         if (E4M3) {  // codes 4 q4 .. 4 q4 + 3 of a key arrive in one register
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + 4 * q4));
+          const uint2 v = *reinterpret_cast<const uint2*>(src + 4 * q4);
           qf[nt][k][0] = v.x;
           qf[nt][k][1] = v.y;
         } else {
-          qf[nt][k][0] = __ldg(reinterpret_cast<const uint32_t*>(src + 2 * q4));
-          qf[nt][k][1] = __ldg(reinterpret_cast<const uint32_t*>(src + 2 * q4 + 8));
+          qf[nt][k][0] = *reinterpret_cast<const uint32_t*>(src + 2 * q4);
+          qf[nt][k][1] = *reinterpret_cast<const uint32_t*>(src + 2 * q4 + 8);
         }
       }
     }

@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kRopeThreads, CACHE == kCacheE4m3 ? 2 : 3) qkv
       const int i = j / kLanes;
       const L o(j % kLanes, p.rot);
       float c = 1.f, s = 0.f;
-      if (o.turns(i)) angle(p, position, turn_step(__ldg(p.inv_freq + o.freq(i))), c, s);
+      if (o.turns(i)) angle(p, position, turn_step(p.inv_freq[o.freq(i)]), c, s);
       #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const __nv_bfloat16* w = k ? p.wk : p.wq;
@@ -338,8 +338,8 @@ __global__ void __launch_bounds__(kRopeThreads, CACHE == kCacheE4m3 ? 2 : 3) qkv
 // turned back, and u = h w:  dx = u - x r^2 mean(u x),  dw += h x.
 // A warp walks (token, share of its groups) tasks.  Its rows come through a ring in shared memory, each
 // lane copying and reading its own chunks, so that kDepth - 1 groups are in flight without holding
-// registers, across tokens too (two groups in registers, per token: 69 us where this takes less;
-// see the launcher for figures).
+// registers, across tokens too (B = 2, N = 4096, H = 32, H_kv = 8, d = 128: two groups in registers, per
+// token, took 69 us, this 54, and with the paths below for heads of one kind 48).
 constexpr int kDepth = 4;
 
 template <int D, bool INTER>
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
   for (int k = 0; k < kPairs; ++k) {
     const int j = lane + 32 * k;
     const L o(j % kLanes, p.rot);
-    turn[k] = o.turns(j / kLanes) ? turn_step(__ldg(p.inv_freq + o.freq(j / kLanes))) : 0;
+    turn[k] = o.turns(j / kLanes) ? turn_step(p.inv_freq[o.freq(j / kLanes)]) : 0;
   }
   __syncthreads();
   float dqa[8], dqb[8], dka[8], dkb[8];
@@ -580,8 +580,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_bwd_kernel(RopeParam
 // dwq (block 0) and dwk (block 1): the CTAs' shares, in runs of every 32nd or 64th CTA summed side by
 // side (four columns a thread, ten loads in flight at most), then joined in order.
 template <int D>
-__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__ partial, int ctas,
-                                                       float* dwq, float* dwk) {
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* partial, int ctas, float* dwq,
+                                                       float* dwk) {
   constexpr int kRuns = 1024 / (D / 4), kLoads = (kRopeBwdCtas + kRuns - 1) / kRuns;
   __shared__ float4 s_sum[kRuns][D / 4];
   float* out = blockIdx.x ? dwk : dwq;
