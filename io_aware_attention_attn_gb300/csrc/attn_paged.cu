@@ -3,7 +3,8 @@
 // For each (request s, K/V head, group of up to 32 of its query rows) -- a unit -- with K, V the
 // request's rows:  S = scale Q K^T,  O = softmax(S) V,  read once in tiles of 64 keys.
 //
-// What bounds it: reading K and V.  A key costs 4 d bytes (bf16) and 4 d operations a query row, so at
+// What bounds it: reading K and V (64 requests of 16384 tokens, 32 query and 8 K/V heads, d = 128: 4.3 GB
+// in 588 us, 7.3 TB/s; 48 requests of up to 16384 from E4M3 pages of 16 rows: 131 us, 6.3 TB/s).  A key costs 4 d bytes (bf16) and 4 d operations a query row, so at
 // up to 32 rows the tensor work is far below what the copy takes and the kernel is built around the
 // copies: a producer warp fills a ring of tiles by TMA (one box per page part), four consumer
 // warps each take 16 of a tile's 64 keys and never wait for one another inside a unit.
@@ -17,7 +18,10 @@
 //
 // Softmax: each warp keeps a reference maximum m of its own keys per row (log2 units) that trails
 // the true one by at most 8, so P <= 256; the maximum is looked for across lanes only when some
-// score passes m + 8.  Row sums stay per lane until a unit ends.
+// score passes m + 8.  Row sums stay per lane, in fp32 and of the unrounded P, until a unit ends.  P is
+// rounded to V's type for the product, as in the whole-sequence forward: its errors average out like
+// the rounding of O itself and are as large (2.2e-3 of O's norm against 1.7e-3 of a correctly rounded
+// O); two bf16 pieces of P would remove them for twice the products.
 //
 // E4M3 cache: codes become f16 on the way from shared memory to the product (exact); q becomes f16
 // after a power-of-two scaling of its row (exact down to 2^-22 of the row's largest element); a
