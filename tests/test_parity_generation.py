@@ -482,6 +482,29 @@ def test_paged_outputs_given_codes_as_bytes_and_one_page_of_any_stride():
     check_paged(o, lse, q, vals, table, [16], 1 / 8, "bf16", "paged one page")
 
 
+def test_refusals_of_the_library_name_the_entry_point():
+    q, cache, table, n, _ = paged_inputs(33, [9], 2, 1, 64, 16, "bf16")
+    small = attn.KVCache(cache.k[:, :, :8].contiguous(), cache.v[:, :, :8].contiguous())
+    with pytest.raises(attn.AttnError, match="attn_fwd_paged failed: ATTN_ERR_UNSUPPORTED") as e:
+        attn.attn_fwd_paged(q, small, table, n)
+    assert e.value.code == -9
+    with pytest.raises(attn.AttnError, match="ATTN_ERR_SCALE"):
+        attn.attn_fwd_paged(q, cache, table, n, 0.0)
+    with pytest.raises(attn.AttnError, match="ATTN_ERR_WORKSPACE"):
+        attn.attn_fwd_paged(q, cache, table, n, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(attn.AttnError, match="attn_qkv_rope failed: ATTN_ERR_SHAPE"):
+        attn.qkv_rope(normal(1, 3, 4 * 64), 2, 1, torch.zeros(3, dtype=torch.int32, device="cuda"),
+                      torch.ones(5, dtype=torch.float64, device="cuda"))
+    with pytest.raises(attn.AttnError, match="attn_kv_slots failed: ATTN_ERR_SHAPE"):
+        attn.kv_slots(i32(1), i32(0, 1), 1, table, i32(1), i32(0), 0)
+    attn.attn_fwd_paged(q, cache, table[:, ::2], n)  # one entry: its stride is free
+    for bad in (dict(seq_lens=n.long()), dict(block_table=table.repeat(2, 1)[::2, ::2].expand(1, 3)),
+                dict(q=q.float()),
+                dict(out=torch.empty_like(q).float()), dict(seq_lens=n.cpu())):
+        with pytest.raises(ValueError):
+            attn.attn_fwd_paged(**{**dict(q=q, cache=cache, block_table=table, seq_lens=n), **bad})
+
+
 def test_rope_without_tokens():
     f = attn.rope_inv_freq(64)
     w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
