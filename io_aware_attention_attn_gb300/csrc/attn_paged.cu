@@ -51,12 +51,12 @@ template <int D, bool E4M3, int NT, int RW>
 struct PagedCfg {
   static constexpr int kWarps = kSlices * RW;                     // consumers; one producer more
   static constexpr int kThreads = (kWarps + 1) * 32;
-  // CTAs an SM holds.  Where a tile is 32 KB two are enough for the copies to run at full rate; a
-  // tile of half that or less has to be through a warp's chain of dependent steps in half the
-  // time, so three or four share it (e4m3, d = 128, 64-row pages: 94 us with two, 84 with three).
-  // Registers set the limit, by the five warps of a CTA on four sub-partitions.
+  // CTAs an SM holds: as many as registers allow, by the five warps of a CTA on four sub-partitions.
+  // The smaller a tile, the less time a warp's chain of dependent steps has for it (e4m3, d = 128,
+  // 64-row pages: 94 us with two CTAs, 84 with three; bf16 is at the HBM rate with two as well, but
+  // short requests are bound by that chain too: 256 of 64 tokens 19.2 us with two, 16.9 with three).
   static constexpr int kCtas = RW == 2 ? 1 : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2)
-                                                     : !E4M3 || NT == 2 ? 2 : 3;
+                                                     : NT == 2 ? 2 : 3;
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
   static constexpr int kBlk = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a row in one box
   static constexpr int kBlks = kRowBytes / kBlk;                  // boxes side by side
@@ -121,12 +121,47 @@ __device__ __forceinline__ int all_places(const PagedParams& p) {
   }
   return __reduce_add_sync(0xffffffffu, n) * (p.H_kv * p.n_rg);
 }
-// Walk at place `at` (a warp's lanes together; w.t past the tiles: in the places after them); returns
-// the first place of its unit.
-__device__ int find(const PagedParams& p, int at, Walk& w) {
+// Places of all requests, by a block of T threads for which one look each is not enough, and s_pre[i]:
+// those of the requests before i's share of ceil(B / T).  Ends with the block in step.
+template <int T>
+__device__ int block_places(const PagedParams& p, int* s_pre, int* s_warp) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int share = (p.B + T - 1) / T, lo = min(tid * share, p.B), hi = min(lo + share, p.B);
+  int sum = 0;
+  #pragma unroll 8
+  for (int s = lo; s < hi; ++s) sum += req_places(p, s);
+  int scan = sum;
+  #pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, scan, off);
+    if (lane >= off) scan += up;
+  }
+  if (lane == 31) s_warp[warp] = scan;
+  __syncthreads();
+  int before = scan - sum, total = 0;
+  #pragma unroll
+  for (int i = 0; i < T / 32; ++i) {
+    if (i < warp) before += s_warp[i];
+    total += s_warp[i];
+  }
+  s_pre[tid] = before * (p.H_kv * p.n_rg);
+  __syncthreads();
+  return total * (p.H_kv * p.n_rg);
+}
+// The share of block_places that holds place `at`.
+template <int T>
+__device__ int share_of(const int* s_pre, int at) {
+  int n = 0;
+  #pragma unroll
+  for (int i = 0; i < T; i += 32)
+    n += __popc(__ballot_sync(0xffffffffu, s_pre[i + (threadIdx.x & 31)] <= at));
+  return n - 1;
+}
+// Walk at place `at` (a warp's lanes together; w.t past the tiles: in the places after them), looked for
+// from request `from` on, before which there are `before` places; returns the first place of its unit.
+__device__ int find(const PagedParams& p, int at, Walk& w, int from = 0, int before = 0) {
   const int lane = threadIdx.x & 31, per = p.H_kv * p.n_rg;
-  int before = 0;
-  for (int s0 = 0; s0 < p.B; s0 += 32) {
+  for (int s0 = from; s0 < p.B; s0 += 32) {
     const int s = s0 + lane;
     const int len = s < p.B ? req_len(p, s) : 0;
     const int n = s < p.B ? req_tiles(len) + p.unit_cost : 0;
@@ -250,29 +285,25 @@ paged_kernel(const __grid_constant__ PagedParams p) {
   }
   pdl_wait();
   // places of all units (fewer than 2^31: the host's check): each warp for itself where eight loads a
-  // lane are enough
-  int total = 0;
-  if (p.B <= 256) {
-    total = all_places(p);
-    __syncthreads();
-  } else {
-    for (int s = tid; s < p.B; s += L::kThreads) total += req_places(p, s);
-    total = __reduce_add_sync(0xffffffffu, total);
-    int* sums = reinterpret_cast<int*>(sm + L::kMerge);
-    if (lane == 0) sums[warp] = total;
-    __syncthreads();
-    total = 0;
-    for (int i = 0; i <= L::kWarps; ++i) total += sums[i];
-    total *= p.H_kv * p.n_rg;
-    __syncthreads();
-  }
+  // lane are enough (2000 requests of 16 tokens: 87 us, each warp for itself 108)
+  const bool few = p.B <= 256;
+  int* s_pre = reinterpret_cast<int*>(sm + L::kMerge);
+  const int total = few ? all_places(p) : block_places<L::kThreads>(p, s_pre, s_pre + L::kThreads);
+  if (few) __syncthreads();
   pdl_launch_dependents();
   const int cta = static_cast<int>(blockIdx.x), G = min(p.ctas, total);
   if (cta >= G) return;
   const Shares shares(static_cast<uint32_t>(total), static_cast<uint32_t>(G));
   const int place0 = shares.start(cta);
   Walk w;
-  const int unit0 = find(p, place0, w);
+  int unit0;
+  if (few) {
+    unit0 = find(p, place0, w);
+  } else {
+    const int k = share_of<L::kThreads>(s_pre, place0);
+    unit0 = find(p, place0, w, k * ((p.B + L::kThreads - 1) / L::kThreads), s_pre[k]);
+    __syncthreads();  // what follows may write where s_pre is
+  }
   int left = shares.start(cta + 1) - place0;  // places of this CTA still to come
   if (w.t >= w.n) {  // it starts behind a unit's last tile
     left -= unit0 + w.n + p.unit_cost - place0;
@@ -668,10 +699,10 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         }
       }
       named_barrier_sync(1 + row_slice, kSlices * 32);
-      for (int e = slice * 32 + lane; e < L::kMergeNt * 8 * (D / 4); e += kSlices * 32) {
-        const int r = e / (D / 4), c4 = e % (D / 4), i = r / 8;
-        const int row = (row_slice * NT + n0) * 8 + r;
-        if (row >= rows) continue;
+      const int base_row = (row_slice * NT + n0) * 8;
+      const int cells = min(L::kMergeNt * 8, rows - base_row) * (D / 4);
+      for (int e = slice * 32 + lane; e < cells; e += kSlices * 32) {
+        const int r = e / (D / 4), c4 = e % (D / 4), i = r / 8, row = base_row + r;
         float top = -INFINITY, sum = 0.f;
         float2 ml[kSlices];
         #pragma unroll
@@ -720,11 +751,16 @@ __host__ __device__ constexpr int join_share(int parts) {  // warps of a row
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __grid_constant__ PagedParams p) {
   constexpr int kPer = D / 32;
-  __shared__ float s_o[kJoinWarps][D];
+  __shared__ __align__(16) float s_o[kJoinWarps][D];
   __shared__ float2 s_ml[kJoinWarps];
+  static_assert(kJoinWarps * D >= kJoinWarps * 32 + kJoinWarps, "s_o holds block_places' sums");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // (the lengths were complete before the first kernel began, and it let this one start only then)
-  const int total = all_places(p), G = min(p.ctas, total), x = static_cast<int>(blockIdx.x);
+  constexpr int kThreads = kJoinWarps * 32;
+  int* s_pre = reinterpret_cast<int*>(s_o);
+  const bool few = p.B <= 256;
+  const int total = few ? all_places(p) : block_places<kThreads>(p, s_pre, s_pre + kThreads);
+  const int G = min(p.ctas, total), x = static_cast<int>(blockIdx.x);
   const Shares shares(static_cast<uint32_t>(total), static_cast<uint32_t>(G));
   int unit, unit0, tiles;  // its number, first place and tiles
   bool mine = true;
@@ -739,7 +775,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __
   } else {
     Walk w;
     mine = x < G;
-    unit0 = find(p, mine ? shares.start(x) : 0, w);
+    const int place = mine ? shares.start(x) : 0, k = few ? 0 : share_of<kThreads>(s_pre, place);
+    unit0 = few ? find(p, place, w)
+                : find(p, place, w, k * ((p.B + kThreads - 1) / kThreads), s_pre[k]);
     unit = (w.s * p.H_kv + w.h) * p.n_rg + w.rg;
     tiles = w.n;
     mine = mine && w.t > 0 && w.t < w.n && shares.owner(unit0 + tiles - 1) == x;
@@ -747,6 +785,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __
   const int i0 = shares.owner(unit0), n = shares.owner(unit0 + tiles - 1) - i0 + 1;
   // the beginning CTA's second part, if it holds tiles of the unit before
   const int second = shares.start(i0) < unit0 - p.unit_cost ? 1 : 0;
+  __syncthreads();  // s_pre has been read
   pdl_wait();  // by every block, so that the work after this one waits for the parts' kernel too
   if (!mine || n == 1) return;
   const int rg = unit % p.n_rg, sh = unit / p.n_rg;
