@@ -83,6 +83,8 @@ constexpr int kPagedMaxRows = 32;      // query rows (heads of one K/V head) of 
 struct PagedParams {
   CUtensorMap tm_k;     // 4-D {d, page_size, H_kv, pages}, box {128 bytes of d, box_rows, 1, 1}
   CUtensorMap tm_v;
+  CUtensorMap tm_k16;   // the same with boxes of 16 rows
+  CUtensorMap tm_v16;
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
   float* lse;

@@ -220,10 +220,12 @@ extern "C" int attn_fwd_paged(const void* q, const attn_kv_cache* cache, const i
   PagedParams p{};
   const bool e4m3 = cache->dtype == ATTN_CACHE_E4M3;
   p.box_rows = cache->page_size < kPagedTile ? cache->page_size : kPagedTile;
-  if (encode_cache_map(&p.tm_k, cache->k, e4m3, d, cache->page_size, H_kv, cache->num_pages,
-                       cache->page_stride, p.box_rows) != CUDA_SUCCESS ||
-      encode_cache_map(&p.tm_v, cache->v, e4m3, d, cache->page_size, H_kv, cache->num_pages,
-                       cache->page_stride, p.box_rows) != CUDA_SUCCESS)
+  auto encode = [&](CUtensorMap* map, const void* base, uint32_t rows) {
+    return encode_cache_map(map, base, e4m3, d, cache->page_size, H_kv, cache->num_pages,
+                            cache->page_stride, rows) == CUDA_SUCCESS;
+  };
+  if (!encode(&p.tm_k, cache->k, p.box_rows) || !encode(&p.tm_v, cache->v, p.box_rows) ||
+      !encode(&p.tm_k16, cache->k, 16) || !encode(&p.tm_v16, cache->v, 16))
     return ATTN_ERR_LAUNCH;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.o = static_cast<__nv_bfloat16*>(o);

@@ -285,7 +285,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
   }
   pdl_wait();
   // places of all units (fewer than 2^31: the host's check): each warp for itself where eight loads a
-  // lane are enough (2000 requests of 16 tokens: 87 us, each warp for itself 108)
+  // lane are enough (2000 requests of 16 tokens: 87 us then, each warp for itself 108)
   const bool few = p.B <= 256;
   int* s_pre = reinterpret_cast<int*>(sm + L::kMerge);
   const int total = few ? all_places(p) : block_places<L::kThreads>(p, s_pre, s_pre + L::kThreads);
@@ -315,17 +315,22 @@ paged_kernel(const __grid_constant__ PagedParams p) {
   if (warp == L::kWarps) {
     // ------------------------------------------------------------------------------ producer
     const uint64_t policy = l2_policy_evict_first();
-    const int box_shift = 31 - __clz(p.box_rows);
-    const int parts_tile = kPagedTile >> box_shift;
+    const int wide_shift = 31 - __clz(p.box_rows);
+    const int pages_tile = max(kPagedTile >> p.page_shift, 1);
     int entries = 0, entry_base = -1, entry_s = -1;  // lane's entry of the 32 looked up last
     bool ok = true;
     int it = 0, st = 0;
     uint32_t phase = 1;  // of the empty barrier waited for, from the second round on
     for (; left > 0; ++it) {
       const int rows = min(kPagedTile, w.len - w.t * kPagedTile);
-      const int parts = rows > 0 ? (rows + p.box_rows - 1) >> box_shift : 0;
+      // A last tile of 32 rows or fewer comes in boxes of 16: a box is read whole, and one more costs the
+      // SM ~43 ns, the time of 2 KB (2000 requests of 16 tokens on 64-row pages, 8 K/V heads,
+      // d = 128: 67 us instead of 87).
+      const bool narrow = rows <= 32 && p.box_rows > 16;
+      const int box_shift = narrow ? 4 : wide_shift, box_rows = 1 << box_shift;
+      const int parts = rows > 0 ? (rows + box_rows - 1) >> box_shift : 0;
       const int page0 = (w.t * kPagedTile) >> p.page_shift;
-      if (parts > 0 && (entry_s != w.s || page0 < entry_base || page0 + parts_tile > entry_base + 32)) {
+      if (parts > 0 && (entry_s != w.s || page0 < entry_base || page0 + pages_tile > entry_base + 32)) {
         entry_s = w.s;
         entry_base = page0;
         const int e = page0 + lane;
@@ -356,19 +361,19 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         __syncwarp();
       }
       if (lane == 0)
-        mbar_arrive_expect_tx(full(st), static_cast<uint32_t>(parts) * p.box_rows * 2 * L::kRowBytes);
+        mbar_arrive_expect_tx(full(st), static_cast<uint32_t>(parts) * box_rows * 2 * L::kRowBytes);
       __syncwarp();
       {  // lane -> (part, block, K or V); every lane takes part in the look-up of its page
         constexpr int kPerPart = 2 * L::kBlks;
         const int q = lane / kPerPart, o = lane % kPerPart;
         const int side = o / L::kBlks, blk = o % L::kBlks;
-        const int row0 = w.t * kPagedTile + q * p.box_rows;
+        const int row0 = w.t * kPagedTile + q * box_rows;
         const int at = (row0 >> p.page_shift) - entry_base;
         const int pg = __shfl_sync(0xffffffffu, entries, at & 31);
         if (q < parts)
           tma_load_4d_hint(stage + side * L::kSide + blk * (kPagedTile * L::kBlk) +
-                               q * p.box_rows * L::kBlk,
-                           side ? &p.tm_v : &p.tm_k, full(st), blk * (L::kBlk / (E4M3 ? 1 : 2)),
+                               q * box_rows * L::kBlk,
+                           narrow ? (side ? &p.tm_v16 : &p.tm_k16) : side ? &p.tm_v : &p.tm_k, full(st), blk * (L::kBlk / (E4M3 ? 1 : 2)),
                            row0 & ((1 << p.page_shift) - 1), w.h, pg >= 0 ? pg : p.num_pages, policy);
       }
       if (++st == L::kStages) {
