@@ -212,7 +212,8 @@ extern "C" int attn_fwd_paged(const void* q, const attn_kv_cache* cache, const i
   const int64_t units = static_cast<int64_t>(B) * H_kv * paged_row_groups(group);
   const int64_t tiles = most > 0 ? (most + kPagedTile - 1) / kPagedTile : 1;
   // the kernel numbers tiles, and the places a unit takes beside them, in 32 bits
-  if (static_cast<int64_t>(B) * H > INT_MAX || units > INT_MAX / (tiles + kPagedMaxCost)) return ATTN_ERR_SHAPE;
+  if (static_cast<int64_t>(B) * H > INT_MAX || units > INT_MAX / (tiles + kPagedMaxCost))
+    return ATTN_ERR_SHAPE;
   const PagedLayout L = paged_layout(group, d);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total)
     return ATTN_ERR_WORKSPACE;
@@ -250,7 +251,8 @@ extern "C" int attn_fwd_paged(const void* q, const attn_kv_cache* cache, const i
   p.page_shift = log2_of(cache->page_size);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.trail = kPagedTrail / p.scale_log2;
-  return launch_fwd_paged(p, d, e4m3, static_cast<int>(units * tiles), static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_fwd_paged(p, d, e4m3, static_cast<int>(units * tiles),
+                          static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? ATTN_OK
              : ATTN_ERR_LAUNCH;
 }

@@ -4,10 +4,11 @@
 // request's rows:  S = scale Q K^T,  O = softmax(S) V,  read once in tiles of 64 keys.
 //
 // What bounds it: reading K and V (64 requests of 16384 tokens, 32 query and 8 K/V heads, d = 128: 4.3 GB
-// in 588 us, 7.3 TB/s; 48 requests of up to 16384 from E4M3 pages of 16 rows: 131 us, 6.3 TB/s).  A key costs 4 d bytes (bf16) and 4 d operations a query row, so at
-// up to 32 rows the tensor work is far below what the copy takes and the kernel is built around the
-// copies: a producer warp fills a ring of tiles by TMA (one box per page part), four consumer
-// warps each take 16 of a tile's 64 keys and never wait for one another inside a unit.
+// in 597 us, 7.2 TB/s; 48 requests of up to 16384 from E4M3 pages of 16 rows: 131 us, 6.3 TB/s).  A key
+// costs 4 d bytes (bf16) and 4 d operations a query row, so at up to 32 rows the tensor work is far
+// below what the copy takes and the kernel is built around the copies: a producer warp fills a ring of
+// tiles by TMA (one box per page part), four consumer warps each take 16 of a tile's 64 keys and never
+// wait for one another inside a unit.
 //
 // Products: with few query rows the keys go on the 16-row side of the warp product,
 // S^T[keys x rows] = K Q^T and O^T[d x rows] += V^T P^T, rows in groups of 8 -- half the products and
@@ -23,10 +24,11 @@
 // the rounding of O itself and are as large (2.2e-3 of O's norm against 1.7e-3 of a correctly rounded
 // O); two bf16 pieces of P would remove them for twice the products.
 //
-// E4M3 cache: codes become f16 on the way from shared memory to the product (exact); q becomes f16
-// after a power-of-two scaling of its row (exact down to 2^-22 of the row's largest element); a
-// key's K scale multiplies its scores, its V scale its P, divided by the largest V scale the warp has
-// seen so that P V operands stay in f16's range.
+// E4M3 cache: codes become f16 on the way from shared memory to the product (exact; the 8-bit products of
+// a warp, with q in two pieces, would take K's codes as they are but were slower: 144 us for the 131);
+// q becomes f16 after a power-of-two scaling of its row (exact down to 2^-22 of the row's largest
+// element); a key's K scale multiplies its scores, its V scale its P, divided by the largest V scale the
+// warp has seen so that P V operands stay in f16's range.
 //
 // Work split: the tiles of all units in order (request, head, row group), each unit with a few more for
 // what its end costs, are cut into equal shares, one a CTA.  A unit inside one share is finished by
@@ -53,8 +55,9 @@ struct PagedCfg {
   static constexpr int kThreads = (kWarps + 1) * 32;
   // CTAs an SM holds: as many as registers allow, by the five warps of a CTA on four sub-partitions.
   // The smaller a tile, the less time a warp's chain of dependent steps has for it (e4m3, d = 128,
-  // 64-row pages: 94 us with two CTAs, 84 with three; bf16 is at the HBM rate with two as well, but
-  // short requests are bound by that chain too: 256 of 64 tokens 19.2 us with two, 16.9 with three).
+  // 64-row pages: 94 us with two CTAs, 84 with three; bf16 is at the HBM rate with two as well, 588 us
+  // for the 4.3 GB above against 597 with three, but short requests are bound by that chain too: 256
+  // of 64 tokens 19.2 us with two, 16.9 with three).
   static constexpr int kCtas = RW == 2 ? 1 : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2)
                                                      : NT == 2 ? 2 : 3;
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
@@ -373,8 +376,10 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         if (q < parts)
           tma_load_4d_hint(stage + side * L::kSide + blk * (kPagedTile * L::kBlk) +
                                q * box_rows * L::kBlk,
-                           narrow ? (side ? &p.tm_v16 : &p.tm_k16) : side ? &p.tm_v : &p.tm_k, full(st), blk * (L::kBlk / (E4M3 ? 1 : 2)),
-                           row0 & ((1 << p.page_shift) - 1), w.h, pg >= 0 ? pg : p.num_pages, policy);
+                           narrow ? (side ? &p.tm_v16 : &p.tm_k16) : side ? &p.tm_v : &p.tm_k,
+                           full(st), blk * (L::kBlk / (E4M3 ? 1 : 2)),
+                           row0 & ((1 << p.page_shift) - 1), w.h, pg >= 0 ? pg : p.num_pages,
+                           policy);
       }
       if (++st == L::kStages) {
         st = 0;
