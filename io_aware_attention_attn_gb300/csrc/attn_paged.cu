@@ -477,7 +477,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
           const float sk0 = sc[g], sk1 = sc[g + 8];
           sv0 = in0 ? sc[kPagedTile + g] : 0.f;
           sv1 = in1 ? sc[kPagedTile + g + 8] : 0.f;
-          grow = sv0 > vref || sv1 > vref;
+          grow = fabsf(sv0) > vref || fabsf(sv1) > vref;  // (a scale may be negative)
           #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             s[nt][0] *= mul[nt][0] * sk0;
@@ -501,7 +501,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         if (__any_sync(0xffffffffu, grow)) {
           float vscale = 1.f;
           if (E4M3) {
-            float vm = fmax3(vref, sv0, sv1);
+            float vm = fmax3(vref, fabsf(sv0), fabsf(sv1));
             #pragma unroll
             for (int off = 4; off < 32; off <<= 1)
               vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, off));
