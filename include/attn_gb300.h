@@ -237,7 +237,8 @@ ATTN_API int attn_fwd_fp8(const void* q8, const float* sq, const void* k8, const
  * page * page_size + row.  Passed by address; the struct itself is host memory, read during the call.
  *   k, v             : device pointers, 16-byte aligned; bf16, or E4M3 codes
  *   k_scale, v_scale : E4M3 only (else ignored): fp32 [num_pages, H_kv, page_size], contiguous,
- *                      16-byte aligned: the value of an element is its code x its row's scale
+ *                      16-byte aligned: the value of an element is its code x its row's scale (of
+ *                      any size and sign; the rows of a request may differ in it by any factor)
  *   page_stride      : elements from one page to the next, of k and of v (>= H_kv * page_size * d;
  *                      a multiple of 16 bytes), so k and v may be interleaved page by page
  *   page_size        : 16, 32, 64, 128 or 256

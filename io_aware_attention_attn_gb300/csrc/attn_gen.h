@@ -77,7 +77,7 @@ cudaError_t launch_qkv_rope_bwd(RopeParams& p, int d, bool interleaved, cudaStre
 constexpr int kPagedTile = 64;         // keys of a tile
 constexpr int kPagedMaxCtas = 608;     // 4 on each of 152 SMs
 constexpr int kPagedMaxCost = 2;       // places that a unit takes beside its tiles, at most
-constexpr float kPagedTrail = 8.f;     // the same in log2 units
+constexpr float kPagedTrail = 8.f;     // how far a score may pass the reference maximum, in log2 units
 constexpr int kPagedMaxRows = 32;      // query rows (heads of one K/V head) of a unit
 
 struct PagedParams {
@@ -101,7 +101,7 @@ struct PagedParams {
   int unit_cost;        // places that a unit takes beside its tiles
   bool by_unit;         // one join a unit, else one a CTA
   float scale_log2;     // scale * log2(e)
-  float trail;          // how far a score may pass the reference maximum, before the scale
+  float trail;          // the same before the scale (bf16 cache)
 };
 struct PagedLayout {
   size_t o_off, ml_off, total;

@@ -17,8 +17,8 @@
 // commit, a load and two hand-offs between warps; a warp product leaves everything in registers.)
 // P^T needs the score tile transposed between the products: two movmatrix per 8 rows.
 //
-// Softmax: each warp keeps a reference maximum m of its own keys per row (log2 units) that trails
-// the true one by at most 8, so P <= 256; the maximum is looked for across lanes only when some
+// Softmax: each warp keeps a reference maximum m of its own keys per row (log2 units) that, over a bf16
+// cache, trails the true one by at most 8, so P <= 256; the maximum is looked for across lanes only when some
 // score passes m + 8.  Row sums stay per lane, in fp32 and of the unrounded P, until a unit ends.  P is
 // rounded to V's type for the product, as in the whole-sequence forward: its errors average out like
 // the rounding of O itself and are as large (2.2e-3 of O's norm against 1.7e-3 of a correctly rounded
@@ -27,8 +27,13 @@
 // E4M3 cache: codes become f16 on the way from shared memory to the product (exact; the 8-bit products of
 // a warp, with q in two pieces, would take K's codes as they are but were slower: 144 us for the 131);
 // q becomes f16 after a power-of-two scaling of its row (exact down to 2^-22 of the row's largest
-// element); a key's K scale multiplies its scores, its V scale its P, divided by the largest V scale the
-// warp has seen so that P V operands stay in f16's range.
+// element); a key's K scale multiplies its scores, its V scale v its P, which is then rounded to f16 (2^-11
+// of the value).  So that f16 holds P v whatever the scales are, the reference m follows P v: it is set to
+// the largest score + log2 |v| of a row, less 6, and moved when P |v| passes 2^15, so an operand falls
+// below f16's normal range only 2^20 under the row's largest.  A key whose weight is nothing cannot set
+// it, nor one whose codes are all zero (its scale may be anything; looked for where m moves only).  P by
+// itself is then anything fp32 holds, 2^124 at most (it is 2^115 where m is set because V's scales are below
+// 2^-109, or nothing but zeros meets the largest scores), and its row sums are kept 2^-16 smaller.
 //
 // Work split: the tiles of all units in order (request, head, row group), each unit with a few more for
 // what its end costs, are cut into equal shares, one a CTA.  A unit inside one share is finished by
@@ -47,6 +52,12 @@ namespace {
 
 constexpr int kSlices = 4;                       // key slices of 16 in a tile, a warp each
 enum : int { kRoleProducer = 7, kRoleConsumer = 8 };
+
+// The reference maximum of a row over an E4M3 cache, in log2 units (see above).
+constexpr float kNoRef = 3.402823466e+38f;        // -m of a row without one: P of any score is infinite
+constexpr float kPvSet = 6.f, kPSet = 115.f;      // P |v| and P at most where m is set
+constexpr float kTrailE4m3 = 9.f;                 // and how far past that m is moved
+constexpr float kSumLog2 = 16.f;                  // row sums are of 2^-16 P
 
 // NT: groups of 8 query rows a warp holds; RW: row slices, each with four warps of its own.
 template <int D, bool E4M3, int NT, int RW>
@@ -265,6 +276,34 @@ __device__ __forceinline__ void load_q(const PagedParams& p, const Walk& w, int 
   }
 }
 
+// The largest value of a row's eight lanes (keys), scores of keys past the request's end, rows of O^T scaled.
+__device__ __forceinline__ float max_of_keys(float v) {
+  #pragma unroll
+  for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+  return v;
+}
+template <int NT>
+__device__ __forceinline__ void mask_tail(float (&s)[NT][4], int live, bool in0, bool in1) {
+  if (live >= 16) return;
+  #pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    s[nt][0] = in0 ? s[nt][0] : -INFINITY;
+    s[nt][1] = in0 ? s[nt][1] : -INFINITY;
+    s[nt][2] = in1 ? s[nt][2] : -INFINITY;
+    s[nt][3] = in1 ? s[nt][3] : -INFINITY;
+  }
+}
+template <int STEPS>
+__device__ __forceinline__ void scale_rows(float (&acc)[STEPS][4], const float (&c)[2]) {
+  #pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    acc[k][0] *= c[0];
+    acc[k][1] *= c[1];
+    acc[k][2] *= c[0];
+    acc[k][3] *= c[1];
+  }
+}
+
 template <int D, bool E4M3, int NT, int RW>
 __global__ void __launch_bounds__((kSlices * RW + 1) * 32, PagedCfg<D, E4M3, NT, RW>::kCtas)
 paged_kernel(const __grid_constant__ PagedParams p) {
@@ -414,13 +453,11 @@ paged_kernel(const __grid_constant__ PagedParams p) {
   load_q<D, E4M3, NT>(p, w, row_slice, qf, mul);
   while (left > 0) {
     const int t_begin = w.t, t_end = min(w.n, w.t + left);
-    // per row: nm = -m (0 while there is no m), and the score above which m is moved (-inf while
-    // there is none), in the units that scores have when they are compared
+    // per row: nm = -m; over bf16, above: the score past which m is moved (-inf while there is no m)
     float acc[NT][kSteps][4], nm[NT][2], above[NT][2], l[NT][2];
-    float vref = 0.f, vinv = 0.f;
     #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      nm[nt][0] = nm[nt][1] = 0.f;
+      nm[nt][0] = nm[nt][1] = E4M3 ? kNoRef : 0.f;
       above[nt][0] = above[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
       #pragma unroll
@@ -428,16 +465,20 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         #pragma unroll
         for (int j = 0; j < 4; ++j) acc[nt][k][j] = 0.f;
     }
+    auto no_ref = [&](int nt, int j) { return E4M3 ? nm[nt][j] == kNoRef : above[nt][j] == -INFINITY; };
 
     for (int t = t_begin; t < t_end; ++t) {
       if (!dead && !mbar_wait_warp(full(st), phase, ctx, kRoleConsumer, 2)) dead = true;
       const int live = w.len - t * kPagedTile - slice * 16;  // of this warp's 16 keys
       if (!dead && live > 0) {
         const uint32_t kst = base + st * L::kStage, vst = kst + L::kSide;
-        float s[NT][4];
-        #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-        if (!E4M3) {
+        // lane (g, q4): s[0], s[1] = key g, rows 2 q4, 2 q4 + 1;  s[2], s[3] = key g + 8
+        const bool in0 = g < live, in1 = g + 8 < live;
+        uint32_t pf[NT][2];
+        if constexpr (!E4M3) {
+          float s[NT][4];
+          #pragma unroll
+          for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
           const int key = slice * 16 + (lane & 15);
           #pragma unroll
           for (int k = 0; k < kSteps; ++k) {
@@ -448,120 +489,138 @@ paged_kernel(const __grid_constant__ PagedParams p) {
             for (int nt = 0; nt < NT; ++nt)
               mma16816<false>(s[nt], a[0], a[1], a[2], a[3], qf[nt][k][0], qf[nt][k][1]);
           }
-        } else {
-          const int key = slice * 16 + (lane & 15);
+          mask_tail<NT>(s, live, in0, in1);
+          bool grow = false;
           #pragma unroll
-          for (int k = 0; k < kSteps; k += 2) {
-            const int chunk = k + (lane >> 4);
-            const int sw = L::kBlk == 128 ? chunk ^ (key & 7) : chunk ^ ((key >> 1) & 3);
-            uint32_t a[4];
-            ldsm4(kst + key * L::kBlk + (sw << 4), a);
+          for (int nt = 0; nt < NT; ++nt)
+            grow |= fmaxf(s[nt][0], s[nt][2]) > above[nt][0] || fmaxf(s[nt][1], s[nt][3]) > above[nt][1];
+          if (__any_sync(0xffffffffu, grow)) {
             #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t lo0 = e4m3x2_to_f16x2(a[2 * j]), hi0 = e4m3x2_to_f16x2(a[2 * j] >> 16);
-              const uint32_t lo1 = e4m3x2_to_f16x2(a[2 * j + 1]),
-                             hi1 = e4m3x2_to_f16x2(a[2 * j + 1] >> 16);
+            for (int nt = 0; nt < NT; ++nt) {
+              float c[2];
               #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma16816<true>(s[nt], lo0, lo1, hi0, hi1, qf[nt][k + j][0], qf[nt][k + j][1]);
+              for (int j = 0; j < 2; ++j) {
+                const float top = max_of_keys(fmaxf(s[nt][j], s[nt][j + 2]));
+                const float m = top * p.scale_log2;
+                const bool none = no_ref(nt, j);  // no m yet: acc and l are 0 (or NaN)
+                c[j] = 1.f;
+                if (top != -INFINITY && (none || m > -nm[nt][j])) {
+                  c[j] = none ? 1.f : ex2_approx(-nm[nt][j] - m);
+                  nm[nt][j] = -m;
+                  above[nt][j] = top + p.trail;
+                }
+                l[nt][j] *= c[j];
+              }
+              scale_rows<kSteps>(acc[nt], c);
             }
           }
-        }
-        // lane (g, q4): s[0], s[1] = key g, rows 2 q4, 2 q4 + 1;  s[2], s[3] = key g + 8
-        const bool in0 = g < live, in1 = g + 8 < live;
-        float sv0 = 0.f, sv1 = 0.f;
-        bool grow = false;
-        if (E4M3) {
+          #pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float p0 = ex2_approx(fmaf(s[nt][0], p.scale_log2, nm[nt][0]));
+            const float p1 = ex2_approx(fmaf(s[nt][1], p.scale_log2, nm[nt][1]));
+            const float p2 = ex2_approx(fmaf(s[nt][2], p.scale_log2, nm[nt][0]));
+            const float p3 = ex2_approx(fmaf(s[nt][3], p.scale_log2, nm[nt][1]));
+            l[nt][0] += p0 + p2;
+            l[nt][1] += p1 + p3;
+            pf[nt][0] = transpose8x8(pack_bf16x2(p0, p1));
+            pf[nt][1] = transpose8x8(pack_bf16x2(p2, p3));
+          }
+        } else {
           const float* sc =
               reinterpret_cast<const float*>(sm + L::kScales) + st * 2 * kPagedTile + slice * 16;
           const float sk0 = sc[g], sk1 = sc[g + 8];
-          sv0 = in0 ? sc[kPagedTile + g] : 0.f;
-          sv1 = in1 ? sc[kPagedTile + g + 8] : 0.f;
-          grow = fabsf(sv0) > vref || fabsf(sv1) > vref;  // (a scale may be negative)
-          #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            s[nt][0] *= mul[nt][0] * sk0;
-            s[nt][1] *= mul[nt][1] * sk0;
-            s[nt][2] *= mul[nt][0] * sk1;
-            s[nt][3] *= mul[nt][1] * sk1;
-          }
-        }
-        if (live < 16) {
-          #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            s[nt][0] = in0 ? s[nt][0] : -INFINITY;
-            s[nt][1] = in0 ? s[nt][1] : -INFINITY;
-            s[nt][2] = in1 ? s[nt][2] : -INFINITY;
-            s[nt][3] = in1 ? s[nt][3] : -INFINITY;
-          }
-        }
-        #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          grow |= fmaxf(s[nt][0], s[nt][2]) > above[nt][0] || fmaxf(s[nt][1], s[nt][3]) > above[nt][1];
-        if (__any_sync(0xffffffffu, grow)) {
-          float vscale = 1.f;
-          if (E4M3) {
-            float vm = fmax3(vref, fabsf(sv0), fabsf(sv1));
+          float sv0 = in0 ? sc[kPagedTile + g] : 0.f, sv1 = in1 ? sc[kPagedTile + g + 8] : 0.f;
+          float sum[NT][2];  // of a lane's P
+          // A second time round where m has to move: the scores are formed again (they are rarely needed
+          // twice, and cost no registers then).
+          for (bool move = t == t_begin;; move = true) {
+            float e[NT][4];
             #pragma unroll
-            for (int off = 4; off < 32; off <<= 1)
-              vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, off));
-            vscale = vm > 0.f ? vref / vm : 1.f;
-            vref = vm;
-            vinv = vm >= 0x1p-126f ? 1.f / vm : 0.f;  // below: its values are below fp32's range too
-          }
-          #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float c[2];
+            for (int nt = 0; nt < NT; ++nt) e[nt][0] = e[nt][1] = e[nt][2] = e[nt][3] = 0.f;
+            const int key = slice * 16 + (lane & 15);
             #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float top = fmaxf(s[nt][j], s[nt][j + 2]);
+            for (int k = 0; k < kSteps; k += 2) {
+              const int chunk = k + (lane >> 4);
+              const int sw = L::kBlk == 128 ? chunk ^ (key & 7) : chunk ^ ((key >> 1) & 3);
+              uint32_t a[4];
+              ldsm4(kst + key * L::kBlk + (sw << 4), a);
               #pragma unroll
-              for (int off = 4; off < 32; off <<= 1)
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-              const float m = E4M3 ? top : top * p.scale_log2;
-              const bool none = above[nt][j] == -INFINITY;  // no m yet: acc and l are 0 (or NaN)
-              c[j] = 1.f;
-              if (top != -INFINITY && (none || m > -nm[nt][j])) {
-                c[j] = none ? 1.f : ex2_approx(-nm[nt][j] - m);
-                nm[nt][j] = -m;
-                above[nt][j] = top + (E4M3 ? kPagedTrail : p.trail);
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t lo0 = e4m3x2_to_f16x2(a[2 * j]), hi0 = e4m3x2_to_f16x2(a[2 * j] >> 16);
+                const uint32_t lo1 = e4m3x2_to_f16x2(a[2 * j + 1]),
+                               hi1 = e4m3x2_to_f16x2(a[2 * j + 1] >> 16);
+                #pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma16816<true>(e[nt], lo0, lo1, hi0, hi1, qf[nt][k + j][0], qf[nt][k + j][1]);
               }
-              l[nt][j] *= c[j];
-              c[j] *= vscale;
             }
             #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-              acc[nt][k][0] *= c[0];
-              acc[nt][k][1] *= c[1];
-              acc[nt][k][2] *= c[0];
-              acc[nt][k][3] *= c[1];
+            for (int nt = 0; nt < NT; ++nt) {
+              e[nt][0] *= mul[nt][0] * sk0;
+              e[nt][1] *= mul[nt][1] * sk0;
+              e[nt][2] *= mul[nt][0] * sk1;
+              e[nt][3] *= mul[nt][1] * sk1;
             }
+            mask_tail<NT>(e, live, in0, in1);
+            if (move) {
+              // a key whose codes are all zero (of either sign) weighs nothing: lane i looks at key i % 16, at
+              // sixteen codes, and at the others only where those of some key are zero
+              const uint8_t* codes = sm + (vst - base) + (slice * 16 + (lane & 15)) * L::kBlk;
+              auto some = [&](int c) {
+                const uint4 x = *reinterpret_cast<const uint4*>(codes + 16 * c);
+                return ((x.x | x.y | x.z | x.w) & 0x7f7f7f7fu) != 0u;
+              };
+              uint32_t keys = __ballot_sync(0xffffffffu, some(0));
+              if (keys != 0xffffffffu) {
+                bool any = false;
+                #pragma unroll
+                for (int c = 1; c < L::kRowBytes / 16; ++c) any |= some(c);
+                keys |= __ballot_sync(0xffffffffu, any);
+                if (!(keys >> g & 1u) && fabsf(sv0) < INFINITY) sv0 = 0.f;
+                if (!(keys >> (g + 8) & 1u) && fabsf(sv1) < INFINITY) sv1 = 0.f;
+              }
+              // (a scale that is infinite or NaN makes O what it is without a reference's help)
+              const float lv0 = fabsf(sv0) < INFINITY ? __log2f(fabsf(sv0)) - kPvSet : -INFINITY;
+              const float lv1 = fabsf(sv1) < INFINITY ? __log2f(fabsf(sv1)) - kPvSet : -INFINITY;
+              #pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float c[2];
+                #pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const float m = floorf(max_of_keys(
+                      fmax3(fmaxf(e[nt][j], e[nt][j + 2]) - kPSet, e[nt][j] + lv0, e[nt][j + 2] + lv1)));
+                  const bool none = no_ref(nt, j);  // no m yet: acc and l are 0 (or NaN)
+                  c[j] = 1.f;
+                  if (m != -INFINITY && (none || m + nm[nt][j] >= kTrailE4m3)) {
+                    c[j] = none ? 1.f : ex2_approx(-nm[nt][j] - m);
+                    nm[nt][j] = -m;
+                  }
+                  l[nt][j] *= c[j];
+                }
+                scale_rows<kSteps>(acc[nt], c);
+              }
+            }
+            float most = 0.f, most_pv = 0.f;
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float p0 = ex2_approx(e[nt][0] + nm[nt][0]), p1 = ex2_approx(e[nt][1] + nm[nt][1]);
+              const float p2 = ex2_approx(e[nt][2] + nm[nt][0]), p3 = ex2_approx(e[nt][3] + nm[nt][1]);
+              const float o0 = p0 * sv0, o1 = p1 * sv0, o2 = p2 * sv1, o3 = p3 * sv1;
+              most_pv = fmax3(fmax3(most_pv, fabsf(o0), fabsf(o1)), fabsf(o2), fabsf(o3));
+              sum[nt][0] = p0 + p2;
+              sum[nt][1] = p1 + p3;
+              most = fmax3(most, sum[nt][0], sum[nt][1]);
+              pf[nt][0] = pack_f16x2(o0, o1);
+              pf[nt][1] = pack_f16x2(o2, o3);
+            }
+            if (move || !__any_sync(0xffffffffu, most > 0x1p124f || most_pv > 0x1p15f)) break;
           }
-        }
-        uint32_t pf[NT][2];
-        #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float p0, p1, p2, p3;
-          if (E4M3) {
-            p0 = ex2_approx(s[nt][0] + nm[nt][0]);
-            p1 = ex2_approx(s[nt][1] + nm[nt][1]);
-            p2 = ex2_approx(s[nt][2] + nm[nt][0]);
-            p3 = ex2_approx(s[nt][3] + nm[nt][1]);
-          } else {
-            p0 = ex2_approx(fmaf(s[nt][0], p.scale_log2, nm[nt][0]));
-            p1 = ex2_approx(fmaf(s[nt][1], p.scale_log2, nm[nt][1]));
-            p2 = ex2_approx(fmaf(s[nt][2], p.scale_log2, nm[nt][0]));
-            p3 = ex2_approx(fmaf(s[nt][3], p.scale_log2, nm[nt][1]));
-          }
-          l[nt][0] += p0 + p2;
-          l[nt][1] += p1 + p3;
-          if (E4M3) {
-            const float f0 = sv0 * vinv, f1 = sv1 * vinv;
-            pf[nt][0] = transpose8x8(pack_f16x2(p0 * f0, p1 * f0));
-            pf[nt][1] = transpose8x8(pack_f16x2(p2 * f1, p3 * f1));
-          } else {
-            pf[nt][0] = transpose8x8(pack_bf16x2(p0, p1));
-            pf[nt][1] = transpose8x8(pack_bf16x2(p2, p3));
+          #pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            l[nt][0] = fmaf(sum[nt][0], 0x1p-16f, l[nt][0]);
+            l[nt][1] = fmaf(sum[nt][1], 0x1p-16f, l[nt][1]);
+            pf[nt][0] = transpose8x8(pf[nt][0]);
+            pf[nt][1] = transpose8x8(pf[nt][1]);
           }
         }
         // V rows past the request's end may hold anything: taken as zero
@@ -634,6 +693,8 @@ paged_kernel(const __grid_constant__ PagedParams p) {
       next_unit(p, w);
       load_q<D, E4M3, NT>(p, w, row_slice, qf, mul);
     }
+    // what the row sums are relative to
+    auto sum_ref = [&](int nt, int j) { return E4M3 ? kSumLog2 - nm[nt][j] : -nm[nt][j]; };
     // element (row, column) of this lane's j-th accumulator of tile k
     auto cell = [&](int k, int j) {
       const int row = 2 * q4 + (j & 1);
@@ -654,7 +715,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
             l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], off);
           if (g == 0)
             *reinterpret_cast<float2*>(st2 + ((i * kSlices + slice) * 8 + 2 * q4 + j) * 2) = make_float2(
-                above[nt][j] == -INFINITY ? -INFINITY : -nm[nt][j], l[nt][j]);
+                no_ref(nt, j) ? -INFINITY : sum_ref(nt, j), l[nt][j]);
         }
       }
       named_barrier_sync(1 + row_slice, kSlices * 32);
@@ -668,8 +729,8 @@ paged_kernel(const __grid_constant__ PagedParams p) {
           for (int x = 0; x < kSlices; ++x)
             top = fmaxf(top, st2[((i * kSlices + x) * 8 + 2 * q4 + j) * 2]);
           // no m: no finite score, so acc and l are 0 (or NaN, which stays)
-          const float c = (above[nt][j] == -INFINITY ? 1.f : ex2_approx(-nm[nt][j] - top)) *
-                          (E4M3 ? vref : 1.f);
+          const float c = (no_ref(nt, j) ? 1.f : ex2_approx(sum_ref(nt, j) - top)) *
+                          (E4M3 ? 0x1p-16f : 1.f);
           #pragma unroll
           for (int k = 0; k < kSteps; ++k) {
             acc[nt][k][j] *= c;
