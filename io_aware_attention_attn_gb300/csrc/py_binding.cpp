@@ -63,6 +63,14 @@ void* address(const at::Tensor& t, at::ScalarType type, at::IntArrayRef shape, a
   return t.data_ptr();
 }
 
+// The workspace given for a call on `dev` (undefined: none).  Its size is the entry point's to check.
+at::Tensor workspace(PyObject* o, at::Device dev) {
+  const at::Tensor ws = maybe(o, "workspace");
+  require(!ws.defined() || (ws.device() == dev && ws.is_contiguous()),
+          "the workspace must be contiguous and on the inputs' device");
+  return ws;
+}
+
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
   return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
@@ -289,6 +297,7 @@ PyObject* py_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   argc(n, 12);
   const at::Tensor &dq = tensor(a[0], "dq"), &dk = tensor(a[1], "dk"), &dv = tensor(a[2], "dv");
   const at::Tensor& qkv = tensor(a[3], "qkv");
+  at::Tensor ws = workspace(a[11], qkv.device());
   require(dq.dim() >= 3 && dk.dim() >= 3, "dq and dk must be [B, heads, N, d] or [heads, T, d]");
   require(dq.size(-3) <= INT32_MAX && dk.size(-3) <= INT32_MAX, "sizes must fit 32 bits");
   const Rope r = rope_inputs(qkv, static_cast<int>(dq.size(-3)), static_cast<int>(dk.size(-3)), a[4],
@@ -298,7 +307,7 @@ PyObject* py_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const void* vp = address(dv, at::kBFloat16, r.shape(r.H_kv), r.dev, "dv");
   const int B = static_cast<int>(r.B), N = static_cast<int>(r.N), d = static_cast<int>(r.d);
   Launch on(r.dev);
-  at::Tensor ws = maybe(a[11], "workspace"), dqkv = make(qkv.sizes(), at::kBFloat16, r.dev);
+  at::Tensor dqkv = make(qkv.sizes(), at::kBFloat16, r.dev);
   at::Tensor dw[2];
   if (r.wq || r.wk) {
     const size_t need = attn_qkv_rope_bwd_workspace_bytes(B, N, r.H, r.H_kv, d);
@@ -325,6 +334,7 @@ PyObject* py_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   argc(n, 11);
   const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "cache.k");
   const at::Tensor &table = tensor(a[5], "block_table"), &lens = tensor(a[6], "seq_lens");
+  at::Tensor ws = workspace(a[8], q.device());
   require(q.scalar_type() == at::kBFloat16 && q.is_cuda() && q.is_contiguous() &&
               (q.dim() == 3 || (q.dim() == 4 && q.size(2) == 1)),
           "q must be a contiguous bf16 CUDA tensor [B, H, 1, d] or [B, H, d]");
@@ -341,10 +351,9 @@ PyObject* py_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto* tp = static_cast<const int32_t*>(address(table, at::kInt, {B, cols}, dev, "block_table"));
   const auto* lp = static_cast<const int32_t*>(address(lens, at::kInt, {B}, dev, "seq_lens"));
   const at::IntArrayRef rows = q.sizes().slice(0, q.dim() - 1);
-  at::Tensor ws = maybe(a[8], "workspace"), out = maybe(a[9], "out"), lse = maybe(a[10], "lse");
+  at::Tensor out = maybe(a[9], "out"), lse = maybe(a[10], "lse");
   address(out, at::kBFloat16, q.sizes(), dev, "out");
   address(lse, at::kFloat, rows, dev, "lse");
-  if (ws.defined()) require(ws.device() == dev && ws.is_contiguous(), "the workspace must be contiguous and on q's device");
   const float scale = a[7] == Py_None ? 1.f / std::sqrt(static_cast<float>(d)) : real(a[7]);
   const int Bi = static_cast<int>(B), Hi = static_cast<int>(H), Ki = static_cast<int>(H_kv);
   Launch on(dev);
