@@ -2,15 +2,19 @@
 
 Each ``csrc/*.cu`` translation unit is compiled to an object in ``_build/`` in parallel, then
 linked into a shared library next to this file.  CUDA's runtime is linked statically, so the
-library only needs the NVIDIA driver at run time.  ``csrc/py_binding.cpp`` (marshalling of torch
-tensors) is compiled alongside with the host compiler and linked against the library and torch.
+library only needs the NVIDIA driver at run time.
 
-Usage: ``python -m io_aware_attention_attn_gb300.build [--verbose-ptxas] [--force]``.
+``csrc/py_binding.cpp`` (marshalling of torch tensors for the generation path) is compiled alongside
+with the host compiler against torch's and Python's headers.  It is kept up to date by itself: the
+library needs neither, is built without them, and does not start over when the binding fails.
+
+Usage: ``python -m io_aware_attention_attn_gb300.build [--library] [--verbose-ptxas] [--force]``.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -24,6 +28,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libattn_gb300.so")
 BINDING = os.path.join(PKG, "_attn_binding.so")
+BINDING_SRC = os.path.join(CSRC, "py_binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -42,15 +47,26 @@ def sources() -> list:
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _newest_input_mtime() -> float:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + \
-        [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [os.path.abspath(__file__)]
-    return max(os.path.getmtime(f) for f in files)
+def _newer_than_inputs(built: str, files: list) -> bool:
+    files = files + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [os.path.abspath(__file__)]
+    return os.path.exists(built) and os.path.getmtime(built) >= max(os.path.getmtime(f) for f in files)
+
+
+def library_up_to_date() -> bool:
+    return _newer_than_inputs(LIB, [os.path.join(CSRC, f) for f in os.listdir(CSRC)
+                                    if not f.endswith(".cpp")])
+
+
+def have_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
+def binding_up_to_date() -> bool:
+    return _newer_than_inputs(BINDING, [BINDING_SRC])
 
 
 def up_to_date() -> bool:
-    newest = _newest_input_mtime()
-    return all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING))
+    return library_up_to_date() and (not have_torch() or binding_up_to_date())
 
 
 def _compile(src: str, verbose_ptxas: bool) -> str:
@@ -82,7 +98,7 @@ def _compile_binding() -> str:
     _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
           *(f for d in dirs for f in ("-isystem" if d is not INCLUDE else "-I", d)),
-          "-c", os.path.join(CSRC, "py_binding.cpp"), "-o", obj], "compiling py_binding.cpp")
+          "-c", BINDING_SRC, "-o", obj], "compiling py_binding.cpp")
     return obj
 
 
@@ -96,19 +112,24 @@ def _link_binding(obj: str):
     os.replace(tmp, BINDING)
 
 
-def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile and link the library if any input changed; returns its path."""
-    if not force and not verbose_ptxas and up_to_date():
+def build(force: bool = False, verbose_ptxas: bool = False, library_only: bool = False) -> str:
+    """Compile and link what is older than its inputs: the library, and the binding where there is a torch
+    to build it for.  Returns the library's path."""
+    want_lib = force or verbose_ptxas or not library_up_to_date()
+    want_binding = not library_only and have_torch() and (force or not binding_up_to_date())
+    if not want_lib and not want_binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    srcs = sources()
+    srcs = sources() if want_lib else []
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = ex.submit(_compile_binding) if want_binding else None
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-    tmp = LIB + ".tmp"
-    _run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-Xlinker", "-soname=libattn_gb300.so"], "link")
-    os.replace(tmp, LIB)
-    _link_binding(binding.result())
+    if want_lib:
+        tmp = LIB + ".tmp"
+        _run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-Xlinker", "-soname=libattn_gb300.so"], "link")
+        os.replace(tmp, LIB)
+    if want_binding:
+        _link_binding(binding.result())
     return LIB
 
 
@@ -116,5 +137,6 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     ap.add_argument("--force", action="store_true")
     ap.add_argument("--verbose-ptxas", action="store_true")
+    ap.add_argument("--library", action="store_true", help="without the binding for torch")
     a = ap.parse_args()
-    print(build(force=a.force, verbose_ptxas=a.verbose_ptxas))
+    print(build(force=a.force, verbose_ptxas=a.verbose_ptxas, library_only=a.library))
