@@ -327,6 +327,11 @@ def _native():
     global _native_module
     if _native_module is None:
         lib()
+        from . import build
+        if not build.binding_matches():  # it takes torch's objects apart: no call into another layout
+            raise RuntimeError(
+                f"{build.BINDING} is missing or was built for another torch or Python than this one: build it "
+                "with `python -m io_aware_attention_attn_gb300.build`")
         from . import _attn_binding
         _attn_binding.set_error(AttnError)
         _native_module = _attn_binding

@@ -7,6 +7,7 @@ library only needs the NVIDIA driver at run time.
 ``csrc/py_binding.cpp`` (marshalling of torch tensors for the generation path) is compiled alongside
 with the host compiler against torch's and Python's headers.  It is kept up to date by itself: the
 library needs neither, is built without them, and does not start over when the binding fails.
+The binding fits one torch and one Python; a key beside it says which.
 
 Usage: ``python -m io_aware_attention_attn_gb300.build [--library] [--verbose-ptxas] [--force]``.
 """
@@ -29,6 +30,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libattn_gb300.so")
 BINDING = os.path.join(PKG, "_attn_binding.so")
 BINDING_SRC = os.path.join(CSRC, "py_binding.cpp")
+BINDING_KEY = BINDING + ".key"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -61,8 +63,23 @@ def have_torch() -> bool:
     return importlib.util.find_spec("torch") is not None
 
 
+def binding_key() -> str:
+    """What the binding is compiled against: torch's version and C++ ABI, Python's version, ABI and machine."""
+    import torch
+    return f"{torch.__version__} {int(torch._C._GLIBCXX_USE_CXX11_ABI)} {sysconfig.get_config_var('EXT_SUFFIX')}"
+
+
+def binding_matches() -> bool:
+    """Whether the binding on disk was built for this torch and this Python."""
+    try:
+        with open(BINDING_KEY) as f:
+            return f.read() == binding_key()
+    except FileNotFoundError:
+        return False
+
+
 def binding_up_to_date() -> bool:
-    return _newer_than_inputs(BINDING, [BINDING_SRC])
+    return _newer_than_inputs(BINDING, [BINDING_SRC]) and binding_matches()
 
 
 def up_to_date() -> bool:
@@ -109,7 +126,11 @@ def _link_binding(obj: str):
     _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", PKG, "-l:libattn_gb300.so",
           "-L", tlib, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda",
           "-Wl,-rpath,$ORIGIN"], "linking the binding")
+    if os.path.exists(BINDING_KEY):
+        os.remove(BINDING_KEY)  # at no time beside a binding that it does not describe
     os.replace(tmp, BINDING)
+    with open(BINDING_KEY, "w") as f:
+        f.write(binding_key())
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, library_only: bool = False) -> str:

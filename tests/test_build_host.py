@@ -20,7 +20,7 @@ def steps(tmp_path, monkeypatch):
     (inc / "h.h").write_text("")
     for name, value in (("PKG", tmp_path), ("CSRC", csrc), ("INCLUDE", inc), ("BUILD", tmp_path / "_build"),
                         ("LIB", tmp_path / "lib.so"), ("BINDING", tmp_path / "binding.so"),
-                        ("BINDING_SRC", csrc / "py_binding.cpp")):
+                        ("BINDING_SRC", csrc / "py_binding.cpp"), ("BINDING_KEY", tmp_path / "binding.so.key")):
         monkeypatch.setattr(build, name, str(value))
 
     def run(cmd, what):
@@ -89,3 +89,38 @@ def test_a_failing_binding_does_not_build_the_library_again(steps, step):
     assert not set(steps.ran) & set(LIBRARY)
     steps.fail.clear()
     assert steps() == BINDING and build.up_to_date()
+
+
+@pytest.mark.parametrize("other", ["2.9.0 1 .cpython-312-x86_64-linux-gnu.so", ""])
+def test_a_binding_of_another_torch_is_built_again(steps, monkeypatch, other):
+    assert steps() == sorted(LIBRARY + BINDING) and build.binding_matches()
+    with open(build.BINDING_KEY, "w") as f:
+        f.write(other)
+    assert not build.binding_matches() and not build.up_to_date() and steps() == BINDING
+    mine = build.binding_key()
+    monkeypatch.setattr(build, "binding_key", lambda: mine + "+new")
+    assert not build.up_to_date() and steps() == BINDING and build.up_to_date()
+    os.remove(build.BINDING_KEY)
+    assert steps() == BINDING
+    # a link that fails leaves no key beside the old binding
+    monkeypatch.setattr(build, "binding_key", lambda: mine)
+    steps.fail.add(BINDING[1])
+    with pytest.raises(RuntimeError):
+        steps()
+    assert not build.binding_matches()
+
+
+def test_a_binding_of_another_torch_is_not_loaded(monkeypatch, tmp_path):
+    from io_aware_attention_attn_gb300 import attn
+    build.build()
+    monkeypatch.setattr(attn, "_native_module", None)
+    key = tmp_path / "key"
+    key.write_text("2.9.0 1 .cpython-312-x86_64-linux-gnu.so")
+    monkeypatch.setattr(build, "BINDING_KEY", str(key))
+    with pytest.raises(RuntimeError, match="another torch"):
+        attn._native()
+    monkeypatch.setattr(build, "BINDING_KEY", str(tmp_path / "none"))
+    with pytest.raises(RuntimeError, match="is missing"):
+        attn._native()
+    monkeypatch.undo()
+    assert attn._native() is not None
