@@ -16,8 +16,6 @@ import math
 import os
 from typing import Any, NamedTuple
 
-import torch
-
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libattn_gb300.so")
 
 STATUS = {
@@ -305,6 +303,7 @@ class KVCache(NamedTuple):
 
 def kv_cache(num_pages: int, H_kv: int, page_size: int, d: int, dtype=None, device="cuda") -> KVCache:
     """An empty cache (zeros): bf16, or E4M3 with dtype torch.float8_e4m3fn."""
+    import torch
     dtype = torch.bfloat16 if dtype is None else dtype
     if dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8):
         raise ValueError("a cache is bf16 or float8_e4m3fn")
@@ -342,6 +341,7 @@ def _on(stream, device):
     """Makes ``stream`` (a torch stream or a cudaStream_t) current: torch's allocations of the call
     are then made on it, and a buffer released after the call is not handed out before its work is
     done."""
+    import torch
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
             torch.cuda.default_stream(device)
@@ -366,6 +366,7 @@ def rope_inv_freq(rot: int, base: float = 10000.0, factor: float = 1.0, original
     stretches them for a longer context: all of them divided by it, or, with original_len, only those
     that turn fewer than ``low`` times over original_len positions, none of those that turn
     more than ``high`` times, and a linear blend between."""
+    import torch
     f = float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64) / max(rot, 1))
     if factor != 1.0:
         if original_len:

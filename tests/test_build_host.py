@@ -1,6 +1,8 @@
 """What build() compiles when, with the compilers replaced: the library and the binding for torch are kept
 up to date apart."""
 import os
+import subprocess
+import sys
 
 import pytest
 
@@ -124,3 +126,14 @@ def test_a_binding_of_another_torch_is_not_loaded(monkeypatch, tmp_path):
         attn._native()
     monkeypatch.undo()
     assert attn._native() is not None
+
+
+def test_the_library_is_called_without_torch():
+    build.build()
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "from io_aware_attention_attn_gb300 import attn\n"
+            "assert attn.paged_workspace_bytes(2, 8, 2, 128) == attn.lib().attn_fwd_paged_workspace_bytes(2, 8, 2, 128) > 0\n"
+            "assert attn.version() > 0 and attn.bwd_workspace_bytes(1, 2, 64, 64) > 0\n"
+            "assert attn.decode_status(0) is not None")
+    r = subprocess.run([sys.executable, "-c", code], cwd=build.ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
