@@ -353,7 +353,9 @@ def kv_slots(seq_lens, cu_new, T: int, block_table, free_pages, free_head, page_
     """Pages, slots and positions of T new tokens (see attn_kv_slots in the header).  seq_lens
     int32 [B], cu_new int32 [B + 1], block_table int32 [B, max_pages] (new entries are written),
     free_pages int32 [n], free_head int32 [1].  Returns (slots int64 [T], positions int32 [T],
-    block_table, new seq_lens, new free_head); the old seq_lens and free_head are left alone."""
+    block_table, new seq_lens, new free_head); the old seq_lens and free_head are left alone.
+    Slots and positions share one storage, and so do lengths and head (all four at up to one new token a
+    request): clone what is saved or handed to another process by itself."""
     if stream is not None:
         with _on(stream, seq_lens.device):
             return kv_slots(seq_lens, cu_new, T, block_table, free_pages, free_head, page_size)
@@ -401,7 +403,8 @@ def qkv_rope(qkv, H: int, H_kv: int, positions=None, inv_freq=None, interleaved:
 def qkv_rope_bwd(dq, dk, dv, qkv, positions=None, inv_freq=None, interleaved: bool = False, wq=None,
                  wk=None, eps: float = 1e-6, rope_scale: float = 1.0, workspace=None, stream=None):
     """Backward of qkv_rope: the gradient of qkv's rows (contiguous, qkv's shape) from dq [B, H, N, d]
-    (or [H, T, d]) and dk, dv, and fp32 gradients of wq and wk (None where not given)."""
+    (or [H, T, d]) and dk, dv, and fp32 gradients of wq and wk (None where not given), the two halves
+    of one storage."""
     if stream is not None:
         with _on(stream, qkv.device):
             return qkv_rope_bwd(dq, dk, dv, qkv, positions, inv_freq, interleaved, wq, wk, eps,

@@ -186,11 +186,14 @@ PyObject* py_slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto* fp = static_cast<const int32_t*>(address(free, at::kInt, {spare}, dev, "free_pages"));
   const auto* hp = static_cast<const int32_t*>(address(head, at::kInt, {1}, dev, "free_head"));
   Launch on(dev);
-  const int64_t t = T;
-  const at::Tensor all = make({12 * t + 4 * B + 4}, at::kByte, dev);
-  at::Tensor slots = carve(all, 0, {t}, at::kLong), pos = carve(all, 8 * t, {t}, at::kInt);
-  at::Tensor lens_out = carve(all, 12 * t, {B}, at::kInt);
-  at::Tensor head_out = carve(all, 12 * t + 4 * B, {1}, at::kInt);
+  // Slots and positions are done with after the step, lengths and head are kept: together in one
+  // allocation only where that holds a token's 12 bytes a request, not a prompt's.
+  const int64_t t = T, kept = 4 * B + 4, at = t <= B ? 12 * t : 0;
+  const at::Tensor step = make({12 * t + (t <= B ? kept : 0)}, at::kByte, dev);
+  const at::Tensor state = t <= B ? step : make({kept}, at::kByte, dev);
+  at::Tensor slots = carve(step, 0, {t}, at::kLong), pos = carve(step, 8 * t, {t}, at::kInt);
+  at::Tensor lens_out = carve(state, at, {B}, at::kInt);
+  at::Tensor head_out = carve(state, at + 4 * B, {1}, at::kInt);
   if (B == 0) head_out.copy_(head);
   check("attn_kv_slots",
         attn_kv_slots(lp, cp, tp, fp, hp, static_cast<int64_t*>(slots.data_ptr()),

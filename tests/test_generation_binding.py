@@ -54,3 +54,27 @@ def test_workspace_of_another_device_or_layout_on_the_gpu(name):
         call(ws)
     torch.cuda.synchronize()
     assert attn.last_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_lengths_do_not_hold_a_prompts_slots():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    build.build()
+
+    def i32(*v):
+        return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+    table = torch.full((2, 80), -1, dtype=torch.int32, device="cuda")
+    free = torch.arange(200, dtype=torch.int32, device="cuda")
+    lens, head = i32(0, 0), i32(0)
+    for cu in ((0, 1000, 1001), (0, 1, 2), (0, 0, 1), (0, 0, 0), (0, 2, 3)):
+        old, T = lens.tolist(), cu[-1]
+        slots, pos, _, lens, head = attn.kv_slots(lens, i32(*cu), T, table, free, head, 16)
+        assert lens.tolist() == [old[0] + cu[1], old[1] + cu[2] - cu[1]]
+        assert int(head) == sum(-(-n // 16) for n in lens.tolist())
+        want = [n + i for n, a, b in zip(old, cu, cu[1:]) for i in range(b - a)]
+        assert pos.tolist() == want and slots.shape == (T,)
+        for t in (lens, head):
+            assert t.untyped_storage().nbytes() <= 4 * 3 + 12 * 2
+        assert slots.data_ptr() % 8 == pos.data_ptr() % 4 == lens.data_ptr() % 4 == 0
