@@ -282,6 +282,12 @@ __device__ __forceinline__ float max_of_keys(float v) {
   for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
   return v;
 }
+// x 2^d.  Row sums over an E4M3 cache may be large where 2^d by itself is below fp32's range: references
+// of two warps' rows are as far apart as log2 |v| of what they saw, and 2^-115 for keys without values.
+__device__ __forceinline__ float times_exp2(float x, float d) {
+  const float a = fmaxf(d, -120.f);
+  return x * ex2_approx(a) * ex2_approx(d - a);
+}
 template <int NT>
 __device__ __forceinline__ void mask_tail(float (&s)[NT][4], int live, bool in0, bool in1) {
   if (live >= 16) return;
@@ -592,10 +598,12 @@ paged_kernel(const __grid_constant__ PagedParams p) {
                   const bool none = no_ref(nt, j);  // no m yet: acc and l are 0 (or NaN)
                   c[j] = 1.f;
                   if (m != -INFINITY && (none || m + nm[nt][j] >= kTrailE4m3)) {
-                    c[j] = none ? 1.f : ex2_approx(-nm[nt][j] - m);
+                    if (!none) {
+                      c[j] = ex2_approx(-nm[nt][j] - m);
+                      l[nt][j] = times_exp2(l[nt][j], -nm[nt][j] - m);
+                    }
                     nm[nt][j] = -m;
                   }
-                  l[nt][j] *= c[j];
                 }
                 scale_rows<kSteps>(acc[nt], c);
               }
@@ -783,7 +791,9 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         }
         #pragma unroll
         for (int x = 0; x < kSlices; ++x)
-          sum += (ml[x].x == -INFINITY ? 1.f : ex2_approx(ml[x].x - top)) * ml[x].y;
+          sum += ml[x].x == -INFINITY ? ml[x].y
+                 : E4M3               ? times_exp2(ml[x].y, ml[x].x - top)
+                                      : ex2_approx(ml[x].x - top) * ml[x].y;
         const float* at0 = merge + (2 * i * 8 + (r & 7)) * L::kMergeLd + 4 * c4;
         const float4 a = *reinterpret_cast<const float4*>(at0);
         const float4 b = *reinterpret_cast<const float4*>(at0 + 8 * L::kMergeLd);
@@ -798,6 +808,13 @@ paged_kernel(const __grid_constant__ PagedParams p) {
                                                 : -INFINITY;
         } else {
           const int64_t at = static_cast<int64_t>(part) * p.rg_rows + row;
+          const uint32_t exponent = __float_as_uint(sum) >> 23;
+          if (E4M3 && exponent - 1u < 253u) {  // relative to a power of two near the sum, as the join expects
+            const float f = __uint_as_float((254u - exponent) << 23);
+            v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+            sum *= f;
+            top += static_cast<float>(static_cast<int>(exponent) - 127);
+          }
           *reinterpret_cast<float4*>(p.part_o + at * D + 4 * c4) = v;
           if (c4 == 0)
             *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(top, sum);

@@ -145,3 +145,21 @@ def test_rows_with_one_code(d, rows):
         cache.v.view(torch.uint8)[p, :, at, i] = 0x81  # -2^-9
         cache.v_scale[p, :, at] = 2.0 ** (9 + i % 12)
     check_weights(q, cache, table, lens, f"paged one code d{d} {rows}", 1 / math.sqrt(d))
+
+
+@pytest.mark.parametrize("d,rows", ROWS)
+@pytest.mark.parametrize("gap", [0, 15, 100, 600])
+def test_weight_on_values_of_zero_apart_from_large_values(d, rows, gap):
+    # the keys with values lie in one warp's share, in one tile or (by the gap) one CTA's, and their scales
+    # are large; all other keys have codes of zero and, from key to key, as much weight
+    lens = [2048, 200]
+    q, cache, table = written(13 + rows, lens, 2 * rows, 2, d, 1.0, range(2048))
+    r = np.random.default_rng(rows + gap)
+    v = torch.from_numpy(r.integers(0x30, 0x78, (2, 3, d), dtype=np.uint8)).cuda()
+    for s in range(2):
+        for i in range(3):
+            at = min(gap + i, lens[s] - 1)
+            p, at = int(table[s, at // 16]), at % 16
+            cache.v.view(torch.uint8)[p, :, at] = v[:, i]
+            cache.v_scale[p, :, at] = 2.0 ** (55 + 10 * i)
+    check_weights(q, cache, table, lens, f"paged apart d{d} {rows} gap {gap}", 1 / math.sqrt(d))
