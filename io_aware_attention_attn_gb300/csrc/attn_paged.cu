@@ -42,6 +42,7 @@
 // lengths, while it waits for them.
 #include "attn_gen.cuh"
 #include "attn_gen.h"
+#include "attn_paged_split.h"
 #include "sm103_ptx.cuh"
 
 #include <atomic>
@@ -193,11 +194,10 @@ __device__ int find(const PagedParams& p, int at, Walk& w, int from = 0, int bef
       w.s = s0 + k;
       w.n = places - p.unit_cost;
       w.len = __shfl_sync(0xffffffffu, len, k);
-      const uint32_t in = at - before;
-      const uint32_t u = in / static_cast<uint32_t>(places);
-      w.t = static_cast<int>(in - u * places);
-      w.h = p.n_rg == 1 ? u : u / p.n_rg;
-      w.rg = static_cast<int>(u) - w.h * p.n_rg;
+      const UnitAt u = unit_at(static_cast<uint32_t>(at - before), static_cast<uint32_t>(places), p.n_rg);
+      w.t = u.t;
+      w.h = u.h;
+      w.rg = u.rg;
       const int after = __shfl_sync(0xffffffffu, len, (k + 1) & 31);
       w.ahead = k < 31 ? after : w.s + 1 < p.B ? req_len(p, w.s + 1) : 0;
       return at - w.t;
@@ -207,18 +207,6 @@ __device__ int find(const PagedParams& p, int at, Walk& w, int from = 0, int bef
   w = Walk{p.B, 0, 0, 0, 1, 0, 0};
   return at;
 }
-
-// CTA i's share of `total` places among G: starts at i * (total / G) plus one for each earlier CTA of
-// the first total % G, which take one place more.
-struct Shares {
-  uint32_t q, r;
-  __device__ __forceinline__ Shares(uint32_t total, uint32_t G) : q(total / G), r(total - q * G) {}
-  __device__ __forceinline__ int start(uint32_t i) const { return static_cast<int>(i * q + min(i, r)); }
-  __device__ __forceinline__ int owner(uint32_t place) const {
-    const uint32_t big = r * (q + 1);
-    return static_cast<int>(place < big ? place / (q + 1) : r + (place - big) / q);
-  }
-};
 
 // This lane's share of the B operand of K Q^T (query row g of each group of 8, the elements that its
 // positions along d stand for), and the factors of scores (log2 units) of rows 2 q4, 2 q4 + 1.  (Plain
@@ -687,7 +675,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         phase ^= 1;
       }
     }
-    left -= t_end - t_begin + (t_end == w.n ? p.unit_cost : 0);
+    left -= places_done(t_begin, t_end, w.n, p.unit_cost);
 
     // ---- end of the unit (or of this CTA's part of it): the four warps' results become one, while
     // the next unit's query rows are on their way
@@ -872,7 +860,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __
   }
   const int i0 = shares.owner(unit0), n = shares.owner(unit0 + tiles - 1) - i0 + 1;
   // the beginning CTA's second part, if it holds tiles of the unit before
-  const int second = shares.start(i0) < unit0 - p.unit_cost ? 1 : 0;
+  const int second = second_part(shares.start(i0), unit0, p.unit_cost);
   __syncthreads();  // s_pre has been read
   pdl_wait();  // by every block, so that the work after this one waits for the parts' kernel too
   if (!mine || n == 1) return;
