@@ -79,6 +79,50 @@ def test_norm_of_rows_of_zeros(d, H, KV, kind):
         within(f64(got), ref, 2.0 ** -16 * (np.concatenate([ga, ga], -1) * np.abs(x) * r).sum((0, 1)), f"zero row dw {d}")
 
 
+@pytest.mark.parametrize("batched", [False, True])
+def test_rows_past_2_32_elements(batched):
+    # the last rows of projection rows of over 2^32 elements, against a call on those rows alone
+    H, KV, d, n = 16, 8, 128, 64
+    width = (H + 2 * KV) * d
+    T = (1 << 32) // width + 4096 + n
+    assert T % 2 == 0
+    rows = torch.zeros(T, width, dtype=torch.bfloat16, device="cuda")
+    assert (T - n) * width > 1 << 32
+    rows[-n:] = normal(70, n, width)
+    pos = torch.zeros(T, dtype=torch.int32, device="cuda")
+    pos[-n:] = torch.arange(n)
+    f = attn.rope_inv_freq(d)
+    wq, wk = (1 + 0.2 * normal(71, 2, d)).unbind(0)
+    kw = dict(inv_freq=f, wq=wq, wk=wk, eps=EPS)
+    lead = (lambda t: t.view(2, T // 2, *t.shape[1:])) if batched else (lambda t: t)
+    tail = (lambda t: t[1, :, -n:]) if batched else (lambda t: t[:, -n:])
+    slots = torch.full((T,), -1, dtype=torch.int64, device="cuda")
+    slots[-n:] = torch.arange(n)
+    caches = [attn.kv_cache(n // 16, KV, 16, d, torch.float8_e4m3fn) for _ in range(2)]
+    got = attn.qkv_rope(lead(rows), H, KV, lead(pos), cache=caches[0], slots=lead(slots), **kw)
+    want = attn.qkv_rope(rows[-n:], H, KV, pos[-n:].contiguous(), cache=caches[1], slots=slots[-n:].contiguous(), **kw)
+    for a, b in zip(got, want):
+        assert torch.equal(tail(a), b)
+    for a, b in zip(*caches):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)) and (a.view(torch.uint8) != 0).any()
+    del got
+    dy = [torch.zeros(*((2, h, T // 2, d) if batched else (h, T, d)), dtype=torch.bfloat16, device="cuda")
+          for h in (H, KV, KV)]
+    small = [normal(72 + i, h, n, d) for i, h in enumerate((H, KV, KV))]
+    for t, g in zip(dy, small):
+        tail(t).copy_(g)
+    dx, dwq, dwk = attn.qkv_rope_bwd(*dy, lead(rows), lead(pos), **kw)
+    rx, rq, rk = attn.qkv_rope_bwd(*small, rows[-n:], pos[-n:].contiguous(), **kw)
+    assert torch.equal(dx.view(T, width)[-n:], rx) and not dx.view(T, width)[0].any()
+    # dw: the same terms g x r in another order, n H <= 2^10 of them, each sum within 2^10 u of sum |g x r|,
+    # |g| at most the sum of a pair's |dy|
+    x = rows[-n:].view(n, H + 2 * KV, d)[:, :H + KV].double()
+    x = (x.abs() / (x.square().mean(-1, keepdim=True) + EPS).sqrt()).transpose(0, 1)
+    for a, b, dyh, xh in ((dwq, rq, small[0], x[:H]), (dwk, rk, small[1], x[H:])):
+        pair = dyh.double().abs().view(-1, n, 2, d // 2).sum(2).repeat(1, 1, 2)
+        assert ((a - b).abs() <= 2 * 2.0 ** -14 * (pair * xh).sum((0, 1))).all() and b.any()
+
+
 # ------------------------------------------------------------------------------------------- slots
 @pytest.mark.parametrize("cu,T", [((0, 2, 4), 6), ((1, 2, 6), 6), ((3, 3, 3), 5), ((0, 9, 4), 6), ((0, 4, 2, 6), 6),
                                   ((-2, 3, 300), 290), ((0, 0, 0), 300)])
