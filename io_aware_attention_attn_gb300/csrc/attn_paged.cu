@@ -778,10 +778,10 @@ paged_kernel(const __grid_constant__ PagedParams p) {
           top = fmaxf(top, ml[x].x);
         }
         #pragma unroll
-        for (int x = 0; x < kSlices; ++x)
-          sum += ml[x].x == -INFINITY ? ml[x].y
-                 : E4M3               ? times_exp2(ml[x].y, ml[x].x - top)
-                                      : ex2_approx(ml[x].x - top) * ml[x].y;
+        for (int x = 0; x < kSlices; ++x) {
+          if (E4M3) sum += ml[x].x == -INFINITY ? ml[x].y : times_exp2(ml[x].y, ml[x].x - top);
+          else sum += (ml[x].x == -INFINITY ? 1.f : ex2_approx(ml[x].x - top)) * ml[x].y;
+        }
         const float* at0 = merge + (2 * i * 8 + (r & 7)) * L::kMergeLd + 4 * c4;
         const float4 a = *reinterpret_cast<const float4*>(at0);
         const float4 b = *reinterpret_cast<const float4*>(at0 + 8 * L::kMergeLd);
