@@ -525,6 +525,23 @@ paged_kernel(const __grid_constant__ PagedParams p) {
           const float sk0 = sc[g], sk1 = sc[g + 8];
           float sv0 = in0 ? sc[kPagedTile + g] : 0.f, sv1 = in1 ? sc[kPagedTile + g + 8] : 0.f;
           float sum[NT][2];  // of a lane's P
+          // A key whose codes are all zero (of either sign) weighs nothing: its scale is taken as 0.  Lane i
+          // looks at key i % 16, at sixteen codes, and at the others only where those of some key are zero.
+          auto drop_zeros = [&] {
+            const uint8_t* codes = sm + (vst - base) + (slice * 16 + (lane & 15)) * L::kBlk;
+            auto some = [&](int c) {
+              const uint4 x = *reinterpret_cast<const uint4*>(codes + 16 * c);
+              return ((x.x | x.y | x.z | x.w) & 0x7f7f7f7fu) != 0u;
+            };
+            uint32_t keys = __ballot_sync(0xffffffffu, some(0));
+            if (keys == 0xffffffffu) return;
+            bool any = false;
+            #pragma unroll
+            for (int c = 1; c < L::kRowBytes / 16; ++c) any |= some(c);
+            keys |= __ballot_sync(0xffffffffu, any);
+            if (!(keys >> g & 1u) && fabsf(sv0) < INFINITY) sv0 = 0.f;
+            if (!(keys >> (g + 8) & 1u) && fabsf(sv1) < INFINITY) sv1 = 0.f;
+          };
           // A second time round where m has to move: the scores are formed again (they are rarely needed
           // twice, and cost no registers then).
           for (bool move = t == t_begin;; move = true) {
@@ -557,22 +574,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
             }
             mask_tail<NT>(e, live, in0, in1);
             if (move) {
-              // a key whose codes are all zero (of either sign) weighs nothing: lane i looks at key i % 16, at
-              // sixteen codes, and at the others only where those of some key are zero
-              const uint8_t* codes = sm + (vst - base) + (slice * 16 + (lane & 15)) * L::kBlk;
-              auto some = [&](int c) {
-                const uint4 x = *reinterpret_cast<const uint4*>(codes + 16 * c);
-                return ((x.x | x.y | x.z | x.w) & 0x7f7f7f7fu) != 0u;
-              };
-              uint32_t keys = __ballot_sync(0xffffffffu, some(0));
-              if (keys != 0xffffffffu) {
-                bool any = false;
-                #pragma unroll
-                for (int c = 1; c < L::kRowBytes / 16; ++c) any |= some(c);
-                keys |= __ballot_sync(0xffffffffu, any);
-                if (!(keys >> g & 1u) && fabsf(sv0) < INFINITY) sv0 = 0.f;
-                if (!(keys >> (g + 8) & 1u) && fabsf(sv1) < INFINITY) sv1 = 0.f;
-              }
+              if (t == t_begin) drop_zeros();
               // (a scale that is infinite or NaN makes O what it is without a reference's help)
               const float lv0 = fabsf(sv0) < INFINITY ? __log2f(fabsf(sv0)) - kPvSet : -INFINITY;
               const float lv1 = fabsf(sv1) < INFINITY ? __log2f(fabsf(sv1)) - kPvSet : -INFINITY;
@@ -596,20 +598,35 @@ paged_kernel(const __grid_constant__ PagedParams p) {
                 scale_rows<kSteps>(acc[nt], c);
               }
             }
-            float most = 0.f, most_pv = 0.f;
+            float most = 0.f, most0 = 0.f, most1 = 0.f;
             #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const float p0 = ex2_approx(e[nt][0] + nm[nt][0]), p1 = ex2_approx(e[nt][1] + nm[nt][1]);
               const float p2 = ex2_approx(e[nt][2] + nm[nt][0]), p3 = ex2_approx(e[nt][3] + nm[nt][1]);
               const float o0 = p0 * sv0, o1 = p1 * sv0, o2 = p2 * sv1, o3 = p3 * sv1;
-              most_pv = fmax3(fmax3(most_pv, fabsf(o0), fabsf(o1)), fabsf(o2), fabsf(o3));
+              most0 = fmax3(most0, fabsf(o0), fabsf(o1));
+              most1 = fmax3(most1, fabsf(o2), fabsf(o3));
               sum[nt][0] = p0 + p2;
               sum[nt][1] = p1 + p3;
               most = fmax3(most, sum[nt][0], sum[nt][1]);
               pf[nt][0] = pack_f16x2(o0, o1);
               pf[nt][1] = pack_f16x2(o2, o3);
             }
-            if (move || !__any_sync(0xffffffffu, most > 0x1p124f || most_pv > 0x1p15f)) break;
+            auto over = [&] {
+              return __any_sync(0xffffffffu, most > 0x1p124f || fmaxf(most0, most1) > 0x1p15f);
+            };
+            if (move || !over()) break;
+            drop_zeros();
+            if (sv0 == 0.f) most0 = 0.f;
+            if (sv1 == 0.f) most1 = 0.f;
+            if (!over()) {  // it was they
+              #pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                pf[nt][0] = sv0 == 0.f ? 0u : pf[nt][0];
+                pf[nt][1] = sv1 == 0.f ? 0u : pf[nt][1];
+              }
+              break;
+            }
           }
           #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
