@@ -279,6 +279,8 @@ typedef struct {
  * entry, if there is one, -1) and the status word reports kind 4; cu_new that is not a
  * non-decreasing prefix sum from 0 to T reports kind 2, is clamped into [0, T], and leaves tokens
  * that belong to no request with slot -1 and position 0.  A negative length counts as 0.
+ * (Several new tokens of a request that holds tokens already get pages and slots too; of the attentions
+ * here, attn_fwd sees only the rows it is given and attn_fwd_paged takes one new token a request.)
  * One launch.  T == 0 copies the lengths and the head; B == 0 does nothing.  Pointers of 4-byte
  * elements must be 4-byte aligned, slots 8-byte.  Returns an attn_status.
  */

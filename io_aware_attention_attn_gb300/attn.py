@@ -354,6 +354,8 @@ def kv_slots(seq_lens, cu_new, T: int, block_table, free_pages, free_head, page_
     int32 [B], cu_new int32 [B + 1], block_table int32 [B, max_pages] (new entries are written),
     free_pages int32 [n], free_head int32 [1].  Returns (slots int64 [T], positions int32 [T],
     block_table, new seq_lens, new free_head); the old seq_lens and free_head are left alone.
+    A request may hold tokens and get several more, but nothing here attends for those: attn_fwd takes
+    whole prompts, attn_fwd_paged one new token a request.
     Slots and positions share one storage, and so do lengths and head (all four at up to one new token a
     request): clone what is saved or handed to another process by itself."""
     if stream is not None:

@@ -4,7 +4,7 @@
 // request's rows:  S = scale Q K^T,  O = softmax(S) V,  read once in tiles of 64 keys.
 //
 // What bounds it: reading K and V (64 requests of 16384 tokens, 32 query and 8 K/V heads, d = 128: 4.3 GB
-// in 597 us, 7.2 TB/s; 48 requests of up to 16384 from E4M3 pages of 16 rows: 131 us, 6.3 TB/s).  A key
+// in 593-602 us, 7.2 TB/s; 48 requests of up to 16384 from E4M3 pages of 16 rows: 130 us, 6.4 TB/s).  A key
 // costs 4 d bytes (bf16) and 4 d operations a query row, so at up to 32 rows the tensor work is far
 // below what the copy takes and the kernel is built around the copies: a producer warp fills a ring of
 // tiles by TMA (one box per page part), four consumer warps each take 16 of a tile's 64 keys and never
@@ -22,17 +22,18 @@
 // score passes m + 8.  Row sums stay per lane, in fp32 and of the unrounded P, until a unit ends.  P is
 // rounded to V's type for the product, as in the whole-sequence forward: its errors average out like
 // the rounding of O itself and are as large (2.2e-3 of O's norm against 1.7e-3 of a correctly rounded
-// O); two bf16 pieces of P would remove them for twice the products.
+// O); two bf16 pieces of P would remove them for twice the products (64 requests of 16384 0.3 % slower,
+// short ones 2 %, 32 rows a K/V head 16 to 19 %).
 //
 // E4M3 cache: codes become f16 on the way from shared memory to the product (exact; the 8-bit products of
-// a warp, with q in two pieces, would take K's codes as they are but were slower: 144 us for the 131);
+// a warp, with q in two pieces, would take K's codes as they are but were slower: 144 us for 131);
 // q becomes f16 after a power-of-two scaling of its row (exact down to 2^-22 of the row's largest
 // element); a key's K scale multiplies its scores, its V scale v its P, which is then rounded to f16 (2^-11
 // of the value).  So that f16 holds P v whatever the scales are, the reference m follows P v: it is set to
 // the largest score + log2 |v| of a row, less 6, and moved when P |v| passes 2^15, so an operand falls
 // below f16's normal range only 2^20 under the row's largest.  A key whose weight is nothing cannot set
-// it, nor one whose codes are all zero (its scale may be anything; looked for where m moves only).  P by
-// itself is then anything fp32 holds, 2^124 at most (it is 2^115 where m is set because V's scales are below
+// it, nor one whose codes are all zero (its scale may be anything; looked for only where m would move: all
+// rows zero, with scale 1, 32 requests of 8192 take 149 us instead of 82).  P by itself is then anything fp32 holds, 2^124 at most (it is 2^115 where m is set because V's scales are below
 // 2^-109, or nothing but zeros meets the largest scores), and its row sums are kept 2^-16 smaller.
 //
 // Work split: the tiles of all units in order (request, head, row group), each unit with a few more for
@@ -66,8 +67,8 @@ struct PagedCfg {
   static constexpr int kWarps = kSlices * RW;                     // consumers; one producer more
   static constexpr int kThreads = (kWarps + 1) * 32;
   // CTAs an SM holds: as many as registers allow, by the five warps of a CTA on four sub-partitions.
-  // The smaller a tile, the less time a warp's chain of dependent steps has for it (e4m3, d = 128,
-  // 64-row pages: 94 us with two CTAs, 84 with three; bf16 is at the HBM rate with two as well, 588 us
+  // The smaller a tile, the less time a warp's chain of dependent steps has for it (e4m3, d = 128, ragged
+  // requests on 16-row pages: 159 us with two CTAs, 135 with three; bf16 is at the HBM rate with two as well, 588 us
   // for the 4.3 GB above against 597 with three, but short requests are bound by that chain too: 256
   // of 64 tokens 19.2 us with two, 16.9 with three).
   static constexpr int kCtas = RW == 2 ? 1 : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2)
@@ -1007,8 +1008,8 @@ cudaError_t launch_rows(const PagedParams& p, int ctas, cudaStream_t stream) {
   if (p.rg_rows <= 16) return launch<D, E4M3, 2, 1>(p, ctas, stream);
   // Up to 32 rows: two slices of warps, so that the accumulators fit, each reading the tile.  For codes
   // that converts them twice, so at d = 64, where four groups of rows fit one warp, they take that
-  // (32 requests of 8192, 8 K/V heads: 117 us against 142); for bf16 the two are near (98 against
-  // 103 us) and the slices' fewer CTAs leave fewer parts to join (37 ragged requests: 17 us
+  // though it spills 300 bytes (32 requests of 8192, 8 K/V heads: 107 us against 140); for bf16 the two are
+  // near (98 against 103 us) and the slices' fewer CTAs leave fewer parts to join (37 ragged requests: 17 us
   // against 20).
   if constexpr (D == 64 && E4M3) return launch<D, E4M3, 4, 1>(p, ctas, stream);
   else return launch<D, E4M3, 2, 2>(p, ctas, stream);
