@@ -543,7 +543,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
             if (!(keys >> g & 1u) && fabsf(sv0) < INFINITY) sv0 = 0.f;
             if (!(keys >> (g + 8) & 1u) && fabsf(sv1) < INFINITY) sv1 = 0.f;
           };
-          // A second time round where m has to move: the scores are formed again (they are rarely needed
+          // Twice where m has to move: the scores are formed again (they are rarely needed
           // twice, and cost no registers then).
           for (bool move = t == t_begin;; move = true) {
             float e[NT][4];
