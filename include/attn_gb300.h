@@ -279,8 +279,8 @@ typedef struct {
  * entry, if there is one, -1) and the status word reports kind 4; cu_new that is not a
  * non-decreasing prefix sum from 0 to T reports kind 2, is clamped into [0, T], and leaves tokens
  * that belong to no request with slot -1 and position 0.  A negative length counts as 0.
- * (Several new tokens of a request that holds tokens already get pages and slots too; of the attentions
- * here, attn_fwd sees only the rows it is given and attn_fwd_paged takes one new token a request.)
+ * (Several new tokens of a request that holds tokens already get pages and slots too: attn_fwd_paged_varlen
+ * attends for those.)
  * One launch.  T == 0 copies the lengths and the head; B == 0 does nothing.  Pointers of 4-byte
  * elements must be 4-byte aligned, slots 8-byte.  Returns an attn_status.
  */
@@ -371,6 +371,96 @@ ATTN_API int attn_fwd_paged(const void* q, const attn_kv_cache* cache, const int
 
 /* Workspace bytes attn_fwd_paged needs (0 for invalid sizes). */
 ATTN_API size_t attn_fwd_paged_workspace_bytes(int B, int H, int H_kv, int d);
+
+/*
+ * Attention of several new tokens of each of B requests over a paged cache: a prompt in chunks, a second prompt of
+ * a conversation, proposed tokens to verify, or a whole prompt through its pages.  Request s owns tokens
+ * cu_new[s] .. cu_new[s+1]-1 of a packed batch of T, the last of the seq_lens[s] rows that its pages
+ * block_table[s][0], [1], ... hold (the new tokens' own K and V are in the cache already, and counted).
+ * Token i of n sees rows 0 .. seq_lens[s] - n + i of its request (causal), or all seq_lens[s] of them (causal = 0);
+ * query head h reads K/V head h / (H / H_kv).  O = softmax(scale q K^T) V, and the log-sum-exp.
+ *   q, o : bf16 [H, T, d];  lse : fp32 [H, T]  (the packed layout of attn_fwd and attn_qkv_rope)
+ *   block_table : int32 [B, max_pages]; only the entries that seq_lens needs are read, and a row past seq_lens
+ *     is never used, whatever it holds.  seq_lens : int32 [B], clamped to 0 .. max_pages * page_size.
+ *   cu_new : int32 [B + 1], from 0 up, at most T.  Requests without new tokens are fine; tokens from cu_new[B]
+ *     on are padding, and o and lse are left as they were there.  cu_new that decreases, does not begin with 0 or passes
+ *     T is clamped into [0, T] and the status word reports kind 2 (o and lse are then unspecified).
+ *   A token that sees no row (more new tokens than rows) gets O = 0 and lse = -inf.
+ *   E4M3 caches: V scales up to 2^100 in magnitude (K scales: any); a query row with an infinity or a NaN
+ *     gives NaN.  A V row that is not finite reaches, besides the tokens that see it, those before it that share its
+ *     tile of 128 rows (as in attn_fwd).
+ *   workspace : attn_fwd_paged_varlen_workspace_bytes(T, H, H_kv, d) bytes (it does not depend on the
+ *     lengths), 256-byte aligned; calls whose work may overlap on the GPU need one each.
+ * The work is cut into equal shares of key tiles, whatever the lengths are, one or more for each pair of SMs, and a
+ * second launch joins what fell to several by the block merge of attn_fwd_splitkv.  Everything that depends on
+ * lengths is decided on the GPU: a captured call can be replayed with other lengths, tables and contents.
+ * Equal inputs give equal bits.  A table entry that is needed and names no page of the cache is read as a page of
+ * zeros, and the status word reports kind 5.
+ * H_kv must divide H; max_pages * page_size and T are below 2^31 - 1024, and so is the number of places
+ * (128-row key tiles, and two more, of every run of new tokens that shares a product: 256 query rows of a
+ * K/V head) that the table's shape allows (ATTN_ERR_SHAPE).  Returns an attn_status.
+ */
+ATTN_API int attn_fwd_paged_varlen(const void* q, const attn_kv_cache* cache, const int32_t* block_table,
+                                   const int32_t* seq_lens, const int32_t* cu_new, void* o, float* lse,
+                                   int B, int T, int H, int H_kv, int d, int max_pages, int causal,
+                                   float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes attn_fwd_paged_varlen needs (0 for invalid sizes). */
+ATTN_API size_t attn_fwd_paged_varlen_workspace_bytes(int T, int H, int H_kv, int d);
+
+/*
+ * Attention of one new token of each of B requests whose first rows are shared: requests cu_groups[g] ..
+ * cu_groups[g+1]-1 have the prefix_lens[g] rows of the pages prefix_table[g][0], [1], ... before the seq_lens[s] rows
+ * of their own, block_table[s][0], [1], ....  O and lse are those of attn_fwd_paged over the rows of both, but the
+ * prefix is read once for a group (once for each 256 / (H / H_kv) of its requests) instead of once a request.  Four
+ * launches: attn_fwd_paged over the own rows, left in fp32, attn_fwd_paged_varlen's kernels over the prefixes,
+ * and the block merge of the two.
+ *   q, o : bf16 [B, H, d] (= [B, H, 1, d]);  lse : fp32 [B, H]
+ *   prefix_table : int32 [groups, max_prefix_pages];  prefix_lens : int32 [groups], clamped to 0 ..
+ *     max_prefix_pages * page_size;  cu_groups : int32 [groups + 1], from 0 up, at most B (as cu_new of
+ *     attn_fwd_paged_varlen: o and lse of requests from cu_groups[groups] on are left as they were)
+ *   block_table, seq_lens : as attn_fwd_paged.  Either length may be 0; with both, O = 0 and lse = -inf.
+ *   workspace : attn_fwd_paged_shared_workspace_bytes(B, H, H_kv, d) bytes, 256-byte aligned; calls whose
+ *     work may overlap on the GPU need one each.
+ * Pages, table entries, graphs, limits and errors as attn_fwd_paged and attn_fwd_paged_varlen.
+ */
+ATTN_API int attn_fwd_paged_shared(const void* q, const attn_kv_cache* cache, const int32_t* prefix_table,
+                                   const int32_t* prefix_lens, const int32_t* cu_groups,
+                                   const int32_t* block_table, const int32_t* seq_lens, void* o, float* lse,
+                                   int groups, int B, int H, int H_kv, int d, int max_prefix_pages,
+                                   int max_pages, float scale, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/* Workspace bytes attn_fwd_paged_shared needs (0 for invalid sizes). */
+ATTN_API size_t attn_fwd_paged_shared_workspace_bytes(int B, int H, int H_kv, int d);
+
+/*
+ * K and V rows into a paged cache, without the step before attention (rows that are rotated already, or need no
+ * rotation, or come from attn_kv_read of another cache): token (b, n)'s rows of every K/V head go to slots[b, n]
+ * (int64 [B, N]; negative: not stored).  E4M3 caches get codes and scales as from attn_qkv_rope.
+ *   k, v : bf16 rows of d contiguous elements, at b * strides[0] + head * strides[1] + n * strides[2]
+ *     elements (k_strides, v_strides: host arrays of three; not negative, multiples of 8 where the
+ *     dimension has more than one element); 16-byte aligned, not overlapping the cache
+ * A slot past the cache is not stored and the status word reports kind 5.  What two tokens with one slot leave
+ * there is unspecified.  One launch.  B * N is below 2^31 - 1024.  Returns an attn_status.
+ */
+ATTN_API int attn_kv_write(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                           const attn_kv_cache* cache, const int64_t* slots, int B, int N, int H_kv, int d,
+                           void* stream);
+
+/*
+ * Rows of B requests back out of a paged cache, packed as attn_fwd and attn_bwd_varlen take them: row
+ * cu_rows[s] + i of k and v is row first[s] + i of request s's pages block_table[s][0], [1], ..., for i <
+ * cu_rows[s+1] - cu_rows[s].  E4M3 rows become code * scale, rounded once to bf16; bf16 rows are copied.
+ *   k, v : bf16 [H_kv, T, d] outputs;  cu_rows : int32 [B + 1], from 0 up, at most T: rows from
+ *     cu_rows[B] on are left as they were (cu_rows that decreases, does not begin with 0 or passes T: kind 2);
+ *   first : int32 [B], or NULL for zeros;  block_table : int32 [B, max_pages]
+ * A row before the first or past the table, or whose entry names no page of the cache, becomes zeros and the
+ * status word reports kind 5.  One launch.  T is below 2^31 - 1024.  Returns an attn_status.
+ */
+ATTN_API int attn_kv_read(const attn_kv_cache* cache, const int32_t* block_table, const int32_t* cu_rows,
+                          const int32_t* first, void* k, void* v, int B, int T, int H_kv, int d, int max_pages,
+                          void* stream);
 
 /*
  * Unfused comparison path (the "standard attention" of the pages: S written to HBM, read back for

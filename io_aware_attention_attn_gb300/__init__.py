@@ -6,7 +6,9 @@ the first call does, and fails loudly if the library is missing.
 """
 __all__ = ["attn_fwd", "attn_bwd", "bwd_workspace_bytes", "attn_fwd_splitkv", "quantize_fp8", "attn_fwd_fp8", "splitkv_workspace_bytes", "attn_fwd_unfused",
            "unfused_workspace_bytes", "last_device_error", "KVCache", "kv_cache", "kv_slots",
-           "rope_inv_freq", "qkv_rope", "qkv_rope_bwd", "attn_fwd_paged", "paged_workspace_bytes"]
+           "rope_inv_freq", "qkv_rope", "qkv_rope_bwd", "attn_fwd_paged", "paged_workspace_bytes",
+           "attn_fwd_paged_varlen", "paged_varlen_workspace_bytes", "attn_fwd_paged_shared",
+           "paged_shared_workspace_bytes", "kv_write", "kv_read"]
 
 
 def __getattr__(name):

@@ -50,6 +50,13 @@ SIGNATURES = {
     "attn_qkv_rope_bwd_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
     "attn_fwd_paged": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _S, _P]),
     "attn_fwd_paged_workspace_bytes": (_S, [_I, _I, _I, _I]),
+    "attn_fwd_paged_varlen": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _S, _P]),
+    "attn_fwd_paged_varlen_workspace_bytes": (_S, [_I, _I, _I, _I]),
+    "attn_fwd_paged_shared": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P,
+                                   _S, _P]),
+    "attn_fwd_paged_shared_workspace_bytes": (_S, [_I, _I, _I, _I]),
+    "attn_kv_write": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
+    "attn_kv_read": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
     "attn_fwd_unfused": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _S, _P]),
     "attn_fwd_unfused_workspace_bytes": (_S, [_I, _I, _I, _I]),
     "attn_fwd_unfused_noalloc": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P]),
@@ -354,8 +361,7 @@ def kv_slots(seq_lens, cu_new, T: int, block_table, free_pages, free_head, page_
     int32 [B], cu_new int32 [B + 1], block_table int32 [B, max_pages] (new entries are written),
     free_pages int32 [n], free_head int32 [1].  Returns (slots int64 [T], positions int32 [T],
     block_table, new seq_lens, new free_head); the old seq_lens and free_head are left alone.
-    A request may hold tokens and get several more, but nothing here attends for those: attn_fwd takes
-    whole prompts, attn_fwd_paged one new token a request.
+    A request may hold tokens and get several more: attn_fwd_paged_varlen attends for those.
     Slots and positions share one storage, and so do lengths and head (all four at up to one new token a
     request): clone what is saved or handed to another process by itself."""
     if stream is not None:
@@ -428,6 +434,64 @@ def attn_fwd_paged(q, cache, block_table, seq_lens, scale: float | None = None, 
         with _on(stream, q.device):
             return attn_fwd_paged(q, cache, block_table, seq_lens, scale, workspace, out, lse)
     return _native().attn_fwd_paged(q, *cache, block_table, seq_lens, scale, workspace, out, lse)
+
+
+def paged_varlen_workspace_bytes(T: int, H: int, H_kv: int, d: int) -> int:
+    return int(lib().attn_fwd_paged_varlen_workspace_bytes(T, H, H_kv, d))
+
+
+def attn_fwd_paged_varlen(q, cache, block_table, seq_lens, cu_new, causal: bool = True,
+                          scale: float | None = None, workspace=None, out=None, lse=None, stream=None):
+    """Attention of several new tokens of each request over a paged cache: q [H, T, d] packed by cu_new int32
+    [B + 1], block_table int32 [B, max_pages], seq_lens int32 [B] (rows in the cache, the new tokens'
+    own among them).  Token i of a request's n sees rows 0 .. seq_lens - n + i, or all of them with
+    causal=False.  Returns (O bf16 like q, LSE fp32 [H, T]); tokens from cu_new[B] on are padding, their
+    rows are left as they were in ``out`` and ``lse`` (unspecified where those are not given)."""
+    if stream is not None:
+        with _on(stream, q.device):
+            return attn_fwd_paged_varlen(q, cache, block_table, seq_lens, cu_new, causal, scale, workspace, out, lse)
+    return _native().attn_fwd_paged_varlen(q, *cache, block_table, seq_lens, cu_new, causal, scale, workspace, out,
+                                           lse)
+
+
+def paged_shared_workspace_bytes(B: int, H: int, H_kv: int, d: int) -> int:
+    return int(lib().attn_fwd_paged_shared_workspace_bytes(B, H, H_kv, d))
+
+
+def attn_fwd_paged_shared(q, cache, prefix_table, prefix_lens, cu_groups, block_table, seq_lens,
+                          scale: float | None = None, workspace=None, out=None, lse=None, stream=None):
+    """attn_fwd_paged for requests that share their first rows, which are read once for all of a group:
+    requests cu_groups[g] .. cu_groups[g+1]-1 (int32 [groups + 1]) have the prefix_lens[g] rows of the pages
+    prefix_table[g] (int32 [groups, max_prefix_pages]) before the seq_lens rows of their own pages block_table.
+    q [B, H, 1, d] (or [B, H, d]).  Returns (O bf16 like q, LSE fp32 [B, H, 1] or [B, H])."""
+    if stream is not None:
+        with _on(stream, q.device):
+            return attn_fwd_paged_shared(q, cache, prefix_table, prefix_lens, cu_groups, block_table, seq_lens, scale,
+                                         workspace, out, lse)
+    return _native().attn_fwd_paged_shared(q, *cache, prefix_table, prefix_lens, cu_groups, block_table, seq_lens,
+                                           scale, workspace, out, lse)
+
+
+def kv_write(k, v, cache, slots, stream=None):
+    """K and V rows into the cache at ``slots`` (int64; negative: not stored), without norm or rotation: k, v
+    [B, H_kv, N, d] with slots [B, N], or [H_kv, T, d] with slots [T]; any strides that keep rows of d
+    contiguous (a projection's token-major rows, transposed, are fine).  E4M3 caches get codes
+    and scales as from qkv_rope.  Returns the cache."""
+    if stream is not None:
+        with _on(stream, k.device):
+            return kv_write(k, v, cache, slots)
+    _native().kv_write(k, v, *cache, slots)
+    return cache
+
+
+def kv_read(cache, block_table, cu_rows, T: int, first=None, out_k=None, out_v=None, stream=None):
+    """Rows of the cache's requests as packed bf16 k, v [H_kv, T, d] (what attn_fwd takes): row
+    cu_rows[s] + i is row first[s] + i (first int32 [B]; None: from the beginning) of request s's pages
+    block_table[s].  Rows from cu_rows[B] on are left as they were in ``out_k`` and ``out_v``."""
+    if stream is not None:
+        with _on(stream, cache.k.device):
+            return kv_read(cache, block_table, cu_rows, T, first, out_k, out_v)
+    return _native().kv_read(*cache, block_table, cu_rows, T, first, out_k, out_v)
 
 
 def unfused_workspace_bytes(B: int, H: int, N: int, d: int) -> int:

@@ -10,6 +10,7 @@
 #include "attn_gb300.h"
 #include "attn_host.h"
 #include "attn_bwd.h"
+#include "attn_chunk.h"
 #include "attn_fp8.h"
 #include "attn_gen.h"
 #include "attn_params.h"
@@ -97,6 +98,36 @@ int encode_cache_map(CUtensorMap* map, const void* base, bool e4m3, uint64_t d, 
   return fn(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+int encode_query_map(CUtensorMap* map, const void* base, uint64_t d, uint64_t heads, uint64_t tokens,
+                     uint64_t head_bytes, uint64_t token_bytes, uint32_t box_heads, uint32_t box_tokens) {
+  auto fn = encode_fn();
+  if (!fn) return CUDA_ERROR_NOT_FOUND;
+  const cuuint64_t dims[3] = {d, heads, tokens};
+  const cuuint64_t strides[2] = {head_bytes, token_bytes};
+  const cuuint32_t box[3] = {64, box_heads, box_tokens};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+int encode_page_map(CUtensorMap* map, const void* base, bool e4m3, uint64_t d, uint64_t page_size,
+                    uint64_t heads, uint64_t pages, uint64_t page_stride, uint32_t cols, uint32_t box_rows,
+                    bool flat) {
+  auto fn = encode_fn();
+  if (!fn) return CUDA_ERROR_NOT_FOUND;
+  const uint64_t size = e4m3 ? 1 : 2;
+  const cuuint64_t dims[4] = {d, page_size, heads, pages};
+  const cuuint64_t strides[3] = {d * size, d * size * page_size, page_stride * size};
+  const cuuint32_t box[4] = {cols, box_rows, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            flat ? CU_TENSOR_MAP_SWIZZLE_NONE
+                 : cols * size == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 

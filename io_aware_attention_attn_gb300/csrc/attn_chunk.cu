@@ -1,0 +1,166 @@
+// attn_chunk.cu -- the join of the parts that attn_chunk_kernel leaves, its instantiations and launcher.
+#include <atomic>
+
+#include "attn_chunk_kernel.cuh"
+
+namespace attn {
+namespace {
+
+// Merge of one unit's parts: M = max m_j, weights 2^(m_j - M).  Block x is for the unit that share x ends and an
+// earlier one began, if there is one.  A warp takes 32 rows and 8 columns -- parts lie column by column, so its
+// loads are contiguous -- and, of a unit of many parts, every second, fourth or eighth, joined through shared
+// memory.  What bounds it is the latency of the few loads in a row.
+constexpr int kJoinWarps = 8, kAtOnce = 4;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const __grid_constant__ ChunkParams p) {
+  __shared__ float s_o[kJoinWarps][8][32];
+  __shared__ float2 s_ml[kJoinWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();  // by every block, so that the work after this one waits for the parts' kernel too
+  const int x = static_cast<int>(blockIdx.x);
+  const int total = p.head[0], n_shares = p.head[1];
+  if (x >= n_shares) return;
+  const ChunkDesc d = p.desc[x];
+  if (d.tiles < 0) return;
+  const Shares shares(static_cast<uint32_t>(total), static_cast<uint32_t>(n_shares));
+  const int i0 = shares.owner(static_cast<uint32_t>(d.unit0)), n = x - i0 + 1;
+  // the beginning share's second part, if it holds tiles of the unit before
+  const int second = second_part(shares.start(i0), d.unit0, p.shape.cost);
+  const int z = d.u / p.n_rg, head0 = (d.u - z * p.n_rg) * p.rg_rows;
+  const int share = n <= kAtOnce ? 1 : n <= 2 * kAtOnce ? 2 : n <= 4 * kAtOnce ? 4 : 8;
+  const int side = kJoinWarps / share, sub = warp % share;
+  constexpr int kTasks = 8 * (D / 8);
+  for (int t0 = blockIdx.y * side; t0 < kTasks; t0 += gridDim.y * side) {
+    const int task = t0 + warp / share, c8 = task % (D / 8);
+    const int at = (task / (D / 8)) * 32 + lane, row = at & (kChunkRows - 1);
+    const int tok_in = row / p.rg_rows, head = row - tok_in * p.rg_rows;
+    const int tok = (at >> 7) * p.cta_tokens + tok_in;
+    const bool valid = tok_in < p.cta_tokens && tok < d.n_tok && head0 + head < p.group;
+    float acc[8], m = -INFINITY, l = 0.f;
+    #pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] = 0.f;
+    if (valid) {
+      for (int j0 = sub; j0 < n; j0 += kAtOnce * share) {
+        float2 ml[kAtOnce];
+        float4 a[kAtOnce], b[kAtOnce];
+        #pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const int j = j0 + k * share;
+          ml[k] = make_float2(-INFINITY, 0.f);
+          a[k] = b[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (j < n) {
+            const int64_t slot = 2 * (i0 + j) + (j == 0 ? second : 0);
+            ml[k] = *reinterpret_cast<const float2*>(p.part_ml + (slot * p.part_rows + at) * 2);
+            const float4* src = reinterpret_cast<const float4*>(p.part_o + slot * p.part_rows * D) + at;
+            a[k] = src[(2 * c8) * p.part_rows];
+            b[k] = src[(2 * c8 + 1) * p.part_rows];
+          }
+        }
+        float top = m;
+        #pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, ml[k].x);
+        // a maximum of -inf: nothing, or NaN, which stays
+        const float keep = m == -INFINITY ? 1.f : ex2_approx(m - top);
+        l *= keep;
+        #pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] *= keep;
+        #pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const float wt = ml[k].x == -INFINITY ? 1.f : ex2_approx(ml[k].x - top);
+          const float v[8] = {a[k].x, a[k].y, a[k].z, a[k].w, b[k].x, b[k].y, b[k].z, b[k].w};
+          l = fmaf(wt, ml[k].y, l);
+          #pragma unroll
+          for (int c = 0; c < 8; ++c) acc[c] = fmaf(wt, v[c], acc[c]);
+        }
+        m = top;
+      }
+    }
+    if (share > 1) {  // the same for the whole block
+      #pragma unroll
+      for (int c = 0; c < 8; ++c) s_o[warp][c][lane] = acc[c];
+      s_ml[warp][lane] = make_float2(m, l);
+      __syncthreads();
+      if (sub == 0) {
+        float top = -INFINITY;
+        for (int k = 0; k < share; ++k) top = fmaxf(top, s_ml[warp + k][lane].x);
+        m = top;
+        l = 0.f;
+        #pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] = 0.f;
+        for (int k = 0; k < share; ++k) {
+          const float2 ml = s_ml[warp + k][lane];
+          const float wt = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - top);
+          l = fmaf(wt, ml.y, l);
+          #pragma unroll
+          for (int c = 0; c < 8; ++c) acc[c] = fmaf(wt, s_o[warp + k][c][lane], acc[c]);
+        }
+      }
+      __syncthreads();
+    }
+    if (sub != 0 || !valid) continue;
+    const int64_t tq = d.tok + tok, hq = z * p.group + head0 + head;
+    float wt = l > 0.f || l != l ? 1.f / l : 0.f;
+    float lse = l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+    #pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] *= wt;
+    if (p.tail_o) {  // the same row over other keys
+      const float other = p.tail_lse[tq * p.H + hq], top = fmaxf(lse, other);
+      const float wa = lse == -INFINITY ? 0.f : ex2_approx((lse - top) * 1.4426950408889634f);
+      const float wb = other == -INFINITY ? 0.f : ex2_approx((other - top) * 1.4426950408889634f);
+      const float sum = wa + wb, inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+      const float4* src = reinterpret_cast<const float4*>(p.tail_o + (tq * p.H + hq) * D + 8 * c8);
+      const float4 a = src[0], b = src[1];
+      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      #pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c] = (acc[c] * wa + v[c] * wb) * inv;
+      lse = sum > 0.f || sum != sum ? top + log2f(sum) * 0.69314718055994530942f : -INFINITY;
+    }
+    const int64_t to = hq * p.o_head + tq * p.o_token;
+    *reinterpret_cast<uint4*>(p.o + to + 8 * c8) =
+        make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
+                   pack_bf16x2(acc[6], acc[7]));
+    if (c8 == 0) p.lse[to / D] = lse;
+  }
+}
+
+template <int D, bool E4M3>
+cudaError_t launch(const ChunkParams& p, cudaStream_t stream) {
+  using L = ChunkLayout<D, E4M3>;
+  auto* kernel = attn_chunk_kernel<D, E4M3>;
+  static std::atomic<int> fit[64] = {};  // clusters that fit at once, per device (0: not known yet)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int clusters = fit[dev & 63].load(std::memory_order_acquire);
+  if (clusters == 0) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDyn);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * kChunkClusters);
+    cfg.blockDim = dim3(L::kThreads);
+    cfg.dynamicSmemBytes = L::kDyn;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+      (void)cudaGetLastError();
+      n = kChunkClusters;
+    }
+    clusters = n < kChunkClusters ? n : kChunkClusters;
+    fit[dev & 63].store(clusters, std::memory_order_release);
+  }
+  ChunkParams q = p;
+  if (q.clusters > clusters) q.clusters = clusters;
+  e = launch_dependent(kernel, dim3(2 * static_cast<unsigned>(q.clusters)), L::kThreads, L::kDyn, stream, q);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(chunk_join_kernel<D>, dim3(static_cast<unsigned>(q.clusters * q.max_rounds), D / 8),
+                          kJoinWarps * 32, 0, stream, q);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk(const ChunkParams& p, int d, bool e4m3, cudaStream_t stream) {
+  if (d == 64) return e4m3 ? launch<64, true>(p, stream) : launch<64, false>(p, stream);
+  return e4m3 ? launch<128, true>(p, stream) : launch<128, false>(p, stream);
+}
+
+}  // namespace attn

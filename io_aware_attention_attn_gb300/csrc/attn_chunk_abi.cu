@@ -1,0 +1,268 @@
+// attn_chunk_abi.cu -- entry points of work over a paged cache beyond one new token a request: argument
+// validation and launch of attention of several new tokens, of requests behind a shared prefix, and of the
+// kernels that write rows into a cache and read them back.
+#include <climits>
+#include <cmath>
+
+#include "attn_cache_host.h"
+#include "attn_chunk.h"
+#include "attn_gb300.h"
+#include "attn_gen.h"
+#include "attn_host.h"
+
+namespace attn {
+namespace {
+
+// Places that a unit takes beside its key tiles: loading the query rows, the first tile's maximum, O out.
+constexpr int kChunkCost = 2;
+
+// The kernel numbers places in 32 bits and rows and tokens with some room to spare.
+bool chunk_sizes_fit(int B, int T, int H, int H_kv, int max_pages, int page_size, const ChunkSizes& z) {
+  const int64_t most = static_cast<int64_t>(max_pages) * page_size;
+  if (most > INT_MAX - 1024 || T > INT_MAX - 1024 || static_cast<int64_t>(H_kv) * z.n_rg > INT_MAX) return false;
+  const int64_t tiles = (most + kChunkTile - 1) / kChunkTile + 1;
+  const int64_t rows = static_cast<int64_t>(T) / (2 * z.cta_tokens) + (B < T ? B : T);  // row tiles, at most
+  return rows <= INT_MAX / (tiles + kChunkCost) / (static_cast<int64_t>(H_kv) * z.n_rg);
+}
+
+struct QueryLayout {
+  int64_t head, token;  // elements from one query head, one token to the next
+};
+
+// Launch on checked arguments.
+int run_chunk(const void* q, const attn_kv_cache& c, const int32_t* table, const int32_t* seq_lens, const int32_t* cu,
+              void* o, float* lse, const float* tail_o, const float* tail_lse, int B, int T, int H, int H_kv, int d,
+              int max_pages, int causal, float scale, QueryLayout at, const ChunkSizes& z, uint8_t* ws,
+              cudaStream_t stream) {
+  const bool e4m3 = c.dtype == ATTN_CACHE_E4M3;
+  ChunkParams p{};
+  p.box_rows = c.page_size < 64 ? c.page_size : 64;
+  if (encode_query_map(&p.tm_q, q, d, H, T, at.head * 2, at.token * 2, z.rg_rows, z.cta_tokens) != CUDA_SUCCESS ||
+      encode_page_map(&p.tm_k, c.k, e4m3, d, c.page_size, H_kv, c.num_pages, c.page_stride, e4m3 ? d : 64, p.box_rows,
+                      false) != CUDA_SUCCESS ||
+      encode_page_map(&p.tm_v, c.v, e4m3, d, c.page_size, H_kv, c.num_pages, c.page_stride, 64, p.box_rows, e4m3) !=
+          CUDA_SUCCESS)
+    return ATTN_ERR_LAUNCH;
+  p.cu = cu;
+  p.seq_lens = seq_lens;
+  p.table = table;
+  p.ks = c.k_scale;
+  p.vs = c.v_scale;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.o_head = at.head;
+  p.o_token = at.token;
+  p.tail_o = tail_o;
+  p.tail_lse = tail_lse;
+  p.part_o = reinterpret_cast<float*>(ws + z.o_off);
+  p.part_ml = reinterpret_cast<float*>(ws + z.ml_off);
+  p.desc = reinterpret_cast<ChunkDesc*>(ws + z.desc_off);
+  p.head = reinterpret_cast<int*>(ws + z.head_off);
+  p.status = status_word();
+  if (!p.status) return ATTN_ERR_LAUNCH;
+  p.B = B;
+  p.T = T;
+  p.H = H;
+  p.H_kv = H_kv;
+  p.group = H / H_kv;
+  p.n_rg = z.n_rg;
+  p.rg_rows = z.rg_rows;
+  p.cta_tokens = z.cta_tokens;
+  p.max_pages = max_pages;
+  p.num_pages = c.num_pages;
+  p.page_shift = log2_of(c.page_size);
+  p.part_rows = z.part_rows;
+  p.max_rounds = z.rounds;
+  p.shape = ChunkShape{2 * z.cta_tokens, causal, kChunkCost};
+  p.scale_log2 = scale * 1.4426950408889634f;
+  // clusters: no more than the largest number of shares that the table's shape allows
+  const int64_t most = static_cast<int64_t>(max_pages) * c.page_size;
+  const int64_t tiles = (most + kChunkTile - 1) / kChunkTile + 1;
+  const int64_t units = (static_cast<int64_t>(T) / (2 * z.cta_tokens) + (B < T ? B : T)) * H_kv * z.n_rg;
+  const int64_t shares = units * (tiles + kChunkCost) / kChunkMinShare + 1;
+  p.clusters = shares < kChunkClusters ? static_cast<int>(shares) : kChunkClusters;
+  return launch_chunk(p, d, e4m3, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct SharedLayout {
+  size_t tail_o, tail_lse, chunk, total;  // the paged attention's workspace comes first
+};
+SharedLayout shared_layout(int B, int H, int group, int d, const ChunkSizes& z) {
+  SharedLayout s{};
+  s.tail_o = paged_layout(group, d).total;
+  s.tail_lse = s.tail_o + up256(static_cast<size_t>(B) * H * d * 4);
+  s.chunk = s.tail_lse + up256(static_cast<size_t>(B) * H * 4);
+  s.total = s.chunk + z.total;
+  return s;
+}
+
+}  // namespace
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" size_t attn_fwd_paged_varlen_workspace_bytes(int T, int H, int H_kv, int d) {
+  if (T <= 0 || H <= 0 || H_kv <= 0 || H % H_kv != 0 || (d != 64 && d != 128)) return 0;
+  return chunk_sizes(H / H_kv, T, d).total;
+}
+
+extern "C" int attn_fwd_paged_varlen(const void* q, const attn_kv_cache* cache, const int32_t* block_table,
+                                     const int32_t* seq_lens, const int32_t* cu_new, void* o, float* lse, int B, int T,
+                                     int H, int H_kv, int d, int max_pages, int causal, float scale, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  if (B < 0 || T < 0 || H < 0 || H_kv < 0 || max_pages < 0 || (B == 0 && T > 0)) return ATTN_ERR_SHAPE;
+  if (B == 0 || T == 0 || H == 0) return ATTN_OK;
+  if (d != 64 && d != 128) return ATTN_ERR_HEAD_DIM;
+  if (H_kv == 0 || H % H_kv != 0) return ATTN_ERR_SHAPE;
+  if (!q || !cache || !seq_lens || !cu_new || !o || !lse || (max_pages > 0 && !block_table)) return ATTN_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(cu_new, 4))
+    return ATTN_ERR_ALIGN;
+  int rc = check_cache(*cache, H_kv, d);
+  if (rc != ATTN_OK) return rc;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_SCALE;
+  const ChunkSizes z = chunk_sizes(H / H_kv, T, d);
+  if (!chunk_sizes_fit(B, T, H, H_kv, max_pages, cache->page_size, z)) return ATTN_ERR_SHAPE;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < z.total) return ATTN_ERR_WORKSPACE;
+  if ((rc = check_device()) != 0) return rc;
+  return run_chunk(q, *cache, block_table, seq_lens, cu_new, o, lse, nullptr, nullptr, B, T, H, H_kv, d, max_pages,
+                   causal != 0, scale, QueryLayout{static_cast<int64_t>(T) * d, d}, z, static_cast<uint8_t*>(workspace),
+                   static_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t attn_fwd_paged_shared_workspace_bytes(int B, int H, int H_kv, int d) {
+  if (B <= 0 || H <= 0 || H_kv <= 0 || H % H_kv != 0 || (d != 64 && d != 128)) return 0;
+  return shared_layout(B, H, H / H_kv, d, chunk_sizes(H / H_kv, B, d)).total;
+}
+
+extern "C" int attn_fwd_paged_shared(const void* q, const attn_kv_cache* cache, const int32_t* prefix_table,
+                                     const int32_t* prefix_lens, const int32_t* cu_groups, const int32_t* block_table,
+                                     const int32_t* seq_lens, void* o, float* lse, int groups, int B, int H, int H_kv,
+                                     int d, int max_prefix_pages, int max_pages, float scale, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  if (groups < 0 || B < 0 || H < 0 || H_kv < 0 || max_prefix_pages < 0 || max_pages < 0 || (groups == 0 && B > 0))
+    return ATTN_ERR_SHAPE;
+  if (groups == 0 || B == 0 || H == 0) return ATTN_OK;
+  if (d != 64 && d != 128) return ATTN_ERR_HEAD_DIM;
+  if (H_kv == 0 || H % H_kv != 0) return ATTN_ERR_SHAPE;
+  if (!q || !cache || !prefix_lens || !cu_groups || !seq_lens || !o || !lse || (max_prefix_pages > 0 && !prefix_table) ||
+      (max_pages > 0 && !block_table))
+    return ATTN_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(prefix_table, 4) || !aligned(prefix_lens, 4) ||
+      !aligned(cu_groups, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4))
+    return ATTN_ERR_ALIGN;
+  int rc = check_cache(*cache, H_kv, d);
+  if (rc != ATTN_OK) return rc;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_SCALE;
+  const ChunkSizes z = chunk_sizes(H / H_kv, B, d);
+  if (!paged_sizes_fit(B, H, H_kv, max_pages, cache->page_size) ||
+      !chunk_sizes_fit(groups, B, H, H_kv, max_prefix_pages, cache->page_size, z))
+    return ATTN_ERR_SHAPE;
+  const SharedLayout s = shared_layout(B, H, H / H_kv, d, z);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < s.total) return ATTN_ERR_WORKSPACE;
+  if ((rc = check_device()) != 0) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* tail_o = reinterpret_cast<float*>(ws + s.tail_o);
+  float* tail_lse = reinterpret_cast<float*>(ws + s.tail_lse);
+  // each request's own rows first, in fp32; the prefix's results are merged with them where they are finished
+  rc = run_fwd_paged(q, *cache, block_table, seq_lens, nullptr, tail_o, tail_lse, B, H, H_kv, d, max_pages, scale, ws,
+                     static_cast<cudaStream_t>(stream));
+  if (rc != ATTN_OK) return rc;
+  return run_chunk(q, *cache, prefix_table, prefix_lens, cu_groups, o, lse, tail_o, tail_lse, groups, B, H, H_kv, d,
+                   max_prefix_pages, 0, scale, QueryLayout{d, static_cast<int64_t>(H) * d}, z, ws + s.chunk,
+                   static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+// What writing and reading take alike.
+void cache_fields(KvRowsParams& p, const attn_kv_cache& c, int H_kv) {
+  p.kc = static_cast<uint8_t*>(c.k);
+  p.vc = static_cast<uint8_t*>(c.v);
+  p.ks = c.k_scale;
+  p.vs = c.v_scale;
+  p.page_stride = c.page_stride;
+  p.num_pages = c.num_pages;
+  p.page_shift = log2_of(c.page_size);
+  p.H_kv = H_kv;
+}
+
+// Whether strides (elements) keep rows on 16 bytes and their offsets within 64 bits.
+bool strides_ok(const int64_t* s, int B, int H, int N) {
+  const int64_t n[3] = {B, H, N};
+  int64_t left = 1ll << 62;
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] <= 1) continue;
+    if (s[i] < 0 || s[i] % 8 != 0 || s[i] > left / n[i]) return false;
+    left -= s[i] * n[i];
+  }
+  return true;
+}
+
+}  // namespace
+
+extern "C" int attn_kv_write(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                             const attn_kv_cache* cache, const int64_t* slots, int B, int N, int H_kv, int d,
+                             void* stream) {
+  if (B < 0 || N < 0 || H_kv < 0) return ATTN_ERR_SHAPE;
+  if (B == 0 || N == 0 || H_kv == 0) return ATTN_OK;
+  if (d != 64 && d != 128) return ATTN_ERR_HEAD_DIM;
+  if (!k || !k_strides || !v || !v_strides || !cache || !slots) return ATTN_ERR_NULL;
+  if (static_cast<int64_t>(B) * N > INT_MAX - 1024 || !strides_ok(k_strides, B, H_kv, N) ||
+      !strides_ok(v_strides, B, H_kv, N))
+    return ATTN_ERR_SHAPE;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8)) return ATTN_ERR_ALIGN;
+  int rc = check_cache(*cache, H_kv, d);
+  if (rc != ATTN_OK) return rc;
+  if ((rc = check_device()) != 0) return rc;
+  KvRowsParams p{};
+  cache_fields(p, *cache, H_kv);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.k_batch = k_strides[0];
+  p.k_head = k_strides[1];
+  p.k_token = k_strides[2];
+  p.v_batch = v_strides[0];
+  p.v_head = v_strides[1];
+  p.v_token = v_strides[2];
+  p.slots = slots;
+  p.B = B;
+  p.N = N;
+  p.status = status_word();
+  if (!p.status) return ATTN_ERR_LAUNCH;
+  return launch_kv_write(p, d, cache->dtype == ATTN_CACHE_E4M3, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_LAUNCH;
+}
+
+extern "C" int attn_kv_read(const attn_kv_cache* cache, const int32_t* block_table, const int32_t* cu_rows,
+                            const int32_t* first, void* k, void* v, int B, int T, int H_kv, int d, int max_pages,
+                            void* stream) {
+  if (B < 0 || T < 0 || H_kv < 0 || max_pages < 0 || (B == 0 && T > 0)) return ATTN_ERR_SHAPE;
+  if (B == 0 || T == 0 || H_kv == 0) return ATTN_OK;
+  if (d != 64 && d != 128) return ATTN_ERR_HEAD_DIM;
+  if (!cache || !cu_rows || !k || !v || (max_pages > 0 && !block_table)) return ATTN_ERR_NULL;
+  if (T > INT_MAX - 1024) return ATTN_ERR_SHAPE;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(block_table, 4) || !aligned(cu_rows, 4) || !aligned(first, 4))
+    return ATTN_ERR_ALIGN;
+  int rc = check_cache(*cache, H_kv, d);
+  if (rc != ATTN_OK) return rc;
+  if ((rc = check_device()) != 0) return rc;
+  KvRowsParams p{};
+  cache_fields(p, *cache, H_kv);
+  p.ko = static_cast<__nv_bfloat16*>(k);
+  p.vo = static_cast<__nv_bfloat16*>(v);
+  p.table = block_table;
+  p.cu = cu_rows;
+  p.first = first;
+  p.max_pages = max_pages;
+  p.B = B;
+  p.T = T;
+  p.status = status_word();
+  if (!p.status) return ATTN_ERR_LAUNCH;
+  return launch_kv_read(p, d, cache->dtype == ATTN_CACHE_E4M3, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_LAUNCH;
+}

@@ -8,6 +8,8 @@
 
 #include <cstdint>
 
+#include "attn_gb300.h"
+
 namespace attn {
 
 // kinds of the status word that this path adds (low byte)
@@ -87,6 +89,7 @@ struct PagedParams {
   CUtensorMap tm_v16;
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
+  float* o32;           // where the rows go instead of o, unrounded (null: to o)
   float* lse;
   const int* table;
   const int* seq_lens;
@@ -120,6 +123,13 @@ inline PagedLayout paged_layout(int group, int d) {
 }
 cudaError_t launch_fwd_paged(const PagedParams& p, int d, bool e4m3, int max_tiles,
                              cudaStream_t stream);
+
+// The sizes that attn_fwd_paged takes, and its launch on checked arguments (attn_gen_abi.cu); with o32 the rows
+// go there in fp32 instead of to o.
+bool paged_sizes_fit(int B, int H, int H_kv, int max_pages, int page_size);
+int run_fwd_paged(const void* q, const attn_kv_cache& cache, const int32_t* block_table,
+                  const int32_t* seq_lens, void* o, float* o32, float* lse, int B, int H, int H_kv,
+                  int d, int max_pages, float scale, void* workspace, cudaStream_t stream);
 
 // Encode the 4-D map of a paged cache's K or V (attn_abi.cu).  Returns a CUresult.
 int encode_cache_map(CUtensorMap* map, const void* base, bool e4m3, uint64_t d, uint64_t page_size,

@@ -3,39 +3,13 @@
 #include <climits>
 #include <cmath>
 
+#include "attn_cache_host.h"
 #include "attn_gb300.h"
 #include "attn_gen.h"
 #include "attn_host.h"
 
 namespace attn {
 namespace {
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-// Checks of a cache that attn_qkv_rope and attn_fwd_paged share.
-int check_cache(const attn_kv_cache& c, int H_kv, int d) {
-  if (c.dtype != ATTN_CACHE_BF16 && c.dtype != ATTN_CACHE_E4M3) return ATTN_ERR_UNSUPPORTED;
-  if (c.page_size < 16 || c.page_size > 256 || (c.page_size & (c.page_size - 1)))
-    return ATTN_ERR_UNSUPPORTED;
-  if (c.num_pages <= 0) return ATTN_ERR_SHAPE;
-  const bool e4m3 = c.dtype == ATTN_CACHE_E4M3;
-  const int64_t size = e4m3 ? 1 : 2;
-  // (the tensor map's strides are below 2^40 bytes)
-  if (c.page_stride < static_cast<int64_t>(H_kv) * c.page_size * d ||
-      c.page_stride * size % 16 != 0 || c.page_stride >= (1ll << 39))
-    return ATTN_ERR_SHAPE;
-  if (!c.k || !c.v || (e4m3 && (!c.k_scale || !c.v_scale))) return ATTN_ERR_NULL;
-  if (!aligned(c.k, 16) || !aligned(c.v, 16) ||
-      (e4m3 && (!aligned(c.k_scale, 16) || !aligned(c.v_scale, 16))))
-    return ATTN_ERR_ALIGN;
-  return ATTN_OK;
-}
-
-int log2_of(int x) {
-  int s = 0;
-  while ((1 << s) < x) ++s;
-  return s;
-}
 
 // Checks that attn_qkv_rope and its backward share; fills the common fields.
 int rope_common(RopeParams& p, const void* qkv, int64_t ld, const void* wq, const void* wk,
@@ -70,6 +44,63 @@ int rope_common(RopeParams& p, const void* qkv, int64_t ld, const void* wq, cons
 }
 
 }  // namespace
+
+// The kernel numbers tiles, and the places a unit takes beside them, in 32 bits.
+bool paged_sizes_fit(int B, int H, int H_kv, int max_pages, int page_size) {
+  const int64_t most = static_cast<int64_t>(max_pages) * page_size;
+  if (most > INT_MAX - kPagedTile) return false;
+  const int64_t units = static_cast<int64_t>(B) * H_kv * paged_row_groups(H / H_kv);
+  const int64_t tiles = most > 0 ? (most + kPagedTile - 1) / kPagedTile : 1;
+  return static_cast<int64_t>(B) * H <= INT_MAX && units <= INT_MAX / (tiles + kPagedMaxCost);
+}
+
+int run_fwd_paged(const void* q, const attn_kv_cache& cache, const int32_t* block_table,
+                  const int32_t* seq_lens, void* o, float* o32, float* lse, int B, int H, int H_kv,
+                  int d, int max_pages, float scale, void* workspace, cudaStream_t stream) {
+  PagedParams p{};
+  const bool e4m3 = cache.dtype == ATTN_CACHE_E4M3;
+  p.box_rows = cache.page_size < kPagedTile ? cache.page_size : kPagedTile;
+  auto encode = [&](CUtensorMap* map, const void* base, uint32_t rows) {
+    return encode_cache_map(map, base, e4m3, d, cache.page_size, H_kv, cache.num_pages,
+                            cache.page_stride, rows) == CUDA_SUCCESS;
+  };
+  if (!encode(&p.tm_k, cache.k, p.box_rows) || !encode(&p.tm_v, cache.v, p.box_rows) ||
+      !encode(&p.tm_k16, cache.k, 16) || !encode(&p.tm_v16, cache.v, 16))
+    return ATTN_ERR_LAUNCH;
+  const int group = H / H_kv;
+  const PagedLayout L = paged_layout(group, d);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.o32 = o32;
+  p.lse = lse;
+  p.table = block_table;
+  p.seq_lens = seq_lens;
+  p.ks = cache.k_scale;
+  p.vs = cache.v_scale;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.part_o = reinterpret_cast<float*>(ws + L.o_off);
+  p.part_ml = reinterpret_cast<float*>(ws + L.ml_off);
+  p.status = status_word();
+  if (!p.status) return ATTN_ERR_LAUNCH;
+  p.B = B;
+  p.H = H;
+  p.H_kv = H_kv;
+  p.group = group;
+  p.n_rg = paged_row_groups(group);
+  p.rg_rows = (group + p.n_rg - 1) / p.n_rg;
+  p.max_pages = max_pages;
+  p.num_pages = cache.num_pages;
+  p.page_shift = log2_of(cache.page_size);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.trail = kPagedTrail / p.scale_log2;
+  const int64_t most = static_cast<int64_t>(max_pages) * cache.page_size;
+  const int64_t tiles = most > 0 ? (most + kPagedTile - 1) / kPagedTile : 1;
+  const int64_t units = static_cast<int64_t>(B) * H_kv * p.n_rg;
+  return launch_fwd_paged(p, d, e4m3, static_cast<int>(units * tiles), stream) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_LAUNCH;
+}
+
 }  // namespace attn
 
 using namespace attn;
@@ -207,52 +238,10 @@ extern "C" int attn_fwd_paged(const void* q, const attn_kv_cache* cache, const i
   if (rc != ATTN_OK) return rc;
   if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_SCALE;
   const int group = H / H_kv;
-  const int64_t most = static_cast<int64_t>(max_pages) * cache->page_size;
-  if (most > INT_MAX - kPagedTile) return ATTN_ERR_SHAPE;
-  const int64_t units = static_cast<int64_t>(B) * H_kv * paged_row_groups(group);
-  const int64_t tiles = most > 0 ? (most + kPagedTile - 1) / kPagedTile : 1;
-  // the kernel numbers tiles, and the places a unit takes beside them, in 32 bits
-  if (static_cast<int64_t>(B) * H > INT_MAX || units > INT_MAX / (tiles + kPagedMaxCost))
-    return ATTN_ERR_SHAPE;
-  const PagedLayout L = paged_layout(group, d);
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total)
+  if (!paged_sizes_fit(B, H, H_kv, max_pages, cache->page_size)) return ATTN_ERR_SHAPE;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < paged_layout(group, d).total)
     return ATTN_ERR_WORKSPACE;
   if ((rc = check_device()) != 0) return rc;
-  PagedParams p{};
-  const bool e4m3 = cache->dtype == ATTN_CACHE_E4M3;
-  p.box_rows = cache->page_size < kPagedTile ? cache->page_size : kPagedTile;
-  auto encode = [&](CUtensorMap* map, const void* base, uint32_t rows) {
-    return encode_cache_map(map, base, e4m3, d, cache->page_size, H_kv, cache->num_pages,
-                            cache->page_stride, rows) == CUDA_SUCCESS;
-  };
-  if (!encode(&p.tm_k, cache->k, p.box_rows) || !encode(&p.tm_v, cache->v, p.box_rows) ||
-      !encode(&p.tm_k16, cache->k, 16) || !encode(&p.tm_v16, cache->v, 16))
-    return ATTN_ERR_LAUNCH;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.o = static_cast<__nv_bfloat16*>(o);
-  p.lse = lse;
-  p.table = block_table;
-  p.seq_lens = seq_lens;
-  p.ks = cache->k_scale;
-  p.vs = cache->v_scale;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.part_o = reinterpret_cast<float*>(ws + L.o_off);
-  p.part_ml = reinterpret_cast<float*>(ws + L.ml_off);
-  p.status = status_word();
-  if (!p.status) return ATTN_ERR_LAUNCH;
-  p.B = B;
-  p.H = H;
-  p.H_kv = H_kv;
-  p.group = group;
-  p.n_rg = paged_row_groups(group);
-  p.rg_rows = (group + p.n_rg - 1) / p.n_rg;
-  p.max_pages = max_pages;
-  p.num_pages = cache->num_pages;
-  p.page_shift = log2_of(cache->page_size);
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.trail = kPagedTrail / p.scale_log2;
-  return launch_fwd_paged(p, d, e4m3, static_cast<int>(units * tiles),
-                          static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? ATTN_OK
-             : ATTN_ERR_LAUNCH;
+  return run_fwd_paged(q, *cache, block_table, seq_lens, o, nullptr, lse, B, H, H_kv, d, max_pages,
+                       scale, workspace, static_cast<cudaStream_t>(stream));
 }

@@ -807,8 +807,12 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         if (whole) {
           const float inv = len > 0 ? 1.f / sum : 0.f;
           const int64_t at = out0 + row;
-          *reinterpret_cast<uint2*>(p.o + at * D + 4 * c4) =
-              make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+          if (p.o32)
+            *reinterpret_cast<float4*>(p.o32 + at * D + 4 * c4) =
+                make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+          else
+            *reinterpret_cast<uint2*>(p.o + at * D + 4 * c4) =
+                make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
           if (c4 == 0)
             p.lse[at] = sum > 0.f || sum != sum ? (top + log2f(sum)) * 0.69314718055994530942f
                                                 : -INFINITY;
@@ -957,12 +961,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __
       const int64_t out = static_cast<int64_t>(sh / p.H_kv) * p.H +
                           static_cast<int64_t>(sh % p.H_kv) * p.group + row0 + row;
       const float inv = 1.f / l;
-      __nv_bfloat16* dst = p.o + out * D + lane * kPer;
-      if constexpr (kPer == 4)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
-                                                    pack_bf16x2(acc[2] * inv, acc[3] * inv));
-      else
-        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+      if (p.o32) {
+        #pragma unroll
+        for (int c = 0; c < kPer; ++c) p.o32[out * D + lane * kPer + c] = acc[c] * inv;
+      } else {
+        __nv_bfloat16* dst = p.o + out * D + lane * kPer;
+        if constexpr (kPer == 4)
+          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                                                      pack_bf16x2(acc[2] * inv, acc[3] * inv));
+        else
+          *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+      }
       if (lane == 0)
         p.lse[out] = l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
     }

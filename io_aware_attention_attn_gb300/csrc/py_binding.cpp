@@ -373,6 +373,163 @@ PyObject* py_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// A head count that H is a multiple of, from a cache's K.
+int64_t kv_heads(const at::Tensor& k, int64_t H) {
+  require(k.dim() == 4 && k.size(1) > 0 && H % k.size(1) == 0,
+          "the number of K/V heads must divide the number of query heads");
+  return k.size(1);
+}
+float scale_or(PyObject* o, int64_t d) {
+  return o == Py_None ? 1.f / std::sqrt(static_cast<float>(d)) : real(o);
+}
+// A two-dimensional int32 table and its row length.
+const int32_t* table_of(const at::Tensor& t, int64_t rows, at::Device dev, const char* name, int& cols) {
+  TORCH_CHECK_VALUE(t.dim() == 2 && t.size(1) <= INT32_MAX, name, " must be [requests, pages]");
+  cols = static_cast<int>(t.size(1));
+  return static_cast<const int32_t*>(address(t, at::kInt, {rows, cols}, dev, name));
+}
+
+// (q, cache k, v, k_scale, v_scale, block_table, seq_lens, cu_new, causal, scale or None, workspace, out, lse)
+PyObject* py_paged_varlen(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  argc(n, 13);
+  const at::Tensor &q = tensor(a[0], "q"), &lens = tensor(a[6], "seq_lens");
+  at::Tensor ws = workspace(a[10], q.device());
+  require(q.scalar_type() == at::kBFloat16 && q.is_cuda() && q.is_contiguous() && q.dim() == 3,
+          "q must be a contiguous bf16 CUDA tensor [H, T, d]");
+  const at::Device dev = q.device();
+  const int64_t H = q.size(0), T = q.size(1), d = q.size(2);
+  const int64_t H_kv = kv_heads(tensor(a[1], "cache.k"), H);
+  const attn_kv_cache c = cache_struct(a + 1, H_kv, d, dev);
+  require(lens.dim() == 1, "seq_lens must be [B]");
+  const int64_t B = lens.size(0);
+  require(B <= INT32_MAX && H <= INT32_MAX && T <= INT32_MAX && d <= INT32_MAX, "sizes must fit 32 bits");
+  int cols = 0;
+  const int32_t* tp = table_of(tensor(a[5], "block_table"), B, dev, "block_table", cols);
+  const auto* lp = static_cast<const int32_t*>(address(lens, at::kInt, {B}, dev, "seq_lens"));
+  const auto* cp = static_cast<const int32_t*>(address(tensor(a[7], "cu_new"), at::kInt, {B + 1}, dev, "cu_new"));
+  at::Tensor out = maybe(a[11], "out"), lse = maybe(a[12], "lse");
+  address(out, at::kBFloat16, q.sizes(), dev, "out");
+  address(lse, at::kFloat, {H, T}, dev, "lse");
+  const bool causal = truth(a[8]);
+  const float scale = scale_or(a[9], d);
+  const int Bi = static_cast<int>(B), Ti = static_cast<int>(T), Hi = static_cast<int>(H);
+  const int Ki = static_cast<int>(H_kv), di = static_cast<int>(d);
+  Launch on(dev);
+  if (!ws.defined())
+    ws = make({static_cast<int64_t>(attn_fwd_paged_varlen_workspace_bytes(Ti, Hi, Ki, di))}, at::kByte, dev);
+  if (!out.defined()) out = make(q.sizes(), at::kBFloat16, dev);
+  if (!lse.defined()) lse = make({H, T}, at::kFloat, dev);
+  check("attn_fwd_paged_varlen",
+        attn_fwd_paged_varlen(q.data_ptr(), &c, tp, lp, cp, out.data_ptr(), static_cast<float*>(lse.data_ptr()), Bi,
+                              Ti, Hi, Ki, di, cols, causal, scale, ws.data_ptr(), ws.nbytes(), on.stream));
+  return pack({out, lse});
+  END_HANDLE_TH_ERRORS
+}
+
+// (q, cache k, v, k_scale, v_scale, prefix_table, prefix_lens, cu_groups, block_table, seq_lens, scale or None,
+//  workspace, out, lse)
+PyObject* py_paged_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  argc(n, 14);
+  const at::Tensor &q = tensor(a[0], "q"), &plens = tensor(a[6], "prefix_lens");
+  at::Tensor ws = workspace(a[11], q.device());
+  require(q.scalar_type() == at::kBFloat16 && q.is_cuda() && q.is_contiguous() &&
+              (q.dim() == 3 || (q.dim() == 4 && q.size(2) == 1)),
+          "q must be a contiguous bf16 CUDA tensor [B, H, 1, d] or [B, H, d]");
+  const at::Device dev = q.device();
+  const int64_t B = q.size(0), H = q.size(1), d = q.size(-1);
+  const int64_t H_kv = kv_heads(tensor(a[1], "cache.k"), H);
+  const attn_kv_cache c = cache_struct(a + 1, H_kv, d, dev);
+  require(plens.dim() == 1, "prefix_lens must be [groups]");
+  const int64_t groups = plens.size(0);
+  require(groups <= INT32_MAX && B <= INT32_MAX && H <= INT32_MAX && d <= INT32_MAX, "sizes must fit 32 bits");
+  int pcols = 0, cols = 0;
+  const int32_t* ptp = table_of(tensor(a[5], "prefix_table"), groups, dev, "prefix_table", pcols);
+  const auto* pp = static_cast<const int32_t*>(address(plens, at::kInt, {groups}, dev, "prefix_lens"));
+  const auto* gp = static_cast<const int32_t*>(
+      address(tensor(a[7], "cu_groups"), at::kInt, {groups + 1}, dev, "cu_groups"));
+  const int32_t* tp = table_of(tensor(a[8], "block_table"), B, dev, "block_table", cols);
+  const auto* lp = static_cast<const int32_t*>(address(tensor(a[9], "seq_lens"), at::kInt, {B}, dev, "seq_lens"));
+  const at::IntArrayRef rows = q.sizes().slice(0, q.dim() - 1);
+  at::Tensor out = maybe(a[12], "out"), lse = maybe(a[13], "lse");
+  address(out, at::kBFloat16, q.sizes(), dev, "out");
+  address(lse, at::kFloat, rows, dev, "lse");
+  const float scale = scale_or(a[10], d);
+  const int Bi = static_cast<int>(B), Hi = static_cast<int>(H), Ki = static_cast<int>(H_kv);
+  const int di = static_cast<int>(d);
+  Launch on(dev);
+  if (!ws.defined())
+    ws = make({static_cast<int64_t>(attn_fwd_paged_shared_workspace_bytes(Bi, Hi, Ki, di))}, at::kByte, dev);
+  if (!out.defined()) out = make(q.sizes(), at::kBFloat16, dev);
+  if (!lse.defined()) lse = make(rows, at::kFloat, dev);
+  check("attn_fwd_paged_shared",
+        attn_fwd_paged_shared(q.data_ptr(), &c, ptp, pp, gp, tp, lp, out.data_ptr(),
+                              static_cast<float*>(lse.data_ptr()), static_cast<int>(groups), Bi, Hi, Ki, di, pcols,
+                              cols, scale, ws.data_ptr(), ws.nbytes(), on.stream));
+  return pack({out, lse});
+  END_HANDLE_TH_ERRORS
+}
+
+// (k, v, cache k, v, k_scale, v_scale, slots)
+PyObject* py_kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  argc(n, 7);
+  const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &slots = tensor(a[6], "slots");
+  require(k.scalar_type() == at::kBFloat16 && v.scalar_type() == at::kBFloat16 && k.is_cuda() &&
+              (k.dim() == 3 || k.dim() == 4) && k.sizes() == v.sizes() && v.device() == k.device(),
+          "k and v must be bf16 CUDA tensors of one shape, [B, H_kv, N, d] or [H_kv, T, d], on one device");
+  const at::Device dev = k.device();
+  const bool packed = k.dim() == 3;
+  const int64_t B = packed ? 1 : k.size(0), H_kv = k.size(-3), N = k.size(-2), d = k.size(-1);
+  require(B <= INT32_MAX && H_kv <= INT32_MAX && N <= INT32_MAX && d <= INT32_MAX, "sizes must fit 32 bits");
+  require(k.numel() == 0 || (k.stride(-1) == 1 && v.stride(-1) == 1), "rows of k and v must be contiguous");
+  const attn_kv_cache c = cache_struct(a + 2, H_kv, d, dev);
+  const int64_t flat[1] = {B * N}, both[2] = {B, N};
+  const auto* sp = static_cast<const int64_t*>(
+      address(slots, at::kLong, packed || slots.dim() == 1 ? at::IntArrayRef(flat) : at::IntArrayRef(both), dev, "slots"));
+  const int64_t ks[3] = {packed ? 0 : k.stride(0), k.stride(-3), k.stride(-2)};
+  const int64_t vs[3] = {packed ? 0 : v.stride(0), v.stride(-3), v.stride(-2)};
+  Launch on(dev);
+  check("attn_kv_write",
+        attn_kv_write(k.data_ptr(), ks, v.data_ptr(), vs, &c, sp, static_cast<int>(B), static_cast<int>(N),
+                      static_cast<int>(H_kv), static_cast<int>(d), on.stream));
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
+// (cache k, v, k_scale, v_scale, block_table, cu_rows, T, first or None, out_k, out_v)
+PyObject* py_kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  argc(n, 10);
+  const at::Tensor &ck = tensor(a[0], "cache.k"), &cu = tensor(a[5], "cu_rows");
+  require(ck.is_cuda() && ck.dim() == 4, "the cache must be [num_pages, H_kv, page_size, d] CUDA tensors");
+  const at::Device dev = ck.device();
+  const int64_t H_kv = ck.size(1), d = ck.size(3);
+  const attn_kv_cache c = cache_struct(a, H_kv, d, dev);
+  require(cu.dim() == 1 && cu.size(0) >= 1, "cu_rows must be [B + 1]");
+  const int64_t B = cu.size(0) - 1;
+  const int T = integer(a[6], "T");
+  require(T >= 0, "T must not be negative");
+  require(B <= INT32_MAX && H_kv <= INT32_MAX && d <= INT32_MAX, "sizes must fit 32 bits");
+  int cols = 0;
+  const int32_t* tp = table_of(tensor(a[4], "block_table"), B, dev, "block_table", cols);
+  const auto* cp = static_cast<const int32_t*>(address(cu, at::kInt, {B + 1}, dev, "cu_rows"));
+  const auto* fp = static_cast<const int32_t*>(address(maybe(a[7], "first"), at::kInt, {B}, dev, "first"));
+  at::Tensor k = maybe(a[8], "out_k"), v = maybe(a[9], "out_v");
+  const int64_t shape[3] = {H_kv, T, d};
+  address(k, at::kBFloat16, shape, dev, "out_k");
+  address(v, at::kBFloat16, shape, dev, "out_v");
+  Launch on(dev);
+  if (!k.defined()) k = make(shape, at::kBFloat16, dev);
+  if (!v.defined()) v = make(shape, at::kBFloat16, dev);
+  check("attn_kv_read",
+        attn_kv_read(&c, tp, cp, fp, k.data_ptr(), v.data_ptr(), static_cast<int>(B), T, static_cast<int>(H_kv),
+                     static_cast<int>(d), cols, on.stream));
+  return pack({k, v});
+  END_HANDLE_TH_ERRORS
+}
+
 PyObject* py_set_error(PyObject*, PyObject* cls) {
   Py_INCREF(cls);
   Py_XSETREF(g_error, cls);
@@ -383,6 +540,9 @@ PyObject* py_set_error(PyObject*, PyObject* cls) {
 PyMethodDef g_methods[] = {FAST("cache_layout", py_cache_layout), FAST("kv_slots", py_slots),
                            FAST("qkv_rope", py_rope), FAST("qkv_rope_bwd", py_rope_bwd),
                            FAST("attn_fwd_paged", py_paged),
+                           FAST("attn_fwd_paged_varlen", py_paged_varlen),
+                           FAST("attn_fwd_paged_shared", py_paged_shared),
+                           FAST("kv_write", py_kv_write), FAST("kv_read", py_kv_read),
                            {"set_error", py_set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_attn_binding", nullptr, -1, g_methods,
