@@ -81,7 +81,7 @@ inline ChunkSizes chunk_sizes(int group, int T, int d) {
 
 template <int D, bool E4M3>
 struct ChunkLayout {
-  static constexpr int kWarps = E4M3 ? 11 : 7;   // E4M3: four more convert
+  static constexpr int kWarps = E4M3 ? 16 : 12;  // three issue, one idles, eight softmax; E4M3: four convert
   static constexpr int kThreads = kWarps * 32;
   static constexpr int SK = kChunkStagesK;
   static constexpr int SV = E4M3 ? kChunkStagesV8 : kChunkStagesV;
@@ -93,11 +93,12 @@ struct ChunkLayout {
   static constexpr int kQ = E4M3 ? kQRaw : 0;                          // [2]
   static constexpr int kK = kQ + 2 * kQBytes;
   static constexpr int kV = kK + SK * kKBytes;
-  static constexpr int kOut = kV + SV * kVBytes;                       // [4 warps][2][32 rows x 128 bytes]
+  static constexpr int kOut = kV + SV * kVBytes;                       // [8 warps][32 rows x half a row]
   static constexpr int kVRaw = kOut + 4 * 8192;                        // E4M3: codes of 64 value columns
   static constexpr int kScale = kVRaw + (E4M3 ? kChunkRawV * 8192 : 0);   // [stage][K, V][128] fp32
   static constexpr int kRow = kScale + (E4M3 ? kChunkScales * 1024 : 0);  // [8][128] factors of query rows
-  static constexpr int kStart = kRow + (E4M3 ? kChunkRowDepth * 512 : 0);
+  static constexpr int kPair = kRow + (E4M3 ? kChunkRowDepth * 512 : 0);  // [8 warps][32] for the other warp of a row
+  static constexpr int kStart = kPair + 1024;
   static constexpr int kBar = kStart + kChunkRounds * 32;
   enum {
     bQF = 0,             // query rows ready in both CTAs (leader)          [2]

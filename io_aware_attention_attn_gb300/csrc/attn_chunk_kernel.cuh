@@ -43,12 +43,29 @@ enum : int { kRoleProducer = 9, kRoleIssuer = 10, kRoleSoftmax = 11, kRoleConver
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
 
-// Arrival on a barrier of the cluster that publishes this CTA's shared memory (after the proxy fence).
-__device__ __forceinline__ void arrive_release_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Barrier of `threads` threads that gives all of them whether any had `x`.
+__device__ __forceinline__ bool named_barrier_or(int id, int threads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x)), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
 }
-// The acquire that goes with it.
-__device__ __forceinline__ void fence_acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
+// The registers of a warp's threads from here on (all four warps of a group together).
+constexpr int kRegsIssue = 96, kRegsSoftmax = 160, kRegsConvert = 96;
+template <int N>
+__device__ __forceinline__ void regs_release() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_take() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert == 4 * 128, "no more than the block was launched with");
 
 // 4-D load whose completion is counted on a barrier that may sit in the peer CTA.
 __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void* tmap, uint32_t bar_cluster, int x,
@@ -215,15 +232,17 @@ __device__ int find(const ChunkParams& p, const int* s_pre, int at, Walk& w) {
   return at;
 }
 
-// sixteen E4M3 codes to bf16, exactly
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes) {
-  const uint32_t h = e4m3x2_to_f16x2(codes);
-  float lo, hi;
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-      : "=f"(lo), "=f"(hi)
-      : "r"(h));
-  return pack_bf16x2(lo, hi);
+// Two E4M3 codes, in bytes 1 and 3 of y, to bf16, exactly but for NaN: exponent and fraction moved to bf16's places
+// are the value times 2^-120 (a code below the normal range becomes a bf16 below its own), and a product with 2^120
+// puts that right.  (The conversion instructions share a pipe of 16 a clock with exp2, which the softmax fills.)
+__device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t y) {
+  const uint32_t x = ((y >> 4) & 0x07f007f0u) | (y & 0x80008000u);
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x7b807b80u));
+  return r;
 }
+// Bits 7 of the bytes that hold a code of NaN.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t v) { return ((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 // value of the E4M3 code nearest to x, two at a time
 __device__ __forceinline__ void e4m3x2_values(uint16_t codes, float& lo, float& hi) {
   const uint32_t h = e4m3x2_to_f16x2(codes);
@@ -244,7 +263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
   constexpr bool kVBoth = D == 128;
   constexpr uint32_t kColO = 128u * NB;
   constexpr uint16_t kBoth = 0x3;
-  constexpr int kSIssuerWarp = 6;
+  constexpr int kSIssuerWarp = 2, kSoftmaxWarp = 4, kConvertWarp = 12;
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_s = smem_u32(smem_raw);
@@ -277,11 +296,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
     }
     for (int b = 0; b < NB; ++b) {
       mbar_init(bar(L::bSF + b), 1);
-      mbar_init(bar(L::bPF + b), 2 * 4);  // one arrival a softmax warp of both CTAs
+      mbar_init(bar(L::bPF + b), 2 * 8);  // one arrival a softmax warp of both CTAs
       mbar_init(bar(L::bPV + b), 1);
     }
     mbar_init(bar(L::bOD), 1);
-    mbar_init(bar(L::bOE), 2 * 4);
+    mbar_init(bar(L::bOE), 2 * 8);
     mbar_init(bar(L::bLF), 1);
     mbar_init(bar(L::bLE), 4);
     for (int s = 0; s < kChunkRawV; ++s) {
@@ -290,7 +309,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
     }
     for (int s = 0; s < kChunkScales; ++s) {
       mbar_init(bar(L::bCF + s), 32);
-      mbar_init(bar(L::bCE + s), 4);
+      mbar_init(bar(L::bCE + s), 8);
     }
     fence_barrier_init();
     misc[1] = 0;
@@ -351,7 +370,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
   const uint32_t tmem = misc[0];
   const int rounds = static_cast<int>(misc[2]);
 
+  // E4M3: registers of the warps that issue and convert go to those of the softmax, which holds a row of 128 scores:
+  // with 168 for all it spilled and took 2.1 us a tile (three groups of four warps: 104 + 240 + 160 = 3 x 168).
   // Counters kept by every role: uq = units (or parts) done so far, g = key tiles done so far.
+  if (warp < kSoftmaxWarp) {
+  if constexpr (E4M3) regs_release<kRegsIssue>();
   if (warp == 0) {
     // ===================================================================== producer
     const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
@@ -493,7 +516,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
       }
     }
   } else if (warp == 1 || warp == kSIssuerWarp) {
-    // ========================================= MMA issuers (rank 0): P V on warp 1, S on warp 6
+    // ========================================= MMA issuers (rank 0): P V on warp 1, S on another
     if (leader) {
       bool ok = true;
       int g = 0, uq = 0;
@@ -507,7 +530,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
             const int qb = uq & 1;
             if (!(ok = mbar_wait_warp(bar(L::bQF + qb), static_cast<uint32_t>(uq >> 1) & 1u, wc, kRoleIssuer, 1)))
               break;
-            if (E4M3) fence_acquire_cluster();
             const uint32_t q_at = sbase + L::kQ + qb * L::kQBytes;
             for (int j = w.j; j < j_end; ++j, ++g) {
               if (g >= NB && !(ok = mbar_wait_warp(bar(L::bPV + g % NB), static_cast<uint32_t>((g - NB) / NB) & 1u,
@@ -562,10 +584,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
               const int b = g % NB, sv = g % SV;
               if (!(ok = mbar_wait_warp(bar(L::bVF + sv), static_cast<uint32_t>(g / SV) & 1u, wc, kRoleIssuer, 4)))
                 break;
-              if (E4M3) fence_acquire_cluster();
-              if (!(ok = mbar_wait_warp(bar(L::bPF + b), static_cast<uint32_t>(g / NB) & 1u, wc, kRoleIssuer, 5)))
-                break;
-              // the first product of a unit overwrites O: the previous unit's epilogue has read it
+                // the first product of a unit overwrites O: the previous unit's epilogue has read it
               if (j == w.j && uq > 0 &&
                   !(ok = mbar_wait_warp(bar(L::bOE), static_cast<uint32_t>(uq - 1) & 1u, wc, kRoleIssuer, 6)))
                 break;
@@ -584,14 +603,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
                 }
                 __syncwarp();
               }
+              if (!(ok = mbar_wait_warp(bar(L::bPF + b), static_cast<uint32_t>(g / NB) & 1u, wc, kRoleIssuer, 5)))
+                break;
               tc_fence_after();
               if (lane == 0) {
                 const uint64_t bv = desc_v + static_cast<uint64_t>(sv * (L::kVBytes >> 4));
                 const uint32_t a = tmem + 128u * static_cast<uint32_t>(b);
                 #pragma unroll
-                for (int k = 0; k < kChunkTile / 16; ++k)
-                  mma_bf16_ts_pair(tmem + kColO, a + k * 8, bv + static_cast<uint64_t>(k * (2048 >> 4)), kIdO,
-                                   (j > w.j || k > 0) ? 1u : 0u);
+                for (int k = 0; k < kChunkTile / 16; ++k)  // P of keys 64 on begins at column 64
+                  mma_bf16_ts_pair(tmem + kColO, a + k * 8 + (k >> 2) * 32, bv + static_cast<uint64_t>(k * (2048 >> 4)),
+                                   kIdO, (j > w.j || k > 0) ? 1u : 0u);
                 mma_commit_pair(bar(L::bPV + b), kBoth);
                 mma_commit_pair(bar(L::bVE + sv), kBoth);
                 if (j == j_end - 1) mma_commit_pair(bar(L::bOD), kBoth);
@@ -610,15 +631,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
         }
       }
     }
-  } else if (warp < kSIssuerWarp) {
+  }
+  } else if (warp < kConvertWarp) {
     // ===================================================================== softmax, epilogue
+    if constexpr (E4M3) regs_take<kRegsSoftmax>();
+    const int half = (warp - kSoftmaxWarp) >> 2;  // keys 64 half .. + 63 of a tile; of O, half of the columns
     const int quarter = warp & 3;       // tensor-memory lanes this warp may access: 32 quarter .. + 31
     const int row = quarter * 32 + lane;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t o_col = t_lane + kColO;
+    const uint32_t o_col = t_lane + kColO + (D / 2) * half;
     // this row's token (within the unit) and query head (within the row group)
     const int my_tok = row / p.rg_rows, my_head = row - my_tok * p.rg_rows;
     const int unit_tok = static_cast<int>(rank) * p.cta_tokens + my_tok;
+    const uint32_t area = L::kOut + static_cast<uint32_t>(quarter * 2 + half) * 4096u;  // rows on their way out
+    // A value of this row with the warp that has the row's other keys (both together).
+    float* mine = reinterpret_cast<float*>(smem + L::kPair) + (quarter * 2 + half) * 32 + lane;
+    const float* theirs = reinterpret_cast<const float*>(smem + L::kPair) + (quarter * 2 + (half ^ 1)) * 32 + lane;
+    auto exchange = [&](float x) {
+      *mine = x;
+      named_barrier_sync(1 + quarter, 64);
+      const float y = *theirs;
+      named_barrier_sync(1 + quarter, 64);
+      return y;
+    };
     bool ok = true;
     int g = 0, uq = 0;
     for (int r = 0; ok && r < rounds; ++r) {
@@ -642,7 +677,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
         for (int j = w.j; j < j_end; ++j, ++g) {
           const int b = g % NB;
           if (!(ok = mbar_wait_warp(bar(L::bSF + b), static_cast<uint32_t>(g / NB) & 1u, wc, kRoleSoftmax, 1))) break;
-          const float* sc = reinterpret_cast<const float*>(smem + L::kScale + (g % kChunkScales) * 1024);
+          const float* sc = reinterpret_cast<const float*>(smem + L::kScale + (g % kChunkScales) * 1024) + 64 * half;
           if (E4M3) {
             // (the factors of the rows were written before the product that this wait is for could be issued)
             if (j == w.j)
@@ -653,47 +688,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
           }
           tc_fence_after();
           if (any) {
-            const uint32_t s_col = t_lane + 128u * static_cast<uint32_t>(b);
-            float s[128];
+            const uint32_t s_col = t_lane + 128u * static_cast<uint32_t>(b) + 64u * half;
+            float s[64];
             {
-              uint32_t u0[32], u1[32], u2[32], u3[32];
-              tmem_ld32(s_col + 0, u0);
-              tmem_ld32(s_col + 32, u1);
-              tmem_ld32(s_col + 64, u2);
-              tmem_ld32(s_col + 96, u3);
-              tmem_wait_ld_regs(u0);
-              tmem_wait_ld_regs(u1);
-              tmem_wait_ld_regs(u2);
-              tmem_wait_ld_regs(u3);
+              uint32_t u[2][32];
               #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                s[i] = u2f(u0[i]);
-                s[32 + i] = u2f(u1[i]);
-                s[64 + i] = u2f(u2[i]);
-                s[96 + i] = u2f(u3[i]);
+              for (int h = 0; h < 2; ++h) tmem_ld32(s_col + 32 * h, u[h]);
+              #pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float4 k4[8];  // K scales of 32 keys, on their way while the scores are
+                if (E4M3) {
+                  #pragma unroll
+                  for (int i = 0; i < 8; ++i) k4[i] = *reinterpret_cast<const float4*>(sc + 32 * h + 4 * i);
+                }
+                tmem_wait_ld_regs(u[h]);
+                #pragma unroll
+                for (int i = 0; i < 32; ++i) s[32 * h + i] = u2f(u[h][i]);
+                if (E4M3) {
+                  #pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    float* x = s + 32 * h + 4 * i;
+                    fmul2(x[0], x[1], x[0], x[1], k4[i].x, k4[i].y);
+                    fmul2(x[2], x[3], x[2], x[3], k4[i].z, k4[i].w);
+                  }
+                }
               }
             }
-            if (E4M3) {
-              #pragma unroll
-              for (int i = 0; i < 128; i += 4) {
-                const float4 k4 = *reinterpret_cast<const float4*>(sc + i);
-                fmul2(s[i], s[i + 1], s[i], s[i + 1], k4.x, k4.y);
-                fmul2(s[i + 2], s[i + 3], s[i + 2], s[i + 3], k4.z, k4.w);
-              }
-            }
-            const int key0 = j * kChunkTile;
-            if (ragged || key0 + kChunkTile > least) {
+            const int key0 = j * kChunkTile + 64 * half;
+            if (ragged || key0 + 64 > least) {
               const int lim = sees - key0;
               #pragma unroll
-              for (int cc = 0; cc < kChunkTile; ++cc) s[cc] = (cc < lim) ? s[cc] : -INFINITY;
+              for (int cc = 0; cc < 64; ++cc) s[cc] = (cc < lim) ? s[cc] : -INFINITY;
             }
-            // P = 2^(t - m) over the first 64 columns of the buffer; ts = this tile's row sums.  Pass 0 takes
-            // the current reference; the row maximum is taken (pass 1) only on the first tile or when
-            // a row's tile sum exceeds kSumLimit.
+            // P = 2^(t - m) over the first 32 of the half's columns; ts = its row sums.  Pass 0 takes the current
+            // reference, the same for both halves of a row; the row maximum is taken (pass 1) only on the first tile
+            // or when a row's sum in one of the halves exceeds kSumLimit.
             float ts[4];
             bool moved = false;
             float alpha = 1.f;
-            bool need = (j == w.j);
+            bool need = j == w.j;
             #pragma unroll 1
             for (int pass = (j == w.j) ? 1 : 0; pass < 2; ++pass) {
               float m_use = m2;
@@ -702,14 +735,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
                 #pragma unroll
                 for (int k = 0; k < 8; ++k) mx[k] = s[k];
                 #pragma unroll
-                for (int cc = 8; cc + 16 <= kChunkTile; cc += 16)
+                for (int cc = 8; cc + 16 <= 64; cc += 16)
                   #pragma unroll
                   for (int k = 0; k < 8; ++k) mx[k] = fmax3(mx[k], s[cc + k], s[cc + 8 + k]);
                 #pragma unroll
-                for (int k = 0; k < 8; ++k) mx[k] = fmaxf(mx[k], s[kChunkTile - 8 + k]);
+                for (int k = 0; k < 8; ++k) mx[k] = fmaxf(mx[k], s[64 - 8 + k]);
                 const float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
                                        fmaxf(mx[6], mx[7])) * sl2;
-                const float m_new = need ? fmaxf(mt, m2) : m2;
+                const float both = fmaxf(mt, exchange(mt));
+                need |= exchange(need ? 1.f : 0.f) != 0.f;
+                const float m_new = need ? fmaxf(both, m2) : m2;
                 moved = (m_new != m2);
                 m_use = (m_new == -INFINITY) ? 0.f : m_new;
                 alpha = moved ? ex2_approx(m2 - m_use) : 1.f;
@@ -724,8 +759,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
               #pragma unroll
               for (int k = 0; k < 4; ++k) ts[k] = 0.f;
               #pragma unroll
-              for (int h = 0; h < 4; ++h) {
+              for (int h = 0; h < 2; ++h) {
                 uint32_t pk[16];
+                float4 v4[8];  // V scales of 32 keys
+                if (E4M3) {
+                  #pragma unroll
+                  for (int i = 0; i < 8; ++i) v4[i] = *reinterpret_cast<const float4*>(sc + 128 + 32 * h + 4 * i);
+                }
                 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                   const int cc = 32 * h + 2 * i;
@@ -734,8 +774,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
                   float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
                   fadd2(ts[2 * (i & 1)], ts[2 * (i & 1) + 1], p0, p1);
                   if (E4M3) {
-                    const float2 v2 = *reinterpret_cast<const float2*>(sc + 128 + cc);
-                    fmul2(p0, p1, p0, p1, v2.x, v2.y);
+                    if (i & 1) fmul2(p0, p1, p0, p1, v4[i / 2].z, v4[i / 2].w);
+                    else fmul2(p0, p1, p0, p1, v4[i / 2].x, v4[i / 2].y);
                   }
                   pk[i] = pack_bf16x2(p0, p1);
                 }
@@ -743,7 +783,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
               }
               if (pass == 0) {
                 need = sees > 0 && !(((ts[0] + ts[1]) + (ts[2] + ts[3])) <= kSumLimit);  // also inf, NaN
-                if (!__any_sync(0xffffffffu, need)) break;
+                if (!named_barrier_or(1 + quarter, 64, need)) break;
               }
             }
             #pragma unroll
@@ -754,8 +794,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
                                         kRoleSoftmax, 3)))
                 break;
               tc_fence_after();
-              #pragma unroll
-              for (int cc = 0; cc < D / 32; ++cc) {
+              #pragma unroll 1
+              for (int cc = 0; cc < D / 64; ++cc) {  // its half of the columns
                 uint32_t o[32];
                 tmem_ld32(o_col + cc * 32, o);
                 tmem_wait_ld_regs(o);
@@ -774,32 +814,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
           }
         }
         if (!ok) break;
-        // ---- O (or this share's part of it) out, then it is free again
+        // ---- O (or this share's part of it) out, half of the columns a warp, then it is free again
         if (!(ok = mbar_wait_warp(bar(L::bOD), static_cast<uint32_t>(uq) & 1u, wc, kRoleSoftmax, 4))) break;
         tc_fence_after();
         if (any) {
           float l = (le[0] + le[1]) + (le[2] + le[3]);
           if (sees <= 0) m2 = -INFINITY, l = 0.f;
-          uint32_t o[D];
-          #pragma unroll
-          for (int cc = 0; cc < D / 32; ++cc)
-            tmem_ld32(o_col + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(o + cc * 32));
-          #pragma unroll
-          for (int cc = 0; cc < D / 32; ++cc) tmem_wait_ld_regs(*reinterpret_cast<uint32_t(*)[32]>(o + cc * 32));
-          if (sees <= 0) {
+          float o[D / 2];
+          {
+            uint32_t u[D / 2];
             #pragma unroll
-            for (int i = 0; i < D; ++i) o[i] = 0u;
+            for (int cc = 0; cc < D / 64; ++cc) tmem_ld32(o_col + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(u + cc * 32));
+            l += exchange(l);
+            #pragma unroll
+            for (int cc = 0; cc < D / 64; ++cc) tmem_wait_ld_regs(*reinterpret_cast<uint32_t(*)[32]>(u + cc * 32));
+            #pragma unroll
+            for (int i = 0; i < D / 2; ++i) o[i] = sees <= 0 ? 0.f : u2f(u[i]);
           }
           if (w.j > 0 || j_end < w.n) {
             const int64_t slot = 2 * share + (first ? 0 : 1);
             const int at = static_cast<int>(rank) * kChunkRows + row;
             if (valid) {
-              *reinterpret_cast<float2*>(p.part_ml + (slot * p.part_rows + at) * 2) = make_float2(m2, l);
+              if (half == 0)
+                *reinterpret_cast<float2*>(p.part_ml + (slot * p.part_rows + at) * 2) = make_float2(m2, l);
               // four columns of all rows together: a warp's stores are contiguous
               float4* dst = reinterpret_cast<float4*>(p.part_o + slot * p.part_rows * D) + at;
               #pragma unroll
-              for (int c = 0; c < D / 4; ++c)
-                dst[c * p.part_rows] = make_float4(u2f(o[4 * c]), u2f(o[4 * c + 1]), u2f(o[4 * c + 2]), u2f(o[4 * c + 3]));
+              for (int c = 0; c < D / 8; ++c)
+                dst[(half * (D / 8) + c) * p.part_rows] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
             }
           } else {
             const int tok = w.tok0 + tok_in, head = z * p.group + head0 + my_head;
@@ -808,46 +850,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
             float lse = l > 0.f || l != l ? (m2 + log2f(l)) * 0.69314718055994530942f : -INFINITY;
             if (p.tail_o && valid) {  // the same row over other keys: the block merge of the two
               const int64_t row_at = static_cast<int64_t>(tok) * p.H + head;
-              const float other = p.tail_lse[row_at];
-              const float top = fmaxf(lse, other);
-              const float wa = lse == -INFINITY ? 0.f : ex2_approx((lse - top) * 1.4426950408889634f);
-              const float wb = other == -INFINITY ? 0.f : ex2_approx((other - top) * 1.4426950408889634f);
-              const float inv = wa + wb > 0.f || wa != wa || wb != wb ? 1.f / (wa + wb) : 0.f;
-              wt *= wa * inv;
-              const float wo = wb * inv;
-              const float4* src = reinterpret_cast<const float4*>(p.tail_o + row_at * D);
+              const float tail = p.tail_lse[row_at], most = fmaxf(lse, tail);
+              const float wp = lse == -INFINITY ? 0.f : ex2_approx((lse - most) * 1.4426950408889634f);
+              const float wt2 = tail == -INFINITY ? 0.f : ex2_approx((tail - most) * 1.4426950408889634f);
+              const float sum = wp + wt2, inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+              wt *= wp * inv;
+              const float wo = wt2 * inv;
+              const float4* src = reinterpret_cast<const float4*>(p.tail_o + row_at * D + half * (D / 2));
               #pragma unroll
-              for (int c = 0; c < D / 4; ++c) {
+              for (int c = 0; c < D / 8; ++c) {
                 const float4 x = src[c];
-                o[4 * c] = f2u(fmaf(u2f(o[4 * c]), wt, x.x * wo));
-                o[4 * c + 1] = f2u(fmaf(u2f(o[4 * c + 1]), wt, x.y * wo));
-                o[4 * c + 2] = f2u(fmaf(u2f(o[4 * c + 2]), wt, x.z * wo));
-                o[4 * c + 3] = f2u(fmaf(u2f(o[4 * c + 3]), wt, x.w * wo));
+                o[4 * c] = fmaf(o[4 * c], wt, x.x * wo);
+                o[4 * c + 1] = fmaf(o[4 * c + 1], wt, x.y * wo);
+                o[4 * c + 2] = fmaf(o[4 * c + 2], wt, x.z * wo);
+                o[4 * c + 3] = fmaf(o[4 * c + 3], wt, x.w * wo);
               }
               wt = 1.f;
-              lse = inv > 0.f || inv != inv ? top - log2f(inv) * 0.69314718055994530942f : -INFINITY;
+              lse = sum > 0.f || sum != sum ? most + log2f(sum) * 0.69314718055994530942f : -INFINITY;
             }
-            if (valid) p.lse[at / D] = lse;
-            // bf16 rows through this warp's area, D/64 halves of 32 rows, 16-byte chunks XOR-ed by the row;
-            // then a row by D/8 lanes
-            const uint32_t stage = sbase + L::kOut + static_cast<uint32_t>(quarter) * 8192u;
+            if (valid && half == 0) p.lse[at / D] = lse;
+            // bf16 rows through this warp's area, 16-byte chunks XOR-ed by the row; then a row by D/16 lanes
+            constexpr int kChunks = D / 16;
             #pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-              st_shared_v4(stage + (c >> 3) * 4096 + lane * 128 + (((c & 7) ^ (lane & 7)) << 4),
-                           pack_bf16x2(u2f(o[8 * c + 0]) * wt, u2f(o[8 * c + 1]) * wt),
-                           pack_bf16x2(u2f(o[8 * c + 2]) * wt, u2f(o[8 * c + 3]) * wt),
-                           pack_bf16x2(u2f(o[8 * c + 4]) * wt, u2f(o[8 * c + 5]) * wt),
-                           pack_bf16x2(u2f(o[8 * c + 6]) * wt, u2f(o[8 * c + 7]) * wt));
+            for (int c = 0; c < kChunks; ++c)
+              st_shared_v4(sbase + area + lane * (16 * kChunks) + ((c ^ (lane & (kChunks - 1))) << 4),
+                           pack_bf16x2(o[8 * c + 0] * wt, o[8 * c + 1] * wt),
+                           pack_bf16x2(o[8 * c + 2] * wt, o[8 * c + 3] * wt),
+                           pack_bf16x2(o[8 * c + 4] * wt, o[8 * c + 5] * wt),
+                           pack_bf16x2(o[8 * c + 6] * wt, o[8 * c + 7] * wt));
             __syncwarp();
-            constexpr int kChunks = D / 8;
             const int cq = lane % kChunks;
-            #pragma unroll 4
+            #pragma unroll
             for (int r0 = 0; r0 < 32; r0 += 32 / kChunks) {
               const int rr = r0 + lane / kChunks;
               const int64_t to = __shfl_sync(0xffffffffu, at, rr);
               if (to >= 0)
-                *reinterpret_cast<uint4*>(p.o + to + cq * 8) = *reinterpret_cast<const uint4*>(
-                    smem + L::kOut + quarter * 8192 + (cq >> 3) * 4096 + rr * 128 + (((cq & 7) ^ (rr & 7)) << 4));
+                *reinterpret_cast<uint4*>(p.o + to + half * (D / 2) + cq * 8) = *reinterpret_cast<const uint4*>(
+                    smem + area + rr * (16 * kChunks) + ((cq ^ (rr & (kChunks - 1))) << 4));
             }
             __syncwarp();
           }
@@ -860,9 +899,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
         advance(p, w, j_end);
       }
     }
-  } else if (E4M3) {
+  } else if constexpr (E4M3) {
     // ===================================================================== converters
-    const int cw = warp - 7, tid = cw * 32 + lane;  // 128 threads
+    if constexpr (E4M3) regs_release<kRegsConvert>();
+    const int tid = (warp - kConvertWarp) * 32 + lane;  // 128 threads
     bool ok = true;
     int g = 0, uq = 0;
     for (int r = 0; ok && r < rounds; ++r) {
@@ -883,7 +923,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
           };
           float amax = 0.f;
           bool bad = false;
-          #pragma unroll
+          #pragma unroll 1
           for (int c = 0; c < D / 8; ++c) {
             const uint4 x = chunk_at(c);
             const uint32_t v[4] = {x.x, x.y, x.z, x.w};
@@ -901,7 +941,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
           // (a row with an infinity or a NaN has no attention: its scores become NaN)
           reinterpret_cast<float*>(smem + L::kRow)[(uq % kChunkRowDepth) * 128 + tid] = bad ? NAN : up;
           const uint32_t q_at = sbase + L::kQ + qb * L::kQBytes;
-          #pragma unroll
+          #pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
             uint32_t hi[4], lo[4];
             #pragma unroll
@@ -929,7 +969,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            arrive_release_cluster(lbar(L::bQF + qb));
+            mbar_arrive_cluster(lbar(L::bQF + qb));
             mbar_arrive(bar(L::bLE));
           }
         }
@@ -942,7 +982,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
                                                kRoleConvert, 4)))
             break;
           const int valid = w.r.L - j * kChunkTile;  // rows past the request's end may hold anything: zeros
-          #pragma unroll
+          #pragma unroll 1
           for (int i = 0; i < 4; ++i) {
             const int key = (tid >> 2) + 32 * i, c = tid & 3;
             const uint4 x = *reinterpret_cast<const uint4*>(smem + L::kVRaw + sr * 8192 + key * 64 + c * 16);
@@ -950,8 +990,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
             uint32_t y[8];
             #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              y[2 * k] = key < valid ? e4m3x2_to_bf16x2(v[k]) : 0u;
-              y[2 * k + 1] = key < valid ? e4m3x2_to_bf16x2(v[k] >> 16) : 0u;
+              y[2 * k] = codes_to_bf16x2(__byte_perm(v[k], 0, 0x1404));
+              y[2 * k + 1] = codes_to_bf16x2(__byte_perm(v[k], 0, 0x3424));
+            }
+            if (nan_codes(v[0]) | nan_codes(v[1]) | nan_codes(v[2]) | nan_codes(v[3])) {
+              #pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t bad = nan_codes(v[k]);
+                y[2 * k] |= ((bad & 0x80u) ? 0x7fc0u : 0u) | ((bad & 0x8000u) ? 0x7fc00000u : 0u);
+                y[2 * k + 1] |= ((bad & 0x800000u) ? 0x7fc0u : 0u) | ((bad & 0x80000000u) ? 0x7fc00000u : 0u);
+              }
+            }
+            if (key >= valid) {
+              #pragma unroll
+              for (int k = 0; k < 8; ++k) y[k] = 0u;
             }
             const uint32_t dst = sbase + L::kV + sv * L::kVBytes + key * 128;
             st_shared_v4(dst + (((2 * c) ^ (key & 7)) << 4), y[0], y[1], y[2], y[3]);
@@ -960,7 +1012,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            arrive_release_cluster(lbar(L::bVF + sv));
+            mbar_arrive_cluster(lbar(L::bVF + sv));
             mbar_arrive(bar(L::bRE + sr));
           }
         }
