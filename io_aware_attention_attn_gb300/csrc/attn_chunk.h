@@ -53,6 +53,7 @@ struct ChunkParams {
   int cta_tokens;        // tokens of a CTA's rows
   int max_pages, num_pages, page_shift, box_rows;
   int part_rows, clusters, max_rounds;
+  int few_rows;          // requests of so many rows a K/V head or fewer have no units here
   ChunkShape shape;
   float scale_log2;
 };

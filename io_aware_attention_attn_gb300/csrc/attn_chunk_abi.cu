@@ -16,24 +16,90 @@ namespace {
 // Places that a unit takes beside its key tiles: loading the query rows, the first tile's maximum, O out.
 constexpr int kChunkCost = 2;
 
+// Which of the two kernels takes a request goes by its rows (new tokens times the query heads of a K/V head): up to
+// kFewRows the one of warp products, whose time is that of reading K and V, above the one of 256-row products.
+// Measured, 32 requests over 4096 keys, 32 query and 8 K/V heads, d = 128: see below.
+constexpr int kFewRows = 32;
+enum Kernels { kFew = 1, kMany = 2 };
+// Rows of one unit of the first, by how many there can be.
+int few_group(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+int few_rows_of(int64_t rows, int B) { return few_group(rows / B * 2 < rows ? rows / B * 2 : rows); }
+// What the host knows: the tokens in all.  Where they may lie either way both kernels are launched, each taking its own
+// requests; requests with more than twice kFewRows rows on average leave the first out (a launch that finds
+// nothing to do takes about 2 us, and the second kernel is right for any request).
+int kernels_for(int64_t rows, int B) {
+  if (rows <= kFewRows) return kFew;
+  return B > 1 && rows <= 2ll * kFewRows * B ? kFew | kMany : kMany;
+}
+size_t chunk_workspace(int T, int group, int d, const ChunkSizes& z) {
+  const size_t few = paged_layout_rows(few_group(static_cast<int64_t>(T) * group), d).total;
+  return few > z.total ? few : z.total;
+}
+
 // The kernel numbers places in 32 bits and rows and tokens with some room to spare.
 bool chunk_sizes_fit(int B, int T, int H, int H_kv, int max_pages, int page_size, const ChunkSizes& z) {
+  if (static_cast<int64_t>(T) * H > INT_MAX) return false;
   const int64_t most = static_cast<int64_t>(max_pages) * page_size;
   if (most > INT_MAX - 1024 || T > INT_MAX - 1024 || static_cast<int64_t>(H_kv) * z.n_rg > INT_MAX) return false;
   const int64_t tiles = (most + kChunkTile - 1) / kChunkTile + 1;
   const int64_t rows = static_cast<int64_t>(T) / (2 * z.cta_tokens) + (B < T ? B : T);  // row tiles, at most
-  return rows <= INT_MAX / (tiles + kChunkCost) / (static_cast<int64_t>(H_kv) * z.n_rg);
+  if (rows > INT_MAX / (tiles + kChunkCost) / (static_cast<int64_t>(H_kv) * z.n_rg)) return false;
+  const int64_t all = static_cast<int64_t>(T) * (H / H_kv);
+  if (!(kernels_for(all, B) & kFew)) return true;
+  const int64_t groups = all / few_rows_of(all, B) + (B < T ? B : T), few_tiles = (most + kPagedTile - 1) / kPagedTile + 1;
+  return groups <= INT_MAX / (few_tiles + kPagedMaxCost) / H_kv;
 }
 
 struct QueryLayout {
   int64_t head, token;  // elements from one query head, one token to the next
 };
 
-// Launch on checked arguments.
-int run_chunk(const void* q, const attn_kv_cache& c, const int32_t* table, const int32_t* seq_lens, const int32_t* cu,
+// Launches on checked arguments: of the kernel for few rows,
+int run_few(const void* q, const attn_kv_cache& c, const int32_t* table, const int32_t* seq_lens, const int32_t* cu,
+            void* o, float* lse, const float* tail_o, const float* tail_lse, int B, int T, int H, int H_kv, int d,
+            int max_pages, int causal, float scale, QueryLayout at, int most_rows, uint8_t* ws, cudaStream_t stream) {
+  PagedParams p{};
+  const int rc = fill_paged(p, c, H_kv, d, scale);
+  if (rc != ATTN_OK) return rc;
+  p.group = H / H_kv;
+  const int64_t rows = static_cast<int64_t>(T) * p.group;
+  p.n_rg = 1;
+  p.rg_rows = few_rows_of(rows, B);
+  const PagedLayout L = paged_layout_rows(p.rg_rows, d);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.table = table;
+  p.seq_lens = seq_lens;
+  p.part_o = reinterpret_cast<float*>(ws + L.o_off);
+  p.part_ml = reinterpret_cast<float*>(ws + L.ml_off);
+  p.B = B;
+  p.H = H;
+  p.max_pages = max_pages;
+  p.cu = cu;
+  p.T = T;
+  p.causal = causal;
+  p.most_rows = most_rows;
+  p.q_head = p.o_head = at.head;
+  p.q_token = p.o_token = at.token;
+  p.tail_o = tail_o;
+  p.tail_lse = tail_lse;
+  const int64_t most = static_cast<int64_t>(max_pages) * c.page_size;
+  const int64_t tiles = most > 0 ? (most + kPagedTile - 1) / kPagedTile : 1;
+  const int64_t units = (rows / p.rg_rows + (B < T ? B : T)) * H_kv;
+  const int64_t places = units * tiles;
+  return launch_fwd_paged_multi(p, d, c.dtype == ATTN_CACHE_E4M3,
+                                places < kPagedMaxCtas ? static_cast<int>(places) : kPagedMaxCtas,
+                                stream) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_LAUNCH;
+}
+
+// of the one for many,
+int run_many(const void* q, const attn_kv_cache& c, const int32_t* table, const int32_t* seq_lens, const int32_t* cu,
               void* o, float* lse, const float* tail_o, const float* tail_lse, int B, int T, int H, int H_kv, int d,
-              int max_pages, int causal, float scale, QueryLayout at, const ChunkSizes& z, uint8_t* ws,
-              cudaStream_t stream) {
+             int max_pages, int causal, float scale, QueryLayout at, int few_rows, const ChunkSizes& z, uint8_t* ws,
+             cudaStream_t stream) {
   const bool e4m3 = c.dtype == ATTN_CACHE_E4M3;
   ChunkParams p{};
   p.box_rows = c.page_size < 64 ? c.page_size : 64;
@@ -73,6 +139,7 @@ int run_chunk(const void* q, const attn_kv_cache& c, const int32_t* table, const
   p.page_shift = log2_of(c.page_size);
   p.part_rows = z.part_rows;
   p.max_rounds = z.rounds;
+  p.few_rows = few_rows;
   p.shape = ChunkShape{2 * z.cta_tokens, causal, kChunkCost};
   p.scale_log2 = scale * 1.4426950408889634f;
   // clusters: no more than the largest number of shares that the table's shape allows
@@ -82,6 +149,22 @@ int run_chunk(const void* q, const attn_kv_cache& c, const int32_t* table, const
   const int64_t shares = units * (tiles + kChunkCost) / kChunkMinShare + 1;
   p.clusters = shares < kChunkClusters ? static_cast<int>(shares) : kChunkClusters;
   return launch_chunk(p, d, e4m3, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+// or of both, one after the other on one workspace.
+int run_chunk(const void* q, const attn_kv_cache& c, const int32_t* table, const int32_t* seq_lens, const int32_t* cu,
+              void* o, float* lse, const float* tail_o, const float* tail_lse, int B, int T, int H, int H_kv, int d,
+              int max_pages, int causal, float scale, QueryLayout at, const ChunkSizes& z, uint8_t* ws,
+              cudaStream_t stream) {
+  const int which = kernels_for(static_cast<int64_t>(T) * (H / H_kv), B);
+  int rc = ATTN_OK;
+  if (which & kFew)
+    rc = run_few(q, c, table, seq_lens, cu, o, lse, tail_o, tail_lse, B, T, H, H_kv, d, max_pages, causal, scale, at,
+                 which & kMany ? kFewRows : INT_MAX, ws, stream);
+  if (rc == ATTN_OK && (which & kMany))
+    rc = run_many(q, c, table, seq_lens, cu, o, lse, tail_o, tail_lse, B, T, H, H_kv, d, max_pages, causal, scale, at,
+                  which & kFew ? kFewRows : 0, z, ws, stream);
+  return rc;
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -94,7 +177,7 @@ SharedLayout shared_layout(int B, int H, int group, int d, const ChunkSizes& z) 
   s.tail_o = paged_layout(group, d).total;
   s.tail_lse = s.tail_o + up256(static_cast<size_t>(B) * H * d * 4);
   s.chunk = s.tail_lse + up256(static_cast<size_t>(B) * H * 4);
-  s.total = s.chunk + z.total;
+  s.total = s.chunk + chunk_workspace(B, group, d, z);
   return s;
 }
 
@@ -105,7 +188,7 @@ using namespace attn;
 
 extern "C" size_t attn_fwd_paged_varlen_workspace_bytes(int T, int H, int H_kv, int d) {
   if (T <= 0 || H <= 0 || H_kv <= 0 || H % H_kv != 0 || (d != 64 && d != 128)) return 0;
-  return chunk_sizes(H / H_kv, T, d).total;
+  return chunk_workspace(T, H / H_kv, d, chunk_sizes(H / H_kv, T, d));
 }
 
 extern "C" int attn_fwd_paged_varlen(const void* q, const attn_kv_cache* cache, const int32_t* block_table,
@@ -125,7 +208,8 @@ extern "C" int attn_fwd_paged_varlen(const void* q, const attn_kv_cache* cache, 
   if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_SCALE;
   const ChunkSizes z = chunk_sizes(H / H_kv, T, d);
   if (!chunk_sizes_fit(B, T, H, H_kv, max_pages, cache->page_size, z)) return ATTN_ERR_SHAPE;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < z.total) return ATTN_ERR_WORKSPACE;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < chunk_workspace(T, H / H_kv, d, z))
+    return ATTN_ERR_WORKSPACE;
   if ((rc = check_device()) != 0) return rc;
   return run_chunk(q, *cache, block_table, seq_lens, cu_new, o, lse, nullptr, nullptr, B, T, H, H_kv, d, max_pages,
                    causal != 0, scale, QueryLayout{static_cast<int64_t>(T) * d, d}, z, static_cast<uint8_t*>(workspace),

@@ -91,11 +91,12 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr) {
          (4ull << 61);
 }
 
-// First token and rows of request s, clamped into the tensors.
+// First token and rows of request s, clamped into the tensors (no new tokens where they are another kernel's).
 __device__ __forceinline__ int cu_at(const ChunkParams& p, int s) { return min(max(p.cu[s], 0), p.T); }
 __device__ __forceinline__ ChunkReq req_at(const ChunkParams& p, int s, int& tok0) {
   tok0 = cu_at(p, s);
-  return ChunkReq{max(cu_at(p, s + 1) - tok0, 0), min(max(p.seq_lens[s], 0), p.max_pages << p.page_shift)};
+  const int n = max(cu_at(p, s + 1) - tok0, 0);
+  return ChunkReq{n * p.group > p.few_rows ? n : 0, min(max(p.seq_lens[s], 0), p.max_pages << p.page_shift)};
 }
 
 // Where a role is: the share's round, and the unit and key tile within the share.

@@ -103,6 +103,12 @@ struct PagedParams {
   int ctas;             // of the parts' kernel
   int unit_cost;        // places that a unit takes beside its tiles
   bool by_unit;         // one join a unit, else one a CTA
+  // several rows a request and K/V head (launch_fwd_paged_multi)
+  const int* cu;        // [B + 1] first token of each request
+  int T, causal, most_rows;  // (requests of more rows have no units)
+  int64_t q_head, q_token, o_head, o_token;  // elements from one query head, one token to the next
+  const float* tail_o;  // fp32 rows [T][H][d] over other keys to merge with (null: none), and their log-sum-exp
+  const float* tail_lse;
   float scale_log2;     // scale * log2(e)
   float trail;          // the same before the scale (bf16 cache)
 };
@@ -112,17 +118,23 @@ struct PagedLayout {
 inline int paged_row_groups(int group) {
   return (group + kPagedMaxRows - 1) / kPagedMaxRows;
 }
-inline PagedLayout paged_layout(int group, int d) {
-  const size_t n_rg = paged_row_groups(group);
-  const size_t rows = (group + n_rg - 1) / n_rg;
+inline PagedLayout paged_layout_rows(size_t rows, int d) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   PagedLayout L{};
   L.ml_off = up(2 * kPagedMaxCtas * rows * d * 4);
   L.total = L.ml_off + up(2 * kPagedMaxCtas * rows * 2 * 4);
   return L;
 }
+inline PagedLayout paged_layout(int group, int d) {
+  const size_t n_rg = paged_row_groups(group);
+  return paged_layout_rows((group + n_rg - 1) / n_rg, d);
+}
 cudaError_t launch_fwd_paged(const PagedParams& p, int d, bool e4m3, int max_tiles,
                              cudaStream_t stream);
+
+// The same of units of up to p.rg_rows (8, 16 or 32) rows of a request's tokens; `max_tiles` as above.
+cudaError_t launch_fwd_paged_multi(const PagedParams& p, int d, bool e4m3, int max_tiles,
+                                   cudaStream_t stream);
 
 // The sizes that attn_fwd_paged takes, and its launch on checked arguments (attn_gen_abi.cu); with o32 the rows
 // go there in fp32 instead of to o.
@@ -130,6 +142,9 @@ bool paged_sizes_fit(int B, int H, int H_kv, int max_pages, int page_size);
 int run_fwd_paged(const void* q, const attn_kv_cache& cache, const int32_t* block_table,
                   const int32_t* seq_lens, void* o, float* o32, float* lse, int B, int H, int H_kv,
                   int d, int max_pages, float scale, void* workspace, cudaStream_t stream);
+
+// The maps of the cache and what else a launch of either kind takes alike (attn_gen_abi.cu); returns a status.
+int fill_paged(PagedParams& p, const attn_kv_cache& cache, int H_kv, int d, float scale);
 
 // Encode the 4-D map of a paged cache's K or V (attn_abi.cu).  Returns a CUresult.
 int encode_cache_map(CUtensorMap* map, const void* base, bool e4m3, uint64_t d, uint64_t page_size,

@@ -54,10 +54,7 @@ bool paged_sizes_fit(int B, int H, int H_kv, int max_pages, int page_size) {
   return static_cast<int64_t>(B) * H <= INT_MAX && units <= INT_MAX / (tiles + kPagedMaxCost);
 }
 
-int run_fwd_paged(const void* q, const attn_kv_cache& cache, const int32_t* block_table,
-                  const int32_t* seq_lens, void* o, float* o32, float* lse, int B, int H, int H_kv,
-                  int d, int max_pages, float scale, void* workspace, cudaStream_t stream) {
-  PagedParams p{};
+int fill_paged(PagedParams& p, const attn_kv_cache& cache, int H_kv, int d, float scale) {
   const bool e4m3 = cache.dtype == ATTN_CACHE_E4M3;
   p.box_rows = cache.page_size < kPagedTile ? cache.page_size : kPagedTile;
   auto encode = [&](CUtensorMap* map, const void* base, uint32_t rows) {
@@ -67,6 +64,23 @@ int run_fwd_paged(const void* q, const attn_kv_cache& cache, const int32_t* bloc
   if (!encode(&p.tm_k, cache.k, p.box_rows) || !encode(&p.tm_v, cache.v, p.box_rows) ||
       !encode(&p.tm_k16, cache.k, 16) || !encode(&p.tm_v16, cache.v, 16))
     return ATTN_ERR_LAUNCH;
+  p.ks = cache.k_scale;
+  p.vs = cache.v_scale;
+  p.H_kv = H_kv;
+  p.num_pages = cache.num_pages;
+  p.page_shift = log2_of(cache.page_size);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.trail = kPagedTrail / p.scale_log2;
+  p.status = status_word();
+  return p.status ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+int run_fwd_paged(const void* q, const attn_kv_cache& cache, const int32_t* block_table,
+                  const int32_t* seq_lens, void* o, float* o32, float* lse, int B, int H, int H_kv,
+                  int d, int max_pages, float scale, void* workspace, cudaStream_t stream) {
+  PagedParams p{};
+  const int rc = fill_paged(p, cache, H_kv, d, scale);
+  if (rc != ATTN_OK) return rc;
   const int group = H / H_kv;
   const PagedLayout L = paged_layout(group, d);
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -75,28 +89,20 @@ int run_fwd_paged(const void* q, const attn_kv_cache& cache, const int32_t* bloc
   p.lse = lse;
   p.table = block_table;
   p.seq_lens = seq_lens;
-  p.ks = cache.k_scale;
-  p.vs = cache.v_scale;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.part_o = reinterpret_cast<float*>(ws + L.o_off);
   p.part_ml = reinterpret_cast<float*>(ws + L.ml_off);
-  p.status = status_word();
-  if (!p.status) return ATTN_ERR_LAUNCH;
   p.B = B;
   p.H = H;
-  p.H_kv = H_kv;
   p.group = group;
   p.n_rg = paged_row_groups(group);
   p.rg_rows = (group + p.n_rg - 1) / p.n_rg;
   p.max_pages = max_pages;
-  p.num_pages = cache.num_pages;
-  p.page_shift = log2_of(cache.page_size);
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.trail = kPagedTrail / p.scale_log2;
   const int64_t most = static_cast<int64_t>(max_pages) * cache.page_size;
   const int64_t tiles = most > 0 ? (most + kPagedTile - 1) / kPagedTile : 1;
   const int64_t units = static_cast<int64_t>(B) * H_kv * p.n_rg;
-  return launch_fwd_paged(p, d, e4m3, static_cast<int>(units * tiles), stream) == cudaSuccess
+  return launch_fwd_paged(p, d, cache.dtype == ATTN_CACHE_E4M3, static_cast<int>(units * tiles),
+                          stream) == cudaSuccess
              ? ATTN_OK
              : ATTN_ERR_LAUNCH;
 }
