@@ -24,6 +24,16 @@ constexpr int kChunkRawV = 3, kChunkStagesV8 = 2, kChunkScales = 4, kChunkRowDep
 struct ChunkStart {
   int s, u, t, j, left, n, tok0, L;
 };
+// What the producer tells the other warps of the unit, or the share's part of it, that comes next.
+struct ChunkUnit {
+  int j, j_end, n, L;    // its key tiles (j -1: nothing comes), those of the whole unit, rows of the request
+  int z, head0;          // K/V head, first query head within its group
+  int tok, n_tok, pos0;  // first token, tokens, rows of the request before the first
+  int slot;              // of the workspace, if it is a part
+};
+// As many of them: the producer is at most three units ahead of the issue of the scores (E4M3), which is at most three
+// tiles, so three units, ahead of the softmax.
+constexpr int kChunkUnits = 8;
 // What the join knows of a share: the unit it begins inside (tiles -1: none that it ends).
 struct ChunkDesc {
   int unit0, tiles;         // the unit's first place, its key tiles
@@ -100,7 +110,8 @@ struct ChunkLayout {
   static constexpr int kRow = kScale + (E4M3 ? kChunkScales * 1024 : 0);  // [8][128] factors of query rows
   static constexpr int kPair = kRow + (E4M3 ? kChunkRowDepth * 512 : 0);  // [8 warps][32] for the other warp of a row
   static constexpr int kStart = kPair + 1024;
-  static constexpr int kBar = kStart + kChunkRounds * 32;
+  static constexpr int kUnits = kStart + kChunkRounds * 32;
+  static constexpr int kBar = kUnits + kChunkUnits * static_cast<int>(sizeof(ChunkUnit));
   enum {
     bQF = 0,             // query rows ready in both CTAs (leader)          [2]
     bQE = bQF + 2,       // query buffer free (both)                        [2]
@@ -120,7 +131,8 @@ struct ChunkLayout {
     bRE = bRF + kChunkRawV,    //   and have been converted
     bCF = bRE + kChunkRawV,    // scales arrived (own CTA)                  [4]
     bCE = bCF + kChunkScales,  //   and have been read
-    kNumBars = bCE + kChunkScales
+    bUF = bCE + kChunkScales,  // a unit is told (own CTA)                  [8]
+    kNumBars = bUF + kChunkUnits
   };
   static constexpr int kMisc = kBar + kNumBars * 8;  // [0] tensor memory [1] abort [2] rounds [3] shares
   static constexpr int kBytes = kMisc + 32;

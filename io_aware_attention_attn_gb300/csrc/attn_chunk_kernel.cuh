@@ -300,6 +300,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
       mbar_init(bar(L::bPF + b), 2 * 8);  // one arrival a softmax warp of both CTAs
       mbar_init(bar(L::bPV + b), 1);
     }
+    for (int i = 0; i < kChunkUnits; ++i) mbar_init(bar(L::bUF + i), 1);
     mbar_init(bar(L::bOD), 1);
     mbar_init(bar(L::bOE), 2 * 8);
     mbar_init(bar(L::bLF), 1);
@@ -369,7 +370,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
   cluster_sync_all();  // barriers initialised and tensor memory allocated in both CTAs
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  const int rounds = static_cast<int>(misc[2]);
+  const int rounds = static_cast<int>(misc[2]);  // of the producer, which tells the others what comes
+  const ChunkUnit* units = reinterpret_cast<const ChunkUnit*>(smem + L::kUnits);
+  // The uq-th unit (or part): false when there is none, or a wait gave up.
+  auto unit_at = [&](int uq, ChunkUnit& w, bool& ok, int role) {
+    const int i = uq % kChunkUnits;
+    ok = mbar_wait_warp(bar(L::bUF + i), static_cast<uint32_t>(uq / kChunkUnits) & 1u, wc, role, 15);
+    if (!ok) return false;
+    w = units[i];
+    return w.j >= 0;
+  };
 
   // E4M3: registers of the warps that issue and convert go to those of the softmax, which holds a row of 128 scores:
   // with 168 for all it spilled and took 2.1 us a tile (three groups of four warps: 104 + 240 + 160 = 3 x 168).
@@ -392,10 +402,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
     int entries = 0, entry_base = 0, entry_s = -1;  // this lane's entry of the 32 looked up last
     for (int r = 0; ok && r < rounds; ++r) {
       Walk w = walk_from(p, starts[r]);
+      bool first = true;  // of the share's units: its part, if it is one, has the share's first place in the workspace
       while (ok && w.left > 0) {
         const int j_end = min(w.n, w.j + w.left);
         const int z = p.n_rg == 1 ? w.u : w.u / p.n_rg;
         const uint64_t policy = w.nt > 1 || p.n_rg > 1 ? keep : once;
+        const int tok_t = w.t * p.shape.tokens;
         {  // query rows of this CTA
           const int qb = uq & 1;
           const uint32_t dst = E4M3 ? sbase + L::kLand : sbase + L::kQ + qb * L::kQBytes;
@@ -408,10 +420,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
           }
           if (!ok) break;
           if (lane == 0) {
+            // (those who read entry uq - kChunkUnits are through with it: nobody is that many units behind)
+            *reinterpret_cast<ChunkUnit*>(smem + L::kUnits + (uq % kChunkUnits) * sizeof(ChunkUnit)) =
+                ChunkUnit{w.j, j_end, w.n, w.r.L, z, (w.u - z * p.n_rg) * p.rg_rows, w.tok0 + tok_t,
+                          min(w.r.n - tok_t, p.shape.tokens), w.r.L - w.r.n + tok_t, 2 * (r * G + c0) + (first ? 0 : 1)};
+            mbar_arrive(bar(L::bUF + uq % kChunkUnits));
             if (E4M3) mbar_arrive_expect_tx(bar(L::bLF), bytes);
             else if (leader) mbar_arrive_expect_tx(bar(L::bQF + qb), 2 * bytes);
             const int head = z * p.group + (w.u - z * p.n_rg) * p.rg_rows;
-            const int tok = w.tok0 + w.t * p.shape.tokens + static_cast<int>(rank) * p.cta_tokens;
+            const int tok = w.tok0 + tok_t + static_cast<int>(rank) * p.cta_tokens;
             #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
               if (E4M3)
@@ -507,8 +524,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
           }
         }
         ++uq;
+        first = false;
         if (ok) advance(p, w, j_end);
       }
+    }
+    if (ok && lane == 0) {
+      *reinterpret_cast<int*>(smem + L::kUnits + (uq % kChunkUnits) * sizeof(ChunkUnit)) = -1;
+      mbar_arrive(bar(L::bUF + uq % kChunkUnits));
     }
     if (!ok) {  // copies in flight land within microseconds: before the cluster exits
       if (E4M3) copy_wait<0>();
@@ -524,19 +546,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
       if (warp == kSIssuerWarp) {
         constexpr uint32_t kIdS = E4M3 ? idesc_e4m3_f32(2 * kChunkRows, kChunkTile)
                                        : idesc_bf16_f32(2 * kChunkRows, kChunkTile, false, false);
-        for (int r = 0; ok && r < rounds; ++r) {
-          Walk w = walk_from(p, starts[r]);
-          while (ok && w.left > 0) {
-            const int j_end = min(w.n, w.j + w.left);
+        for (ChunkUnit w; unit_at(uq, w, ok, kRoleIssuer);) {
+            const int j_end = w.j_end;
             const int qb = uq & 1;
             if (!(ok = mbar_wait_warp(bar(L::bQF + qb), static_cast<uint32_t>(uq >> 1) & 1u, wc, kRoleIssuer, 1)))
               break;
             const uint32_t q_at = sbase + L::kQ + qb * L::kQBytes;
             for (int j = w.j; j < j_end; ++j, ++g) {
+              if (!(ok = mbar_wait_warp(bar(L::bKF + g % SK), static_cast<uint32_t>(g / SK) & 1u, wc, kRoleIssuer, 3)))
+                break;
               if (g >= NB && !(ok = mbar_wait_warp(bar(L::bPV + g % NB), static_cast<uint32_t>((g - NB) / NB) & 1u,
                                                    wc, kRoleIssuer, 2)))
-                break;
-              if (!(ok = mbar_wait_warp(bar(L::bKF + g % SK), static_cast<uint32_t>(g / SK) & 1u, wc, kRoleIssuer, 3)))
                 break;
               tc_fence_after();
               if (lane == 0) {
@@ -565,9 +585,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
               }
               __syncwarp();
             }
+            if (!ok) break;
             ++uq;
-            if (ok) advance(p, w, j_end);
-          }
         }
         if (!ok) {  // unwinding: wait for every MMA this thread issued
           if (lane == 0) mma_commit_pair(bar(L::bDR), 0x1);
@@ -577,10 +596,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
       } else {
         constexpr uint32_t kIdO = idesc_bf16_f32(2 * kChunkRows, k2smPVN, false, true);  // P, V MN
         const uint64_t desc_v = sdesc_sw128(sbase + L::kV, 16384, 1024);
-        for (int r = 0; ok && r < rounds; ++r) {
-          Walk w = walk_from(p, starts[r]);
-          while (ok && w.left > 0) {
-            const int j_end = min(w.n, w.j + w.left);
+        for (ChunkUnit w; unit_at(uq, w, ok, kRoleIssuer);) {
+            const int j_end = w.j_end;
             for (int j = w.j; j < j_end; ++j, ++g) {
               const int b = g % NB, sv = g % SV;
               if (!(ok = mbar_wait_warp(bar(L::bVF + sv), static_cast<uint32_t>(g / SV) & 1u, wc, kRoleIssuer, 4)))
@@ -592,7 +609,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
               if constexpr (!E4M3) {
                 // rows of the last page past the request's end may hold anything: zeroed in both CTAs' halves,
                 // so that P = 0 there meets no value that is not finite
-                const int valid = w.r.L - j * kChunkTile;
+                const int valid = w.L - j * kChunkTile;
                 if (valid < kChunkTile) {
                   const uint32_t vbase = sbase + L::kV + sv * L::kVBytes;
                   const uint32_t vpeer = mapa_shared(vbase, 1);
@@ -622,8 +639,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
             }
             if (!ok) break;
             ++uq;
-            advance(p, w, j_end);
-          }
         }
         if (!ok) {
           if (lane == 0) mma_commit_pair(bar(L::bDR + 1), 0x1);
@@ -657,19 +672,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
     };
     bool ok = true;
     int g = 0, uq = 0;
-    for (int r = 0; ok && r < rounds; ++r) {
-      Walk w = walk_from(p, starts[r]);
-      const int share = r * G + c0;
-      bool first = true;
-      while (ok && w.left > 0) {
-        const int j_end = min(w.n, w.j + w.left);
-        const int z = p.n_rg == 1 ? w.u : w.u / p.n_rg;
-        const int head0 = (w.u - z * p.n_rg) * p.rg_rows;  // within the K/V head's group
-        const int tok_in = w.t * p.shape.tokens + unit_tok;
-        const bool valid = my_tok < p.cta_tokens && tok_in < w.r.n && head0 + my_head < p.group;
+    for (ChunkUnit w; unit_at(uq, w, ok, kRoleSoftmax);) {
+        const int j_end = w.j_end;
+        const bool valid = my_tok < p.cta_tokens && unit_tok < w.n_tok && w.head0 + my_head < p.group;
         const bool any = __any_sync(0xffffffffu, valid);   // a warp without rows only keeps step
         // keys that this row sees, and the fewest that a row of this warp sees (without the rows past the end)
-        const int sees = !valid ? 0 : p.shape.causal ? min(w.r.L, w.r.L - w.r.n + tok_in + 1) : w.r.L;
+        const int sees = !valid ? 0 : p.shape.causal ? min(w.L, w.pos0 + unit_tok + 1) : w.L;
         const int least = __reduce_min_sync(0xffffffffu, valid ? sees : 0x7fffffff);
         const bool ragged = __any_sync(0xffffffffu, !valid);
         float sl2 = p.scale_log2;
@@ -833,7 +841,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
             for (int i = 0; i < D / 2; ++i) o[i] = sees <= 0 ? 0.f : u2f(u[i]);
           }
           if (w.j > 0 || j_end < w.n) {
-            const int64_t slot = 2 * share + (first ? 0 : 1);
+            const int64_t slot = w.slot;
             const int at = static_cast<int>(rank) * kChunkRows + row;
             if (valid) {
               if (half == 0)
@@ -845,7 +853,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
                 dst[(half * (D / 8) + c) * p.part_rows] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
             }
           } else {
-            const int tok = w.tok0 + tok_in, head = z * p.group + head0 + my_head;
+            const int tok = w.tok + unit_tok, head = w.z * p.group + w.head0 + my_head;
             const int64_t at = valid ? head * p.o_head + tok * p.o_token : -1;  // this row's elements
             float wt = l > 0.f || l != l ? 1.f / l : 0.f;  // a row that sees nothing: zeros
             float lse = l > 0.f || l != l ? (m2 + log2f(l)) * 0.69314718055994530942f : -INFINITY;
@@ -895,10 +903,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(lbar(L::bOE));
-        first = false;
         ++uq;
-        advance(p, w, j_end);
-      }
     }
   } else if constexpr (E4M3) {
     // ===================================================================== converters
@@ -906,10 +911,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
     const int tid = (warp - kConvertWarp) * 32 + lane;  // 128 threads
     bool ok = true;
     int g = 0, uq = 0;
-    for (int r = 0; ok && r < rounds; ++r) {
-      Walk w = walk_from(p, starts[r]);
-      while (ok && w.left > 0) {
-        const int j_end = min(w.n, w.j + w.left);
+    for (ChunkUnit w; unit_at(uq, w, ok, kRoleConvert);) {
+        const int j_end = w.j_end;
         {
           // query row tid: scaled by a power of two to a largest element of 2^7 .. 2^8, then hi = its E4M3
           // rounding and lo = that of what is left
@@ -982,7 +985,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
           if (g >= SV && !(ok = mbar_wait_warp(bar(L::bVE + sv), (static_cast<uint32_t>(g / SV) & 1u) ^ 1u, wc,
                                                kRoleConvert, 4)))
             break;
-          const int valid = w.r.L - j * kChunkTile;  // rows past the request's end may hold anything: zeros
+          const int valid = w.L - j * kChunkTile;  // rows past the request's end may hold anything: zeros
           #pragma unroll 1
           for (int i = 0; i < 4; ++i) {
             const int key = (tid >> 2) + 32 * i, c = tid & 3;
@@ -1017,9 +1020,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
             mbar_arrive(bar(L::bRE + sr));
           }
         }
+        if (!ok) break;
         ++uq;
-        if (ok) advance(p, w, j_end);
-      }
     }
   }
   tc_fence_before();
