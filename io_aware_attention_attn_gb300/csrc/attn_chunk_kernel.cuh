@@ -55,6 +55,22 @@ __device__ __forceinline__ bool named_barrier_or(int id, int threads, bool x) {
   return r != 0;
 }
 
+// A bounded wait as mbar_wait_warp, in few instructions: it is written out some forty times, and what the warps of a
+// sub-partition run in turn should fit its instruction cache.  What gave up is kept in the CTA's abort word, which
+// goes to the status word at the kernel's end.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, int role, int site) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const unsigned long long t0 = global_timer_ns();
+  bool stop;
+  do {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    stop = global_timer_ns() - t0 > kWaitLimitNs;
+    if (stop && *abort == 0) *abort = kStatusTimeout | (role << 8) | (site << 16);
+    stop = *abort != 0;
+  } while (!__any_sync(0xffffffffu, stop));
+  return false;
+}
+
 // The registers of a warp's threads from here on (all four warps of a group together).
 constexpr int kRegsIssue = 96, kRegsSoftmax = 160, kRegsConvert = 96;
 template <int N>
@@ -272,7 +288,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
   uint8_t* smem = smem_raw + (sbase - raw_s);
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   ChunkStart* starts = reinterpret_cast<ChunkStart*>(smem + L::kStart);
-  const WaitCtx wc{reinterpret_cast<volatile int*>(misc + 1), p.status};
+  volatile int* wc = reinterpret_cast<volatile int*>(misc + 1);  // set where a wait gave up
   auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * static_cast<uint32_t>(i); };
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
@@ -375,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
   // The uq-th unit (or part): false when there is none, or a wait gave up.
   auto unit_at = [&](int uq, ChunkUnit& w, bool& ok, int role) {
     const int i = uq % kChunkUnits;
-    ok = mbar_wait_warp(bar(L::bUF + i), static_cast<uint32_t>(uq / kChunkUnits) & 1u, wc, role, 15);
+    ok = wait_warp(bar(L::bUF + i), static_cast<uint32_t>(uq / kChunkUnits) & 1u, wc, role, 15);
     if (!ok) return false;
     w = units[i];
     return w.j >= 0;
@@ -413,10 +429,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
           const uint32_t dst = E4M3 ? sbase + L::kLand : sbase + L::kQ + qb * L::kQBytes;
           const int bytes = p.rg_rows * p.cta_tokens * 128 * (D / 64);
           if (E4M3) {
-            if (uq >= 1) ok = mbar_wait_warp(bar(L::bLE), static_cast<uint32_t>(uq - 1) & 1u, wc, kRoleProducer, 1);
+            if (uq >= 1) ok = wait_warp(bar(L::bLE), static_cast<uint32_t>(uq - 1) & 1u, wc, kRoleProducer, 1);
           } else {
             if (uq >= 2)
-              ok = mbar_wait_warp(bar(L::bQE + qb), static_cast<uint32_t>((uq - 2) >> 1) & 1u, wc, kRoleProducer, 2);
+              ok = wait_warp(bar(L::bQE + qb), static_cast<uint32_t>((uq - 2) >> 1) & 1u, wc, kRoleProducer, 2);
           }
           if (!ok) break;
           if (lane == 0) {
@@ -458,7 +474,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
           const int k_pg = __shfl_sync(0xffffffffu, entries, (((key0 + k_row) >> p.page_shift) - entry_base) & 31);
           const int v_pg = __shfl_sync(0xffffffffu, entries, (((key0 + v_row) >> p.page_shift) - entry_base) & 31);
           const int sk = g % SK;
-          if (g >= SK && !(ok = mbar_wait_warp(bar(L::bKE + sk), (static_cast<uint32_t>(g / SK) & 1u) ^ 1u, wc,
+          if (g >= SK && !(ok = wait_warp(bar(L::bKE + sk), (static_cast<uint32_t>(g / SK) & 1u) ^ 1u, wc,
                                                kRoleProducer, 3)))
             break;
           if (leader && lane == 0) mbar_arrive_expect_tx(bar(L::bKF + sk), 2 * L::kKBytes);
@@ -472,7 +488,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
             // scales of keys 4 lane .. 4 lane + 3; past the request's rows: zeros
             const int sc = g % kChunkScales;
             if (g >= kChunkScales &&
-                !(ok = mbar_wait_warp(bar(L::bCE + sc), (static_cast<uint32_t>(g / kChunkScales) & 1u) ^ 1u, wc,
+                !(ok = wait_warp(bar(L::bCE + sc), (static_cast<uint32_t>(g / kChunkScales) & 1u) ^ 1u, wc,
                                       kRoleProducer, 4)))
               break;
             const int key = key0 + 4 * lane;
@@ -501,7 +517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
           if (E4M3) {
             const int sv = g % kChunkRawV;
             if (g >= kChunkRawV &&
-                !(ok = mbar_wait_warp(bar(L::bRE + sv), (static_cast<uint32_t>(g / kChunkRawV) & 1u) ^ 1u, wc,
+                !(ok = wait_warp(bar(L::bRE + sv), (static_cast<uint32_t>(g / kChunkRawV) & 1u) ^ 1u, wc,
                                       kRoleProducer, 5)))
               break;
             if (lane == 0) mbar_arrive_expect_tx(bar(L::bRF + sv), 8192);
@@ -512,7 +528,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
                                v_pg >= 0 ? v_pg : p.num_pages, policy);
           } else {
             const int sv = g % SV;
-            if (g >= SV && !(ok = mbar_wait_warp(bar(L::bVE + sv), (static_cast<uint32_t>(g / SV) & 1u) ^ 1u, wc,
+            if (g >= SV && !(ok = wait_warp(bar(L::bVE + sv), (static_cast<uint32_t>(g / SV) & 1u) ^ 1u, wc,
                                                  kRoleProducer, 6)))
               break;
             if (leader && lane == 0) mbar_arrive_expect_tx(bar(L::bVF + sv), (kVBoth ? 2 : 1) * L::kVBytes);
@@ -549,13 +565,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
         for (ChunkUnit w; unit_at(uq, w, ok, kRoleIssuer);) {
             const int j_end = w.j_end;
             const int qb = uq & 1;
-            if (!(ok = mbar_wait_warp(bar(L::bQF + qb), static_cast<uint32_t>(uq >> 1) & 1u, wc, kRoleIssuer, 1)))
+            if (!(ok = wait_warp(bar(L::bQF + qb), static_cast<uint32_t>(uq >> 1) & 1u, wc, kRoleIssuer, 1)))
               break;
             const uint32_t q_at = sbase + L::kQ + qb * L::kQBytes;
             for (int j = w.j; j < j_end; ++j, ++g) {
-              if (!(ok = mbar_wait_warp(bar(L::bKF + g % SK), static_cast<uint32_t>(g / SK) & 1u, wc, kRoleIssuer, 3)))
+              if (!(ok = wait_warp(bar(L::bKF + g % SK), static_cast<uint32_t>(g / SK) & 1u, wc, kRoleIssuer, 3)))
                 break;
-              if (g >= NB && !(ok = mbar_wait_warp(bar(L::bPV + g % NB), static_cast<uint32_t>((g - NB) / NB) & 1u,
+              if (g >= NB && !(ok = wait_warp(bar(L::bPV + g % NB), static_cast<uint32_t>((g - NB) / NB) & 1u,
                                                    wc, kRoleIssuer, 2)))
                 break;
               tc_fence_after();
@@ -600,11 +616,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
             const int j_end = w.j_end;
             for (int j = w.j; j < j_end; ++j, ++g) {
               const int b = g % NB, sv = g % SV;
-              if (!(ok = mbar_wait_warp(bar(L::bVF + sv), static_cast<uint32_t>(g / SV) & 1u, wc, kRoleIssuer, 4)))
+              if (!(ok = wait_warp(bar(L::bVF + sv), static_cast<uint32_t>(g / SV) & 1u, wc, kRoleIssuer, 4)))
                 break;
                 // the first product of a unit overwrites O: the previous unit's epilogue has read it
               if (j == w.j && uq > 0 &&
-                  !(ok = mbar_wait_warp(bar(L::bOE), static_cast<uint32_t>(uq - 1) & 1u, wc, kRoleIssuer, 6)))
+                  !(ok = wait_warp(bar(L::bOE), static_cast<uint32_t>(uq - 1) & 1u, wc, kRoleIssuer, 6)))
                 break;
               if constexpr (!E4M3) {
                 // rows of the last page past the request's end may hold anything: zeroed in both CTAs' halves,
@@ -621,7 +637,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
                 }
                 __syncwarp();
               }
-              if (!(ok = mbar_wait_warp(bar(L::bPF + b), static_cast<uint32_t>(g / NB) & 1u, wc, kRoleIssuer, 5)))
+              if (!(ok = wait_warp(bar(L::bPF + b), static_cast<uint32_t>(g / NB) & 1u, wc, kRoleIssuer, 5)))
                 break;
               tc_fence_after();
               if (lane == 0) {
@@ -685,13 +701,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
         float le[4] = {0.f, 0.f, 0.f, 0.f};  // sums of 2^(t - m)
         for (int j = w.j; j < j_end; ++j, ++g) {
           const int b = g % NB;
-          if (!(ok = mbar_wait_warp(bar(L::bSF + b), static_cast<uint32_t>(g / NB) & 1u, wc, kRoleSoftmax, 1))) break;
+          if (!(ok = wait_warp(bar(L::bSF + b), static_cast<uint32_t>(g / NB) & 1u, wc, kRoleSoftmax, 1))) break;
           const float* sc = reinterpret_cast<const float*>(smem + L::kScale + (g % kChunkScales) * 1024) + 64 * half;
           if (E4M3) {
             // (the factors of the rows were written before the product that this wait is for could be issued)
             if (j == w.j)
               sl2 = p.scale_log2 * reinterpret_cast<const float*>(smem + L::kRow)[(uq % kChunkRowDepth) * 128 + row];
-            if (!(ok = mbar_wait_warp(bar(L::bCF + g % kChunkScales), static_cast<uint32_t>(g / kChunkScales) & 1u, wc,
+            if (!(ok = wait_warp(bar(L::bCF + g % kChunkScales), static_cast<uint32_t>(g / kChunkScales) & 1u, wc,
                                       kRoleSoftmax, 2)))
               break;
           }
@@ -799,7 +815,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
             for (int k = 0; k < 4; ++k) le[k] += ts[k];
             // O holds P V up to the tile before once that product completes; bring it to the new reference
             if (j > w.j && __any_sync(0xffffffffu, moved)) {
-              if (!(ok = mbar_wait_warp(bar(L::bPV + (g - 1) % NB), static_cast<uint32_t>((g - 1) / NB) & 1u, wc,
+              if (!(ok = wait_warp(bar(L::bPV + (g - 1) % NB), static_cast<uint32_t>((g - 1) / NB) & 1u, wc,
                                         kRoleSoftmax, 3)))
                 break;
               tc_fence_after();
@@ -824,7 +840,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
         }
         if (!ok) break;
         // ---- O (or this share's part of it) out, half of the columns a warp, then it is free again
-        if (!(ok = mbar_wait_warp(bar(L::bOD), static_cast<uint32_t>(uq) & 1u, wc, kRoleSoftmax, 4))) break;
+        if (!(ok = wait_warp(bar(L::bOD), static_cast<uint32_t>(uq) & 1u, wc, kRoleSoftmax, 4))) break;
         tc_fence_after();
         if (any) {
           float l = (le[0] + le[1]) + (le[2] + le[3]);
@@ -917,8 +933,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
           // query row tid: scaled by a power of two to a largest element of 2^7 .. 2^8, then hi = its E4M3
           // rounding and lo = that of what is left
           const int qb = uq & 1;
-          if (!(ok = mbar_wait_warp(bar(L::bLF), static_cast<uint32_t>(uq) & 1u, wc, kRoleConvert, 1))) break;
-          if (uq >= 2 && !(ok = mbar_wait_warp(bar(L::bQE + qb), static_cast<uint32_t>((uq - 2) >> 1) & 1u, wc,
+          if (!(ok = wait_warp(bar(L::bLF), static_cast<uint32_t>(uq) & 1u, wc, kRoleConvert, 1))) break;
+          if (uq >= 2 && !(ok = wait_warp(bar(L::bQE + qb), static_cast<uint32_t>((uq - 2) >> 1) & 1u, wc,
                                                kRoleConvert, 2)))
             break;
           const uint8_t* land = smem + L::kLand;
@@ -980,9 +996,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
         for (int j = w.j; j < j_end; ++j, ++g) {
           if (!kVBoth && !leader) continue;
           const int sr = g % kChunkRawV, sv = g % SV;
-          if (!(ok = mbar_wait_warp(bar(L::bRF + sr), static_cast<uint32_t>(g / kChunkRawV) & 1u, wc, kRoleConvert, 3)))
+          if (!(ok = wait_warp(bar(L::bRF + sr), static_cast<uint32_t>(g / kChunkRawV) & 1u, wc, kRoleConvert, 3)))
             break;
-          if (g >= SV && !(ok = mbar_wait_warp(bar(L::bVE + sv), (static_cast<uint32_t>(g / SV) & 1u) ^ 1u, wc,
+          if (g >= SV && !(ok = wait_warp(bar(L::bVE + sv), (static_cast<uint32_t>(g / SV) & 1u) ^ 1u, wc,
                                                kRoleConvert, 4)))
             break;
           const int valid = w.L - j * kChunkTile;  // rows past the request's end may hold anything: zeros
@@ -1026,6 +1042,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
   }
   tc_fence_before();
   cluster_sync_all();  // no MMA, copy or remote arrival of either CTA is still in flight
+  if (threadIdx.x == 0 && misc[1] != 0) atomicCAS(p.status, 0, static_cast<int>(misc[1]));
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
