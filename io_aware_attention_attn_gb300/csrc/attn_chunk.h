@@ -34,6 +34,8 @@ struct ChunkUnit {
 // As many of them: the producer is at most three units ahead of the issue of the scores (E4M3), which is at most three
 // tiles, so three units, ahead of the softmax.
 constexpr int kChunkUnits = 8;
+// Units whose statistics are kept: the softmax is at most three tiles ahead of a unit whose O is not stored.
+constexpr int kChunkStats = 4;
 // What the join knows of a share: the unit it begins inside (tiles -1: none that it ends).
 struct ChunkDesc {
   int unit0, tiles;         // the unit's first place, its key tiles
@@ -92,7 +94,7 @@ inline ChunkSizes chunk_sizes(int group, int T, int d) {
 
 template <int D, bool E4M3>
 struct ChunkLayout {
-  static constexpr int kWarps = E4M3 ? 16 : 12;  // three issue, one idles, eight softmax; E4M3: four convert
+  static constexpr int kWarps = E4M3 ? 20 : 16;  // three issue, one idles, eight softmax, four store; E4M3: four convert
   static constexpr int kThreads = kWarps * 32;
   static constexpr int SK = kChunkStagesK;
   static constexpr int SV = E4M3 ? kChunkStagesV8 : kChunkStagesV;
@@ -104,8 +106,9 @@ struct ChunkLayout {
   static constexpr int kQ = E4M3 ? kQRaw : 0;                          // [2]
   static constexpr int kK = kQ + 2 * kQBytes;
   static constexpr int kV = kK + SK * kKBytes;
-  static constexpr int kOut = kV + SV * kVBytes;                       // [8 warps][32 rows x half a row]
-  static constexpr int kVRaw = kOut + 4 * 8192;                        // E4M3: codes of 64 value columns
+  static constexpr int kOut = kV + SV * kVBytes;                       // [4 warps][32 rows x 64 bytes]
+  static constexpr int kStats = kOut + 4 * 2048;                       // [4][sums of two halves, maximum][128]
+  static constexpr int kVRaw = kStats + kChunkStats * 1536;                        // E4M3: codes of 64 value columns
   static constexpr int kScale = kVRaw + (E4M3 ? kChunkRawV * 8192 : 0);   // [stage][K, V][128] fp32
   static constexpr int kRow = kScale + (E4M3 ? kChunkScales * 1024 : 0);  // [8][128] factors of query rows
   static constexpr int kPair = kRow + (E4M3 ? kChunkRowDepth * 512 : 0);  // [8 warps][32] for the other warp of a row
@@ -132,7 +135,8 @@ struct ChunkLayout {
     bCF = bRE + kChunkRawV,    // scales arrived (own CTA)                  [4]
     bCE = bCF + kChunkScales,  //   and have been read
     bUF = bCE + kChunkScales,  // a unit is told (own CTA)                  [8]
-    kNumBars = bUF + kChunkUnits
+    bEL = bUF + kChunkUnits,   // a unit's statistics are there (own CTA)   [4]
+    kNumBars = bEL + kChunkStats
   };
   static constexpr int kMisc = kBar + kNumBars * 8;  // [0] tensor memory [1] abort [2] rounds [3] shares
   static constexpr int kBytes = kMisc + 32;

@@ -38,7 +38,7 @@
 namespace attn {
 namespace chunk {
 
-enum : int { kRoleProducer = 9, kRoleIssuer = 10, kRoleSoftmax = 11, kRoleConvert = 12 };
+enum : int { kRoleProducer = 9, kRoleIssuer = 10, kRoleSoftmax = 11, kRoleConvert = 12, kRoleStore = 13 };
 
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
@@ -72,7 +72,12 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
 }
 
 // The registers of a warp's threads from here on (all four warps of a group together).
-constexpr int kRegsIssue = 96, kRegsSoftmax = 160, kRegsConvert = 96;
+// Issue + 2 softmax + store (+ convert): no more than the block was launched with, 4 x 128 (E4M3: 5 x 96).
+template <bool E4M3>
+struct ChunkRegs {
+  static constexpr int kIssue = E4M3 ? 72 : 80, kSoftmax = E4M3 ? 144 : 160, kStore = E4M3 ? 64 : 112, kConvert = 56;
+  static_assert(kIssue + 2 * kSoftmax + kStore + (E4M3 ? kConvert : 0) == (E4M3 ? 5 * 96 : 4 * 128), "registers");
+};
 template <int N>
 __device__ __forceinline__ void regs_release() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -81,7 +86,6 @@ template <int N>
 __device__ __forceinline__ void regs_take() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
-static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert == 4 * 128, "no more than the block was launched with");
 
 // 4-D load whose completion is counted on a barrier that may sit in the peer CTA.
 __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void* tmap, uint32_t bar_cluster, int x,
@@ -280,7 +284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
   constexpr bool kVBoth = D == 128;
   constexpr uint32_t kColO = 128u * NB;
   constexpr uint16_t kBoth = 0x3;
-  constexpr int kSIssuerWarp = 2, kSoftmaxWarp = 4, kConvertWarp = 12;
+  constexpr int kSIssuerWarp = 2, kSoftmaxWarp = 4, kStoreWarp = 12, kConvertWarp = 16;
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_s = smem_u32(smem_raw);
@@ -318,7 +322,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
     }
     for (int i = 0; i < kChunkUnits; ++i) mbar_init(bar(L::bUF + i), 1);
     mbar_init(bar(L::bOD), 1);
-    mbar_init(bar(L::bOE), 2 * 8);
+    mbar_init(bar(L::bOE), 2 * 4);
+    for (int i = 0; i < kChunkStats; ++i) mbar_init(bar(L::bEL + i), 8);
     mbar_init(bar(L::bLF), 1);
     mbar_init(bar(L::bLE), 4);
     for (int s = 0; s < kChunkRawV; ++s) {
@@ -397,11 +402,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
     return w.j >= 0;
   };
 
-  // E4M3: registers of the warps that issue and convert go to those of the softmax, which holds a row of 128 scores:
-  // with 168 for all it spilled and took 2.1 us a tile (three groups of four warps: 104 + 240 + 160 = 3 x 168).
+  // Registers of the warps that issue, store and convert go to those of the softmax (with the same for all the
+  // E4M3 kernel spilled and took 2.1 us a tile).
   // Counters kept by every role: uq = units (or parts) done so far, g = key tiles done so far.
   if (warp < kSoftmaxWarp) {
-  if constexpr (E4M3) regs_release<kRegsIssue>();
+  regs_release<ChunkRegs<E4M3>::kIssue>();
   if (warp == 0) {
     // ===================================================================== producer
     const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
@@ -664,9 +669,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
       }
     }
   }
-  } else if (warp < kConvertWarp) {
-    // ===================================================================== softmax, epilogue
-    if constexpr (E4M3) regs_take<kRegsSoftmax>();
+  } else if (warp < kStoreWarp) {
+    // ===================================================================== softmax
+    regs_take<ChunkRegs<E4M3>::kSoftmax>();
     const int half = (warp - kSoftmaxWarp) >> 2;  // keys 64 half .. + 63 of a tile; of O, half of the columns
     const int quarter = warp & 3;       // tensor-memory lanes this warp may access: 32 quarter .. + 31
     const int row = quarter * 32 + lane;
@@ -675,7 +680,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
     // this row's token (within the unit) and query head (within the row group)
     const int my_tok = row / p.rg_rows, my_head = row - my_tok * p.rg_rows;
     const int unit_tok = static_cast<int>(rank) * p.cta_tokens + my_tok;
-    const uint32_t area = L::kOut + static_cast<uint32_t>(quarter * 2 + half) * 4096u;  // rows on their way out
     // A value of this row with the warp that has the row's other keys (both together).
     float* mine = reinterpret_cast<float*>(smem + L::kPair) + (quarter * 2 + half) * 32 + lane;
     const float* theirs = reinterpret_cast<const float*>(smem + L::kPair) + (quarter * 2 + (half ^ 1)) * 32 + lane;
@@ -839,91 +843,121 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
           }
         }
         if (!ok) break;
-        // ---- O (or this share's part of it) out, half of the columns a warp, then it is free again
-        if (!(ok = wait_warp(bar(L::bOD), static_cast<uint32_t>(uq) & 1u, wc, kRoleSoftmax, 4))) break;
+        // the row's maximum and sums for the warps that store O
+        float* stats = reinterpret_cast<float*>(smem + L::kStats) + (uq % kChunkStats) * 384;
+        const float l = (le[0] + le[1]) + (le[2] + le[3]);
+        stats[half * 128 + row] = sees > 0 ? l : 0.f;
+        if (half == 0) stats[256 + row] = sees > 0 ? m2 : -INFINITY;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::bEL + uq % kChunkStats));
+        ++uq;
+    }
+  } else if (warp < kConvertWarp) {
+    // ===================================================================== O out
+    // Warps of their own, so that the softmax goes on with the next unit while a unit's last product runs and its
+    // rows are stored (with the softmax's warps doing it, a unit cost 2.6 us beside its tiles).
+    regs_release<ChunkRegs<E4M3>::kStore>();
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t o_col = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kColO;
+    const int my_tok = row / p.rg_rows, my_head = row - my_tok * p.rg_rows;
+    const int unit_tok = static_cast<int>(rank) * p.cta_tokens + my_tok;
+    const uint32_t area = L::kOut + static_cast<uint32_t>(quarter) * 2048u;  // 32 rows of 32 columns on their way out
+    bool ok = true;
+    int uq = 0;
+    for (ChunkUnit w; unit_at(uq, w, ok, kRoleStore);) {
+        const bool valid = my_tok < p.cta_tokens && unit_tok < w.n_tok && w.head0 + my_head < p.group;
+        const bool any = __any_sync(0xffffffffu, valid);
+        const int sees = !valid ? 0 : p.shape.causal ? min(w.L, w.pos0 + unit_tok + 1) : w.L;
+        if (!(ok = wait_warp(bar(L::bEL + uq % kChunkStats), static_cast<uint32_t>(uq / kChunkStats) & 1u, wc, kRoleStore, 1)))
+          break;
+        const float* stats = reinterpret_cast<const float*>(smem + L::kStats) + (uq % kChunkStats) * 384;
+        const float l = stats[row] + stats[128 + row], m2 = stats[256 + row];
+        const bool part = w.j > 0 || w.j_end < w.n;
+        const int tok = w.tok + unit_tok, head = w.z * p.group + w.head0 + my_head;
+        const int64_t at = valid ? head * p.o_head + tok * p.o_token : -1;  // this row's elements
+        const int64_t row_at = static_cast<int64_t>(tok) * p.H + head;
+        float wt = 1.f, wo = 0.f;  // weights of this row's O and of the same row over other keys
+        if (!part) {
+          wt = l > 0.f || l != l ? 1.f / l : 0.f;  // a row that sees nothing: zeros
+          float lse = l > 0.f || l != l ? (m2 + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+          if (p.tail_o && valid) {  // the block merge of the two
+            const float tail = p.tail_lse[row_at], most = fmaxf(lse, tail);
+            const float a = lse == -INFINITY ? 0.f : ex2_approx((lse - most) * 1.4426950408889634f);
+            const float b = tail == -INFINITY ? 0.f : ex2_approx((tail - most) * 1.4426950408889634f);
+            const float sum = a + b, inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+            wt *= a * inv;
+            wo = b * inv;
+            lse = sum > 0.f || sum != sum ? most + log2f(sum) * 0.69314718055994530942f : -INFINITY;
+          }
+          if (valid) p.lse[at / D] = lse;
+        } else if (valid) {
+          *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(w.slot) * p.part_rows + rank * kChunkRows + row) * 2) =
+              make_float2(m2, l);
+        }
+        if (!(ok = wait_warp(bar(L::bOD), static_cast<uint32_t>(uq) & 1u, wc, kRoleStore, 2))) break;
         tc_fence_after();
         if (any) {
-          float l = (le[0] + le[1]) + (le[2] + le[3]);
-          if (sees <= 0) m2 = -INFINITY, l = 0.f;
-          float o[D / 2];
-          {
-            uint32_t u[D / 2];
-            #pragma unroll
-            for (int cc = 0; cc < D / 64; ++cc) tmem_ld32(o_col + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(u + cc * 32));
-            l += exchange(l);
-            #pragma unroll
-            for (int cc = 0; cc < D / 64; ++cc) tmem_wait_ld_regs(*reinterpret_cast<uint32_t(*)[32]>(u + cc * 32));
-            #pragma unroll
-            for (int i = 0; i < D / 2; ++i) o[i] = sees <= 0 ? 0.f : u2f(u[i]);
-          }
-          if (w.j > 0 || j_end < w.n) {
-            const int64_t slot = w.slot;
-            const int at = static_cast<int>(rank) * kChunkRows + row;
-            if (valid) {
-              if (half == 0)
-                *reinterpret_cast<float2*>(p.part_ml + (slot * p.part_rows + at) * 2) = make_float2(m2, l);
-              // four columns of all rows together: a warp's stores are contiguous
-              float4* dst = reinterpret_cast<float4*>(p.part_o + slot * p.part_rows * D) + at;
-              #pragma unroll
-              for (int c = 0; c < D / 8; ++c)
-                dst[(half * (D / 8) + c) * p.part_rows] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+          #pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t u[32];
+            tmem_ld32(o_col + c * 32, u);
+            tmem_wait_ld_regs(u);
+            if (c == D / 32 - 1) {  // all of O is read: the next unit's first product may overwrite it
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(lbar(L::bOE));
             }
-          } else {
-            const int tok = w.tok + unit_tok, head = w.z * p.group + w.head0 + my_head;
-            const int64_t at = valid ? head * p.o_head + tok * p.o_token : -1;  // this row's elements
-            float wt = l > 0.f || l != l ? 1.f / l : 0.f;  // a row that sees nothing: zeros
-            float lse = l > 0.f || l != l ? (m2 + log2f(l)) * 0.69314718055994530942f : -INFINITY;
-            if (p.tail_o && valid) {  // the same row over other keys: the block merge of the two
-              const int64_t row_at = static_cast<int64_t>(tok) * p.H + head;
-              const float tail = p.tail_lse[row_at], most = fmaxf(lse, tail);
-              const float wp = lse == -INFINITY ? 0.f : ex2_approx((lse - most) * 1.4426950408889634f);
-              const float wt2 = tail == -INFINITY ? 0.f : ex2_approx((tail - most) * 1.4426950408889634f);
-              const float sum = wp + wt2, inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-              wt *= wp * inv;
-              const float wo = wt2 * inv;
-              const float4* src = reinterpret_cast<const float4*>(p.tail_o + row_at * D + half * (D / 2));
-              #pragma unroll
-              for (int c = 0; c < D / 8; ++c) {
-                const float4 x = src[c];
-                o[4 * c] = fmaf(o[4 * c], wt, x.x * wo);
-                o[4 * c + 1] = fmaf(o[4 * c + 1], wt, x.y * wo);
-                o[4 * c + 2] = fmaf(o[4 * c + 2], wt, x.z * wo);
-                o[4 * c + 3] = fmaf(o[4 * c + 3], wt, x.w * wo);
+            float o[32];
+            #pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = sees <= 0 ? 0.f : u2f(u[i]) * wt;
+            if (part) {
+              if (valid) {
+                // four columns of all rows together: a warp's stores are contiguous
+                float4* dst = reinterpret_cast<float4*>(p.part_o + static_cast<int64_t>(w.slot) * p.part_rows * D) +
+                              c * 8 * p.part_rows + rank * kChunkRows + row;
+                #pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  dst[i * p.part_rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
               }
-              wt = 1.f;
-              lse = sum > 0.f || sum != sum ? most + log2f(sum) * 0.69314718055994530942f : -INFINITY;
+              continue;
             }
-            if (valid && half == 0) p.lse[at / D] = lse;
-            // bf16 rows through this warp's area, 16-byte chunks XOR-ed by the row; then a row by D/16 lanes
-            constexpr int kChunks = D / 16;
+            if (p.tail_o && valid) {
+              const float4* src = reinterpret_cast<const float4*>(p.tail_o + row_at * D + c * 32);
+              #pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 x = src[i];
+                o[4 * i] = fmaf(x.x, wo, o[4 * i]);
+                o[4 * i + 1] = fmaf(x.y, wo, o[4 * i + 1]);
+                o[4 * i + 2] = fmaf(x.z, wo, o[4 * i + 2]);
+                o[4 * i + 3] = fmaf(x.w, wo, o[4 * i + 3]);
+              }
+            }
+            // bf16 rows through this warp's area, 16-byte chunks XOR-ed by the row; then a row by four lanes
             #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-              st_shared_v4(sbase + area + lane * (16 * kChunks) + ((c ^ (lane & (kChunks - 1))) << 4),
-                           pack_bf16x2(o[8 * c + 0] * wt, o[8 * c + 1] * wt),
-                           pack_bf16x2(o[8 * c + 2] * wt, o[8 * c + 3] * wt),
-                           pack_bf16x2(o[8 * c + 4] * wt, o[8 * c + 5] * wt),
-                           pack_bf16x2(o[8 * c + 6] * wt, o[8 * c + 7] * wt));
+            for (int i = 0; i < 4; ++i)
+              st_shared_v4(sbase + area + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), pack_bf16x2(o[8 * i], o[8 * i + 1]),
+                           pack_bf16x2(o[8 * i + 2], o[8 * i + 3]), pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
+                           pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
             __syncwarp();
-            const int cq = lane % kChunks;
             #pragma unroll
-            for (int r0 = 0; r0 < 32; r0 += 32 / kChunks) {
-              const int rr = r0 + lane / kChunks;
+            for (int r0 = 0; r0 < 32; r0 += 8) {
+              const int rr = r0 + (lane >> 2), q = lane & 3;
               const int64_t to = __shfl_sync(0xffffffffu, at, rr);
               if (to >= 0)
-                *reinterpret_cast<uint4*>(p.o + to + half * (D / 2) + cq * 8) = *reinterpret_cast<const uint4*>(
-                    smem + area + rr * (16 * kChunks) + ((cq ^ (rr & (kChunks - 1))) << 4));
+                *reinterpret_cast<uint4*>(p.o + to + c * 32 + q * 8) = *reinterpret_cast<const uint4*>(
+                    smem + area + rr * 64 + ((q ^ ((rr >> 1) & 3)) << 4));
             }
             __syncwarp();
           }
+        } else {
+          tc_fence_before();
+          if (lane == 0) mbar_arrive_cluster(lbar(L::bOE));
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lbar(L::bOE));
         ++uq;
     }
   } else if constexpr (E4M3) {
     // ===================================================================== converters
-    if constexpr (E4M3) regs_release<kRegsConvert>();
+    regs_release<ChunkRegs<E4M3>::kConvert>();
     const int tid = (warp - kConvertWarp) * 32 + lane;  // 128 threads
     bool ok = true;
     int g = 0, uq = 0;
