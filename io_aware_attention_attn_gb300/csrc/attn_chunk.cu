@@ -6,37 +6,63 @@
 namespace attn {
 namespace {
 
-// Merge of one unit's parts: M = max m_j, weights 2^(m_j - M).  Block x is for the unit that share x ends and an
-// earlier one began, if there is one.  A warp takes 32 rows and 8 columns -- parts lie column by column, so its
-// loads are contiguous -- and, of a unit of many parts, every second, fourth or eighth, joined through shared
-// memory.  What bounds it is the latency of the few loads in a row.
-constexpr int kJoinWarps = 8, kAtOnce = 4;
+// Merge of units' parts: M = max m_j, weights 2^(m_j - M).  A unit is merged that one share ends and an earlier one began;
+// every block looks the shares' records through for those, and the units' pieces -- 32 rows and 8 columns, a warp each;
+// parts lie column by column, so its loads are contiguous -- go round the blocks.  Of units of many parts a warp takes every
+// second, fourth or eighth, joined through shared memory.  What bounds it is the latency of the few loads in a row (blocks
+// of their own for each share, most of which end no unit: 15 us for 8 units of 10 parts, 30 for 150 of 2).
+constexpr int kJoinWarps = 8, kAtOnce = 4, kJoinBlocks = 4 * 152;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const __grid_constant__ ChunkParams p) {
   __shared__ float s_o[kJoinWarps][8][32];
   __shared__ float2 s_ml[kJoinWarps][32];
+  __shared__ int s_ends[kChunkMaxShares];  // shares that end a unit of several
+  __shared__ int s_count;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) s_count = 0;
   pdl_wait();  // by every block, so that the work after this one waits for the parts' kernel too
-  const int x = static_cast<int>(blockIdx.x);
   const int total = p.head[0], n_shares = p.head[1];
-  if (x >= n_shares) return;
-  const ChunkDesc d = p.desc[x];
-  if (d.tiles < 0) return;
+  if (warp == 0) {  // in order, by one warp
+    int n = 0;
+    for (int x0 = 0; x0 < n_shares; x0 += 32 * 10) {
+      int tiles[10];
+      #pragma unroll
+      for (int k = 0; k < 10; ++k) {
+        const int x = x0 + 32 * k + lane;
+        tiles[k] = x < n_shares ? p.desc[x].tiles : -1;
+      }
+      #pragma unroll
+      for (int k = 0; k < 10; ++k) {
+        const uint32_t has = __ballot_sync(0xffffffffu, tiles[k] >= 0);
+        if (tiles[k] >= 0) s_ends[n + __popc(has & ((1u << lane) - 1u))] = x0 + 32 * k + lane;
+        n += __popc(has);
+      }
+    }
+    if (lane == 0) s_count = n;
+  }
+  __syncthreads();
+  const int units = s_count;
+  if (units == 0) return;
   const Shares shares(static_cast<uint32_t>(total), static_cast<uint32_t>(n_shares));
-  const int i0 = shares.owner(static_cast<uint32_t>(d.unit0)), n = x - i0 + 1;
-  // the beginning share's second part, if it holds tiles of the unit before
-  const int second = second_part(shares.start(i0), d.unit0, p.shape.cost);
-  const int z = d.u / p.n_rg, head0 = (d.u - z * p.n_rg) * p.rg_rows;
-  const int share = n <= kAtOnce ? 1 : n <= 2 * kAtOnce ? 2 : n <= 4 * kAtOnce ? 4 : 8;
+  // warps of a piece, by the parts of a unit on average
+  const int mean = n_shares / units + 1;
+  const int share = mean <= kAtOnce ? 1 : mean <= 2 * kAtOnce ? 2 : mean <= 4 * kAtOnce ? 4 : 8;
   const int side = kJoinWarps / share, sub = warp % share;
-  constexpr int kTasks = 8 * (D / 8);
-  for (int t0 = blockIdx.y * side; t0 < kTasks; t0 += gridDim.y * side) {
-    const int task = t0 + warp / share, c8 = task % (D / 8);
+  const int groups = (p.part_rows + 31) / 32;             // of 32 rows
+  const int per = (groups * (D / 8) + side - 1) / side;   // blocks of a unit
+  for (int it = blockIdx.x; it < units * per; it += gridDim.x) {
+    const int x = s_ends[it / per];
+    const ChunkDesc d = p.desc[x];
+    const int i0 = shares.owner(static_cast<uint32_t>(d.unit0)), n = x - i0 + 1;
+    // the beginning share's second part, if it holds tiles of the unit before
+    const int second = second_part(shares.start(i0), d.unit0, p.shape.cost);
+    const int z = d.u / p.n_rg, head0 = (d.u - z * p.n_rg) * p.rg_rows;
+    const int task = (it % per) * side + warp / share, c8 = task % (D / 8);
     const int at = (task / (D / 8)) * 32 + lane, row = at & (kChunkRows - 1);
     const int tok_in = row / p.rg_rows, head = row - tok_in * p.rg_rows;
     const int tok = (at >> 7) * p.cta_tokens + tok_in;
-    const bool valid = tok_in < p.cta_tokens && tok < d.n_tok && head0 + head < p.group;
+    const bool valid = at < p.part_rows && tok_in < p.cta_tokens && tok < d.n_tok && head0 + head < p.group;
     float acc[8], m = -INFINITY, l = 0.f;
     #pragma unroll
     for (int c = 0; c < 8; ++c) acc[c] = 0.f;
@@ -152,8 +178,7 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t stream) {
   if (q.clusters > clusters) q.clusters = clusters;
   e = launch_dependent(kernel, dim3(2 * static_cast<unsigned>(q.clusters)), L::kThreads, L::kDyn, stream, q);
   if (e != cudaSuccess) return e;
-  return launch_dependent(chunk_join_kernel<D>, dim3(static_cast<unsigned>(q.clusters * q.max_rounds), D / 8),
-                          kJoinWarps * 32, 0, stream, q);
+  return launch_dependent(chunk_join_kernel<D>, dim3(kJoinBlocks), kJoinWarps * 32, 0, stream, q);
 }
 
 }  // namespace

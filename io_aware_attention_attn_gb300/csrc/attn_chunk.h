@@ -17,7 +17,7 @@ constexpr int kChunkRows = 128;      // query rows of a CTA; a unit has two CTAs
 constexpr int kChunkClusters = 76;   // CTA pairs at once, at most
 constexpr int kChunkMaxShares = kChunkClusters * kChunkRounds;
 constexpr int kChunkStagesK = 4, kChunkStagesV = 4, kChunkSBufs = 3;
-constexpr int kChunkRawV = 3, kChunkStagesV8 = 2, kChunkScales = 4, kChunkRowDepth = 8;  // E4M3
+constexpr int kChunkRawV = 3, kChunkStagesV8 = 3, kChunkScales = 4, kChunkRowDepth = 8;  // E4M3
 
 // Where a share begins: request, unit of it (K/V head, row group), row tile, key tile, places of the share,
 // and the request's new tokens, first token and rows.

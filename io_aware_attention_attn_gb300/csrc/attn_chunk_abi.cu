@@ -23,7 +23,10 @@ constexpr int kFewRows = 32;
 enum Kernels { kFew = 1, kMany = 2 };
 // Rows of one unit of the first, by how many there can be.
 int few_group(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
-int few_rows_of(int64_t rows, int B) { return few_group(rows / B * 2 < rows ? rows / B * 2 : rows); }
+int few_rows_of(int64_t rows, int B, bool wide_codes) {
+  const int n = few_group((rows + B - 1) / B);
+  return wide_codes && n > 16 ? 16 : n;
+}
 // What the host knows: the tokens in all.  Where they may lie either way both kernels are launched, each taking its own
 // requests; requests with more than twice kFewRows rows on average leave the first out (a launch that finds
 // nothing to do takes about 2 us, and the second kernel is right for any request).
@@ -46,7 +49,7 @@ bool chunk_sizes_fit(int B, int T, int H, int H_kv, int max_pages, int page_size
   if (rows > INT_MAX / (tiles + kChunkCost) / (static_cast<int64_t>(H_kv) * z.n_rg)) return false;
   const int64_t all = static_cast<int64_t>(T) * (H / H_kv);
   if (!(kernels_for(all, B) & kFew)) return true;
-  const int64_t groups = all / few_rows_of(all, B) + (B < T ? B : T), few_tiles = (most + kPagedTile - 1) / kPagedTile + 1;
+  const int64_t groups = all / 8 + (B < T ? B : T), few_tiles = (most + kPagedTile - 1) / kPagedTile + 1;
   return groups <= INT_MAX / (few_tiles + kPagedMaxCost) / H_kv;
 }
 
@@ -64,7 +67,7 @@ int run_few(const void* q, const attn_kv_cache& c, const int32_t* table, const i
   p.group = H / H_kv;
   const int64_t rows = static_cast<int64_t>(T) * p.group;
   p.n_rg = 1;
-  p.rg_rows = few_rows_of(rows, B);
+  p.rg_rows = few_rows_of(rows, B, c.dtype == ATTN_CACHE_E4M3 && d == 128);
   const PagedLayout L = paged_layout_rows(p.rg_rows, d);
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.o = static_cast<__nv_bfloat16*>(o);

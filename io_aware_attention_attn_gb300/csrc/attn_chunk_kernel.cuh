@@ -75,7 +75,7 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
 // Issue + 2 softmax + store (+ convert): no more than the block was launched with, 4 x 128 (E4M3: 5 x 96).
 template <bool E4M3>
 struct ChunkRegs {
-  static constexpr int kIssue = E4M3 ? 72 : 80, kSoftmax = E4M3 ? 144 : 160, kStore = E4M3 ? 64 : 112, kConvert = 56;
+  static constexpr int kIssue = E4M3 ? 64 : 80, kSoftmax = E4M3 ? 152 : 160, kStore = E4M3 ? 64 : 112, kConvert = 48;
   static_assert(kIssue + 2 * kSoftmax + kStore + (E4M3 ? kConvert : 0) == (E4M3 ? 5 * 96 : 4 * 128), "registers");
 };
 template <int N>
