@@ -20,6 +20,7 @@ constexpr int kChunkCost = 2;
 // kFewRows the one of warp products, whose time is that of reading K and V, above the one of 256-row products.
 // Measured, 32 requests over 4096 keys, 32 query and 8 K/V heads, d = 128: see below.
 constexpr int kFewRows = 32;
+constexpr int kOneCtaTiles = 8;
 enum Kernels { kFew = 1, kMany = 2 };
 // Rows of one unit of the first, by how many there can be.
 int few_group(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
@@ -35,7 +36,7 @@ int kernels_for(int64_t rows, int B) {
   return B > 1 && rows <= 2ll * kFewRows * B ? kFew | kMany : kMany;
 }
 size_t chunk_workspace(int T, int group, int d, const ChunkSizes& z) {
-  const size_t few = paged_layout_rows(few_group(static_cast<int64_t>(T) * group), d).total;
+  const size_t few = few_layout(few_group(static_cast<int64_t>(T) * group), d).total;
   return few > z.total ? few : z.total;
 }
 
@@ -48,7 +49,6 @@ bool chunk_sizes_fit(int B, int T, int H, int H_kv, int max_pages, int page_size
   const int64_t rows = static_cast<int64_t>(T) / (2 * z.cta_tokens) + (B < T ? B : T);  // row tiles, at most
   if (rows > INT_MAX / (tiles + kChunkCost) / (static_cast<int64_t>(H_kv) * z.n_rg)) return false;
   const int64_t all = static_cast<int64_t>(T) * (H / H_kv);
-  if (!(kernels_for(all, B) & kFew)) return true;
   const int64_t groups = all / 8 + (B < T ? B : T), few_tiles = (most + kPagedTile - 1) / kPagedTile + 1;
   return groups <= INT_MAX / (few_tiles + kPagedMaxCost) / H_kv;
 }
@@ -68,7 +68,7 @@ int run_few(const void* q, const attn_kv_cache& c, const int32_t* table, const i
   const int64_t rows = static_cast<int64_t>(T) * p.group;
   p.n_rg = 1;
   p.rg_rows = few_rows_of(rows, B, c.dtype == ATTN_CACHE_E4M3 && d == 128);
-  const PagedLayout L = paged_layout_rows(p.rg_rows, d);
+  const FewLayout L = few_layout(p.rg_rows, d);
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
@@ -76,6 +76,8 @@ int run_few(const void* q, const attn_kv_cache& c, const int32_t* table, const i
   p.seq_lens = seq_lens;
   p.part_o = reinterpret_cast<float*>(ws + L.o_off);
   p.part_ml = reinterpret_cast<float*>(ws + L.ml_off);
+  p.desc = reinterpret_cast<PagedDesc*>(ws + L.desc_off);
+  p.head = reinterpret_cast<int*>(ws + L.head_off);
   p.B = B;
   p.H = H;
   p.max_pages = max_pages;
@@ -90,7 +92,10 @@ int run_few(const void* q, const attn_kv_cache& c, const int32_t* table, const i
   const int64_t most = static_cast<int64_t>(max_pages) * c.page_size;
   const int64_t tiles = most > 0 ? (most + kPagedTile - 1) / kPagedTile : 1;
   const int64_t units = (rows / p.rg_rows + (B < T ? B : T)) * H_kv;
-  const int64_t places = units * tiles;
+  // One request over a few tiles: a CTA goes through all of a unit's in less time than a second launch takes to join
+  // its parts (5 tokens behind 295, 16 query and 4 K/V heads, d = 64: 7.8 us, with the join 13.4).
+  p.one_cta = B == 1 && tiles <= kOneCtaTiles && units <= kPagedMaxCtas / 4;
+  const int64_t places = p.one_cta ? units : units * tiles;
   return launch_fwd_paged_multi(p, d, c.dtype == ATTN_CACHE_E4M3,
                                 places < kPagedMaxCtas ? static_cast<int>(places) : kPagedMaxCtas,
                                 stream) == cudaSuccess
@@ -154,12 +159,14 @@ int run_many(const void* q, const attn_kv_cache& c, const int32_t* table, const 
   return launch_chunk(p, d, e4m3, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
-// or of both, one after the other on one workspace.
+// or of both, one after the other on one workspace.  `behind_prefix`: requests that share a prefix are about as many in
+// each group, so one of the kernels takes them all, by their mean.
 int run_chunk(const void* q, const attn_kv_cache& c, const int32_t* table, const int32_t* seq_lens, const int32_t* cu,
               void* o, float* lse, const float* tail_o, const float* tail_lse, int B, int T, int H, int H_kv, int d,
-              int max_pages, int causal, float scale, QueryLayout at, const ChunkSizes& z, uint8_t* ws,
-              cudaStream_t stream) {
-  const int which = kernels_for(static_cast<int64_t>(T) * (H / H_kv), B);
+              int max_pages, int causal, float scale, QueryLayout at, bool behind_prefix, const ChunkSizes& z,
+              uint8_t* ws, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(T) * (H / H_kv);
+  const int which = behind_prefix ? (rows <= static_cast<int64_t>(kFewRows) * B ? kFew : kMany) : kernels_for(rows, B);
   int rc = ATTN_OK;
   if (which & kFew)
     rc = run_few(q, c, table, seq_lens, cu, o, lse, tail_o, tail_lse, B, T, H, H_kv, d, max_pages, causal, scale, at,
@@ -215,7 +222,7 @@ extern "C" int attn_fwd_paged_varlen(const void* q, const attn_kv_cache* cache, 
     return ATTN_ERR_WORKSPACE;
   if ((rc = check_device()) != 0) return rc;
   return run_chunk(q, *cache, block_table, seq_lens, cu_new, o, lse, nullptr, nullptr, B, T, H, H_kv, d, max_pages,
-                   causal != 0, scale, QueryLayout{static_cast<int64_t>(T) * d, d}, z, static_cast<uint8_t*>(workspace),
+                   causal != 0, scale, QueryLayout{static_cast<int64_t>(T) * d, d}, false, z, static_cast<uint8_t*>(workspace),
                    static_cast<cudaStream_t>(stream));
 }
 
@@ -258,7 +265,7 @@ extern "C" int attn_fwd_paged_shared(const void* q, const attn_kv_cache* cache, 
                      static_cast<cudaStream_t>(stream));
   if (rc != ATTN_OK) return rc;
   return run_chunk(q, *cache, prefix_table, prefix_lens, cu_groups, o, lse, tail_o, tail_lse, groups, B, H, H_kv, d,
-                   max_prefix_pages, 0, scale, QueryLayout{d, static_cast<int64_t>(H) * d}, z, ws + s.chunk,
+                   max_prefix_pages, 0, scale, QueryLayout{d, static_cast<int64_t>(H) * d}, true, z, ws + s.chunk,
                    static_cast<cudaStream_t>(stream));
 }
 

@@ -24,21 +24,24 @@ struct ChunkShape {
 };
 
 // sum of floor((a i + b) / m) over i < n, as lattice points below a line: whole parts out, then the axes
-// swapped, as in Euclid's algorithm.  The result is below 2^32.
+// swapped, as in Euclid's algorithm.  The result and a n + b are below 2^32 (a row of units has fewer than 2^31 places, and
+// so, where each row tile sees `tokens` keys more than the one before, fewer than 2^20 that see any).
 ATTN_HD uint32_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   uint32_t sum = 0;
   while (n > 0) {
     if (a >= m) {
-      sum += static_cast<uint32_t>(static_cast<uint64_t>(n) * (n - 1) / 2) * (a / m);
-      a %= m;
+      const uint32_t q = a / m;
+      sum += static_cast<uint32_t>(static_cast<uint64_t>(n) * (n - 1) / 2) * q;
+      a -= q * m;
     }
     if (b >= m) {
-      sum += n * (b / m);
-      b %= m;
+      const uint32_t q = b / m;
+      sum += n * q;
+      b -= q * m;
     }
-    const uint64_t y = static_cast<uint64_t>(a) * n + b;
-    n = static_cast<uint32_t>(y / m);
-    b = static_cast<uint32_t>(y % m);
+    const uint32_t y = a * n + b;
+    n = y / m;
+    b = y - n * m;
     const uint32_t t = m;
     m = a;
     a = t;

@@ -82,6 +82,12 @@ constexpr int kPagedMaxCost = 2;       // places that a unit takes beside its ti
 constexpr float kPagedTrail = 8.f;     // how far a score may pass the reference maximum, in log2 units
 constexpr int kPagedMaxRows = 32;      // query rows (heads of one K/V head) of a unit
 
+// What the join of several rows a request knows of a CTA (tiles -1: of no unit): the unit's first place and tiles, its K/V
+// head, first row, rows, and its request's first token.
+struct PagedDesc {
+  int unit0, tiles, h, row0, rows, tok0;
+};
+
 struct PagedParams {
   CUtensorMap tm_k;     // 4-D {d, page_size, H_kv, pages}, box {128 bytes of d, box_rows, 1, 1}
   CUtensorMap tm_v;
@@ -107,6 +113,9 @@ struct PagedParams {
   const int* cu;        // [B + 1] first token of each request
   int T, causal, most_rows;  // (requests of more rows have no units)
   int64_t q_head, q_token, o_head, o_token;  // elements from one query head, one token to the next
+  bool one_cta;         // a unit a CTA, nothing to join (one request of few tiles)
+  PagedDesc* desc;      // [CTAs]
+  int* head;            // [0] places in all, [1] CTAs with a share
   const float* tail_o;  // fp32 rows [T][H][d] over other keys to merge with (null: none), and their log-sum-exp
   const float* tail_lse;
   float scale_log2;     // scale * log2(e)
@@ -128,6 +137,18 @@ inline PagedLayout paged_layout_rows(size_t rows, int d) {
 inline PagedLayout paged_layout(int group, int d) {
   const size_t n_rg = paged_row_groups(group);
   return paged_layout_rows((group + n_rg - 1) / n_rg, d);
+}
+// With several rows a request: the records of the join behind them.
+struct FewLayout : PagedLayout {
+  size_t desc_off, head_off;
+};
+inline FewLayout few_layout(size_t rows, int d) {
+  FewLayout L{};
+  static_cast<PagedLayout&>(L) = paged_layout_rows(rows, d);
+  L.desc_off = L.total;
+  L.head_off = (L.desc_off + kPagedMaxCtas * sizeof(PagedDesc) + 255) / 256 * 256;
+  L.total = L.head_off + 256;
+  return L;
 }
 cudaError_t launch_fwd_paged(const PagedParams& p, int d, bool e4m3, int max_tiles,
                              cudaStream_t stream);

@@ -41,7 +41,7 @@
 // what its end costs, are cut into equal shares, one a CTA.  A unit inside one share is finished by
 // its CTA; the parts of a unit that spans several go to the workspace, at most two a CTA, and
 // paged_join_kernel merges them.  It works out for itself which CTAs hold a unit's parts, from the
-// lengths, while it waits for them.
+// lengths, while it waits for them (MULTI: each CTA leaves a record of the unit that it ends).
 //
 // MULTI: a unit's rows are (token, query head) of a request's new tokens, in groups of up to 32, as many groups as
 // the request has rows for, each over all of the request's keys; causal from the end, row by row (token i
@@ -434,7 +434,16 @@ paged_kernel(const __grid_constant__ PagedParams p) {
       if (p.cu[s + 1] < p.cu[s] || (s == 0 && p.cu[0] != 0) || p.cu[s + 1] > p.T)
         atomicCAS(p.status, 0, kStatusBadSeqlens);
   }
-  const int cta = static_cast<int>(blockIdx.x), G = min(p.ctas, total);
+  const int cta = static_cast<int>(blockIdx.x);
+  int G = min(p.ctas, total);
+  if (MULTI && p.one_cta && total > 0) {  // one request: its units are alike
+    const Fresh f = fresh_of<MULTI>(p, 0);
+    G = p.H_kv * f.n_rg;
+  }
+  if (MULTI && cta == 0 && tid == 0) {
+    p.head[0] = total;
+    p.head[1] = G;
+  }
   if (cta >= G) return;
   const Shares shares(static_cast<uint32_t>(total), static_cast<uint32_t>(G));
   const int place0 = shares.start(cta);
@@ -448,6 +457,14 @@ paged_kernel(const __grid_constant__ PagedParams p) {
     __syncthreads();  // what follows may write where s_pre is
   }
   int left = shares.start(cta + 1) - place0;  // places of this CTA still to come
+  if (MULTI && tid == 0) {  // for the join: the unit that this CTA ends and an earlier one began
+    PagedDesc d{0, -1, 0, 0, 0, 0};
+    if (w.t > 0 && w.t < w.n && unit0 + w.n <= place0 + left) {
+      const int row0 = w.rg * p.rg_rows;
+      d = PagedDesc{unit0, w.n, w.h, row0, min(p.rg_rows, w.tokens * p.group - row0), w.tok0};
+    }
+    p.desc[cta] = d;
+  }
   if (w.t >= w.n) {  // it starts behind a unit's last tile
     left -= unit0 + w.n + p.unit_cost - place0;
     if (left <= 0) return;
@@ -977,46 +994,60 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __
   __shared__ float2 s_ml[kJoinWarps];
   static_assert(kJoinWarps * D >= kJoinWarps * 32 + kJoinWarps, "s_o holds block_places' sums");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // (the lengths were complete before the first kernel began, and it let this one start only then)
-  constexpr int kThreads = kJoinWarps * 32;
-  int* s_pre = reinterpret_cast<int*>(s_o);
-  const bool few = p.B <= 256;
-  const int total = few ? all_places<MULTI>(p) : block_places<kThreads, MULTI>(p, s_pre, s_pre + kThreads);
-  const int G = min(p.ctas, total), x = static_cast<int>(blockIdx.x);
-  if (MULTI && total == 0) {
-    pdl_wait();
-    return;
+  const int x = static_cast<int>(blockIdx.x);
+  int unit, unit0, tiles;  // its number, first place and tiles
+  int total, G;
+  bool mine = true;
+  PagedDesc d{};
+  if constexpr (MULTI) {  // each CTA left a record of the unit that it ends
+    pdl_wait();  // by every block, so that the work after this one waits for the parts' kernel too
+    total = p.head[0];
+    G = p.head[1];
+    if (x >= G) return;
+    d = p.desc[x];
+    if (d.tiles < 0) return;
+    unit = 0;
+    unit0 = d.unit0;
+    tiles = d.tiles;
+  } else {
+    // (the lengths were complete before the first kernel began, and it let this one start only then)
+    constexpr int kThreads = kJoinWarps * 32;
+    int* s_pre = reinterpret_cast<int*>(s_o);
+    const bool few = p.B <= 256;
+    total = few ? all_places<MULTI>(p) : block_places<kThreads, MULTI>(p, s_pre, s_pre + kThreads);
+    G = min(p.ctas, total);
+    const Shares shares(static_cast<uint32_t>(total), static_cast<uint32_t>(G));
+    if (p.by_unit) {
+      const int per = p.H_kv * p.n_rg, s = x / per;
+      int before = 0;
+      for (int r = lane; r < s; r += 32) before += req_places<MULTI>(p, r);
+      const int places = req_places<MULTI>(p, s);
+      unit = x;
+      unit0 = __reduce_add_sync(0xffffffffu, before) * per + (x - s * per) * places;
+      tiles = places - p.unit_cost;
+    } else {
+      Walk w;
+      mine = x < G;
+      const int place = mine ? shares.start(x) : 0, k = few ? 0 : share_of<kThreads>(s_pre, place);
+      unit0 = few ? find<MULTI>(p, place, w)
+                  : find<MULTI>(p, place, w, k * ((p.B + kThreads - 1) / kThreads), s_pre[k]);
+      unit = (w.s * p.H_kv + w.h) * p.n_rg + w.rg;
+      tiles = w.n;
+      mine = mine && w.t > 0 && w.t < w.n && shares.owner(unit0 + tiles - 1) == x;
+    }
   }
   const Shares shares(static_cast<uint32_t>(total), static_cast<uint32_t>(G));
-  int unit, unit0, tiles;  // its number, first place and tiles
-  bool mine = true;
-  Walk w{};
-  if (!MULTI && p.by_unit) {
-    const int per = p.H_kv * p.n_rg, s = x / per;
-    int before = 0;
-    for (int r = lane; r < s; r += 32) before += req_places<MULTI>(p, r);
-    const int places = req_places<MULTI>(p, s);
-    unit = x;
-    unit0 = __reduce_add_sync(0xffffffffu, before) * per + (x - s * per) * places;
-    tiles = places - p.unit_cost;
-  } else {
-    mine = x < G;
-    const int place = mine ? shares.start(x) : 0, k = few ? 0 : share_of<kThreads>(s_pre, place);
-    unit0 = few ? find<MULTI>(p, place, w)
-                : find<MULTI>(p, place, w, k * ((p.B + kThreads - 1) / kThreads), s_pre[k]);
-    unit = (w.s * p.H_kv + w.h) * p.n_rg + w.rg;
-    tiles = w.n;
-    mine = mine && w.t > 0 && w.t < w.n && shares.owner(unit0 + tiles - 1) == x;
-  }
   const int i0 = shares.owner(unit0), n = shares.owner(unit0 + tiles - 1) - i0 + 1;
   // the beginning CTA's second part, if it holds tiles of the unit before
   const int second = second_part(shares.start(i0), unit0, p.unit_cost);
-  __syncthreads();  // s_pre has been read
-  pdl_wait();  // by every block, so that the work after this one waits for the parts' kernel too
-  if (!mine || n == 1) return;
+  if constexpr (!MULTI) {
+    __syncthreads();  // s_pre has been read
+    pdl_wait();  // by every block, so that the work after this one waits for the parts' kernel too
+    if (!mine || n == 1) return;
+  }
   const int rg = unit % p.n_rg, sh = unit / p.n_rg;
-  const int row0 = (MULTI ? w.rg : rg) * p.rg_rows;
-  const int rows = min(p.rg_rows, (MULTI ? w.tokens * p.group : p.group) - row0);
+  const int row0 = MULTI ? d.row0 : rg * p.rg_rows;
+  const int rows = MULTI ? d.rows : min(p.rg_rows, p.group - row0);
   const int share = join_share(n);
   const int side = kJoinWarps / share, sub = warp % share;
   for (int r0 = blockIdx.y * side; r0 < rows; r0 += gridDim.y * side) {
@@ -1088,10 +1119,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __
     }
     if (MULTI && sub == 0 && row < rows) {
       if constexpr (kPer == 4) {
-        store_row<D>(p, w.h, w.tok0, row0 + row, lane, make_float4(acc[0], acc[1], acc[2], acc[3]), m, l);
+        store_row<D>(p, d.h, d.tok0, row0 + row, lane, make_float4(acc[0], acc[1], acc[2], acc[3]), m, l);
       } else {  // two columns a lane: the even lanes store four
         const float c2 = __shfl_down_sync(0xffffffffu, acc[0], 1), c3 = __shfl_down_sync(0xffffffffu, acc[1], 1);
-        if (lane % 2 == 0) store_row<D>(p, w.h, w.tok0, row0 + row, lane / 2, make_float4(acc[0], acc[1], c2, c3), m, l);
+        if (lane % 2 == 0) store_row<D>(p, d.h, d.tok0, row0 + row, lane / 2, make_float4(acc[0], acc[1], c2, c3), m, l);
       }
     } else if (sub == 0 && row < rows) {
       const int64_t out = static_cast<int64_t>(sh / p.H_kv) * p.H +
@@ -1141,7 +1172,7 @@ cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
   // blocks of a join: as many as its rows keep busy at the mean number of parts
   const int blocks = (p.rg_rows * join_share(ctas / joins + 2) + kJoinWarps - 1) / kJoinWarps;
   e = launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), L::kThreads, L::kDyn, stream, q);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || (MULTI && p.one_cta)) return e;
   return launch_dependent(paged_join_kernel<D, MULTI>,
                           dim3(static_cast<unsigned>(joins), static_cast<unsigned>(blocks)),
                           kJoinWarps * 32, 0, stream, q);
