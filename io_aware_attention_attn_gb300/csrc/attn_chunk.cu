@@ -22,20 +22,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const __gri
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) s_count = 0;
   pdl_wait();  // by every block, so that the work after this one waits for the parts' kernel too
-  const int total = p.head[0], n_shares = p.head[1];
+  const int total = p.head[0], n_shares = p.head[1], most = p.clusters * p.max_rounds;
   if (warp == 0) {  // in order, by one warp
     int n = 0;
-    for (int x0 = 0; x0 < n_shares; x0 += 32 * 10) {
+    for (int x0 = 0; x0 < most; x0 += 32 * 10) {  // (all records, so that they need not wait for the count)
       int tiles[10];
       #pragma unroll
       for (int k = 0; k < 10; ++k) {
         const int x = x0 + 32 * k + lane;
-        tiles[k] = x < n_shares ? p.desc[x].tiles : -1;
+        tiles[k] = x < most ? p.desc[x].tiles : -1;
       }
       #pragma unroll
       for (int k = 0; k < 10; ++k) {
-        const uint32_t has = __ballot_sync(0xffffffffu, tiles[k] >= 0);
-        if (tiles[k] >= 0) s_ends[n + __popc(has & ((1u << lane) - 1u))] = x0 + 32 * k + lane;
+        const bool ends = tiles[k] >= 0 && x0 + 32 * k + lane < n_shares;
+        const uint32_t has = __ballot_sync(0xffffffffu, ends);
+        if (ends) s_ends[n + __popc(has & ((1u << lane) - 1u))] = x0 + 32 * k + lane;
         n += __popc(has);
       }
     }

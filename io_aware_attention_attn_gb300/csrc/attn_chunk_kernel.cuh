@@ -38,6 +38,7 @@
 namespace attn {
 namespace chunk {
 
+constexpr int kStartsBarrier = 5;  // (1 to 4: the two warps of a row)
 enum : int { kRoleProducer = 9, kRoleIssuer = 10, kRoleSoftmax = 11, kRoleConvert = 12, kRoleStore = 13 };
 
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
@@ -199,8 +200,47 @@ __device__ uint32_t block_places(const ChunkParams& p, int* s_pre, int* s_warp, 
   return static_cast<uint32_t>(total) * per;
 }
 
-// The unit at place `at` (a warp's lanes together): w.j past its tiles means in the places after them.
-// Returns the unit's first place.
+// The unit at place `at` (a warp's lanes together; w.j past its tiles means in the places after them), if it is of one of the 32
+// requests from s0 on, before which there are `before` places: lane i has request s0 + i, its places over all heads and
+// `scan`, their sum up to there.  Returns the unit's first place, or -1.
+__device__ int find_among(const ChunkParams& p, int at, int before, int s0, const ChunkReq& r, int tok0, int places,
+                          int scan, Walk& w) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t past = __ballot_sync(0xffffffffu, before + scan > at);
+  if (!past) return -1;
+  const int src = __ffs(past) - 1;
+  before += __shfl_sync(0xffffffffu, scan - places, src);
+  w.s = s0 + src;
+  w.r.n = __shfl_sync(0xffffffffu, r.n, src);
+  w.r.L = __shfl_sync(0xffffffffu, r.L, src);
+  w.tok0 = __shfl_sync(0xffffffffu, tok0, src);
+  const int row = __shfl_sync(0xffffffffu, places, src) / (p.H_kv * p.n_rg);
+  w.nt = row_tiles(w.r, p.shape);
+  w.u = (at - before) / row;
+  const int in = at - before - w.u * row;
+  int lo = 0, len = w.nt;  // the row tile is among lo .. lo + len - 1
+  while (len > 1) {
+    const int step = (len + 31) >> 5, t = lo + step * lane;
+    const bool le = step * lane < len && places_before(w.r, p.shape, t) <= in;
+    const int c = __popc(__ballot_sync(0xffffffffu, le)) - 1;
+    const int end = lo + len;
+    lo += step * c;
+    len = min(step, end - lo);
+  }
+  w.t = lo;
+  w.j = in - places_before(w.r, p.shape, lo);
+  w.n = key_tiles(w.r, p.shape, lo);
+  return at - w.j;
+}
+__device__ __forceinline__ int scan_lanes(int x) {
+  #pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, x, off);
+    if ((threadIdx.x & 31) >= off) x += up;
+  }
+  return x;
+}
+// The same among all requests, from the sums of block_places.
 template <int T>
 __device__ int find(const ChunkParams& p, const int* s_pre, int at, Walk& w) {
   const int lane = threadIdx.x & 31, per = p.H_kv * p.n_rg;
@@ -214,39 +254,10 @@ __device__ int find(const ChunkParams& p, const int* s_pre, int at, Walk& w) {
     int tok0 = 0;
     ChunkReq r{0, 0};
     if (s < p.B) r = req_at(p, s, tok0);
-    const int places = s < p.B ? unit_row_places(r, p.shape) : 0;
-    int scan = places * per;
-    #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, scan, off);
-      if (lane >= off) scan += up;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, before + scan > at);
-    if (past) {
-      const int src = __ffs(past) - 1;
-      before += __shfl_sync(0xffffffffu, scan - places * per, src);
-      w.s = s0 + src;
-      w.r.n = __shfl_sync(0xffffffffu, r.n, src);
-      w.r.L = __shfl_sync(0xffffffffu, r.L, src);
-      w.tok0 = __shfl_sync(0xffffffffu, tok0, src);
-      const int row = __shfl_sync(0xffffffffu, places, src);
-      w.nt = row_tiles(w.r, p.shape);
-      w.u = (at - before) / row;
-      const int in = at - before - w.u * row;
-      int lo = 0, len = w.nt;  // the row tile is among lo .. lo + len - 1
-      while (len > 1) {
-        const int step = (len + 31) >> 5, t = lo + step * lane;
-        const bool le = step * lane < len && places_before(w.r, p.shape, t) <= in;
-        const int c = __popc(__ballot_sync(0xffffffffu, le)) - 1;
-        const int end = lo + len;
-        lo += step * c;
-        len = min(step, end - lo);
-      }
-      w.t = lo;
-      w.j = in - places_before(w.r, p.shape, lo);
-      w.n = key_tiles(w.r, p.shape, lo);
-      return at - w.j;
-    }
+    const int places = s < p.B ? unit_row_places(r, p.shape) * per : 0;
+    const int scan = scan_lanes(places);
+    const int unit0 = find_among(p, at, before, s0, r, tok0, places, scan, w);
+    if (unit0 >= 0) return unit0;
     before += __shfl_sync(0xffffffffu, scan, 31);
   }
   w = Walk{p.B, 0, 0, 0, 0, {0, 0}, 0, 0, 1};  // (not reached: at is below the number of places)
@@ -349,30 +360,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
     tmem_alloc_pair(sbase + L::kMisc, 512);
     tmem_relinquish_pair();
   }
+  tc_fence_before();
+  cluster_sync_all();  // barriers initialised and tensor memory allocated in both CTAs
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
   pdl_wait();
+  pdl_launch_dependents();
+  // The shares of this cluster, one a round, and for the join the unit that each begins inside: by a warp each, from the
+  // lengths in its lanes where that is enough (2.7 us less for the block's sums and barriers to the first copy), else from
+  // sums of the whole block.  The other warps wait for the producer, warp 0, to tell them what comes.
+  int rounds = 0;
+  Walk w0{};  // the first share's beginning
   {
-    // the shares of this cluster, one a round, and for the join the unit that each begins inside
+    const bool few = p.B <= 32;
     int* s_pre = reinterpret_cast<int*>(smem + L::kOut);
-    float wide;
-    const uint32_t total = block_places<T>(p, s_pre, s_pre + T, wide);
-    pdl_launch_dependents();
-    const int rounds = chunk_rounds(total, G, wide * static_cast<float>(p.H_kv * D * (E4M3 ? 2 : 4)), p.max_rounds);
-    const int n_shares = total == 0 ? 0 : chunk_shares(total, G, rounds);
-    if (threadIdx.x == 0) {
-      misc[2] = static_cast<uint32_t>((n_shares + G - 1) / G);
-      if (blockIdx.x == 0) {
+    float wide = 0.f;
+    uint32_t total = 0;
+    ChunkReq mine{0, 0};
+    int tok0 = 0, places = 0, scan = 0;
+    if (!few) {
+      total = block_places<T>(p, s_pre, s_pre + T, wide);
+    } else if (warp < kChunkRounds) {
+      bool bad = false;
+      if (lane < p.B) {
+        mine = req_at(p, lane, tok0);
+        const int x = p.cu[lane], y = p.cu[lane + 1];
+        bad = y < x || (lane == 0 && x != 0) || y > p.T;
+        places = unit_row_places(mine, p.shape) * (p.H_kv * p.n_rg);
+        if (row_tiles(mine, p.shape) > 1) wide = static_cast<float>(mine.L);
+      }
+      if (bad && blockIdx.x == 0) atomicCAS(p.status, 0, kStatusBadSeqlens);
+      scan = scan_lanes(places);
+      total = static_cast<uint32_t>(__shfl_sync(0xffffffffu, scan, 31));
+      #pragma unroll
+      for (int off = 16; off > 0; off >>= 1) wide += __shfl_xor_sync(0xffffffffu, wide, off);
+    }
+    if (warp < p.max_rounds) {
+      const int most = chunk_rounds(total, G, wide * static_cast<float>(p.H_kv * D * (E4M3 ? 2 : 4)), p.max_rounds);
+      const int n_shares = total == 0 ? 0 : chunk_shares(total, G, most);
+      rounds = (n_shares + G - 1) / G;
+      if (blockIdx.x == 0 && threadIdx.x == 0) {
         p.head[0] = static_cast<int>(total);
         p.head[1] = n_shares;
       }
-    }
-    const int share = warp * G + c0;
-    if (warp < p.max_rounds) {
+      const int share = warp * G + c0;
       Walk w{};
       if (share < n_shares) {
         const Shares shares(total, static_cast<uint32_t>(n_shares));
         const int at = shares.start(share), next = shares.start(share + 1);
         int left = next - at;
-        const int unit0 = find<T>(p, s_pre, at, w);
+        const int unit0 = few ? find_among(p, at, 0, 0, mine, tok0, places, scan, w) : find<T>(p, s_pre, at, w);
         ChunkDesc d{0, -1, 0, 0, 0, 0};
         // inside a unit of an earlier share, whose last tile is in this one
         if (w.j > 0 && w.j < w.n && unit0 + w.n <= next)
@@ -384,14 +421,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
         }
         w.left = left;
       }
-      if (lane == 0) starts[warp] = ChunkStart{w.s, w.u, w.t, w.j, w.left, w.r.n, w.tok0, w.r.L};
+      if (warp == 0) w0 = w;
+      else if (lane == 0) starts[warp] = ChunkStart{w.s, w.u, w.t, w.j, w.left, w.r.n, w.tok0, w.r.L};
     }
   }
-  tc_fence_before();
-  cluster_sync_all();  // barriers initialised and tensor memory allocated in both CTAs
-  tc_fence_after();
-  const uint32_t tmem = misc[0];
-  const int rounds = static_cast<int>(misc[2]);  // of the producer, which tells the others what comes
   const ChunkUnit* units = reinterpret_cast<const ChunkUnit*>(smem + L::kUnits);
   // The uq-th unit (or part): false when there is none, or a wait gave up.
   auto unit_at = [&](int uq, ChunkUnit& w, bool& ok, int role) {
@@ -407,6 +440,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
   // Counters kept by every role: uq = units (or parts) done so far, g = key tiles done so far.
   if (warp < kSoftmaxWarp) {
   regs_release<ChunkRegs<E4M3>::kIssue>();
+  if (warp > 0 && warp < kChunkRounds && rounds > 1)
+    asm volatile("bar.arrive %0, %1;" ::"r"(kStartsBarrier), "r"(kChunkRounds * 32) : "memory");
   if (warp == 0) {
     // ===================================================================== producer
     const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
@@ -422,7 +457,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
     int g = 0, uq = 0;
     int entries = 0, entry_base = 0, entry_s = -1;  // this lane's entry of the 32 looked up last
     for (int r = 0; ok && r < rounds; ++r) {
-      Walk w = walk_from(p, starts[r]);
+      if (r == 1) named_barrier_sync(kStartsBarrier, kChunkRounds * 32);  // the later rounds' starts are there
+      Walk w = r == 0 ? w0 : walk_from(p, starts[r]);
       bool first = true;  // of the share's units: its part, if it is one, has the share's first place in the workspace
       while (ok && w.left > 0) {
         const int j_end = min(w.n, w.j + w.left);

@@ -79,13 +79,15 @@ ATTN_HD int unit_row_places(const ChunkReq& r, const ChunkShape& c) {
 }
 
 // Rounds: the shares are taken in so many rounds, one a cluster in each, so that the clusters are near one another on
-// the line and read the same K and V from L2 while they last.  `wide` rows of requests with several row
-// tiles, each of row_bytes over all heads: as many rounds as keep what a round reads near 32 MB.
+// the line and read the same K and V from L2 while they last: `wide_bytes`, what requests with several row tiles keep in the
+// cache over all heads, shared out to rounds of up to 96 MB, where a share stays long beside the parts that its ends
+// leave.  (4096 tokens behind 12288, 32 K/V heads, 268 MB: 620 us in one round, 600 in two; 16 prompts of 181 to 3879
+// tokens, 16 heads, 277 MB: 356 in one, 373 in two, whose shares are 107 tiles long.)
 constexpr int kChunkRounds = 4;
 constexpr int kChunkMinShare = 4;   // places of a share, at least
 ATTN_HD int chunk_rounds(uint32_t total, int clusters, float wide_bytes, int most) {
   int r = 1;
-  while (r < most && wide_bytes > r * 33554432.f && total / (2u * r * clusters) >= 64u) r *= 2;
+  while (r < most && wide_bytes > r * 100663296.f && total / (2u * r * clusters) >= 256u) r *= 2;
   return r;
 }
 ATTN_HD int chunk_shares(uint32_t total, int clusters, int rounds) {
