@@ -139,6 +139,7 @@ __device__ __forceinline__ void next_unit(const ChunkParams& p, Walk& w) {
       w.u = 0;
       w.r.n = 0;
       w.r.L = 0;
+      #pragma unroll 1
       while (w.r.n == 0 && ++w.s < p.B) w.r = req_at(p, w.s, w.tok0);  // (no new tokens: no units)
       w.nt = row_tiles(w.r, p.shape);
     }
@@ -165,6 +166,7 @@ __device__ uint32_t block_places(const ChunkParams& p, int* s_pre, int* s_warp, 
   int sum = 0;
   float rows = 0.f;
   bool bad = false;
+  #pragma unroll 1
   for (int s = lo; s < hi; ++s) {
     int tok0;
     const ChunkReq r = req_at(p, s, tok0);
@@ -219,6 +221,7 @@ __device__ int find_among(const ChunkParams& p, int at, int before, int s0, cons
   w.u = (at - before) / row;
   const int in = at - before - w.u * row;
   int lo = 0, len = w.nt;  // the row tile is among lo .. lo + len - 1
+  #pragma unroll 1
   while (len > 1) {
     const int step = (len + 31) >> 5, t = lo + step * lane;
     const bool le = step * lane < len && places_before(w.r, p.shape, t) <= in;
@@ -249,6 +252,7 @@ __device__ int find(const ChunkParams& p, const int* s_pre, int at, Walk& w) {
   for (int i = 0; i < T; i += 32) k += __popc(__ballot_sync(0xffffffffu, s_pre[i + lane] <= at));
   --k;
   int before = s_pre[k];
+  #pragma unroll 1
   for (int s0 = k * ((p.B + T - 1) / T); s0 < p.B; s0 += 32) {
     const int s = s0 + lane;
     int tok0 = 0;

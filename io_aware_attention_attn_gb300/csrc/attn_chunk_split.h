@@ -28,6 +28,9 @@ struct ChunkShape {
 // so, where each row tile sees `tokens` keys more than the one before, fewer than 2^20 that see any).
 ATTN_HD uint32_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   uint32_t sum = 0;
+#ifdef __CUDACC__
+  #pragma unroll 1
+#endif
   while (n > 0) {
     if (a >= m) {
       const uint32_t q = a / m;
