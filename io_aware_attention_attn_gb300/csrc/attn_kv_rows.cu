@@ -15,41 +15,63 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 256, kDeep = 4;
+constexpr int kThreads = 256, kDeep = 4;  // (writing E4M3 rows takes its eight rows of a lane together)
 
-// x / sc rounded to nearest fp32 from rc = RN(1 / sc) and one remainder correction (Markstein's method, as in the
-// quantizer of attn_fp8.cu, whose check covers every bf16 x and scale that a bf16 row can have).
-__device__ __forceinline__ float quotient(float x, float sc, float rc) {
-  const float q0 = __fmul_rn(x, rc);
-  return copysignf(__fmaf_rn(__fmaf_rn(-sc, q0, x), rc, q0), x);
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {  // (a NaN gives way to a number)
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
-// 8 bf16 values -> 8 codes, with the D/8 lanes that hold the row; returns the row's scale.
+// The largest magnitude in each of eight rows, of which this lane (one of D/8 that hold a row together) has x[0..7]: the
+// lanes hand each other half of the rows in each step, so lane i is left with row i % 8 alone (8 steps across lanes
+// instead of 32).
 template <int D>
-__device__ __forceinline__ float quantize(const uint4& x, uint2& codes) {
+__device__ __forceinline__ float amax_of_rows(const uint4 (&x)[8], int i) {
+  uint32_t m[8];
+  #pragma unroll
+  for (int r = 0; r < 8; ++r)
+    m[r] = max_bf16x2(max_bf16x2(x[r].x & 0x7fff7fffu, x[r].y & 0x7fff7fffu),
+                      max_bf16x2(x[r].z & 0x7fff7fffu, x[r].w & 0x7fff7fffu));
+  #pragma unroll
+  for (int bit = 4; bit > 0; bit >>= 1) {  // rows with this bit of their number go to the lanes that have it
+    const bool up = i & bit;
+    #pragma unroll
+    for (int r = 0; r < bit; ++r) {
+      const uint32_t keep = up ? m[r + bit] : m[r], give = up ? m[r] : m[r + bit];
+      m[r] = max_bf16x2(keep, __shfl_xor_sync(0xffffffffu, give, bit));
+    }
+  }
+  if (D == 128) m[0] = max_bf16x2(m[0], __shfl_xor_sync(0xffffffffu, m[0], 8));
+  return fmaxf(bf16lo_to_f32(m[0]), bf16hi_to_f32(m[0]));
+}
+
+// 8 bf16 values -> 8 codes of x / sc rounded to nearest fp32, from rc = RN(1 / sc) and one remainder correction
+// (Markstein's method, as in the quantizer of attn_fp8.cu, whose check covers every bf16 x and scale that a bf16 row can
+// have), two at a time; the sign of a value that rounds to zero is x's.
+__device__ __forceinline__ uint2 quantize(const uint4& x, float sc, float rc) {
   const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-  float f[8], amax = 0.f;
+  const bool fast = sc >= 0x1p-100f && sc <= 0x1p100f;
+  uint32_t c[4];
   #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16lo_to_f32(v[i]);
-    f[2 * i + 1] = bf16hi_to_f32(v[i]);
-    amax = fmax3(amax, fabsf(f[2 * i]), fabsf(f[2 * i + 1]));
+    const float a = bf16lo_to_f32(v[i]), b = bf16hi_to_f32(v[i]);
+    float q0, q1, r0, r1;
+    fmul2(q0, q1, a, b, rc, rc);
+    ffma2(r0, r1, -sc, -sc, q0, q1, a, b);
+    ffma2(q0, q1, r0, r1, rc, rc, q0, q1);
+    c[i] = pack_e4m3x2(q0, q1);
   }
+  if (!fast) {
+    #pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c[i] = pack_e4m3x2(__fdiv_rn(bf16lo_to_f32(v[i]), sc), __fdiv_rn(bf16hi_to_f32(v[i]), sc));
+  }
+  uint32_t out[2];
   #pragma unroll
-  for (int off = D / 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-  float sc = __fdiv_rn(amax, 448.f);
-  if (!(sc >= 0x1p-126f)) sc = 1.f;
-  uint16_t c[4];
-  if (sc >= 0x1p-100f && sc <= 0x1p100f) {
-    const float rc = __frcp_rn(sc);
-    #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = pack_e4m3x2(quotient(f[2 * i], sc, rc), quotient(f[2 * i + 1], sc, rc));
-  } else {
-    #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = pack_e4m3x2(__fdiv_rn(f[2 * i], sc), __fdiv_rn(f[2 * i + 1], sc));
-  }
-  codes = make_uint2(c[0] | static_cast<uint32_t>(c[1]) << 16, c[2] | static_cast<uint32_t>(c[3]) << 16);
-  return sc;
+  for (int i = 0; i < 2; ++i)
+    out[i] = ((c[2 * i] | c[2 * i + 1] << 16) & 0x7f7f7f7fu) | (__byte_perm(v[2 * i], v[2 * i + 1], 0x7531) & 0x80808080u);
+  return make_uint2(out[0], out[1]);
 }
 
 // 8 codes x scale -> 8 bf16 values
@@ -73,7 +95,7 @@ struct Place {
 };
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constant__ KvRowsParams p) {
+__global__ void __launch_bounds__(kThreads, 4) kv_write_kernel(const __grid_constant__ KvRowsParams p) {
   constexpr int kLanes = D / 8, kGroups = kThreads / kLanes, kTokens = kGroups * kDeep;
   __shared__ Place s_place[kTokens];
   pdl_wait();
@@ -90,38 +112,44 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constan
     s_place[i] = at;
   }
   __syncthreads();
-  const int group = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+  const int group = threadIdx.x / kLanes, c = threadIdx.x % kLanes, lane = threadIdx.x & 31;
   for (int h = blockIdx.y; h < p.H_kv; h += gridDim.y) {
-    uint4 x[2][kDeep];
+    uint4 x[2 * kDeep];  // K rows of the four tokens, then V rows
     Place at[kDeep];
     #pragma unroll
     for (int u = 0; u < kDeep; ++u) {
       const int i = group + u * kGroups;
       at[u] = s_place[i];
-      x[0][u] = x[1][u] = make_uint4(0, 0, 0, 0);
+      x[u] = x[kDeep + u] = make_uint4(0, 0, 0, 0);
       if (at[u].page >= 0) {
         const int64_t t = t0 + i, b = p.N == 1 ? t : p.B == 1 ? 0 : t / p.N, n = t - b * p.N;
-        x[0][u] = *reinterpret_cast<const uint4*>(p.k + b * p.k_batch + h * p.k_head + n * p.k_token + 8 * c);
-        x[1][u] = *reinterpret_cast<const uint4*>(p.v + b * p.v_batch + h * p.v_head + n * p.v_token + 8 * c);
+        x[u] = *reinterpret_cast<const uint4*>(p.k + b * p.k_batch + h * p.k_head + n * p.k_token + 8 * c);
+        x[kDeep + u] = *reinterpret_cast<const uint4*>(p.v + b * p.v_batch + h * p.v_head + n * p.v_token + 8 * c);
       }
     }
+    float sc = 1.f, rc = 1.f;
+    if constexpr (E4M3) {  // of row c % 8
+      const float amax = amax_of_rows<D>(x, c);
+      sc = __fdiv_rn(amax, 448.f);
+      if (!(sc >= 0x1p-126f)) sc = 1.f;
+      rc = __frcp_rn(sc);
+      const Place mine = s_place[group + (c & 3) * kGroups];
+      if (c < 8 && mine.page >= 0)
+        (c < kDeep ? p.ks : p.vs)[((static_cast<int64_t>(mine.page) * p.H_kv + h) << p.page_shift) + mine.row] = sc;
+    }
     #pragma unroll
-    for (int u = 0; u < kDeep; ++u) {
-      const int64_t in = (static_cast<int64_t>(h) << p.page_shift) + at[u].row;
+    for (int side = 0; side < 2; ++side) {
+      uint8_t* cache = side ? p.vc : p.kc;
       #pragma unroll
-      for (int side = 0; side < 2; ++side) {
-        uint8_t* cache = side ? p.vc : p.kc;
-        const int64_t to = at[u].page * p.page_stride + in * D + 8 * c;
+      for (int u = 0; u < kDeep; ++u) {
+        const int64_t to = at[u].page * p.page_stride + ((static_cast<int64_t>(h) << p.page_shift) + at[u].row) * D + 8 * c;
         if constexpr (E4M3) {
-          uint2 codes;
-          const float sc = quantize<D>(x[side][u], codes);
-          if (at[u].page >= 0) {
-            *reinterpret_cast<uint2*>(cache + to) = codes;
-            if (c == 0)
-              (side ? p.vs : p.ks)[((static_cast<int64_t>(at[u].page) * p.H_kv) << p.page_shift) + in] = sc;
-          }
+          const int from = (lane & ~(kLanes - 1)) + side * kDeep + u;  // the lane that has this row's scale
+          const uint2 codes = quantize(x[side * kDeep + u], __shfl_sync(0xffffffffu, sc, from),
+                                       __shfl_sync(0xffffffffu, rc, from));
+          if (at[u].page >= 0) *reinterpret_cast<uint2*>(cache + to) = codes;
         } else {
-          if (at[u].page >= 0) *reinterpret_cast<uint4*>(cache + 2 * to) = x[side][u];
+          if (at[u].page >= 0) *reinterpret_cast<uint4*>(cache + 2 * to) = x[side * kDeep + u];
         }
       }
     }
@@ -200,11 +228,11 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
   }
 }
 
-// Blocks along heads: enough to fill the GPU where tokens alone are too few, else a block takes several heads
-// for each look at its tokens' places.
+// Blocks along heads: enough for several rounds of the GPU's blocks, else a block takes several heads for each look at its
+// tokens' places.
 dim3 grid_of(int64_t tokens, int H_kv, int d) {
   const int64_t per = kThreads / (d / 8) * kDeep, x = (tokens + per - 1) / per;
-  const int64_t want = (8 * 152 + x - 1) / x;
+  const int64_t want = (32 * 152 + x - 1) / x;
   int64_t y = want < H_kv ? want : H_kv;
   if (y > 65535) y = 65535;
   return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
