@@ -736,10 +736,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
         const int j_end = w.j_end;
         const bool valid = my_tok < p.cta_tokens && unit_tok < w.n_tok && w.head0 + my_head < p.group;
         const bool any = __any_sync(0xffffffffu, valid);   // a warp without rows only keeps step
-        // keys that this row sees, and the fewest that a row of this warp sees (without the rows past the end)
+        // keys that this row sees, and the fewest that a row of this warp sees (what the lanes without a row compute, of
+        // whatever lies in their rows of the products, is not used)
         const int sees = !valid ? 0 : p.shape.causal ? min(w.L, w.pos0 + unit_tok + 1) : w.L;
         const int least = __reduce_min_sync(0xffffffffu, valid ? sees : 0x7fffffff);
-        const bool ragged = __any_sync(0xffffffffu, !valid);
         float sl2 = p.scale_log2;
         float m2 = -INFINITY;                // reference maximum of the scaled scores (log2 units)
         float le[4] = {0.f, 0.f, 0.f, 0.f};  // sums of 2^(t - m)
@@ -784,7 +784,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
               }
             }
             const int key0 = j * kChunkTile + 64 * half;
-            if (ragged || key0 + 64 > least) {
+            if (key0 + 64 > least) {
               const int lim = sees - key0;
               #pragma unroll
               for (int cc = 0; cc < 64; ++cc) s[cc] = (cc < lim) ? s[cc] : -INFINITY;
