@@ -412,9 +412,9 @@ ATTN_API size_t attn_fwd_paged_varlen_workspace_bytes(int T, int H, int H_kv, in
  * Attention of one new token of each of B requests whose first rows are shared: requests cu_groups[g] ..
  * cu_groups[g+1]-1 have the prefix_lens[g] rows of the pages prefix_table[g][0], [1], ... before the seq_lens[s] rows
  * of their own, block_table[s][0], [1], ....  O and lse are those of attn_fwd_paged over the rows of both, but the
- * prefix is read once for a group (once for each 256 / (H / H_kv) of its requests) instead of once a request.  Four
- * launches: attn_fwd_paged over the own rows, left in fp32, attn_fwd_paged_varlen's kernels over the prefixes,
- * and the block merge of the two.
+ * prefix is read once for a group (once for each 16 to 256 query rows of a K/V head, by how many there are) instead of
+ * once a request.  The attentions over the prefixes and over the own rows are left in fp32 and joined by the
+ * block merge; three or four launches.
  *   q, o : bf16 [B, H, d] (= [B, H, 1, d]);  lse : fp32 [B, H]
  *   prefix_table : int32 [groups, max_prefix_pages];  prefix_lens : int32 [groups], clamped to 0 ..
  *     max_prefix_pages * page_size;  cu_groups : int32 [groups + 1], from 0 up, at most B (as cu_new of

@@ -50,7 +50,7 @@ bool chunk_sizes_fit(int B, int T, int H, int H_kv, int max_pages, int page_size
   if (rows > INT_MAX / (tiles + kChunkCost) / (static_cast<int64_t>(H_kv) * z.n_rg)) return false;
   const int64_t all = static_cast<int64_t>(T) * (H / H_kv);
   const int64_t groups = all / 8 + (B < T ? B : T), few_tiles = (most + kPagedTile - 1) / kPagedTile + 1;
-  return groups <= INT_MAX / (few_tiles + kPagedMaxCost) / H_kv;
+  return groups <= INT_MAX / (few_tiles + kFewCost) / H_kv;
 }
 
 struct QueryLayout {
@@ -58,9 +58,17 @@ struct QueryLayout {
 };
 
 // Launches on checked arguments: of the kernel for few rows,
+// (own: the tokens are requests that share a prefix and have rows of their own as well)
+struct OwnRows {
+  const int32_t* table;
+  const int32_t* lens;
+  int max_pages;
+  float* pair_o;
+  float* pair_lse;
+};
 int run_few(const void* q, const attn_kv_cache& c, const int32_t* table, const int32_t* seq_lens, const int32_t* cu,
-            void* o, float* lse, const float* tail_o, const float* tail_lse, int B, int T, int H, int H_kv, int d,
-            int max_pages, int causal, float scale, QueryLayout at, int most_rows, uint8_t* ws, cudaStream_t stream) {
+            void* o, float* lse, const OwnRows* own, int B, int T, int H, int H_kv, int d, int max_pages, int causal,
+            float scale, QueryLayout at, int most_rows, uint8_t* ws, cudaStream_t stream) {
   PagedParams p{};
   const int rc = fill_paged(p, c, H_kv, d, scale);
   if (rc != ATTN_OK) return rc;
@@ -87,20 +95,29 @@ int run_few(const void* q, const attn_kv_cache& c, const int32_t* table, const i
   p.most_rows = most_rows;
   p.q_head = p.o_head = at.head;
   p.q_token = p.o_token = at.token;
-  p.tail_o = tail_o;
-  p.tail_lse = tail_lse;
-  const int64_t most = static_cast<int64_t>(max_pages) * c.page_size;
+  p.own_first = INT_MAX;
+  int64_t most = static_cast<int64_t>(max_pages) * c.page_size;
+  int64_t units = (rows / p.rg_rows + (B < T ? B : T)) * H_kv;
+  if (own) {
+    p.B = B + T;
+    p.own_first = B;
+    p.own_table = own->table;
+    p.own_lens = own->lens;
+    p.own_max_pages = own->max_pages;
+    p.pair_o = own->pair_o;
+    p.pair_lse = own->pair_lse;
+    units += static_cast<int64_t>(T) * H_kv;
+    if (own->max_pages > max_pages) most = static_cast<int64_t>(own->max_pages) * c.page_size;
+  }
   const int64_t tiles = most > 0 ? (most + kPagedTile - 1) / kPagedTile : 1;
-  const int64_t units = (rows / p.rg_rows + (B < T ? B : T)) * H_kv;
   // One request over a few tiles: a CTA goes through all of a unit's in less time than a second launch takes to join
   // its parts (5 tokens behind 295, 16 query and 4 K/V heads, d = 64: 7.8 us, with the join 13.4).
-  p.one_cta = B == 1 && tiles <= kOneCtaTiles && units <= kPagedMaxCtas / 4;
+  p.one_cta = p.B == 1 && tiles <= kOneCtaTiles && units <= kPagedMaxCtas / 4;
   const int64_t places = p.one_cta ? units : units * tiles;
-  return launch_fwd_paged_multi(p, d, c.dtype == ATTN_CACHE_E4M3,
-                                places < kPagedMaxCtas ? static_cast<int>(places) : kPagedMaxCtas,
-                                stream) == cudaSuccess
-             ? ATTN_OK
-             : ATTN_ERR_LAUNCH;
+  if (launch_fwd_paged_multi(p, d, c.dtype == ATTN_CACHE_E4M3,
+                             places < kPagedMaxCtas ? static_cast<int>(places) : kPagedMaxCtas, stream) != cudaSuccess)
+    return ATTN_ERR_LAUNCH;
+  return !own || launch_pair_merge(p, B, d, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
 // of the one for many,
@@ -159,22 +176,15 @@ int run_many(const void* q, const attn_kv_cache& c, const int32_t* table, const 
   return launch_chunk(p, d, e4m3, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
-// or of both, one after the other on one workspace.  `behind_prefix`: requests that share a prefix are about as many in
-// each group, so one of the kernels takes them all, by their mean.
-int run_chunk(const void* q, const attn_kv_cache& c, const int32_t* table, const int32_t* seq_lens, const int32_t* cu,
-              void* o, float* lse, const float* tail_o, const float* tail_lse, int B, int T, int H, int H_kv, int d,
-              int max_pages, int causal, float scale, QueryLayout at, bool behind_prefix, const ChunkSizes& z,
-              uint8_t* ws, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(T) * (H / H_kv);
-  const int which = behind_prefix ? (rows <= static_cast<int64_t>(kFewRows) * B ? kFew : kMany) : kernels_for(rows, B);
-  int rc = ATTN_OK;
-  if (which & kFew)
-    rc = run_few(q, c, table, seq_lens, cu, o, lse, tail_o, tail_lse, B, T, H, H_kv, d, max_pages, causal, scale, at,
-                 which & kMany ? kFewRows : INT_MAX, ws, stream);
-  if (rc == ATTN_OK && (which & kMany))
-    rc = run_many(q, c, table, seq_lens, cu, o, lse, tail_o, tail_lse, B, T, H, H_kv, d, max_pages, causal, scale, at,
-                  which & kFew ? kFewRows : 0, z, ws, stream);
-  return rc;
+// Whether the first takes requests that share prefixes: they are about as many in each group, so one kernel takes them
+// all, by their mean, and the first takes each request's own rows in the same launch (12 groups of 4 behind up to 4096
+// rows, E4M3: 31 us with launches of their own for those).
+bool few_behind_prefix(int groups, int B, int H, int H_kv, int max_prefix_pages, int max_pages, int page_size) {
+  const int64_t rows = static_cast<int64_t>(B) * (H / H_kv);
+  if (rows > static_cast<int64_t>(kFewRows) * groups) return false;
+  const int64_t most = static_cast<int64_t>(max_prefix_pages > max_pages ? max_prefix_pages : max_pages) * page_size;
+  const int64_t units = rows / 8 + (groups < B ? groups : B) + static_cast<int64_t>(B) * (H / H_kv / 8 + 1);
+  return units <= INT_MAX / ((most + kPagedTile - 1) / kPagedTile + 1 + kFewCost) / H_kv;  // places in 32 bits
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -185,8 +195,8 @@ struct SharedLayout {
 SharedLayout shared_layout(int B, int H, int group, int d, const ChunkSizes& z) {
   SharedLayout s{};
   s.tail_o = paged_layout(group, d).total;
-  s.tail_lse = s.tail_o + up256(static_cast<size_t>(B) * H * d * 4);
-  s.chunk = s.tail_lse + up256(static_cast<size_t>(B) * H * 4);
+  s.tail_lse = s.tail_o + up256(2ull * B * H * d * 4);  // (two halves where one launch takes prefixes and own rows)
+  s.chunk = s.tail_lse + up256(2ull * B * H * 4);
   s.total = s.chunk + chunk_workspace(B, group, d, z);
   return s;
 }
@@ -221,9 +231,17 @@ extern "C" int attn_fwd_paged_varlen(const void* q, const attn_kv_cache* cache, 
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < chunk_workspace(T, H / H_kv, d, z))
     return ATTN_ERR_WORKSPACE;
   if ((rc = check_device()) != 0) return rc;
-  return run_chunk(q, *cache, block_table, seq_lens, cu_new, o, lse, nullptr, nullptr, B, T, H, H_kv, d, max_pages,
-                   causal != 0, scale, QueryLayout{static_cast<int64_t>(T) * d, d}, false, z, static_cast<uint8_t*>(workspace),
-                   static_cast<cudaStream_t>(stream));
+  const QueryLayout at{static_cast<int64_t>(T) * d, d};
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const int which = kernels_for(static_cast<int64_t>(T) * (H / H_kv), B);
+  // of both, one after the other on one workspace
+  if (which & kFew)
+    rc = run_few(q, *cache, block_table, seq_lens, cu_new, o, lse, nullptr, B, T, H, H_kv, d, max_pages, causal != 0, scale,
+                 at, which & kMany ? kFewRows : INT_MAX, ws, static_cast<cudaStream_t>(stream));
+  if (rc == ATTN_OK && (which & kMany))
+    rc = run_many(q, *cache, block_table, seq_lens, cu_new, o, lse, nullptr, nullptr, B, T, H, H_kv, d, max_pages,
+                  causal != 0, scale, at, which & kFew ? kFewRows : 0, z, ws, static_cast<cudaStream_t>(stream));
+  return rc;
 }
 
 extern "C" size_t attn_fwd_paged_shared_workspace_bytes(int B, int H, int H_kv, int d) {
@@ -260,13 +278,18 @@ extern "C" int attn_fwd_paged_shared(const void* q, const attn_kv_cache* cache, 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* tail_o = reinterpret_cast<float*>(ws + s.tail_o);
   float* tail_lse = reinterpret_cast<float*>(ws + s.tail_lse);
+  const QueryLayout at{d, static_cast<int64_t>(H) * d};
+  if (few_behind_prefix(groups, B, H, H_kv, max_prefix_pages, max_pages, cache->page_size)) {
+    const OwnRows own{block_table, seq_lens, max_pages, tail_o, tail_lse};
+    return run_few(q, *cache, prefix_table, prefix_lens, cu_groups, o, lse, &own, groups, B, H, H_kv, d, max_prefix_pages, 0,
+                   scale, at, INT_MAX, ws + s.chunk, static_cast<cudaStream_t>(stream));
+  }
   // each request's own rows first, in fp32; the prefix's results are merged with them where they are finished
   rc = run_fwd_paged(q, *cache, block_table, seq_lens, nullptr, tail_o, tail_lse, B, H, H_kv, d, max_pages, scale, ws,
                      static_cast<cudaStream_t>(stream));
   if (rc != ATTN_OK) return rc;
-  return run_chunk(q, *cache, prefix_table, prefix_lens, cu_groups, o, lse, tail_o, tail_lse, groups, B, H, H_kv, d,
-                   max_prefix_pages, 0, scale, QueryLayout{d, static_cast<int64_t>(H) * d}, true, z, ws + s.chunk,
-                   static_cast<cudaStream_t>(stream));
+  return run_many(q, *cache, prefix_table, prefix_lens, cu_groups, o, lse, tail_o, tail_lse, groups, B, H, H_kv, d,
+                  max_prefix_pages, 0, scale, at, 0, z, ws + s.chunk, static_cast<cudaStream_t>(stream));
 }
 
 namespace {

@@ -79,13 +79,16 @@ cudaError_t launch_qkv_rope_bwd(RopeParams& p, int d, bool interleaved, cudaStre
 constexpr int kPagedTile = 64;         // keys of a tile
 constexpr int kPagedMaxCtas = 608;     // 4 on each of 152 SMs
 constexpr int kPagedMaxCost = 2;       // places that a unit takes beside its tiles, at most
+// the same with several rows a request, where units of a tile lie beside long ones (64 groups of 4 requests of up to 64 rows
+// behind 4000, E4M3, d = 128: 234 us with 1, 177 with 2, 159 with 4, 171 with 6)
+constexpr int kFewCost = 4;
 constexpr float kPagedTrail = 8.f;     // how far a score may pass the reference maximum, in log2 units
 constexpr int kPagedMaxRows = 32;      // query rows (heads of one K/V head) of a unit
 
 // What the join of several rows a request knows of a CTA (tiles -1: of no unit): the unit's first place and tiles, its K/V
-// head, first row, rows, and its request's first token.
+// head, first row, rows, its request's first token, and whether that is from own_first on.
 struct PagedDesc {
-  int unit0, tiles, h, row0, rows, tok0;
+  int unit0, tiles, h, row0, rows, tok0, own;
 };
 
 struct PagedParams {
@@ -116,8 +119,13 @@ struct PagedParams {
   bool one_cta;         // a unit a CTA, nothing to join (one request of few tiles)
   PagedDesc* desc;      // [CTAs]
   int* head;            // [0] places in all, [1] CTAs with a share
-  const float* tail_o;  // fp32 rows [T][H][d] over other keys to merge with (null: none), and their log-sum-exp
-  const float* tail_lse;
+  // Requests that share a prefix: requests from own_first on are the tokens again, one each, over rows of their own;
+  // results go unrounded to pair_o [2][T][H][d] and pair_lse [2][T][H], prefixes first (null: to o and lse).
+  int own_first, own_max_pages;
+  const int* own_table;
+  const int* own_lens;
+  float* pair_o;
+  float* pair_lse;
   float scale_log2;     // scale * log2(e)
   float trail;          // the same before the scale (bf16 cache)
 };
@@ -156,6 +164,9 @@ cudaError_t launch_fwd_paged(const PagedParams& p, int d, bool e4m3, int max_til
 // The same of units of up to p.rg_rows (8, 16 or 32) rows of a request's tokens; `max_tiles` as above.
 cudaError_t launch_fwd_paged_multi(const PagedParams& p, int d, bool e4m3, int max_tiles,
                                    cudaStream_t stream);
+
+// o and lse of tokens 0 .. min(cu[groups], T) - 1 from the two halves of pair_o and pair_lse.
+cudaError_t launch_pair_merge(const PagedParams& p, int groups, int d, cudaStream_t stream);
 
 // The sizes that attn_fwd_paged takes, and its launch on checked arguments (attn_gen_abi.cu); with o32 the rows
 // go there in fp32 instead of to o.

@@ -114,7 +114,9 @@ struct Walk {
   int tok0, tokens, n_rg;   // MULTI: the request's first new token, their number, its row groups
 };
 
+template <bool MULTI>
 __device__ __forceinline__ int req_len(const PagedParams& p, int s) {
+  if (MULTI && s >= p.own_first) return min(max(p.own_lens[s - p.own_first], 0), p.own_max_pages << p.page_shift);
   const int most = p.max_pages << p.page_shift;
   return min(max(p.seq_lens[s], 0), most);
 }
@@ -131,6 +133,7 @@ __device__ __forceinline__ Fresh fresh_of(const PagedParams& p, int s) {
   if constexpr (!MULTI) {
     return {0, 1, p.n_rg};
   } else {
+    if (s >= p.own_first) return {s - p.own_first, 1, (p.group + p.rg_rows - 1) / p.rg_rows};
     const int a = min(max(p.cu[s], 0), p.T), n = max(min(p.cu[s + 1], p.T) - a, 0);
     const int rows = n * p.group;
     return {a, n, rows <= p.most_rows ? (rows + p.rg_rows - 1) / p.rg_rows : 0};
@@ -151,13 +154,13 @@ __device__ __forceinline__ void next_unit(const PagedParams& p, Walk& w) {
       w.tokens = f.tokens;
       w.n_rg = f.n_rg;
     }
-    if (w.s < p.B) w.len = req_len(p, w.s);
+    if (w.s < p.B) w.len = req_len<MULTI>(p, w.s);
     w.n = req_tiles(w.len);
   } else {
     ++w.s;
     w.len = w.ahead;
     w.n = req_tiles(w.len);
-    w.ahead = w.s + 1 < p.B ? req_len(p, w.s + 1) : 0;
+    w.ahead = w.s + 1 < p.B ? req_len<MULTI>(p, w.s + 1) : 0;
   }
 }
 // Places in the order of all units: a unit takes its tiles and `p.unit_cost` places more.  Those of a K/V head's
@@ -165,7 +168,7 @@ __device__ __forceinline__ void next_unit(const PagedParams& p, Walk& w) {
 template <bool MULTI>
 __device__ __forceinline__ int req_places(const PagedParams& p, int s) {
   if (s >= p.B) return 0;
-  return (req_tiles(req_len(p, s)) + p.unit_cost) * (MULTI ? fresh_of<MULTI>(p, s).n_rg : 1);
+  return (req_tiles(req_len<MULTI>(p, s)) + p.unit_cost) * (MULTI ? fresh_of<MULTI>(p, s).n_rg : 1);
 }
 // What they are to be multiplied by.
 template <bool MULTI>
@@ -226,7 +229,7 @@ __device__ int find(const PagedParams& p, int at, Walk& w, int from = 0, int bef
   int per = p.H_kv * p.n_rg;
   for (int s0 = from; s0 < p.B; s0 += 32) {
     const int s = s0 + lane;
-    const int len = s < p.B ? req_len(p, s) : 0;
+    const int len = s < p.B ? req_len<MULTI>(p, s) : 0;
     const int n = s < p.B ? req_tiles(len) + p.unit_cost : 0;
     Fresh f{0, 1, 0};
     if constexpr (MULTI) {
@@ -257,7 +260,7 @@ __device__ int find(const PagedParams& p, int at, Walk& w, int from = 0, int bef
       w.h = u.h;
       w.rg = u.rg;
       const int after = __shfl_sync(0xffffffffu, len, (k + 1) & 31);
-      w.ahead = k < 31 ? after : w.s + 1 < p.B ? req_len(p, w.s + 1) : 0;
+      w.ahead = k < 31 ? after : w.s + 1 < p.B ? req_len<MULTI>(p, w.s + 1) : 0;
       return at - w.t;
     }
     before += __shfl_sync(0xffffffffu, scan, 31);
@@ -373,27 +376,20 @@ __device__ __forceinline__ void scale_rows(float (&acc)[STEPS][4], const float (
   }
 }
 
-// MULTI: four columns of a finished row, of unnormalised values v relative to 2^top and their sum, merged with the same
-// row over other keys where p.tail_o has it.
+// MULTI: four columns of a finished row, of unnormalised values v relative to 2^top and their sum.
 template <int D>
-__device__ __forceinline__ void store_row(const PagedParams& p, int h, int tok0, int r, int c4, float4 v, float top,
-                                          float sum) {
+__device__ __forceinline__ void store_row(const PagedParams& p, bool own, int h, int tok0, int r, int c4, float4 v,
+                                          float top, float sum) {
   const int tok = r / p.group;
   const int64_t head = static_cast<int64_t>(h) * p.group + (r - tok * p.group), token = tok0 + tok;
   const bool some = sum > 0.f || sum != sum;  // (a row that sees nothing: zeros)
-  float inv = some ? 1.f / sum : 0.f, lse = some ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+  const float inv = some ? 1.f / sum : 0.f, lse = some ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
   v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-  if (p.tail_o) {
-    const int64_t at = token * p.H + head;
-    const float tail = p.tail_lse[at], most = fmaxf(lse, tail);
-    const float a = lse == -INFINITY ? 0.f : ex2_approx((lse - most) * 1.4426950408889634f);
-    const float b = tail == -INFINITY ? 0.f : ex2_approx((tail - most) * 1.4426950408889634f);
-    const float all = a + b;
-    inv = all > 0.f || all != all ? 1.f / all : 0.f;
-    lse = all > 0.f || all != all ? most + log2f(all) * 0.69314718055994530942f : -INFINITY;
-    const float4 x = *reinterpret_cast<const float4*>(p.tail_o + at * D + 4 * c4);
-    v = make_float4((v.x * a + x.x * b) * inv, (v.y * a + x.y * b) * inv, (v.z * a + x.z * b) * inv,
-                    (v.w * a + x.w * b) * inv);
+  if (p.pair_o) {
+    const int64_t at = (own ? static_cast<int64_t>(p.T) * p.H : 0) + token * p.H + head;
+    *reinterpret_cast<float4*>(p.pair_o + at * D + 4 * c4) = v;
+    if (c4 == 0) p.pair_lse[at] = lse;
+    return;
   }
   const int64_t to = head * p.o_head + token * p.o_token;
   *reinterpret_cast<uint2*>(p.o + to + 4 * c4) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
@@ -430,7 +426,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
   if (few) __syncthreads();
   pdl_launch_dependents();
   if (MULTI && blockIdx.x == 0) {
-    for (int s = tid; s < p.B; s += L::kThreads)
+    for (int s = tid; s < min(p.B, p.own_first); s += L::kThreads)
       if (p.cu[s + 1] < p.cu[s] || (s == 0 && p.cu[0] != 0) || p.cu[s + 1] > p.T)
         atomicCAS(p.status, 0, kStatusBadSeqlens);
   }
@@ -458,10 +454,11 @@ paged_kernel(const __grid_constant__ PagedParams p) {
   }
   int left = shares.start(cta + 1) - place0;  // places of this CTA still to come
   if (MULTI && tid == 0) {  // for the join: the unit that this CTA ends and an earlier one began
-    PagedDesc d{0, -1, 0, 0, 0, 0};
+    PagedDesc d{0, -1, 0, 0, 0, 0, 0};
     if (w.t > 0 && w.t < w.n && unit0 + w.n <= place0 + left) {
       const int row0 = w.rg * p.rg_rows;
-      d = PagedDesc{unit0, w.n, w.h, row0, min(p.rg_rows, w.tokens * p.group - row0), w.tok0};
+      d = PagedDesc{unit0, w.n, w.h, row0, min(p.rg_rows, w.tokens * p.group - row0), w.tok0,
+                    w.s >= p.own_first};
     }
     p.desc[cta] = d;
   }
@@ -495,7 +492,10 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         entry_base = page0;
         const int e = page0 + lane;
         const int have = (w.len + (1 << p.page_shift) - 1) >> p.page_shift;
-        entries = e < have ? p.table[static_cast<size_t>(w.s) * p.max_pages + e] : 0;
+        const int* row = MULTI && w.s >= p.own_first
+                             ? p.own_table + static_cast<size_t>(w.s - p.own_first) * p.own_max_pages
+                             : p.table + static_cast<size_t>(w.s) * p.max_pages;
+        entries = e < have ? row[e] : 0;
         if (e < have && static_cast<unsigned>(entries) >= static_cast<unsigned>(p.num_pages)) {
           atomicCAS(p.status, 0, kStatusBadPage);
           entries = -1;
@@ -842,6 +842,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
     const int row0 = w.rg * p.rg_rows, rows = min(p.rg_rows, (MULTI ? w.tokens * p.group : p.group) - row0);
     const int64_t out0 = static_cast<int64_t>(w.s) * p.H + static_cast<int64_t>(w.h) * p.group + row0;
     const int out_h = w.h, out_tok0 = w.tok0;
+    const bool out_own = MULTI && w.s >= p.own_first;
     if (left > 0) {
       next_unit<MULTI>(p, w);
       load_q<D, E4M3, NT, MULTI>(p, w, row_slice, qf, mul);
@@ -944,7 +945,7 @@ paged_kernel(const __grid_constant__ PagedParams p) {
         const float4 b = *reinterpret_cast<const float4*>(at0 + 8 * L::kMergeLd);
         float4 v = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
         if (MULTI && whole) {
-          store_row<D>(p, out_h, out_tok0, row0 + row, c4, v, top, sum);
+          store_row<D>(p, out_own, out_h, out_tok0, row0 + row, c4, v, top, sum);
         } else if (whole) {
           const float inv = len > 0 ? 1.f / sum : 0.f;
           const int64_t at = out0 + row;
@@ -1119,10 +1120,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __
     }
     if (MULTI && sub == 0 && row < rows) {
       if constexpr (kPer == 4) {
-        store_row<D>(p, d.h, d.tok0, row0 + row, lane, make_float4(acc[0], acc[1], acc[2], acc[3]), m, l);
+        store_row<D>(p, d.own != 0, d.h, d.tok0, row0 + row, lane, make_float4(acc[0], acc[1], acc[2], acc[3]), m, l);
       } else {  // two columns a lane: the even lanes store four
         const float c2 = __shfl_down_sync(0xffffffffu, acc[0], 1), c3 = __shfl_down_sync(0xffffffffu, acc[1], 1);
-        if (lane % 2 == 0) store_row<D>(p, d.h, d.tok0, row0 + row, lane / 2, make_float4(acc[0], acc[1], c2, c3), m, l);
+        if (lane % 2 == 0) store_row<D>(p, d.own != 0, d.h, d.tok0, row0 + row, lane / 2, make_float4(acc[0], acc[1], c2, c3), m, l);
       }
     } else if (sub == 0 && row < rows) {
       const int64_t out = static_cast<int64_t>(sh / p.H_kv) * p.H +
@@ -1166,7 +1167,7 @@ cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
   const long long units = static_cast<long long>(p.B) * p.H_kv * p.n_rg;
   PagedParams q = p;
   q.ctas = ctas;
-  q.unit_cost = NT * RW == 4 ? kPagedMaxCost : 1;
+  q.unit_cost = MULTI ? kFewCost : NT * RW == 4 ? kPagedMaxCost : 1;
   q.by_unit = !MULTI && units <= ctas;
   const int joins = q.by_unit ? static_cast<int>(units) : ctas;
   // blocks of a join: as many as its rows keep busy at the mean number of parts

@@ -307,14 +307,15 @@ def test_shared(each, prefix, H, KV, d, page, seed, most, kind):
 def test_shared_peaky_and_padding(kind):
     # what dominates lies in the prefix for some rows and in the own rows for others
     args, own, vals = shared_inputs([5, 6], [400, 333], 12, 4, 128, 32, 21, 200, kind, 3.0)
-    cu = args[4]
     o, lse = attn.attn_fwd_paged_shared(*args)
     check_shared(o, lse, args, vals, 1 / math.sqrt(128), kind, f"shared {kind} peaky")
-    out = torch.full_like(o, 7.0)
-    lse2 = torch.full_like(lse, 7.0)
-    attn.attn_fwd_paged_shared(*args[:4], i32(0, 5, 8), *args[5:], out=out, lse=lse2)
-    assert (out[8:] == 7).all() and (lse2[8:] == 7).all() and torch.equal(out[:8], o[:8]) and torch.equal(lse2[:8], lse[:8])
-    assert cu.tolist() == [0, 5, 11]
+    # the last three requests are padding (the work is cut differently then, so bits may differ)
+    out, lse = torch.full_like(o, 7.0), torch.full_like(lse, 7.0)
+    attn.attn_fwd_paged_shared(*args[:4], i32(0, 5, 8), *args[5:], out=out, lse=lse)
+    assert (out[8:] == 7).all() and (lse[8:] == 7).all()
+    q, cache, pt, pl, _, table, n = args
+    check_shared(out[:8], lse[:8], (q[:8], cache, pt, pl, i32(0, 5, 8), table[:8], n[:8]), vals, 1 / math.sqrt(128), kind,
+                 f"shared {kind} padded")
 
 
 def test_shared_without_pages_of_one_kind():
