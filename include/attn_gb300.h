@@ -386,14 +386,17 @@ ATTN_API size_t attn_fwd_paged_workspace_bytes(int B, int H, int H_kv, int d);
  *     on are padding, and o and lse are left as they were there.  cu_new that decreases, does not begin with 0 or passes
  *     T is clamped into [0, T] and the status word reports kind 2 (o and lse are then unspecified).
  *   A token that sees no row (more new tokens than rows) gets O = 0 and lse = -inf.
- *   E4M3 caches: V scales up to 2^100 in magnitude (K scales: any); a query row with an infinity or a NaN
- *     gives NaN.  A V row that is not finite reaches, besides the tokens that see it, those before it that share its
+ *   E4M3 caches: V scales of 2^-100 to 2^100 in magnitude, or 0 (K scales: any; attn_fwd_paged takes any of either);
+ *     a query row with an infinity or a NaN gives NaN.  A V row that is not finite reaches, besides the tokens that see it, those before it that share its
  *     tile of 128 rows (as in attn_fwd).
  *   workspace : attn_fwd_paged_varlen_workspace_bytes(T, H, H_kv, d) bytes (it does not depend on the
  *     lengths), 256-byte aligned; calls whose work may overlap on the GPU need one each.
- * The work is cut into equal shares of key tiles, whatever the lengths are, one or more for each pair of SMs, and a
- * second launch joins what fell to several by the block merge of attn_fwd_splitkv.  Everything that depends on
- * lengths is decided on the GPU: a captured call can be replayed with other lengths, tables and contents.
+ * Requests with up to 32 query rows a K/V head (new tokens times H / H_kv) are taken by a kernel that works as
+ * attn_fwd_paged does, those with more by one whose products take 256 rows at once.  Each cuts its work into equal
+ * shares of key tiles, whatever the lengths are, and a second launch joins what fell to several shares by the block
+ * merge of attn_fwd_splitkv: one to four launches, by B, T and the table's shape alone (with 32 rows in all, only the
+ * first kernel's; with over 64 a request on average, or one request of over 32, only the second's).  Everything that
+ * depends on lengths is decided on the GPU: a captured call can be replayed with other lengths, tables and contents.
  * Equal inputs give equal bits.  A table entry that is needed and names no page of the cache is read as a page of
  * zeros, and the status word reports kind 5.
  * H_kv must divide H; max_pages * page_size and T are below 2^31 - 1024, and so is the number of places
