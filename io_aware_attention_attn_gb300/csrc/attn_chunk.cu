@@ -21,7 +21,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const __gri
   __shared__ int s_count;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) s_count = 0;
+  const bool idle = p.few_rows > 0 && chunk::all_few(p);
   pdl_wait();  // by every block, so that the work after this one waits for the parts' kernel too
+  if (idle) return;
   const int total = p.head[0], n_shares = p.head[1], most = p.clusters * p.max_rounds;
   if (warp == 0) {  // in order, by one warp
     int n = 0;

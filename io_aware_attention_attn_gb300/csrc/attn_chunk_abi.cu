@@ -26,7 +26,7 @@ enum Kernels { kFew = 1, kMany = 2 };
 int few_group(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 int few_rows_of(int64_t rows, int B, bool wide_codes) {
   const int n = few_group((rows + B - 1) / B);
-  return wide_codes && n > 16 ? 16 : n;
+  return n;
 }
 // What the host knows: the tokens in all.  Where they may lie either way both kernels are launched, each taking its own
 // requests; requests with more than twice kFewRows rows on average leave the first out (a launch that finds

@@ -60,6 +60,10 @@
 namespace attn {
 namespace {
 
+#ifndef COLS_FROM
+#define COLS_FROM 4
+#endif
+constexpr int kColsFrom = COLS_FROM;
 constexpr int kSlices = 4;                       // key slices of 16 in a tile, a warp each
 enum : int { kRoleProducer = 7, kRoleConsumer = 8 };
 
@@ -69,8 +73,11 @@ constexpr float kPvSet = 6.f, kPSet = 115.f;      // P |v| and P at most where m
 constexpr float kTrailE4m3 = 9.f;                 // and how far past that m is moved
 constexpr float kSumLog2 = 16.f;                  // row sums are of 2^-16 P
 
+// Whether a CTA's warps share out the columns of O, and not only the keys of S (MULTI).
+__host__ __device__ constexpr bool by_columns(int D, bool e4m3, int NT, bool multi) { return multi && D == 128 && e4m3 && NT >= kColsFrom; }
+
 // NT: groups of 8 query rows a warp holds; RW: row slices, each with four warps of its own.
-template <int D, bool E4M3, int NT, int RW>
+template <int D, bool E4M3, int NT, int RW, bool COLS = false>
 struct PagedCfg {
   static constexpr int kWarps = kSlices * RW;                     // consumers; one producer more
   static constexpr int kThreads = (kWarps + 1) * 32;
@@ -80,7 +87,7 @@ struct PagedCfg {
   // for the 4.3 GB above against 597 with three, but short requests are bound by that chain too: 256
   // of 64 tokens 19.2 us with two, 16.9 with three).
   static constexpr int kCtas = RW == 2 ? 1 : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2)
-                                                     : NT == 2 ? 2 : 3;
+                                                     : NT >= 2 ? 2 : 3;
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
   static constexpr int kBlk = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a row in one box
   static constexpr int kBlks = kRowBytes / kBlk;                  // boxes side by side
@@ -89,8 +96,12 @@ struct PagedCfg {
   static constexpr int kMergeLd = D + 4;                          // spreads rows over the banks
   // row groups merged at once: all, but where that would cost the ring one of its three tiles
   static constexpr int kMergeNt = kCtas == 2 && kStage == 32768 ? 1 : NT;
-  static constexpr int kMergeBytes = kMergeNt * 2 * 8 * kMergeLd * 4;  // of one row slice
-  static constexpr int kStatBytes = 2 * kMergeNt * kSlices * 8 * 2 * 4;  // likewise, of two merges
+  static constexpr int kMergeBytes = (COLS ? NT : kMergeNt * 2) * 8 * kMergeLd * 4;  // of one row slice
+  // likewise, of two merges; COLS: row sums and references, candidates for those, P of two tiles
+  // and query rows with their factors
+  static constexpr int kRefs = (kSlices + 1) * NT * 8, kMul = kRefs + kSlices * NT * 8;  // words before them
+  static constexpr int kP = kMul + NT * 8, kPTile = kSlices * NT * 2 * 32, kQ = kP + 2 * kPTile;
+  static constexpr int kStatBytes = COLS ? (kQ + NT * D / 8 * 32) * 4 : 2 * kMergeNt * kSlices * 8 * 2 * 4;
   // tiles in the ring: what shared memory holds beside the rest (each CTA's 1 KB of the system's and
   // 1 KB for alignment), 8 at most
   static constexpr int kScaleBytes = E4M3 ? 2 * kPagedTile * 4 : 0;
@@ -396,10 +407,367 @@ __device__ __forceinline__ void store_row(const PagedParams& p, bool own, int h,
   if (c4 == 0) p.lse[to / D] = lse;
 }
 
+// Consumers that share out the columns of O: a warp forms S and P of 16 keys of a tile, as above, leaves P in shared memory,
+// and multiplies the P of all 64 with a quarter of V's columns.  A code of V is then turned once and O takes an
+// eighth of the registers of four row groups, so one warp holds the query rows of all of them.  The warps agree
+// on the reference of a row: one barrier a tile (P is there, and does no warp need a reference moved?), and two where one
+// does.  32 requests of 32 rows over 4096 keys, 8 K/V heads, E4M3, d = 128: TODO us; 16-row units, which read and
+// turn each tile twice, 136.
+template <int D, bool E4M3, int NT>
+__device__ __forceinline__ void consume_columns(const PagedParams& p, uint8_t* sm, uint32_t base, Walk& w, int left,
+                                                const WaitCtx& ctx) {
+  static_assert(D == 128, "a warp's columns are two tiles of 16");
+  using L = PagedCfg<D, E4M3, NT, 1, true>;
+  constexpr int kSteps = D / 16, kRows = NT * 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q4 = lane & 3;
+  const int cta = static_cast<int>(blockIdx.x);
+  auto full = [&](int st) { return base + L::kBar + st * 8; };
+  auto empty = [&](int st) { return base + L::kBar + (L::kStages + st) * 8; };
+  float* merge = reinterpret_cast<float*>(sm + L::kMerge);
+  float* sums = reinterpret_cast<float*>(sm + L::kStat);  // [slice][row], then the references
+  float* cands = sums + L::kRefs;                         // [slice][row]
+  uint4* qbuf = reinterpret_cast<uint4*>(sums + L::kQ);   // [two steps along d][row group][lane]
+  float* muls = sums + L::kMul;
+  uint4* pbuf = reinterpret_cast<uint4*>(sums + L::kP);   // [tile's parity][slice][two row groups][lane]
+  bool dead = false;  // a wait gave up: go through the motions, compute nothing
+  int st = 0, at_p = 0;
+  uint32_t phase = 0;
+  bool first = true;
+  uint32_t qf[1][kSteps][2];  // of row group `warp`, on their way to where all warps read them
+  float mul[1][2];
+  load_q<D, E4M3, 1, true>(p, w, warp, qf, mul);
+  auto leave_q = [&] {
+    if (warp < NT) {
+      #pragma unroll
+      for (int k = 0; k < kSteps; k += 2)
+        qbuf[(k / 2 * NT + warp) * 32 + lane] = make_uint4(qf[0][k][0], qf[0][k][1], qf[0][k + 1][0], qf[0][k + 1][1]);
+      if (E4M3 && g == 0) *reinterpret_cast<float2*>(muls + warp * 8 + 2 * q4) = make_float2(mul[0][0], mul[0][1]);
+    }
+    named_barrier_sync(1, kSlices * 32);
+  };
+  leave_q();
+  while (left > 0) {
+    const int t_begin = w.t, t_end = min(w.n, w.t + left);
+    const int row0 = w.rg * p.rg_rows;
+    // keys that the unit's first token sees, the fewest of all
+    const int least = p.causal ? w.len - w.tokens + row0 / p.group + 1 : 0x7fffffff;
+    float acc[NT][2][4], nm[NT][2], above[NT][2], l[NT][2];
+    #pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      nm[nt][0] = nm[nt][1] = E4M3 ? kNoRef : 0.f;
+      above[nt][0] = above[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+      #pragma unroll
+      for (int j = 0; j < 4; ++j) acc[nt][0][j] = acc[nt][1][j] = 0.f;
+    }
+    auto no_ref = [&](int nt, int j) { return E4M3 ? nm[nt][j] == kNoRef : above[nt][j] == -INFINITY; };
+
+    for (int t = t_begin; t < t_end; ++t) {
+      if (!dead && !mbar_wait_warp(full(st), phase, ctx, kRoleConsumer, 2)) dead = true;
+      const int tile_live = dead ? 0 : w.len - t * kPagedTile, live = tile_live - warp * 16;
+      const uint32_t kst = base + st * L::kStage, vst = kst + L::kSide;
+      const bool in0 = g < live, in1 = g + 8 < live;
+      const int key = warp * 16 + (lane & 15);
+      const float* sc = reinterpret_cast<const float*>(sm + L::kScales) + st * 2 * kPagedTile + warp * 16;
+      const float sk0 = E4M3 ? sc[g] : 1.f, sk1 = E4M3 ? sc[g + 8] : 1.f;
+      float sv0 = !E4M3 ? 1.f : in0 ? sc[kPagedTile + g] : 0.f, sv1 = !E4M3 ? 1.f : in1 ? sc[kPagedTile + g + 8] : 0.f;
+      // as in paged_kernel: codes that are all zero weigh nothing
+      auto drop_zeros = [&] {
+        const uint8_t* codes = sm + (vst - base) + key * L::kBlk;
+        auto some = [&](int c) {
+          const uint4 x = *reinterpret_cast<const uint4*>(codes + 16 * c);
+          return ((x.x | x.y | x.z | x.w) & 0x7f7f7f7fu) != 0u;
+        };
+        uint32_t keys = __ballot_sync(0xffffffffu, some(0));
+        if (keys == 0xffffffffu) return;
+        bool any = false;
+        #pragma unroll
+        for (int c = 1; c < L::kRowBytes / 16; ++c) any |= some(c);
+        keys |= __ballot_sync(0xffffffffu, any);
+        if (!(keys >> g & 1u) && fabsf(sv0) < INFINITY) sv0 = 0.f;
+        if (!(keys >> (g + 8) & 1u) && fabsf(sv1) < INFINITY) sv1 = 0.f;
+      };
+      uint4* mine = pbuf + at_p * (L::kPTile / 4) + warp * (NT / 2) * 32 + lane;
+      float sum[NT][2];
+      for (bool move = t == t_begin;; move = true) {
+        float e[NT][4];
+        #pragma unroll
+        for (int nt = 0; nt < NT; ++nt) e[nt][0] = e[nt][1] = e[nt][2] = e[nt][3] = 0.f;
+        if constexpr (E4M3) {
+          #pragma unroll
+          for (int k = 0; k < kSteps; k += 2) {
+            const int chunk = k + (lane >> 4);
+            uint32_t a[4];
+            ldsm4(kst + key * L::kBlk + ((chunk ^ (key & 7)) << 4), a);
+            uint4 q[NT];
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt) q[nt] = qbuf[(k / 2 * NT + nt) * 32 + lane];
+            #pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t lo0 = e4m3x2_to_f16x2(a[2 * j]), hi0 = e4m3x2_to_f16x2(a[2 * j] >> 16);
+              const uint32_t lo1 = e4m3x2_to_f16x2(a[2 * j + 1]), hi1 = e4m3x2_to_f16x2(a[2 * j + 1] >> 16);
+              #pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816<true>(e[nt], lo0, lo1, hi0, hi1, j ? q[nt].z : q[nt].x, j ? q[nt].w : q[nt].y);
+            }
+          }
+          #pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float2 m = *reinterpret_cast<const float2*>(muls + nt * 8 + 2 * q4);
+            e[nt][0] *= m.x * sk0;
+            e[nt][1] *= m.y * sk0;
+            e[nt][2] *= m.x * sk1;
+            e[nt][3] *= m.y * sk1;
+          }
+        } else {
+          uint4 q[NT];
+          #pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            if (k % 2 == 0) {
+              #pragma unroll
+              for (int nt = 0; nt < NT; ++nt) q[nt] = qbuf[(k / 2 * NT + nt) * 32 + lane];
+            }
+            const int chunk = (k & 3) * 2 + (lane >> 4);
+            uint32_t a[4];
+            ldsm4(kst + (k >> 2) * (kPagedTile * 128) + key * 128 + ((chunk ^ (key & 7)) << 4), a);
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816<false>(e[nt], a[0], a[1], a[2], a[3], k & 1 ? q[nt].z : q[nt].x, k & 1 ? q[nt].w : q[nt].y);
+          }
+        }
+        mask_tail<NT>(e, live, in0, in1);
+        if (t * kPagedTile + warp * 16 + 16 > least) {
+          int sees[NT][2];
+          #pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            #pragma unroll
+            for (int j = 0; j < 2; ++j) sees[nt][j] = w.len - w.tokens + (row0 + nt * 8 + 2 * q4 + j) / p.group + 1;
+          mask_rows<NT>(e, t * kPagedTile + warp * 16 + g, sees);
+        }
+        if (move) {
+          float lv0 = 0.f, lv1 = 0.f;
+          if constexpr (E4M3) {
+            if (t == t_begin) drop_zeros();
+            lv0 = fabsf(sv0) < INFINITY ? __log2f(fabsf(sv0)) - kPvSet : -INFINITY;
+            lv1 = fabsf(sv1) < INFINITY ? __log2f(fabsf(sv1)) - kPvSet : -INFINITY;
+          }
+          #pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float c[2];
+            #pragma unroll
+            for (int j = 0; j < 2; ++j)
+              c[j] = max_of_keys(E4M3 ? fmax3(fmaxf(e[nt][j], e[nt][j + 2]) - kPSet, e[nt][j] + lv0, e[nt][j + 2] + lv1)
+                                      : fmaxf(e[nt][j], e[nt][j + 2]));
+            if (g == 0) *reinterpret_cast<float2*>(cands + warp * kRows + nt * 8 + 2 * q4) = make_float2(c[0], c[1]);
+          }
+          named_barrier_sync(1, kSlices * 32);
+          #pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float c[2];
+            #pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float top = -INFINITY;
+              #pragma unroll
+              for (int x = 0; x < kSlices; ++x) top = fmaxf(top, cands[x * kRows + nt * 8 + 2 * q4 + j]);
+              const float m = E4M3 ? floorf(top) : top * p.scale_log2;
+              const bool none = no_ref(nt, j);  // no m yet: acc and l are 0 (or NaN)
+              c[j] = 1.f;
+              if (top != -INFINITY && (none || m + nm[nt][j] >= (E4M3 ? kTrailE4m3 : 0.f))) {
+                if (!none) {
+                  c[j] = ex2_approx(-nm[nt][j] - m);
+                  l[nt][j] = E4M3 ? times_exp2(l[nt][j], -nm[nt][j] - m) : l[nt][j] * c[j];
+                }
+                nm[nt][j] = -m;
+                above[nt][j] = top + p.trail;
+              }
+            }
+            scale_rows<2>(acc[nt], c);
+          }
+        }
+        uint32_t pf[NT][2];
+        bool need = false;
+        if constexpr (E4M3) {
+          float most = 0.f, most0 = 0.f, most1 = 0.f;
+          #pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float p0 = ex2_approx(e[nt][0] + nm[nt][0]), p1 = ex2_approx(e[nt][1] + nm[nt][1]);
+            const float p2 = ex2_approx(e[nt][2] + nm[nt][0]), p3 = ex2_approx(e[nt][3] + nm[nt][1]);
+            const float o0 = p0 * sv0, o1 = p1 * sv0, o2 = p2 * sv1, o3 = p3 * sv1;
+            most0 = fmax3(most0, fabsf(o0), fabsf(o1));
+            most1 = fmax3(most1, fabsf(o2), fabsf(o3));
+            sum[nt][0] = p0 + p2;
+            sum[nt][1] = p1 + p3;
+            most = fmax3(most, sum[nt][0], sum[nt][1]);
+            pf[nt][0] = pack_f16x2(o0, o1);
+            pf[nt][1] = pack_f16x2(o2, o3);
+          }
+          auto over = [&] { return most > 0x1p124f || fmaxf(most0, most1) > 0x1p15f; };
+          need = over();
+          if (!move && __any_sync(0xffffffffu, need)) {
+            drop_zeros();
+            if (sv0 == 0.f) most0 = 0.f;
+            if (sv1 == 0.f) most1 = 0.f;
+            need = over();  // if it was they, no
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              pf[nt][0] = sv0 == 0.f ? 0u : pf[nt][0];
+              pf[nt][1] = sv1 == 0.f ? 0u : pf[nt][1];
+            }
+          }
+        } else {
+          #pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            need |= fmaxf(e[nt][0], e[nt][2]) > above[nt][0] || fmaxf(e[nt][1], e[nt][3]) > above[nt][1];
+            const float p0 = ex2_approx(fmaf(e[nt][0], p.scale_log2, nm[nt][0]));
+            const float p1 = ex2_approx(fmaf(e[nt][1], p.scale_log2, nm[nt][1]));
+            const float p2 = ex2_approx(fmaf(e[nt][2], p.scale_log2, nm[nt][0]));
+            const float p3 = ex2_approx(fmaf(e[nt][3], p.scale_log2, nm[nt][1]));
+            sum[nt][0] = p0 + p2;
+            sum[nt][1] = p1 + p3;
+            pf[nt][0] = pack_bf16x2(p0, p1);
+            pf[nt][1] = pack_bf16x2(p2, p3);
+          }
+        }
+        #pragma unroll
+        for (int i = 0; i < NT / 2; ++i)
+          mine[i * 32] = make_uint4(transpose8x8(pf[2 * i][0]), transpose8x8(pf[2 * i][1]), transpose8x8(pf[2 * i + 1][0]),
+                                    transpose8x8(pf[2 * i + 1][1]));
+        if (move) {
+          named_barrier_sync(1, kSlices * 32);
+          break;
+        }
+        if (!named_barrier_or(1, kSlices * 32, need)) break;
+      }
+      #pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        #pragma unroll
+        for (int j = 0; j < 2; ++j) l[nt][j] = E4M3 ? fmaf(sum[nt][j], 0x1p-16f, l[nt][j]) : l[nt][j] + sum[nt][j];
+      const uint4* theirs = pbuf + at_p * (L::kPTile / 4) + lane;
+      at_p ^= 1;
+      #pragma unroll
+      for (int x = 0; x < kSlices; ++x) {
+        const int lv = tile_live - x * 16;
+        if (lv <= 0) break;
+        uint32_t b[NT][2];
+        #pragma unroll
+        for (int i = 0; i < NT / 2; ++i) {
+          const uint4 v = theirs[(x * (NT / 2) + i) * 32];
+          b[2 * i][0] = v.x;
+          b[2 * i][1] = v.y;
+          b[2 * i + 1][0] = v.z;
+          b[2 * i + 1][1] = v.w;
+        }
+        // V rows past the request's end may hold anything: taken as zero
+        const bool tail = lv < 16;
+        const uint32_t keep0 = (2 * q4 < lv ? 0xffffu : 0u) | (2 * q4 + 1 < lv ? 0xffff0000u : 0u);
+        const uint32_t keep1 = (2 * q4 + 8 < lv ? 0xffffu : 0u) | (2 * q4 + 9 < lv ? 0xffff0000u : 0u);
+        if constexpr (E4M3) {
+          const int vk = x * 16 + (lane & 15), chunk = 2 * warp + (lane >> 4);
+          uint32_t a[4];
+          ldsm4_t(vst + vk * L::kBlk + ((chunk ^ (vk & 7)) << 4), a);
+          #pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t x0 = __byte_perm(a[2 * j], 0, 0x3120), x1 = __byte_perm(a[2 * j + 1], 0, 0x3120);
+            uint32_t v0 = e4m3x2_to_f16x2(x0), v1 = e4m3x2_to_f16x2(x0 >> 16);
+            uint32_t v2 = e4m3x2_to_f16x2(x1), v3 = e4m3x2_to_f16x2(x1 >> 16);
+            if (tail) {
+              v0 &= keep0;
+              v1 &= keep0;
+              v2 &= keep1;
+              v3 &= keep1;
+            }
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<true>(acc[nt][j], v0, v1, v2, v3, b[nt][0], b[nt][1]);
+          }
+        } else {
+          const int vk = x * 16 + ((lane >> 4) << 3) + (lane & 7);
+          #pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int k = 2 * warp + j, chunk = (k & 3) * 2 + ((lane >> 3) & 1);
+            uint32_t a[4];
+            ldsm4_t(vst + (k >> 2) * (kPagedTile * 128) + vk * 128 + ((chunk ^ (vk & 7)) << 4), a);
+            if (tail) {
+              a[0] &= keep0;
+              a[1] &= keep0;
+              a[2] &= keep1;
+              a[3] &= keep1;
+            }
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816<false>(acc[nt][j], a[0], a[1], a[2], a[3], b[nt][0], b[nt][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(st));
+      if (++st == L::kStages) {
+        st = 0;
+        phase ^= 1;
+      }
+    }
+    left -= places_done(t_begin, t_end, w.n, p.unit_cost);
+
+    // ---- end of the unit, or of this CTA's part of it, while the next unit's query rows are on their way
+    const bool whole = t_begin == 0 && t_end == w.n;
+    const int part = 2 * cta + (first ? 0 : 1);
+    first = false;
+    const int rows = min(p.rg_rows, w.tokens * p.group - row0);
+    const int out_h = w.h, out_tok0 = w.tok0;
+    const bool out_own = w.s >= p.own_first;
+    if (left > 0) {
+      next_unit<true>(p, w);
+      load_q<D, E4M3, 1, true>(p, w, warp, qf, mul);
+    }
+    #pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      #pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        #pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], off);
+        const int row = nt * 8 + 2 * q4 + j;
+        if (g == 0) {
+          sums[warp * kRows + row] = l[nt][j];
+          if (warp == 0) sums[kSlices * kRows + row] = no_ref(nt, j) ? -INFINITY : (E4M3 ? kSumLog2 : 0.f) - nm[nt][j];
+        }
+        #pragma unroll
+        for (int k = 0; k < 2; ++k)
+          #pragma unroll
+          for (int i = 0; i < 2; ++i)
+            merge[row * L::kMergeLd + 32 * warp + 16 * k + (E4M3 ? 2 * g + i : g + 8 * i)] =
+                acc[nt][k][j + 2 * i] * (E4M3 ? 0x1p-16f : 1.f);
+      }
+    }
+    named_barrier_sync(1, kSlices * 32);
+    for (int i = warp * 32 + lane; i < rows * (D / 4); i += kSlices * 32) {
+      const int row = i / (D / 4), c4 = i % (D / 4);
+      float top = sums[kSlices * kRows + row], sum = 0.f;
+      #pragma unroll
+      for (int x = 0; x < kSlices; ++x) sum += sums[x * kRows + row];
+      float4 v = *reinterpret_cast<const float4*>(merge + row * L::kMergeLd + 4 * c4);
+      if (whole) {
+        store_row<D>(p, out_own, out_h, out_tok0, row0 + row, c4, v, top, sum);
+      } else {
+        const int64_t at = static_cast<int64_t>(part) * p.rg_rows + row;
+        const uint32_t exponent = __float_as_uint(sum) >> 23;
+        if (E4M3 && exponent - 1u < 253u) {  // relative to a power of two near the sum, as the join expects
+          const float f = __uint_as_float((254u - exponent) << 23);
+          v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+          sum *= f;
+          top += static_cast<float>(static_cast<int>(exponent) - 127);
+        }
+        *reinterpret_cast<float4*>(p.part_o + at * D + 4 * c4) = v;
+        if (c4 == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(top, sum);
+      }
+    }
+    if (left > 0) leave_q();
+  }
+}
+
 template <int D, bool E4M3, int NT, int RW, bool MULTI>
 __global__ void __launch_bounds__((kSlices * RW + 1) * 32, PagedCfg<D, E4M3, NT, RW>::kCtas)
 paged_kernel(const __grid_constant__ PagedParams p) {
-  using L = PagedCfg<D, E4M3, NT, RW>;
+  constexpr bool kCols = by_columns(D, E4M3, NT, MULTI);
+  using L = PagedCfg<D, E4M3, NT, RW, kCols>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - smem_u32(smem_raw));
@@ -557,6 +925,10 @@ paged_kernel(const __grid_constant__ PagedParams p) {
   }
 
   // -------------------------------------------------------------------------------- consumers
+  if constexpr (kCols) {
+    consume_columns<D, E4M3, NT>(p, sm, base, w, left, ctx);
+    return;
+  }
   const int g = lane >> 2, q4 = lane & 3;
   const int slice = warp % kSlices, row_slice = RW == 1 ? 0 : warp / kSlices;
   constexpr int kSteps = D / 16;      // k16 steps of S, m16 tiles of O^T
@@ -1002,6 +1374,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __
   PagedDesc d{};
   if constexpr (MULTI) {  // each CTA left a record of the unit that it ends
     pdl_wait();  // by every block, so that the work after this one waits for the parts' kernel too
+    pdl_launch_dependents();  // (attn_chunk_kernel looks for requests of its own meanwhile)
     total = p.head[0];
     G = p.head[1];
     if (x >= G) return;
@@ -1148,7 +1521,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __
 
 template <int D, bool E4M3, int NT, int RW, bool MULTI>
 cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
-  using L = PagedCfg<D, E4M3, NT, RW>;
+  using L = PagedCfg<D, E4M3, NT, RW, by_columns(D, E4M3, NT, MULTI)>;
   auto* kernel = paged_kernel<D, E4M3, NT, RW, MULTI>;
   static std::atomic<uint64_t> attr_done{0};
   int dev = 0;
@@ -1188,7 +1561,7 @@ cudaError_t launch_rows(const PagedParams& p, int ctas, cudaStream_t stream) {
   // though it spills 300 bytes (32 requests of 8192, 8 K/V heads: 107 us against 140); for bf16 the two are
   // near (98 against 103 us) and the slices' fewer CTAs leave fewer parts to join (37 ragged requests: 17 us
   // against 20).
-  if constexpr (D == 64 && E4M3) return launch<D, E4M3, 4, 1, MULTI>(p, ctas, stream);
+  if constexpr ((D == 64 && E4M3) || by_columns(D, E4M3, 4, MULTI)) return launch<D, E4M3, 4, 1, MULTI>(p, ctas, stream);
   else return launch<D, E4M3, 2, 2, MULTI>(p, ctas, stream);
 }
 

@@ -497,6 +497,14 @@ __device__ __forceinline__ void named_barrier_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// The same, and whether `pred` holds in any of the threads.
+__device__ __forceinline__ bool named_barrier_or(int id, int nthreads, bool pred) {
+  int any;
+  asm volatile(
+      "{.reg .pred in, out;\n setp.ne.s32 in, %3, 0;\n bar.red.or.pred out, %1, %2, in;\n selp.s32 %0, 1, 0, out;}"
+      : "=r"(any) : "r"(id), "r"(nthreads), "r"(static_cast<int>(pred)) : "memory");
+  return any != 0;
+}
 
 // ------------------------------------------------------------------ two-SM (CTA pair) forms
 // A cluster of two CTAs on the two SMs of a TPC can run one tcgen05 MMA across both SMs
