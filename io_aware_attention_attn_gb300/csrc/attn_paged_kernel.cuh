@@ -60,10 +60,6 @@
 namespace attn {
 namespace {
 
-#ifndef COLS_FROM
-#define COLS_FROM 4
-#endif
-constexpr int kColsFrom = COLS_FROM;
 constexpr int kSlices = 4;                       // key slices of 16 in a tile, a warp each
 enum : int { kRoleProducer = 7, kRoleConsumer = 8 };
 
@@ -73,8 +69,8 @@ constexpr float kPvSet = 6.f, kPSet = 115.f;      // P |v| and P at most where m
 constexpr float kTrailE4m3 = 9.f;                 // and how far past that m is moved
 constexpr float kSumLog2 = 16.f;                  // row sums are of 2^-16 P
 
-// Whether a CTA's warps share out the columns of O, and not only the keys of S (MULTI).
-__host__ __device__ constexpr bool by_columns(int D, bool e4m3, int NT, bool multi) { return multi && D == 128 && e4m3 && NT >= kColsFrom; }
+// Whether a CTA's warps share out the columns of O, and not only the keys of S (consume_columns).
+__host__ __device__ constexpr bool by_columns(int NT, int RW, bool multi) { return multi && NT > 1 && RW == 1; }
 
 // NT: groups of 8 query rows a warp holds; RW: row slices, each with four warps of its own.
 template <int D, bool E4M3, int NT, int RW, bool COLS = false>
@@ -408,17 +404,19 @@ __device__ __forceinline__ void store_row(const PagedParams& p, bool own, int h,
 }
 
 // Consumers that share out the columns of O: a warp forms S and P of 16 keys of a tile, as above, leaves P in shared memory,
-// and multiplies the P of all 64 with a quarter of V's columns.  A code of V is then turned once and O takes an
-// eighth of the registers of four row groups, so one warp holds the query rows of all of them.  The warps agree
-// on the reference of a row: one barrier a tile (P is there, and does no warp need a reference moved?), and two where one
-// does.  32 requests of 32 rows over 4096 keys, 8 K/V heads, E4M3, d = 128: TODO us; 16-row units, which read and
-// turn each tile twice, 136.
+// and multiplies the P of all 64 with a quarter of V's columns.  O then takes a quarter of the registers, so one warp holds
+// all of 32 rows and a code of K or V is turned once, where 16-row units read and turn each tile twice and two slices
+// of warps turn it twice; and a unit's end adds nothing up between warps.  The query rows lie in shared memory as the
+// products take them.  The warps agree on the reference of a row: one barrier a tile (P is there; does any warp need a
+// reference moved?), and two more where one does.
+// Measured, 32 requests over 4096 keys, 32 query and 8 K/V heads: 32 rows, E4M3, d = 128: 99 us (16-row units: 136), d = 64:
+// 77 (91), bf16 106 and 69 (113 and 73); 16 rows, d = 128: E4M3 79 (81), bf16 101 (103).  At 32 rows a tile's 620 instructions a
+// warp bound it, eight warps an SM: 43 % of the issue slots, half the waits for a fixed latency.
 template <int D, bool E4M3, int NT>
 __device__ __forceinline__ void consume_columns(const PagedParams& p, uint8_t* sm, uint32_t base, Walk& w, int left,
                                                 const WaitCtx& ctx) {
-  static_assert(D == 128, "a warp's columns are two tiles of 16");
   using L = PagedCfg<D, E4M3, NT, 1, true>;
-  constexpr int kSteps = D / 16, kRows = NT * 8;
+  constexpr int kSteps = D / 16, kRows = NT * 8, kOwn = D / 64;  // tiles of 16 columns that a warp has
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q4 = lane & 3;
   const int cta = static_cast<int>(blockIdx.x);
   auto full = [&](int st) { return base + L::kBar + st * 8; };
@@ -451,14 +449,14 @@ __device__ __forceinline__ void consume_columns(const PagedParams& p, uint8_t* s
     const int row0 = w.rg * p.rg_rows;
     // keys that the unit's first token sees, the fewest of all
     const int least = p.causal ? w.len - w.tokens + row0 / p.group + 1 : 0x7fffffff;
-    float acc[NT][2][4], nm[NT][2], above[NT][2], l[NT][2];
+    float acc[NT][kOwn][4], nm[NT][2], above[NT][2], l[NT][2];
     #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       nm[nt][0] = nm[nt][1] = E4M3 ? kNoRef : 0.f;
       above[nt][0] = above[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
       #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[nt][0][j] = acc[nt][1][j] = 0.f;
+      for (int k = 0; k < kOwn; ++k) acc[nt][k][0] = acc[nt][k][1] = acc[nt][k][2] = acc[nt][k][3] = 0.f;
     }
     auto no_ref = [&](int nt, int j) { return E4M3 ? nm[nt][j] == kNoRef : above[nt][j] == -INFINITY; };
 
@@ -497,8 +495,9 @@ __device__ __forceinline__ void consume_columns(const PagedParams& p, uint8_t* s
           #pragma unroll
           for (int k = 0; k < kSteps; k += 2) {
             const int chunk = k + (lane >> 4);
+            const int sw = L::kBlk == 128 ? chunk ^ (key & 7) : chunk ^ ((key >> 1) & 3);
             uint32_t a[4];
-            ldsm4(kst + key * L::kBlk + ((chunk ^ (key & 7)) << 4), a);
+            ldsm4(kst + key * L::kBlk + (sw << 4), a);
             uint4 q[NT];
             #pragma unroll
             for (int nt = 0; nt < NT; ++nt) q[nt] = qbuf[(k / 2 * NT + nt) * 32 + lane];
@@ -581,7 +580,7 @@ __device__ __forceinline__ void consume_columns(const PagedParams& p, uint8_t* s
                 above[nt][j] = top + p.trail;
               }
             }
-            scale_rows<2>(acc[nt], c);
+            scale_rows<kOwn>(acc[nt], c);
           }
         }
         uint32_t pf[NT][2];
@@ -644,6 +643,7 @@ __device__ __forceinline__ void consume_columns(const PagedParams& p, uint8_t* s
         for (int j = 0; j < 2; ++j) l[nt][j] = E4M3 ? fmaf(sum[nt][j], 0x1p-16f, l[nt][j]) : l[nt][j] + sum[nt][j];
       const uint4* theirs = pbuf + at_p * (L::kPTile / 4) + lane;
       at_p ^= 1;
+      uint32_t a[4];
       #pragma unroll
       for (int x = 0; x < kSlices; ++x) {
         const int lv = tile_live - x * 16;
@@ -662,12 +662,17 @@ __device__ __forceinline__ void consume_columns(const PagedParams& p, uint8_t* s
         const uint32_t keep0 = (2 * q4 < lv ? 0xffffu : 0u) | (2 * q4 + 1 < lv ? 0xffff0000u : 0u);
         const uint32_t keep1 = (2 * q4 + 8 < lv ? 0xffffu : 0u) | (2 * q4 + 9 < lv ? 0xffff0000u : 0u);
         if constexpr (E4M3) {
-          const int vk = x * 16 + (lane & 15), chunk = 2 * warp + (lane >> 4);
-          uint32_t a[4];
-          ldsm4_t(vst + vk * L::kBlk + ((chunk ^ (vk & 7)) << 4), a);
+          if (D == 128) {  // 16 keys, two tiles of columns
+            const int vk = x * 16 + (lane & 15), chunk = 2 * warp + (lane >> 4);
+            ldsm4_t(vst + vk * L::kBlk + ((chunk ^ (vk & 7)) << 4), a);
+          } else if (x % 2 == 0) {  // 32 keys, one
+            const int vk = x * 16 + lane;
+            ldsm4_t(vst + vk * L::kBlk + ((warp ^ ((vk >> 1) & 3)) << 4), a);
+          }
           #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t x0 = __byte_perm(a[2 * j], 0, 0x3120), x1 = __byte_perm(a[2 * j + 1], 0, 0x3120);
+          for (int j = 0; j < kOwn; ++j) {
+            const int at = D == 128 ? 2 * j : 2 * (x % 2);
+            const uint32_t x0 = __byte_perm(a[at], 0, 0x3120), x1 = __byte_perm(a[at + 1], 0, 0x3120);
             uint32_t v0 = e4m3x2_to_f16x2(x0), v1 = e4m3x2_to_f16x2(x0 >> 16);
             uint32_t v2 = e4m3x2_to_f16x2(x1), v3 = e4m3x2_to_f16x2(x1 >> 16);
             if (tail) {
@@ -682,9 +687,8 @@ __device__ __forceinline__ void consume_columns(const PagedParams& p, uint8_t* s
         } else {
           const int vk = x * 16 + ((lane >> 4) << 3) + (lane & 7);
           #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int k = 2 * warp + j, chunk = (k & 3) * 2 + ((lane >> 3) & 1);
-            uint32_t a[4];
+          for (int j = 0; j < kOwn; ++j) {
+            const int k = kOwn * warp + j, chunk = (k & 3) * 2 + ((lane >> 3) & 1);
             ldsm4_t(vst + (k >> 2) * (kPagedTile * 128) + vk * 128 + ((chunk ^ (vk & 7)) << 4), a);
             if (tail) {
               a[0] &= keep0;
@@ -730,10 +734,10 @@ __device__ __forceinline__ void consume_columns(const PagedParams& p, uint8_t* s
           if (warp == 0) sums[kSlices * kRows + row] = no_ref(nt, j) ? -INFINITY : (E4M3 ? kSumLog2 : 0.f) - nm[nt][j];
         }
         #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < kOwn; ++k)
           #pragma unroll
           for (int i = 0; i < 2; ++i)
-            merge[row * L::kMergeLd + 32 * warp + 16 * k + (E4M3 ? 2 * g + i : g + 8 * i)] =
+            merge[row * L::kMergeLd + 16 * (kOwn * warp + k) + (E4M3 ? 2 * g + i : g + 8 * i)] =
                 acc[nt][k][j + 2 * i] * (E4M3 ? 0x1p-16f : 1.f);
       }
     }
@@ -766,7 +770,7 @@ __device__ __forceinline__ void consume_columns(const PagedParams& p, uint8_t* s
 template <int D, bool E4M3, int NT, int RW, bool MULTI>
 __global__ void __launch_bounds__((kSlices * RW + 1) * 32, PagedCfg<D, E4M3, NT, RW>::kCtas)
 paged_kernel(const __grid_constant__ PagedParams p) {
-  constexpr bool kCols = by_columns(D, E4M3, NT, MULTI);
+  constexpr bool kCols = by_columns(NT, RW, MULTI);
   using L = PagedCfg<D, E4M3, NT, RW, kCols>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -1521,7 +1525,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __
 
 template <int D, bool E4M3, int NT, int RW, bool MULTI>
 cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
-  using L = PagedCfg<D, E4M3, NT, RW, by_columns(D, E4M3, NT, MULTI)>;
+  using L = PagedCfg<D, E4M3, NT, RW, by_columns(NT, RW, MULTI)>;
   auto* kernel = paged_kernel<D, E4M3, NT, RW, MULTI>;
   static std::atomic<uint64_t> attr_done{0};
   int dev = 0;
@@ -1560,9 +1564,14 @@ cudaError_t launch_rows(const PagedParams& p, int ctas, cudaStream_t stream) {
   // that converts them twice, so at d = 64, where four groups of rows fit one warp, they take that
   // though it spills 300 bytes (32 requests of 8192, 8 K/V heads: 107 us against 140); for bf16 the two are
   // near (98 against 103 us) and the slices' fewer CTAs leave fewer parts to join (37 ragged requests: 17 us
-  // against 20).
-  if constexpr ((D == 64 && E4M3) || by_columns(D, E4M3, 4, MULTI)) return launch<D, E4M3, 4, 1, MULTI>(p, ctas, stream);
-  else return launch<D, E4M3, 2, 2, MULTI>(p, ctas, stream);
+  // against 20).  MULTI: by columns, but for bf16 where there are no more tiles than CTAs and so nothing but a tile's own
+  // chain of steps, which is shorter in two slices (5 tokens of 4 heads behind 295, d = 64: 8.0 us, by columns 9.5).
+  if constexpr (MULTI) {
+    if (E4M3 || ctas > PagedCfg<D, E4M3, 4, 1, true>::kCtas * 152) return launch<D, E4M3, 4, 1, MULTI>(p, ctas, stream);
+  }
+  if constexpr (D == 64 && E4M3) return launch<D, E4M3, 4, 1, MULTI>(p, ctas, stream);
+  else if constexpr (!MULTI || !E4M3) return launch<D, E4M3, 2, 2, MULTI>(p, ctas, stream);
+  return cudaErrorInvalidValue;  // (not reached)
 }
 
 }  // namespace
