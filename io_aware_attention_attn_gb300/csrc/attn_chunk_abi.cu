@@ -19,8 +19,8 @@ constexpr int kChunkCost = 2;
 
 // Which of the two kernels takes a request goes by its rows (new tokens times the query heads of a K/V head): up to
 // kFewRows the one of warp products, whose time is that of reading K and V, above the one of 256-row products.
-// Measured, 32 requests over 4096 keys, 32 query and 8 K/V heads, d = 128, bf16 / E4M3 pages, us: 4 rows 99 / 64, 16 rows
-// 101 / 79, 32 rows 106 / 99 by the first (with the second's empty launch); any up to 256 by the second, 115 / 154.
+// Measured, 32 requests over 4096 keys, 32 query and 8 K/V heads, d = 128, bf16 / E4M3 pages, us: 4 rows 99 / 63, 16 rows
+// 101 / 73, 32 rows 106 / 99 by the first (with the second's empty launch); any up to 256 by the second, 115 / 154.
 constexpr int kFewRows = 32;
 constexpr int kOneCtaTiles = 8;  // tiles that a CTA goes through sooner than a second launch joins its parts
 enum Kernels { kFew = 1, kMany = 2 };
@@ -114,7 +114,7 @@ int run_few(const void* q, const attn_kv_cache& c, const int32_t* table, const i
   p.one_cta = p.B == 1 && tiles <= kOneCtaTiles && units <= kPagedMaxCtas / 4;
   const int64_t places = p.one_cta ? units : units * tiles;
   if (launch_fwd_paged_multi(p, d, c.dtype == ATTN_CACHE_E4M3,
-                             places < kPagedMaxCtas ? static_cast<int>(places) : kPagedMaxCtas, stream) != cudaSuccess)
+                             places < INT_MAX ? static_cast<int>(places) : INT_MAX, stream) != cudaSuccess)
     return ATTN_ERR_LAUNCH;
   return !own || launch_pair_merge(p, B, d, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }

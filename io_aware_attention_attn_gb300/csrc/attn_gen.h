@@ -161,7 +161,7 @@ inline FewLayout few_layout(size_t rows, int d) {
 cudaError_t launch_fwd_paged(const PagedParams& p, int d, bool e4m3, int max_tiles,
                              cudaStream_t stream);
 
-// The same of units of up to p.rg_rows (8, 16 or 32) rows of a request's tokens; `max_tiles` as above.
+// The same of units of up to p.rg_rows (8, 16 or 32) rows of a request's tokens; `max_tiles`: places of all units, at most.
 cudaError_t launch_fwd_paged_multi(const PagedParams& p, int d, bool e4m3, int max_tiles,
                                    cudaStream_t stream);
 

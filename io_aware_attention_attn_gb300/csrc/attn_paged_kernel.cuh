@@ -81,9 +81,10 @@ struct PagedCfg {
   // The smaller a tile, the less time a warp's chain of dependent steps has for it (e4m3, d = 128, ragged
   // requests on 16-row pages: 159 us with two CTAs, 135 with three; bf16 is at the HBM rate with two as well, 588 us
   // for the 4.3 GB above against 597 with three, but short requests are bound by that chain too: 256
-  // of 64 tokens 19.2 us with two, 16.9 with three).
+  // of 64 tokens 19.2 us with two, 16.9 with three).  By columns, 16 rows over E4M3: 32 requests of 4 tokens over 4096 keys
+  // 70 us with two, 65 with three (spilling 8 bytes); 64 groups of 4 behind 4000 154 and 139.
   static constexpr int kCtas = RW == 2 ? 1 : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2)
-                                                     : NT >= 2 ? 2 : 3;
+                                                     : COLS && E4M3 && NT == 2 ? 3 : NT >= 2 ? 2 : 3;
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
   static constexpr int kBlk = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a row in one box
   static constexpr int kBlks = kRowBytes / kBlk;                  // boxes side by side
@@ -410,7 +411,7 @@ __device__ __forceinline__ void store_row(const PagedParams& p, bool own, int h,
 // products take them.  The warps agree on the reference of a row: one barrier a tile (P is there; does any warp need a
 // reference moved?), and two more where one does.
 // Measured, 32 requests over 4096 keys, 32 query and 8 K/V heads: 32 rows, E4M3, d = 128: 99 us (16-row units: 136), d = 64:
-// 77 (91), bf16 106 and 69 (113 and 73); 16 rows, d = 128: E4M3 79 (81), bf16 101 (103).  At 32 rows a tile's 620 instructions a
+// 77 (91), bf16 106 and 69 (113 and 73); 16 rows, d = 128: E4M3 73 (81), bf16 101 (103).  At 32 rows a tile's 620 instructions a
 // warp bound it, eight warps an SM: 43 % of the issue slots, half the waits for a fixed latency.
 template <int D, bool E4M3, int NT>
 __device__ __forceinline__ void consume_columns(const PagedParams& p, uint8_t* sm, uint32_t base, Walk& w, int left,
@@ -768,7 +769,7 @@ __device__ __forceinline__ void consume_columns(const PagedParams& p, uint8_t* s
 }
 
 template <int D, bool E4M3, int NT, int RW, bool MULTI>
-__global__ void __launch_bounds__((kSlices * RW + 1) * 32, PagedCfg<D, E4M3, NT, RW>::kCtas)
+__global__ void __launch_bounds__((kSlices * RW + 1) * 32, PagedCfg<D, E4M3, NT, RW, by_columns(NT, RW, MULTI)>::kCtas)
 paged_kernel(const __grid_constant__ PagedParams p) {
   constexpr bool kCols = by_columns(NT, RW, MULTI);
   using L = PagedCfg<D, E4M3, NT, RW, kCols>;
@@ -1538,8 +1539,16 @@ cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
     attr_done.fetch_or(bit, std::memory_order_acq_rel);
   }
   const int most = L::kCtas * 152;
+  // MULTI: fewer CTAs an SM where each would have few of the (at most) `ctas` places, as parts cost more than they
+  // save then: four a CTA, down to one CTA an SM with one row group and two with more (4 requests over 900 keys, 32 query and
+  // 8 K/V heads, d = 128, bf16: of two tokens 13.6 us with three an SM, 11.6 with two, 10.4 with one; of four, E4M3, 18.2,
+  // 15.6 and 16.4).
+  int sm_ctas = L::kCtas;
+  if (MULTI)
+    while (sm_ctas > (NT == 1 ? 1 : 2) && ctas < 4 * 152 * sm_ctas) --sm_ctas;
   static_assert(L::kCtas * 152 <= kPagedMaxCtas, "the workspace holds the parts of fewer CTAs");
   if (ctas > most) ctas = most;
+  if (MULTI && sm_ctas * 152 < ctas) ctas = sm_ctas * 152;
   // one join a unit where there are no more units than CTAs, else one a CTA
   const long long units = static_cast<long long>(p.B) * p.H_kv * p.n_rg;
   PagedParams q = p;

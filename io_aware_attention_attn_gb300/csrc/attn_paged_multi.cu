@@ -33,10 +33,9 @@ __global__ void __launch_bounds__(256) pair_merge_kernel(const __grid_constant__
 
 cudaError_t launch_fwd_paged_multi(const PagedParams& p, int d, bool e4m3, int max_tiles,
                                    cudaStream_t stream) {
-  const int ctas = max_tiles < kPagedMaxCtas ? max_tiles : kPagedMaxCtas;
   if (d == 64)
-    return e4m3 ? launch_rows<64, true, true>(p, ctas, stream) : launch_rows<64, false, true>(p, ctas, stream);
-  return e4m3 ? launch_rows<128, true, true>(p, ctas, stream) : launch_rows<128, false, true>(p, ctas, stream);
+    return e4m3 ? launch_rows<64, true, true>(p, max_tiles, stream) : launch_rows<64, false, true>(p, max_tiles, stream);
+  return e4m3 ? launch_rows<128, true, true>(p, max_tiles, stream) : launch_rows<128, false, true>(p, max_tiles, stream);
 }
 
 cudaError_t launch_pair_merge(const PagedParams& p, int groups, int d, cudaStream_t stream) {
