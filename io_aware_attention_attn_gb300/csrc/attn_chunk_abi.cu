@@ -20,7 +20,7 @@ constexpr int kChunkCost = 2;
 // Which of the two kernels takes a request goes by its rows (new tokens times the query heads of a K/V head): up to
 // kFewRows the one of warp products, whose time is that of reading K and V, above the one of 256-row products.
 // Measured, 32 requests over 4096 keys, 32 query and 8 K/V heads, d = 128, bf16 / E4M3 pages, us: 4 rows 99 / 63, 16 rows
-// 101 / 73, 32 rows 106 / 99 by the first (with the second's empty launch); any up to 256 by the second, 115 / 154.
+// 101 / 73, 32 rows 106 / 93 by the first (with the second's empty launch); any up to 256 by the second, 115 / 154.
 constexpr int kFewRows = 32;
 constexpr int kOneCtaTiles = 8;  // tiles that a CTA goes through sooner than a second launch joins its parts
 enum Kernels { kFew = 1, kMany = 2 };

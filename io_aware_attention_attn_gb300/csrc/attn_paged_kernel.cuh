@@ -81,10 +81,12 @@ struct PagedCfg {
   // The smaller a tile, the less time a warp's chain of dependent steps has for it (e4m3, d = 128, ragged
   // requests on 16-row pages: 159 us with two CTAs, 135 with three; bf16 is at the HBM rate with two as well, 588 us
   // for the 4.3 GB above against 597 with three, but short requests are bound by that chain too: 256
-  // of 64 tokens 19.2 us with two, 16.9 with three).  By columns, 16 rows over E4M3: 32 requests of 4 tokens over 4096 keys
-  // 70 us with two, 65 with three (spilling 8 bytes); 64 groups of 4 behind 4000 154 and 139.
-  static constexpr int kCtas = RW == 2 ? 1 : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2)
-                                                     : COLS && E4M3 && NT == 2 ? 3 : NT >= 2 ? 2 : 3;
+  // of 64 tokens 19.2 us with two, 16.9 with three).  By columns, three (bf16 rows of d = 128 leave room for two), though
+  // that spills 256 bytes at 32 rows, d = 128 and up to 20 at others: 32 requests over 4096 keys, E4M3, 16 rows 70 us with two
+  // and 65 with three, 32 rows 99 and 93, d = 64 79 and 69; with four 16 rows take 62, but 4 requests over 3000 26 for 21,
+  // as the ring then holds two tiles.
+  static constexpr int kCtas = RW == 2 ? 1 : D == 64 ? (NT == 1 ? 4 : NT == 2 || COLS ? 3 : 2)
+                                                     : COLS && E4M3 ? 3 : NT >= 2 ? 2 : 3;
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
   static constexpr int kBlk = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a row in one box
   static constexpr int kBlks = kRowBytes / kBlk;                  // boxes side by side
@@ -410,9 +412,9 @@ __device__ __forceinline__ void store_row(const PagedParams& p, bool own, int h,
 // of warps turn it twice; and a unit's end adds nothing up between warps.  The query rows lie in shared memory as the
 // products take them.  The warps agree on the reference of a row: one barrier a tile (P is there; does any warp need a
 // reference moved?), and two more where one does.
-// Measured, 32 requests over 4096 keys, 32 query and 8 K/V heads: 32 rows, E4M3, d = 128: 99 us (16-row units: 136), d = 64:
-// 77 (91), bf16 106 and 69 (113 and 73); 16 rows, d = 128: E4M3 73 (81), bf16 101 (103).  At 32 rows a tile's 620 instructions a
-// warp bound it, eight warps an SM: 43 % of the issue slots, half the waits for a fixed latency.
+// Measured, 32 requests over 4096 keys, 32 query and 8 K/V heads: 32 rows, E4M3, d = 128: 93 us (16-row units: 136), d = 64:
+// 69 (91), bf16 106 and 65 (113 and 73); 16 rows, d = 128: E4M3 73 (81), bf16 101 (103).  At 32 rows over E4M3 a tile's 620
+// instructions a warp bound it (two CTAs an SM: 43 % of the issue slots, half the waits for a fixed latency).
 template <int D, bool E4M3, int NT>
 __device__ __forceinline__ void consume_columns(const PagedParams& p, uint8_t* sm, uint32_t base, Walk& w, int left,
                                                 const WaitCtx& ctx) {
