@@ -1543,8 +1543,8 @@ cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
   const int most = L::kCtas * 152;
   // MULTI: fewer CTAs an SM where each would have few of the (at most) `ctas` places, as parts cost more than they
   // save then: four a CTA, down to one CTA an SM with one row group and two with more (4 requests over 900 keys, 32 query and
-  // 8 K/V heads, d = 128, bf16: of two tokens 13.6 us with three an SM, 11.6 with two, 10.4 with one; of four, E4M3, 18.2,
-  // 15.6 and 16.4).
+  // 8 K/V heads, d = 128: of two tokens, bf16, 10.9 us with three an SM, 10.1 with one; of four, E4M3, 16.0 with three, 14.5
+  // with two).
   int sm_ctas = L::kCtas;
   if (MULTI)
     while (sm_ctas > (NT == 1 ? 1 : 2) && ctas < 4 * 152 * sm_ctas) --sm_ctas;
@@ -1558,8 +1558,16 @@ cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
   q.unit_cost = MULTI ? kFewCost : NT * RW == 4 ? kPagedMaxCost : 1;
   q.by_unit = !MULTI && units <= ctas;
   const int joins = q.by_unit ? static_cast<int>(units) : ctas;
-  // blocks of a join: as many as its rows keep busy at the mean number of parts
-  const int blocks = (p.rg_rows * join_share(ctas / joins + 2) + kJoinWarps - 1) / kJoinWarps;
+  // Blocks of a join: as many as its rows keep busy at the mean number of parts.  MULTI: at that of units that are one a
+  // request and K/V head, while a block's look at a CTA that ends none of them costs less than it saves, 16 blocks an SM
+  // (4 requests of 2 tokens over 3000 keys, 32 query and 8 K/V heads, bf16, d = 64: 12.5 us; 13.5 with 8, 13.7 with 32, 17.2 by
+  // units as many as CTAs).
+  const int parts = MULTI ? static_cast<int>(ctas / (units < ctas ? units : ctas)) : ctas / joins;
+  int blocks = (p.rg_rows * join_share(parts + 2) + kJoinWarps - 1) / kJoinWarps;
+  if (MULTI) {
+    const int least = (p.rg_rows + kJoinWarps - 1) / kJoinWarps, room = 16 * 152 / ctas;
+    blocks = blocks < room ? blocks : least > room ? least : room;
+  }
   e = launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), L::kThreads, L::kDyn, stream, q);
   if (e != cudaSuccess || (MULTI && p.one_cta)) return e;
   return launch_dependent(paged_join_kernel<D, MULTI>,
