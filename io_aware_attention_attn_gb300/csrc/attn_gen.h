@@ -79,9 +79,10 @@ cudaError_t launch_qkv_rope_bwd(RopeParams& p, int d, bool interleaved, cudaStre
 constexpr int kPagedTile = 64;         // keys of a tile
 constexpr int kPagedMaxCtas = 608;     // 4 on each of 152 SMs
 constexpr int kPagedMaxCost = 2;       // places that a unit takes beside its tiles, at most
-// the same with several rows a request, where units of a tile lie beside long ones (64 groups of 4 requests of up to 64 rows
-// behind 4000, E4M3, d = 128: 234 us with 1, 177 with 2, 159 with 4, 171 with 6)
-constexpr int kFewCost = 4;
+// The same with several rows a request, whose ends take longer (4 requests of 8 tokens over 3000 keys, E4M3: 25 us, with 2
+// 29; 100 of 1 to 8 over up to 2000 78 and 89), and behind shared prefixes, where most units are the few own rows of one
+// request (64 groups of 4 behind 4000, E4M3: 139 us with 4, 129 with 2; 30 groups of 8 behind 500 60 and 54).
+constexpr int kFewCost = 4, kSharedCost = 2;
 constexpr float kPagedTrail = 8.f;     // how far a score may pass the reference maximum, in log2 units
 constexpr int kPagedMaxRows = 32;      // query rows (heads of one K/V head) of a unit
 

@@ -1555,7 +1555,7 @@ cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
   const long long units = static_cast<long long>(p.B) * p.H_kv * p.n_rg;
   PagedParams q = p;
   q.ctas = ctas;
-  q.unit_cost = MULTI ? kFewCost : NT * RW == 4 ? kPagedMaxCost : 1;
+  q.unit_cost = MULTI ? (p.pair_o ? kSharedCost : kFewCost) : NT * RW == 4 ? kPagedMaxCost : 1;
   q.by_unit = !MULTI && units <= ctas;
   const int joins = q.by_unit ? static_cast<int>(units) : ctas;
   // Blocks of a join: as many as its rows keep busy at the mean number of parts.  MULTI: at that of units that are one a
