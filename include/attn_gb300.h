@@ -391,11 +391,11 @@ ATTN_API size_t attn_fwd_paged_workspace_bytes(int B, int H, int H_kv, int d);
  *     tile of 128 rows (as in attn_fwd).
  *   workspace : attn_fwd_paged_varlen_workspace_bytes(T, H, H_kv, d) bytes (it does not depend on the
  *     lengths), 256-byte aligned; calls whose work may overlap on the GPU need one each.
- * Requests with up to 32 query rows a K/V head (new tokens times H / H_kv) are taken by a kernel that works as
+ * Requests with up to 32 query rows a K/V head (new tokens times H / H_kv; 64 over E4M3 pages) are taken by a kernel that works as
  * attn_fwd_paged does, those with more by one whose products take 256 rows at once.  Each cuts its work into equal
  * shares of key tiles, whatever the lengths are, and a second launch joins what fell to several shares by the block
- * merge of attn_fwd_splitkv: one to four launches, by B, T and the table's shape alone (with 32 rows in all, only the
- * first kernel's; with over 64 a request on average, or one request of over 32, only the second's).  Everything that
+ * merge of attn_fwd_splitkv: one to four launches, by B, T and the table's shape alone (with so many rows in all, only the
+ * first kernel's; with over 64 a request on average, or one request of more, only the second's).  Everything that
  * depends on lengths is decided on the GPU: a captured call can be replayed with other lengths, tables and contents.
  * Equal inputs give equal bits.  A table entry that is needed and names no page of the cache is read as a page of
  * zeros, and the status word reports kind 5.

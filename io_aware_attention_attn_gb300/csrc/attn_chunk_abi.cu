@@ -21,7 +21,10 @@ constexpr int kChunkCost = 2;
 // kFewRows the one of warp products, whose time is that of reading K and V, above the one of 256-row products.
 // Measured, 32 requests over 4096 keys, 32 query and 8 K/V heads, d = 128, bf16 / E4M3 pages, us: 4 rows 99 / 63, 16 rows
 // 101 / 73, 32 rows 106 / 93 by the first (with the second's empty launch); any up to 256 by the second, 115 / 154.
-constexpr int kFewRows = 32;
+// Over E4M3 the first takes up to 64, in two units: 33 to 64 rows of 32 requests 150 to 153 us and 149, of 8 requests over 2000
+// keys 34 and 41 (bf16: 171 and 108, 32 and 33).
+constexpr int kFewRows = 32, kFewRowsE4m3 = 64;
+int few_most(const attn_kv_cache& c) { return c.dtype == ATTN_CACHE_E4M3 ? kFewRowsE4m3 : kFewRows; }
 constexpr int kOneCtaTiles = 8;  // tiles that a CTA goes through sooner than a second launch joins its parts
 enum Kernels { kFew = 1, kMany = 2 };
 // Rows of one unit of the first, by how many there can be; a call's units, by the mean of its requests.
@@ -30,8 +33,8 @@ int few_rows_of(int64_t rows, int B) { return few_group((rows + B - 1) / B); }
 // What the host knows: the tokens in all.  Where they may lie either way both kernels are launched, each taking its own
 // requests; requests with more than twice kFewRows rows on average leave the first out (a kernel that finds nothing to do, and its
 // join, take 3 to 7 us, and the second kernel is right for any request).
-int kernels_for(int64_t rows, int B) {
-  if (rows <= kFewRows) return kFew;
+int kernels_for(int64_t rows, int B, int few) {
+  if (rows <= few) return kFew;
   return B > 1 && rows <= 2ll * kFewRows * B ? kFew | kMany : kMany;
 }
 size_t chunk_workspace(int T, int group, int d, const ChunkSizes& z) {
@@ -178,10 +181,10 @@ int run_many(const void* q, const attn_kv_cache& c, const int32_t* table, const 
 // Whether the first takes requests that share prefixes: they are about as many in each group, so one kernel takes them
 // all, by their mean, and the first takes each request's own rows in the same launch (12 groups of 4 behind up to 4096
 // rows, E4M3: 31 us with launches of their own for those).
-bool few_behind_prefix(int groups, int B, int H, int H_kv, int max_prefix_pages, int max_pages, int page_size) {
+bool few_behind_prefix(int groups, int B, int H, int H_kv, int max_prefix_pages, int max_pages, const attn_kv_cache& c) {
   const int64_t rows = static_cast<int64_t>(B) * (H / H_kv);
-  if (rows > static_cast<int64_t>(kFewRows) * groups) return false;
-  const int64_t most = static_cast<int64_t>(max_prefix_pages > max_pages ? max_prefix_pages : max_pages) * page_size;
+  if (rows > static_cast<int64_t>(few_most(c)) * groups) return false;
+  const int64_t most = static_cast<int64_t>(max_prefix_pages > max_pages ? max_prefix_pages : max_pages) * c.page_size;
   const int64_t units = rows / 8 + (groups < B ? groups : B) + static_cast<int64_t>(B) * (H / H_kv / 8 + 1);
   return units <= INT_MAX / ((most + kPagedTile - 1) / kPagedTile + 1 + kFewCost) / H_kv;  // places in 32 bits
 }
@@ -232,14 +235,14 @@ extern "C" int attn_fwd_paged_varlen(const void* q, const attn_kv_cache* cache, 
   if ((rc = check_device()) != 0) return rc;
   const QueryLayout at{static_cast<int64_t>(T) * d, d};
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const int which = kernels_for(static_cast<int64_t>(T) * (H / H_kv), B);
+  const int few_rows = few_most(*cache), which = kernels_for(static_cast<int64_t>(T) * (H / H_kv), B, few_rows);
   // of both, one after the other on one workspace
   if (which & kFew)
     rc = run_few(q, *cache, block_table, seq_lens, cu_new, o, lse, nullptr, B, T, H, H_kv, d, max_pages, causal != 0, scale,
-                 at, which & kMany ? kFewRows : INT_MAX, ws, static_cast<cudaStream_t>(stream));
+                 at, which & kMany ? few_rows : INT_MAX, ws, static_cast<cudaStream_t>(stream));
   if (rc == ATTN_OK && (which & kMany))
     rc = run_many(q, *cache, block_table, seq_lens, cu_new, o, lse, nullptr, nullptr, B, T, H, H_kv, d, max_pages,
-                  causal != 0, scale, at, which & kFew ? kFewRows : 0, z, ws, static_cast<cudaStream_t>(stream));
+                  causal != 0, scale, at, which & kFew ? few_rows : 0, z, ws, static_cast<cudaStream_t>(stream));
   return rc;
 }
 
@@ -278,7 +281,7 @@ extern "C" int attn_fwd_paged_shared(const void* q, const attn_kv_cache* cache, 
   float* tail_o = reinterpret_cast<float*>(ws + s.tail_o);
   float* tail_lse = reinterpret_cast<float*>(ws + s.tail_lse);
   const QueryLayout at{d, static_cast<int64_t>(H) * d};
-  if (few_behind_prefix(groups, B, H, H_kv, max_prefix_pages, max_pages, cache->page_size)) {
+  if (few_behind_prefix(groups, B, H, H_kv, max_prefix_pages, max_pages, *cache)) {
     const OwnRows own{block_table, seq_lens, max_pages, tail_o, tail_lse};
     return run_few(q, *cache, prefix_table, prefix_lens, cu_groups, o, lse, &own, groups, B, H, H_kv, d, max_prefix_pages, 0,
                    scale, at, INT_MAX, ws + s.chunk, static_cast<cudaStream_t>(stream));
