@@ -112,6 +112,13 @@ int run_few(const void* q, const attn_kv_cache& c, const int32_t* table, const i
     if (own->max_pages > max_pages) most = static_cast<int64_t>(own->max_pages) * c.page_size;
   }
   const int64_t tiles = most > 0 ? (most + kPagedTile - 1) / kPagedTile : 1;
+  int64_t like = static_cast<int64_t>(B) * H_kv;
+  if (own) {  // the own rows' units, by their places
+    const int64_t own_tiles = static_cast<int64_t>(own->max_pages) * c.page_size / kPagedTile + 1;
+    const int64_t prefix_tiles = static_cast<int64_t>(max_pages) * c.page_size / kPagedTile + 1;
+    like += static_cast<int64_t>(T) * H_kv * (own_tiles + kSharedCost) / (prefix_tiles + kSharedCost);
+  }
+  p.long_units = like < INT_MAX ? static_cast<int>(like) : INT_MAX;
   // One request over a few tiles: a CTA goes through all of a unit's in less time than a second launch takes to join
   // its parts (5 tokens behind 295, 16 query and 4 K/V heads, d = 64: 7.8 us, with the join 13.4).
   p.one_cta = p.B == 1 && tiles <= kOneCtaTiles && units <= kPagedMaxCtas / 4;

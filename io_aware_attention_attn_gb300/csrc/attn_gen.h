@@ -118,6 +118,7 @@ struct PagedParams {
   int T, causal, most_rows;  // (requests of more rows have no units)
   int64_t q_head, q_token, o_head, o_token;  // elements from one query head, one token to the next
   bool one_cta;         // a unit a CTA, nothing to join (one request of few tiles)
+  int long_units;       // how many units of the longest request all units are together, by the shape of the tables
   PagedDesc* desc;      // [CTAs]
   int* head;            // [0] places in all, [1] CTAs with a share
   // Requests that share a prefix: requests from own_first on are the tokens again, one each, over rows of their own;

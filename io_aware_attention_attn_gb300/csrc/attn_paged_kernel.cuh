@@ -1559,10 +1559,10 @@ cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
   q.by_unit = !MULTI && units <= ctas;
   const int joins = q.by_unit ? static_cast<int>(units) : ctas;
   // Blocks of a join: as many as its rows keep busy at the mean number of parts.  MULTI: at that of units that are one a
-  // request and K/V head, while a block's look at a CTA that ends none of them costs less than it saves, 16 blocks an SM
+  // request and K/V head (12 groups of 4 behind 128 to 4096, E4M3: 19.3 us; counting the own rows' short units too 21.4), while a block's look at a CTA that ends none of them costs less than it saves, 16 blocks an SM
   // (4 requests of 2 tokens over 3000 keys, 32 query and 8 K/V heads, bf16, d = 64: 12.5 us; 13.5 with 8, 13.7 with 32, 17.2 by
   // units as many as CTAs).
-  const int parts = MULTI ? static_cast<int>(ctas / (units < ctas ? units : ctas)) : ctas / joins;
+  const int parts = MULTI ? ctas / (p.long_units < ctas ? p.long_units : ctas) : ctas / joins;
   int blocks = (p.rg_rows * join_share(parts + 2) + kJoinWarps - 1) / kJoinWarps;
   if (MULTI) {
     const int least = (p.rg_rows + kJoinWarps - 1) / kJoinWarps, room = 16 * 152 / ctas;
