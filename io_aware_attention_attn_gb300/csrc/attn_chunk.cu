@@ -66,6 +66,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const __gri
     const int tok_in = row / p.rg_rows, head = row - tok_in * p.rg_rows;
     const int tok = (at >> 7) * p.cta_tokens + tok_in;
     const bool valid = at < p.part_rows && tok_in < p.cta_tokens && tok < d.n_tok && head0 + head < p.group;
+    const int64_t tq = d.tok + tok, hq = z * p.group + head0 + head;
+    // the same row over other keys, on its way while the parts are
+    float other = -INFINITY;
+    float4 ta = make_float4(0.f, 0.f, 0.f, 0.f), tb = ta;
+    if (p.tail_o && sub == 0 && valid) {
+      other = p.tail_lse[tq * p.H + hq];
+      const float4* src = reinterpret_cast<const float4*>(p.tail_o + (tq * p.H + hq) * D + 8 * c8);
+      ta = src[0];
+      tb = src[1];
+    }
     float acc[8], m = -INFINITY, l = 0.f;
     #pragma unroll
     for (int c = 0; c < 8; ++c) acc[c] = 0.f;
@@ -128,19 +138,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const __gri
       __syncthreads();
     }
     if (sub != 0 || !valid) continue;
-    const int64_t tq = d.tok + tok, hq = z * p.group + head0 + head;
     float wt = l > 0.f || l != l ? 1.f / l : 0.f;
     float lse = l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
     #pragma unroll
     for (int c = 0; c < 8; ++c) acc[c] *= wt;
-    if (p.tail_o) {  // the same row over other keys
-      const float other = p.tail_lse[tq * p.H + hq], top = fmaxf(lse, other);
+    if (p.tail_o) {
+      const float top = fmaxf(lse, other);
       const float wa = lse == -INFINITY ? 0.f : ex2_approx((lse - top) * 1.4426950408889634f);
       const float wb = other == -INFINITY ? 0.f : ex2_approx((other - top) * 1.4426950408889634f);
       const float sum = wa + wb, inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-      const float4* src = reinterpret_cast<const float4*>(p.tail_o + (tq * p.H + hq) * D + 8 * c8);
-      const float4 a = src[0], b = src[1];
-      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      const float v[8] = {ta.x, ta.y, ta.z, ta.w, tb.x, tb.y, tb.z, tb.w};
       #pragma unroll
       for (int c = 0; c < 8; ++c) acc[c] = (acc[c] * wa + v[c] * wb) * inv;
       lse = sum > 0.f || sum != sum ? top + log2f(sum) * 0.69314718055994530942f : -INFINITY;
