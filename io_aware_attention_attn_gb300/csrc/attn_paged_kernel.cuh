@@ -1542,12 +1542,12 @@ cudaError_t launch(const PagedParams& p, int ctas, cudaStream_t stream) {
   }
   const int most = L::kCtas * 152;
   // MULTI: fewer CTAs an SM where each would have few of the (at most) `ctas` places, as parts cost more than they
-  // save then: four a CTA, down to one CTA an SM with one row group and two with more (4 requests over 900 keys, 32 query and
-  // 8 K/V heads, d = 128: of two tokens, bf16, 10.9 us with three an SM, 10.1 with one; of four, E4M3, 16.0 with three, 14.5
-  // with two).
+  // save then: four a CTA (4 requests over 900 keys, 32 query and 8 K/V heads, d = 128, of two tokens, bf16: 10.9 us with
+  // three an SM, 10.1 with one; one request of 8 over 4000, 19.2 with two, 16.8 with one, E4M3 20.9 and 18.3; but 4
+  // requests of 4 over 900, E4M3, 14.5 and 15.2).
   int sm_ctas = L::kCtas;
   if (MULTI)
-    while (sm_ctas > (NT == 1 ? 1 : 2) && ctas < 4 * 152 * sm_ctas) --sm_ctas;
+    while (sm_ctas > 1 && ctas < 4 * 152 * sm_ctas) --sm_ctas;
   static_assert(L::kCtas * 152 <= kPagedMaxCtas, "the workspace holds the parts of fewer CTAs");
   if (ctas > most) ctas = most;
   if (MULTI && sm_ctas * 152 < ctas) ctas = sm_ctas * 152;
