@@ -440,6 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
       if (warp == 0) w0 = w;
       else if (lane == 0) starts[warp] = ChunkStart{w.s, w.u, w.t, w.j, w.left, w.r.n, w.tok0, w.r.L};
     }
+    if (!few) __syncthreads();  // O goes out through where s_pre is, which the searching warps have read
   }
   const ChunkUnit* units = reinterpret_cast<const ChunkUnit*>(smem + L::kUnits);
   // The uq-th unit (or part): false when there is none, or a wait gave up.
