@@ -383,8 +383,9 @@ ATTN_API size_t attn_fwd_paged_workspace_bytes(int B, int H, int H_kv, int d);
  *   block_table : int32 [B, max_pages]; only the entries that seq_lens needs are read, and a row past seq_lens
  *     is never used, whatever it holds.  seq_lens : int32 [B], clamped to 0 .. max_pages * page_size.
  *   cu_new : int32 [B + 1], from 0 up, at most T.  Requests without new tokens are fine; tokens from cu_new[B]
- *     on are padding, and o and lse are left as they were there.  cu_new that decreases, does not begin with 0 or passes
- *     T is clamped into [0, T] and the status word reports kind 2 (o and lse are then unspecified).
+ *     on are padding, and o and lse are left as they were there.  cu_new that does not begin with 0 or passes T is
+ *     clamped into [0, T] and the status word reports kind 2 (o and lse are then unspecified); with one that
+ *     decreases nothing is computed, with the same report.
  *   A token that sees no row (more new tokens than rows) gets O = 0 and lse = -inf.
  *   E4M3 caches: V scales of 2^-100 to 2^100 in magnitude, or 0 (K scales: any; attn_fwd_paged takes any of either);
  *     a query row with an infinity or a NaN gives NaN.  A V row that is not finite reaches, besides the tokens that see it, those before it that share its

@@ -165,14 +165,15 @@ __device__ __forceinline__ void advance(const ChunkParams& p, Walk& w, int end) 
 }
 
 // Places of all units, by a block of T threads, and s_pre[i]: those of the requests before i's share of
-// ceil(B / T); `wide`: rows of requests with several row tiles.  Ends with the block in step.
+// ceil(B / T); `wide`: rows of requests with several row tiles.  Where cu falls the requests' tokens are more than T, and their
+// places may not fit 32 bits: there are none.  Ends with the block in step.
 template <int T>
 __device__ uint32_t block_places(const ChunkParams& p, int* s_pre, int* s_warp, float& wide) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per = p.H_kv * p.n_rg;
   const int share = (p.B + T - 1) / T, lo = min(tid * share, p.B), hi = min(lo + share, p.B);
   int sum = 0;
   float rows = 0.f;
-  bool bad = false;
+  bool bad = false, falls = false;
   #pragma unroll 1
   for (int s = lo; s < hi; ++s) {
     int tok0;
@@ -180,6 +181,7 @@ __device__ uint32_t block_places(const ChunkParams& p, int* s_pre, int* s_warp, 
     sum += unit_row_places(r, p.shape);
     if (row_tiles(r, p.shape) > 1) rows += static_cast<float>(r.L);
     const int x = p.cu[s], y = p.cu[s + 1];
+    falls |= y < x;
     bad |= y < x || (s == 0 && x != 0) || y > p.T;
   }
   if (bad && blockIdx.x == 0) atomicCAS(p.status, 0, kStatusBadSeqlens);
@@ -195,7 +197,7 @@ __device__ uint32_t block_places(const ChunkParams& p, int* s_pre, int* s_warp, 
     s_warp[2 * warp] = scan;
     s_warp[2 * warp + 1] = __float_as_int(rows);
   }
-  __syncthreads();
+  falls = __syncthreads_or(falls);
   int before = scan - sum, total = 0;
   wide = 0.f;
   #pragma unroll
@@ -206,7 +208,7 @@ __device__ uint32_t block_places(const ChunkParams& p, int* s_pre, int* s_warp, 
   }
   s_pre[tid] = before * per;
   __syncthreads();
-  return static_cast<uint32_t>(total) * per;
+  return falls ? 0u : static_cast<uint32_t>(total) * per;
 }
 
 // The unit at place `at` (a warp's lanes together; w.j past its tiles means in the places after them), if it is of one of the 32
@@ -397,10 +399,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
     if (!few) {
       total = block_places<T>(p, s_pre, s_pre + T, wide);
     } else if (warp < kChunkRounds) {
-      bool bad = false;
+      bool bad = false, falls = false;
       if (lane < p.B) {
         mine = req_at(p, lane, tok0);
         const int x = p.cu[lane], y = p.cu[lane + 1];
+        falls = y < x;
         bad = y < x || (lane == 0 && x != 0) || y > p.T;
         places = unit_row_places(mine, p.shape) * (p.H_kv * p.n_rg);
         if (row_tiles(mine, p.shape) > 1) wide = static_cast<float>(mine.L);
@@ -408,6 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
       if (bad && blockIdx.x == 0) atomicCAS(p.status, 0, kStatusBadSeqlens);
       scan = scan_lanes(places);
       total = static_cast<uint32_t>(__shfl_sync(0xffffffffu, scan, 31));
+      if (__any_sync(0xffffffffu, falls)) total = 0;  // (as block_places)
       #pragma unroll
       for (int off = 16; off > 0; off >>= 1) wide += __shfl_xor_sync(0xffffffffu, wide, off);
     }

@@ -185,14 +185,25 @@ template <bool MULTI>
 __device__ __forceinline__ int places_per(const PagedParams& p) {
   return MULTI ? p.H_kv : p.H_kv * p.n_rg;
 }
+// MULTI: whether cu falls behind request s.  The requests' tokens are then more than T, and their places may not fit 32
+// bits: no request has any.
+template <bool MULTI>
+__device__ __forceinline__ bool falls(const PagedParams& p, int s) {
+  return MULTI && s < min(p.B, p.own_first) && p.cu[s + 1] < p.cu[s];
+}
 // Places of all requests, by one warp.
 template <bool MULTI>
 __device__ __forceinline__ int all_places(const PagedParams& p) {
   int n = 0;
+  bool bad = false;
   for (int s0 = threadIdx.x & 31; s0 < p.B; s0 += 256) {
     #pragma unroll
-    for (int k = 0; k < 8; ++k) n += req_places<MULTI>(p, s0 + 32 * k);
+    for (int k = 0; k < 8; ++k) {
+      n += req_places<MULTI>(p, s0 + 32 * k);
+      bad |= falls<MULTI>(p, s0 + 32 * k);
+    }
   }
+  if (MULTI && __any_sync(0xffffffffu, bad)) return 0;
   return __reduce_add_sync(0xffffffffu, n) * places_per<MULTI>(p);
 }
 // Places of all requests, by a block of T threads for which one look each is not enough, and s_pre[i]:
@@ -202,8 +213,12 @@ __device__ int block_places(const PagedParams& p, int* s_pre, int* s_warp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int share = (p.B + T - 1) / T, lo = min(tid * share, p.B), hi = min(lo + share, p.B);
   int sum = 0;
+  bool bad = false;
   #pragma unroll 8
-  for (int s = lo; s < hi; ++s) sum += req_places<MULTI>(p, s);
+  for (int s = lo; s < hi; ++s) {
+    sum += req_places<MULTI>(p, s);
+    bad |= falls<MULTI>(p, s);
+  }
   int scan = sum;
   #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -211,7 +226,8 @@ __device__ int block_places(const PagedParams& p, int* s_pre, int* s_warp) {
     if (lane >= off) scan += up;
   }
   if (lane == 31) s_warp[warp] = scan;
-  __syncthreads();
+  if constexpr (MULTI) bad = __syncthreads_or(bad);
+  else __syncthreads();
   int before = scan - sum, total = 0;
   #pragma unroll
   for (int i = 0; i < T / 32; ++i) {
@@ -220,7 +236,7 @@ __device__ int block_places(const PagedParams& p, int* s_pre, int* s_warp) {
   }
   s_pre[tid] = before * places_per<MULTI>(p);
   __syncthreads();
-  return total * places_per<MULTI>(p);
+  return bad ? 0 : total * places_per<MULTI>(p);
 }
 // The share of block_places that holds place `at`.
 template <int T>
