@@ -400,7 +400,7 @@ ATTN_API size_t attn_fwd_paged_workspace_bytes(int B, int H, int H_kv, int d);
  * depends on lengths is decided on the GPU: a captured call can be replayed with other lengths, tables and contents.
  * Equal inputs give equal bits.  A table entry that is needed and names no page of the cache is read as a page of
  * zeros, and the status word reports kind 5.
- * H_kv must divide H; max_pages * page_size and T are below 2^31 - 1024, and so is the number of places
+ * H_kv must divide H; B, max_pages * page_size and T are below 2^31 - 1024, and so is the number of places
  * (128-row key tiles, and two more, of every run of new tokens that shares a product: 256 query rows of a
  * K/V head) that the table's shape allows (ATTN_ERR_SHAPE).  Returns an attn_status.
  */
@@ -426,7 +426,7 @@ ATTN_API size_t attn_fwd_paged_varlen_workspace_bytes(int T, int H, int H_kv, in
  *   block_table, seq_lens : as attn_fwd_paged.  Either length may be 0; with both, O = 0 and lse = -inf.
  *   workspace : attn_fwd_paged_shared_workspace_bytes(B, H, H_kv, d) bytes, 256-byte aligned; calls whose
  *     work may overlap on the GPU need one each.
- * Pages, table entries, graphs, limits and errors as attn_fwd_paged and attn_fwd_paged_varlen.
+ * Pages, table entries, graphs, limits and errors as attn_fwd_paged and attn_fwd_paged_varlen (groups + B as its B).
  */
 ATTN_API int attn_fwd_paged_shared(const void* q, const attn_kv_cache* cache, const int32_t* prefix_table,
                                    const int32_t* prefix_lens, const int32_t* cu_groups,
@@ -460,7 +460,7 @@ ATTN_API int attn_kv_write(const void* k, const int64_t* k_strides, const void* 
  *     cu_rows[B] on are left as they were (cu_rows that decreases, does not begin with 0 or passes T: kind 2);
  *   first : int32 [B], or NULL for zeros;  block_table : int32 [B, max_pages]
  * A row before the first or past the table, or whose entry names no page of the cache, becomes zeros and the
- * status word reports kind 5.  One launch.  T is below 2^31 - 1024.  Returns an attn_status.
+ * status word reports kind 5.  One launch.  B and T are below 2^31 - 1024.  Returns an attn_status.
  */
 ATTN_API int attn_kv_read(const attn_kv_cache* cache, const int32_t* block_table, const int32_t* cu_rows,
                           const int32_t* first, void* k, void* v, int B, int T, int H_kv, int d, int max_pages,

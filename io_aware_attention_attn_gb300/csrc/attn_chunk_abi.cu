@@ -42,9 +42,11 @@ size_t chunk_workspace(int T, int group, int d, const ChunkSizes& z) {
   return few > z.total ? few : z.total;
 }
 
+constexpr int kMostRequests = INT_MAX - 1024;  // the kernels step over them by blocks
+
 // The kernel numbers places in 32 bits and rows and tokens with some room to spare.
 bool chunk_sizes_fit(int B, int T, int H, int H_kv, int max_pages, int page_size, const ChunkSizes& z) {
-  if (static_cast<int64_t>(T) * H > INT_MAX) return false;
+  if (B > kMostRequests || static_cast<int64_t>(T) * H > INT_MAX) return false;
   const int64_t most = static_cast<int64_t>(max_pages) * page_size;
   if (most > INT_MAX - 1024 || T > INT_MAX - 1024 || static_cast<int64_t>(H_kv) * z.n_rg > INT_MAX) return false;
   const int64_t tiles = (most + kChunkTile - 1) / kChunkTile + 1;
@@ -278,7 +280,7 @@ extern "C" int attn_fwd_paged_shared(const void* q, const attn_kv_cache* cache, 
   if (rc != ATTN_OK) return rc;
   if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_SCALE;
   const ChunkSizes z = chunk_sizes(H / H_kv, B, d);
-  if (!paged_sizes_fit(B, H, H_kv, max_pages, cache->page_size) ||
+  if (groups > kMostRequests - B || !paged_sizes_fit(B, H, H_kv, max_pages, cache->page_size) ||
       !chunk_sizes_fit(groups, B, H, H_kv, max_prefix_pages, cache->page_size, z))
     return ATTN_ERR_SHAPE;
   const SharedLayout s = shared_layout(B, H, H / H_kv, d, z);
@@ -370,7 +372,7 @@ extern "C" int attn_kv_read(const attn_kv_cache* cache, const int32_t* block_tab
   if (B == 0 || T == 0 || H_kv == 0) return ATTN_OK;
   if (d != 64 && d != 128) return ATTN_ERR_HEAD_DIM;
   if (!cache || !cu_rows || !k || !v || (max_pages > 0 && !block_table)) return ATTN_ERR_NULL;
-  if (T > INT_MAX - 1024) return ATTN_ERR_SHAPE;
+  if (T > INT_MAX - 1024 || B > kMostRequests) return ATTN_ERR_SHAPE;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(block_table, 4) || !aligned(cu_rows, 4) || !aligned(first, 4))
     return ATTN_ERR_ALIGN;
   int rc = check_cache(*cache, H_kv, d);

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
     if (t < p.T) {
       int a = 0, b = p.B;  // the request whose rows hold t, if one does
       while (b - a > 1) {
-        const int m = (a + b) >> 1;
+        const int m = a + ((b - a) >> 1);
         if (cu(m) <= t) a = m;
         else b = m;
       }
