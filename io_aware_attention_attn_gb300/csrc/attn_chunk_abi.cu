@@ -51,10 +51,14 @@ bool chunk_sizes_fit(int B, int T, int H, int H_kv, int max_pages, int page_size
   if (most > INT_MAX - 1024 || T > INT_MAX - 1024 || static_cast<int64_t>(H_kv) * z.n_rg > INT_MAX) return false;
   const int64_t tiles = (most + kChunkTile - 1) / kChunkTile + 1;
   const int64_t rows = static_cast<int64_t>(T) / (2 * z.cta_tokens) + (B < T ? B : T);  // row tiles, at most
-  if (rows > INT_MAX / (tiles + kChunkCost) / (static_cast<int64_t>(H_kv) * z.n_rg)) return false;
-  const int64_t all = static_cast<int64_t>(T) * (H / H_kv);
-  const int64_t groups = all / 8 + (B < T ? B : T), few_tiles = (most + kPagedTile - 1) / kPagedTile + 1;
-  return groups <= INT_MAX / (few_tiles + kFewCost) / H_kv;
+  return rows <= INT_MAX / (tiles + kChunkCost) / (static_cast<int64_t>(H_kv) * z.n_rg);
+}
+// Whether the kernel for few rows can number the places of `rows` rows a K/V head, too: its units are of fewer rows and its
+// tiles of fewer keys.
+bool few_sizes_fit(int B, int T, int64_t rows, int H_kv, int max_pages, int page_size) {
+  const int64_t most = static_cast<int64_t>(max_pages) * page_size, tiles = (most + kPagedTile - 1) / kPagedTile + 1;
+  const int64_t units = rows / few_rows_of(rows, B) + (B < T ? B : T);
+  return units <= INT_MAX / (tiles + kFewCost) / H_kv;
 }
 
 struct QueryLayout {
@@ -244,7 +248,10 @@ extern "C" int attn_fwd_paged_varlen(const void* q, const attn_kv_cache* cache, 
   if ((rc = check_device()) != 0) return rc;
   const QueryLayout at{static_cast<int64_t>(T) * d, d};
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const int few_rows = few_most(*cache), which = kernels_for(static_cast<int64_t>(T) * (H / H_kv), B, few_rows);
+  const int64_t rows = static_cast<int64_t>(T) * (H / H_kv);
+  const int few_rows = few_most(*cache);
+  // (where only the kernel for many rows can number the places, it takes all requests)
+  const int which = few_sizes_fit(B, T, rows, H_kv, max_pages, cache->page_size) ? kernels_for(rows, B, few_rows) : kMany;
   // of both, one after the other on one workspace
   if (which & kFew)
     rc = run_few(q, *cache, block_table, seq_lens, cu_new, o, lse, nullptr, B, T, H, H_kv, d, max_pages, causal != 0, scale,

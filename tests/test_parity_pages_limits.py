@@ -10,7 +10,7 @@ import torch
 
 from io_aware_attention_attn_gb300 import attn
 from test_parity_generation import _gpu, i32, normal, paged_inputs  # noqa: F401
-from test_parity_pages import check_varlen, sums
+from test_parity_pages import check_shared, check_varlen, shared_inputs, sums
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,48 @@ def test_nothing_is_computed_for_sums_that_fall(T, B, kind):
     cu = [0] * B + [T]
     o, lse = attn.attn_fwd_paged_varlen(q, cache, table, n, i32(*cu))
     assert torch.isfinite(o.float()[:, -40:]).all() and attn.last_device_error() == 0
+
+
+def wide(table, pages):
+    """The table in rows of `pages` entries: what lies behind a request's own is never read."""
+    out = torch.full((table.shape[0], pages), -7, dtype=torch.int32, device="cuda")
+    out[:, :table.shape[1]] = table
+    return out
+
+
+def test_batch_padded_to_a_long_context():
+    # 32768 tokens' room over a table for 2^20 keys, of which one request uses little
+    T, H, KV, d, new, L = 32768, 32, 8, 64, 700, 3000
+    _, cache, table, n, vals = paged_inputs(3, [L], H, KV, d, 64, "bf16")
+    q = normal(4, H, T, d)
+    out = torch.full((H, T, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((H, T), 7.0, device="cuda")
+    attn.attn_fwd_paged_varlen(q, cache, wide(table, 1 << 14), n, i32(0, new), out=out, lse=lse)
+    assert attn.last_device_error() == 0 and (out[:, new:] == 7).all() and (lse[:, new:] == 7).all()
+    check_varlen(out[:, :new], lse[:, :new], q[:, :new], vals, table, [L], [0, new], True, 1 / 8, "bf16", "varlen long context",
+                 set(range(0, new, 23)) | {new - 1})
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,old,H,KV,d", [([5], [295], 16, 4, 64), ([2] * 4, [900, 1, 0, 500], 32, 8, 128),
+                                            ([8], [4000], 32, 8, 128), ([1, 3, 60], [100, 0, 40], 8, 2, 64)])
+def test_tables_wider_than_the_lengths(new, old, H, KV, d, kind):
+    # as a server keeps them, for its longest context: other shares, joins where the narrow table has none
+    lens = [a + b for a, b in zip(new, old)]
+    _, cache, table, n, vals = paged_inputs(5, lens, H, KV, d, 16, kind)
+    q, cu = normal(6, H, sum(new), d), sums(new)
+    for pages in (table.shape[1], 4 * table.shape[1], 2048):
+        o, lse = attn.attn_fwd_paged_varlen(q, cache, wide(table, pages), n, i32(*cu))
+        check_varlen(o, lse, q, vals, table, lens, cu, True, 1 / math.sqrt(d), kind, f"varlen {kind} table of {pages}")
+    assert attn.last_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("each,H,KV", [([4], 16, 16), ([4] * 12, 16, 4), ([40, 1], 16, 2)])
+def test_shared_tables_wider_than_the_lengths(each, H, KV, kind):
+    args, own, vals = shared_inputs(each, [90 * (i + 1) for i in range(len(each))], H, KV, 64, 16, 7, 30, kind)
+    q, cache, pt, pl, cu, table, lens = args
+    for a, b in ((pt.shape[1], 2048), (2048, table.shape[1]), (2048, 2048)):
+        o, lse = attn.attn_fwd_paged_shared(q, cache, wide(pt, a), pl, cu, wide(table, b), lens)
+        check_shared(o, lse, args, vals, 1 / 8, kind, f"shared {kind} tables of {a}, {b}")
+    assert attn.last_device_error() == 0
