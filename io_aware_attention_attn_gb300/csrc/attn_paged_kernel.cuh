@@ -408,9 +408,10 @@ __device__ __forceinline__ void store_row(const PagedParams& p, bool own, int h,
                                           float top, float sum) {
   const int tok = r / p.group;
   const int64_t head = static_cast<int64_t>(h) * p.group + (r - tok * p.group), token = tok0 + tok;
-  const bool some = sum > 0.f || sum != sum;  // (a row that sees nothing: zeros)
-  const float inv = some ? 1.f / sum : 0.f, lse = some ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
-  v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+  // a row that sees nothing: zeros, whatever its products with the values that others see were
+  const bool some = sum > 0.f || sum != sum;
+  const float inv = 1.f / sum, lse = some ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+  v = some ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
   if (p.pair_o) {
     const int64_t at = (own ? static_cast<int64_t>(p.T) * p.H : 0) + token * p.H + head;
     *reinterpret_cast<float4*>(p.pair_o + at * D + 4 * c4) = v;

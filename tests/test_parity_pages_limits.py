@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from io_aware_attention_attn_gb300 import attn
+from oracle import fp8 as ofp8
 from test_parity_generation import _gpu, i32, normal, paged_inputs  # noqa: F401
 from test_parity_pages import check_shared, check_varlen, shared_inputs, sums
 
@@ -96,3 +97,21 @@ def test_shared_tables_wider_than_the_lengths(each, H, KV, kind):
         o, lse = attn.attn_fwd_paged_shared(q, cache, wide(pt, a), pl, cu, wide(table, b), lens)
         check_shared(o, lse, args, vals, 1 / 8, kind, f"shared {kind} tables of {a}, {b}")
     assert attn.last_device_error() == 0
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,L,H,KV", [(10, 4, 4, 2), (10, 4, 8, 1), (20, 7, 1, 1), (60, 9, 1, 1), (200, 130, 4, 2)])
+def test_tokens_that_see_nothing_beside_values_that_are_not_finite(new, L, H, KV, kind, bad):
+    # more tokens than rows: O = 0 and lse = -inf for the first ones, whatever the rows hold that others of their unit see
+    _, cache, table, n, vals = paged_inputs(3, [L], H, KV, 64, 16, kind, junk=False)
+    page = table[0, 0].long()
+    if kind == "bf16":
+        cache.v[page, :, 2, 5] = bad
+    else:
+        cache.v_scale[page, :, 2] = bad
+    q = normal(4, H, new, 64)
+    o, lse = attn.attn_fwd_paged_varlen(q, cache, table, n, i32(0, new))
+    blind = new - L
+    assert (o[:, :blind] == 0).all() and torch.isneginf(lse[:, :blind]).all()
+    assert not torch.isfinite(o[:, blind + 2:, 5].float()).any() and torch.isfinite(lse[:, blind:]).all()
