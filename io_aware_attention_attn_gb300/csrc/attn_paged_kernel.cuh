@@ -342,7 +342,9 @@ __device__ __forceinline__ void load_q(const PagedParams& p, const Walk& w, int 
       // largest element to 2^8 .. 2^9: its exponent field, kept where both factors are normal
       const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23), 16), 254) - 8;
       const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^(127 - e)
-      const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);          // 2^(e - 127)
+      // 2^(e - 127); MULTI: a row with an infinity has no attention, as with a NaN, and as in attn_chunk_kernel (its scores
+      // may all be -inf)
+      const float up = MULTI && !(amax < INFINITY) ? NAN : __uint_as_float(static_cast<uint32_t>(e) << 23);
       #pragma unroll
       for (int k = 0; k < D / 16; ++k)
         #pragma unroll

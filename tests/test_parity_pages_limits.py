@@ -115,3 +115,36 @@ def test_tokens_that_see_nothing_beside_values_that_are_not_finite(new, L, H, KV
     blind = new - L
     assert (o[:, :blind] == 0).all() and torch.isneginf(lse[:, :blind]).all()
     assert not torch.isfinite(o[:, blind + 2:, 5].float()).any() and torch.isfinite(lse[:, blind:]).all()
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("new,H,KV", [([3, 3], 2, 1), ([4, 2], 4, 1), ([6, 5], 4, 1), ([9, 12], 4, 1), ([40, 70], 4, 2)])
+def test_query_rows_with_an_infinity(new, H, KV, sign):
+    # over E4M3 pages such a row gives NaN, also where all its products have one sign; the other rows are as without it
+    lens = [n + 150 for n in new]
+    _, cache, table, n, _ = paged_inputs(3, lens, H, KV, 64, 16, "e4m3", junk=False)
+    codes = cache.k.view(torch.uint8)
+    codes[..., 7] = 0x80 | codes[..., 7].clamp(1, 0x7E)    # negative, none of them zero
+    q, cu = normal(4, H, sum(new), 64), sums(new)
+    clean = attn.attn_fwd_paged_varlen(q, cache, table, n, i32(*cu))
+    q[H - 1, 1, 7] = sign * math.inf
+    o, lse = attn.attn_fwd_paged_varlen(q, cache, table, n, i32(*cu))
+    assert torch.isnan(o[H - 1, 1]).all() and torch.isnan(lse[H - 1, 1])
+    o[H - 1, 1], lse[H - 1, 1] = clean[0][H - 1, 1], clean[1][H - 1, 1]
+    assert same((o, lse), clean)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("each,H,KV", [([2, 1], 2, 1), ([4, 3], 4, 1), ([40, 30], 4, 2)])
+def test_shared_query_rows_with_an_infinity(each, H, KV, sign):
+    args, own, _ = shared_inputs(each, [200, 90], H, KV, 64, 16, 31, 60, "e4m3")
+    q, cache, *rest = args
+    cache = attn.KVCache(*(torch.nan_to_num(t.float(), 0.5).to(t.dtype) if t.dtype == torch.float32 else t for t in cache))
+    codes = cache.k.view(torch.uint8)
+    codes[..., 7] = 0x80 | codes[..., 7].clamp(1, 0x7E)
+    clean = attn.attn_fwd_paged_shared(q, cache, *rest)
+    q[1, H - 1, 0, 7] = sign * math.inf
+    o, lse = attn.attn_fwd_paged_shared(q, cache, *rest)
+    assert torch.isnan(o[1, H - 1]).all() and torch.isnan(lse[1, H - 1]).all()
+    o[1, H - 1], lse[1, H - 1] = clean[0][1, H - 1], clean[1][1, H - 1]
+    assert same((o, lse), clean)
