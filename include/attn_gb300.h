@@ -387,8 +387,9 @@ ATTN_API size_t attn_fwd_paged_workspace_bytes(int B, int H, int H_kv, int d);
  *     clamped into [0, T] and the status word reports kind 2 (o and lse are then unspecified); with one that
  *     decreases nothing is computed, with the same report.
  *   A token that sees no row (more new tokens than rows) gets O = 0 and lse = -inf.
- *   E4M3 caches: V scales of 2^-100 to 2^100 in magnitude, or 0 (K scales: any; attn_fwd_paged takes any of either);
- *     a query row with an infinity or a NaN gives NaN.  A V row that is not finite reaches, besides the tokens that see it, those before it that share its
+ *   E4M3 caches: K scales of at most 2^100 in magnitude, V scales of 2^-100 to 2^100, or 0 (attn_fwd_paged takes any of
+ *     either; these are the limits of the kernel for many rows, see below); a query row with an infinity or a NaN gives NaN.
+ *     A V row that is not finite reaches, besides the tokens that see it, those before it that share its
  *     tile of 128 rows (as in attn_fwd).
  *   workspace : attn_fwd_paged_varlen_workspace_bytes(T, H, H_kv, d) bytes (it does not depend on the
  *     lengths), 256-byte aligned; calls whose work may overlap on the GPU need one each.

@@ -27,7 +27,8 @@
 //   - E4M3 pages.  Scores: K's codes go to the product as they are (kind::f8f6f4); a query row becomes two
 //     E4M3 pieces, x = hi + lo, after scaling by a power of two (8 significant bits, as bf16 has; what
 //     is smaller than 2^-9 of a row's largest element loses bits, 2^-17 of that element at most), for the
-//     time of one bf16 product.  A key's K scale multiplies its scores.  Values: four warps turn V's codes into bf16
+//     time of one bf16 product.  A key's K scale multiplies its scores, which are below 2^24 before (d 2^8 448): scales of up to
+//     2^100 keep them finite before the row's factor does.  Values: four warps turn V's codes into bf16
 //     (exact), and a key's V scale multiplies its P before that is rounded to bf16, whose range holds any product
 //     of a P below 2^16 and a scale below 2^100.
 //

@@ -148,3 +148,18 @@ def test_shared_query_rows_with_an_infinity(each, H, KV, sign):
     assert torch.isnan(o[1, H - 1]).all() and torch.isnan(lse[1, H - 1]).all()
     o[1, H - 1], lse[1, H - 1] = clean[0][1, H - 1], clean[1][1, H - 1]
     assert same((o, lse), clean)
+
+
+@pytest.mark.parametrize("new", [[200, 70], [3, 5], [1]])
+@pytest.mark.parametrize("d", [64, 128])
+def test_key_scales_at_their_limit(new, d):
+    # a power of two that K's scales have and the query does not changes no bit, up to 2^100 and far down
+    lens = [n + 150 * i + 90 for i, n in enumerate(new)]
+    _, cache, table, n, _ = paged_inputs(3, lens, 8, 2, d, 16, "e4m3", junk=False)
+    top = math.floor(math.log2(100.0 * float(cache.k_scale.abs().max()))) - 6
+    q, cu = normal(4, 8, sum(new), d), sums(new)
+    clean = attn.attn_fwd_paged_varlen(q, cache, table, n, i32(*cu))
+    for by in (2.0 ** (99 - top), -2.0 ** (99 - top), 2.0 ** -100):
+        c = cache._replace(k_scale=cache.k_scale * by)
+        assert float(c.k_scale.abs().max()) <= 2.0 ** 100
+        assert same(attn.attn_fwd_paged_varlen((q.float() / by).to(torch.bfloat16), c, table, n, i32(*cu)), clean)
