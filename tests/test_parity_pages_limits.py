@@ -163,3 +163,44 @@ def test_key_scales_at_their_limit(new, d):
         c = cache._replace(k_scale=cache.k_scale * by)
         assert float(c.k_scale.abs().max()) <= 2.0 ** 100
         assert same(attn.attn_fwd_paged_varlen((q.float() / by).to(torch.bfloat16), c, table, n, i32(*cu)), clean)
+
+
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("at", [0, 60, -1])
+@pytest.mark.parametrize("new", [[3, 5, 2], [16, 12, 9], [8, 300, 33], [256, 256, 1]])
+def test_values_that_are_not_finite_stay_in_their_request_and_column(new, at, kind, bad):
+    # a row of V that some or none of its request's other new tokens see: what it reaches is not finite, and nothing else
+    # changes a bit; a row of K reaches the tokens that see it, all of them and only those
+    H, KV, d = 8, 2, 64
+    lens = [n + 64 * (i % 2) for i, n in enumerate(new)]
+    _, cache, table, n, _ = paged_inputs(3, lens, H, KV, d, 16, kind, junk=False)
+    q, cu = normal(4, H, sum(new), d), sums(new)
+    clean = attn.attn_fwd_paged_varlen(q, cache, table, n, i32(*cu))
+    row = min(at % lens[1], lens[1] - 1) if at >= 0 else lens[1] - 1
+    page = table[1, row // 16].long()
+    mine = slice(cu[1], cu[2])
+    sees = torch.arange(new[1], device="cuda") + lens[1] - new[1] >= row
+    assert sees.any()
+
+    def with_bad(side):
+        x = getattr(cache, side).clone()
+        if kind == "bf16":
+            x[page, 0, row % 16, 5] = bad
+        else:
+            x.view(torch.uint8)[page, 0, row % 16, 5] = 0x7F
+        return attn.attn_fwd_paged_varlen(q, cache._replace(**{side: x}), table, n, i32(*cu))
+
+    o, lse = with_bad("v")
+    part = o[:H // KV, mine, 5]
+    assert not torch.isfinite(part[:, sees].float()).any()
+    kept = torch.isfinite(part.float())
+    assert torch.equal(part[kept], clean[0][:H // KV, mine, 5][kept])
+    part.copy_(clean[0][:H // KV, mine, 5])
+    assert same((o, lse), clean)
+
+    o, lse = with_bad("k")
+    part = o[:H // KV, mine]
+    assert torch.isnan(part[:, sees].float()).all() if bad != bad else not torch.isfinite(lse[:H // KV, mine][:, sees]).all()
+    part[:, sees], lse[:H // KV, mine][:, sees] = clean[0][:H // KV, mine][:, sees], clean[1][:H // KV, mine][:, sees]
+    assert same((o, lse), clean)
