@@ -74,6 +74,13 @@ __device__ __forceinline__ uint2 quantize(const uint4& x, float sc, float rc) {
   return make_uint2(out[0], out[1]);
 }
 
+// x y, of 28 significant bits here, as the fp32 number that rounds to bf16 as it does: of the two around it the odd one (no
+// middle of two bf16 numbers is odd), itself where it is one.
+__device__ __forceinline__ float mul_odd(float x, float y) {
+  const float lo = __fmul_rd(x, y), hi = __fmul_ru(x, y);
+  return (__float_as_uint(lo) & 1u) ? lo : hi;
+}
+
 // 8 codes x scale -> 8 bf16 values
 __device__ __forceinline__ uint4 dequantize(const uint2& codes, float sc) {
   uint32_t out[4];
@@ -84,7 +91,7 @@ __device__ __forceinline__ uint4 dequantize(const uint2& codes, float sc) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
         : "=f"(lo), "=f"(hi)
         : "r"(h));
-    out[i] = pack_bf16x2(lo * sc, hi * sc);
+    out[i] = pack_bf16x2(mul_odd(lo, sc), mul_odd(hi, sc));
   }
   return make_uint4(out[0], out[1], out[2], out[3]);
 }

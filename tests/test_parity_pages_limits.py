@@ -204,3 +204,50 @@ def test_values_that_are_not_finite_stay_in_their_request_and_column(new, at, ki
     assert torch.isnan(part[:, sees].float()).all() if bad != bad else not torch.isfinite(lse[:H // KV, mine][:, sees]).all()
     part[:, sees], lse[:H // KV, mine][:, sees] = clean[0][:H // KV, mine][:, sees], clean[1][:H // KV, mine][:, sees]
     assert same((o, lse), clean)
+
+
+def bf16_of(x):
+    """float64 values rounded once to bf16, as float64."""
+    m, e = np.frexp(x)
+    step = np.ldexp(1.0, np.maximum(e, -125) - 8)
+    with np.errstate(invalid="ignore", over="ignore"):
+        y = np.where(np.isfinite(x), np.rint(x / step) * step, x)
+        return np.where(np.abs(y) >= 2.0 ** 128, np.copysign(np.inf, y), y)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_read_are_rounded_once(d):
+    # every code against scales whose products lie beside the middle of two bf16 numbers, where a rounding to fp32 on the way
+    # would be seen, and the ends of the range
+    r = np.random.default_rng(5)
+    sig = []
+    for s in (9, 11, 13, 15, 8):                            # significands of codes
+        middle = (2 * r.integers(1 << 7, 1 << 8, 300) + 1) * 2.0 ** r.integers(18, 20, 300)
+        sig += [np.floor(middle / s), np.floor(middle / s) + 1]
+    sig = np.concatenate(sig)
+    m, _ = np.frexp(sig)
+    scale = np.concatenate([m, -m * 2.0 ** 20, m * 2.0 ** -120, m * 2.0 ** -130, m * 2.0 ** -140, m * 2.0 ** 127, m * 2.0 ** 119,
+                            [0.0, -0.0, np.inf, -np.inf, np.nan, 1.0, 2.0 ** -149]]).astype(np.float32)
+    rows = 256 // d                                        # of one scale, so that it meets every code
+    n = len(scale) * rows
+    page, KV = 16, 2
+    pages = -(-n // page)
+    cache = attn.kv_cache(pages, KV, page, d, torch.float8_e4m3fn)
+    flat = torch.zeros(pages * page, dtype=torch.float32)
+    flat[:n] = torch.from_numpy(np.repeat(scale, rows))
+    codes = torch.arange(256, dtype=torch.uint8).view(rows, d).repeat(-(-pages * page // rows), 1)[:pages * page]
+    for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        c.view(torch.uint8).copy_(codes.view(pages, 1, page, d).expand(-1, KV, -1, -1))
+        s.copy_(flat.view(pages, 1, page).expand(-1, KV, -1))
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, -1)
+    k, v = attn.kv_read(cache, table, i32(0, n), n)
+    with np.errstate(invalid="ignore", over="ignore"):
+        exact = ofp8.e4m3_value(codes.numpy())[:n] * flat[:n].numpy().astype(np.float64)[:, None]  # 28 bits: exact
+    want = bf16_of(exact)
+    twice = torch.from_numpy(exact).float().to(torch.bfloat16).double().numpy()
+    assert (twice != want).sum() > 100 + np.isnan(want).sum()        # (the inputs do tell the two apart)
+    for x in (k, v):
+        for h in range(KV):
+            got = x[h].double().cpu().numpy()
+            assert np.array_equal(got, want, equal_nan=True)
+            assert np.array_equal(np.signbit(got[~np.isnan(want)]), np.signbit(want[~np.isnan(want)]))
