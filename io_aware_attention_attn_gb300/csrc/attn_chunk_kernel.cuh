@@ -748,6 +748,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
       named_barrier_sync(1 + quarter, 64);
       return y;
     };
+    // The two meet at barriers that have no limit, so neither leaves the other there: one whose wait gave up says so (a value
+    // of 2) where they meet next, and both stop.  What that is for this warp: nothing, the other knows (0); as in a first
+    // tile, which is the next unit's, or the other's leave (1); as in a later tile (2).
+    int meet = 1;
     bool ok = true;
     int g = 0, uq = 0;
     for (ChunkUnit w; unit_at(uq, w, ok, kRoleSoftmax);) {
@@ -763,15 +767,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
       float le[4] = {0.f, 0.f, 0.f, 0.f};  // sums of 2^(t - m)
       for (int j = w.j; j < j_end; ++j, ++g) {
         const int b = g % NB;
-        if (!(ok = wait_warp(bar(L::bSF + b), static_cast<uint32_t>(g / NB) & 1u, wc, kRoleSoftmax, 1))) break;
+        if (!(ok = wait_warp(bar(L::bSF + b), static_cast<uint32_t>(g / NB) & 1u, wc, kRoleSoftmax, 1))) {
+          meet = any && j > w.j ? 2 : 1;
+          break;
+        }
         const float* sc = reinterpret_cast<const float*>(smem + L::kScale + (g % kChunkScales) * 1024) + 64 * half;
         if (E4M3) {
           // (the factors of the rows were written before the product that this wait is for could be issued)
           if (j == w.j)
             sl2 = p.scale_log2 * reinterpret_cast<const float*>(smem + L::kRow)[(uq % kChunkRowDepth) * 128 + row];
           if (!(ok = wait_warp(bar(L::bCF + g % kChunkScales), static_cast<uint32_t>(g / kChunkScales) & 1u, wc,
-                                    kRoleSoftmax, 2)))
+                               kRoleSoftmax, 2))) {
+            meet = any && j > w.j ? 2 : 1;
             break;
+          }
         }
         tc_fence_after();
         if (any) {
@@ -830,7 +839,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
               const float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
                                      fmaxf(mx[6], mx[7])) * sl2;
               const float both = fmaxf(mt, exchange(mt));
-              need |= exchange(need ? 1.f : 0.f) != 0.f;
+              const float other = exchange(need ? 1.f : 0.f);
+              if (other == 2.f) {
+                ok = false;
+                break;
+              }
+              need |= other != 0.f;
               const float m_new = need ? fmaxf(both, m2) : m2;
               moved = (m_new != m2);
               m_use = (m_new == -INFINITY) ? 0.f : m_new;
@@ -873,13 +887,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
               if (!named_barrier_or(1 + quarter, 64, need)) break;
             }
           }
+          if (!ok) {
+            meet = 0;
+            break;
+          }
           #pragma unroll
           for (int k = 0; k < 4; ++k) le[k] += ts[k];
           // O holds P V up to the tile before once that product completes; bring it to the new reference
           if (j > w.j && __any_sync(0xffffffffu, moved)) {
             if (!(ok = wait_warp(bar(L::bPV + (g - 1) % NB), static_cast<uint32_t>((g - 1) / NB) & 1u, wc,
-                                      kRoleSoftmax, 3)))
+                                 kRoleSoftmax, 3))) {
+              meet = j + 1 < j_end ? 2 : 1;
               break;
+            }
             tc_fence_after();
             #pragma unroll 1
             for (int cc = 0; cc < D / 64; ++cc) {  // its half of the columns
@@ -910,6 +930,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((ChunkLayout<D, E4M3
       if (lane == 0) mbar_arrive(bar(L::bEL + uq % kChunkStats));
       ++uq;
     }
+    if (meet == 2) named_barrier_or(1 + quarter, 64, true);
+    #pragma unroll 1
+    for (int i = 0; meet > 0 && i < 2; ++i) exchange(2.f);
   } else if (warp < kConvertWarp) {
     // ===================================================================== O out
     // Warps of their own, so that the softmax goes on with the next unit while a unit's last product runs and its
