@@ -418,14 +418,17 @@ ATTN_API size_t attn_fwd_paged_varlen_workspace_bytes(int T, int H, int H_kv, in
  * Attention of one new token of each of B requests whose first rows are shared: requests cu_groups[g] ..
  * cu_groups[g+1]-1 have the prefix_lens[g] rows of the pages prefix_table[g][0], [1], ... before the seq_lens[s] rows
  * of their own, block_table[s][0], [1], ....  O and lse are those of attn_fwd_paged over the rows of both, but the
- * prefix is read once for a group (once for each 16 to 256 query rows of a K/V head, by how many there are) instead of
- * once a request.  The attentions over the prefixes and over the own rows are left in fp32 and joined by the
- * block merge; three or four launches.
+ * prefix is read once for all requests of a group that a product takes together, 8 to 256 query rows of a K/V head, instead
+ * of once a request.  How many those are goes by the mean over all `groups`, also those without requests: a group much
+ * larger than that, or few groups with requests among many, have their prefix read more often (64 requests behind 8192
+ * rows, 32 query and 8 K/V heads: 52 us as the only group, 97 as one of 32).  The attentions over the prefixes and over the
+ * own rows are left in fp32 and joined by the block merge; three or four launches.
  *   q, o : bf16 [B, H, d] (= [B, H, 1, d]);  lse : fp32 [B, H]
  *   prefix_table : int32 [groups, max_prefix_pages];  prefix_lens : int32 [groups], clamped to 0 ..
  *     max_prefix_pages * page_size;  cu_groups : int32 [groups + 1], from 0 up, at most B (as cu_new of
  *     attn_fwd_paged_varlen: o and lse of requests from cu_groups[groups] on are left as they were)
- *   block_table, seq_lens : as attn_fwd_paged.  Either length may be 0; with both, O = 0 and lse = -inf.
+ *   block_table, seq_lens : as attn_fwd_paged, read for all B requests (0 is a fit length for one past cu_groups[groups]).
+ *     Either length may be 0; with both, O = 0 and lse = -inf.
  *   workspace : attn_fwd_paged_shared_workspace_bytes(B, H, H_kv, d) bytes, 256-byte aligned; calls whose
  *     work may overlap on the GPU need one each.
  * Pages, table entries, graphs, limits and errors as attn_fwd_paged and attn_fwd_paged_varlen (groups + B as its B).

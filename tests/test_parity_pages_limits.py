@@ -251,3 +251,34 @@ def test_rows_read_are_rounded_once(d):
             got = x[h].double().cpu().numpy()
             assert np.array_equal(got, want, equal_nan=True)
             assert np.array_equal(np.signbit(got[~np.isnan(want)]), np.signbit(want[~np.isnan(want)]))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("each,H,KV", [([64] + [0] * 31, 32, 8), ([0] * 7 + [40, 3], 8, 2), ([30] + [1] * 7, 16, 4), ([1] * 40 + [90], 4, 1)])
+def test_shared_groups_much_unlike(each, H, KV, kind):
+    # which kernel and how many rows at once go by the mean over the groups, also those without requests
+    args, own, vals = shared_inputs(each, [300 + 41 * (i % 5) for i in range(len(each))], H, KV, 64, 16, 41, 30, kind)
+    o, lse = attn.attn_fwd_paged_shared(*args)
+    check_shared(o, lse, args, vals, 1 / 8, kind, f"shared {kind} {each[:1]}x{len(each)} unlike")
+    assert attn.last_device_error() == 0
+
+
+def test_rows_written_with_values_that_are_not_finite():
+    # a row's scale is of its numbers; with an infinity the numbers' codes are 0 (x / inf) and the infinity's that of NaN
+    KV, d, T = 2, 64, 6
+    k = normal(1, KV, T, d)
+    k[:, 1, 3] = math.nan
+    k[:, 2, 5] = -math.inf
+    k[:, 3] = math.nan
+    k[:, 4, :9] = math.inf
+    cache = attn.kv_cache(1, KV, 16, d, torch.float8_e4m3fn)
+    both = attn.kv_cache(1, KV, 16, d, torch.float8_e4m3fn)
+    slots = torch.arange(T, device="cuda")
+    attn.kv_write(k, k, cache, slots)
+    x = torch.cat([k, k, k]).transpose(0, 1).reshape(T, -1).contiguous()
+    attn.qkv_rope(x, KV, KV, cache=both, slots=slots)
+    for a, b in ((cache.k, both.k), (cache.v, both.v)):
+        va, vb = (ofp8.e4m3_value(c.view(torch.uint8).cpu().numpy())[:, :, :T] for c in (a, b))
+        assert np.array_equal(va, vb, equal_nan=True) and np.isnan(va).sum() == KV * (1 + 1 + d + 9)
+    for a, b in ((cache.k_scale, both.k_scale), (cache.v_scale, both.v_scale)):
+        assert torch.equal(a[:, :, :T], b[:, :, :T]) and not torch.isnan(a[:, :, :T]).any()
