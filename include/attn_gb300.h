@@ -388,7 +388,8 @@ ATTN_API size_t attn_fwd_paged_workspace_bytes(int B, int H, int H_kv, int d);
  *     decreases nothing is computed, with the same report.
  *   A token that sees no row (more new tokens than rows) gets O = 0 and lse = -inf.
  *   E4M3 caches: K scales of at most 2^100 in magnitude, V scales of 2^-100 to 2^100, or 0 (attn_fwd_paged takes any of
- *     either; these are the limits of the kernel for many rows, see below); a query row with an infinity or a NaN gives NaN.
+ *     either; these are the limits of the kernel for many rows, see below, which takes a query row as two E4M3 pieces:
+ *     elements under 2^-9 of its largest are off by up to 2^-17 of that); a query row with an infinity or a NaN gives NaN.
  *   A V row that is not finite may reach, besides the tokens that see it, the other new tokens of its request, in the columns
  *     where it is not finite: keys that a token does not see have the weight 0, and 0 x inf is NaN, as where S is masked
  *     before a plain softmax(S) V.  It reaches no other request.  (A K row reaches only the tokens that see it.)

@@ -19,8 +19,9 @@ constexpr int kChunkCost = 2;
 
 // Which of the two kernels takes a request goes by its rows (new tokens times the query heads of a K/V head): up to
 // kFewRows the one of warp products, whose time is that of reading K and V, above the one of 256-row products.
-// Measured, 32 requests over 4096 keys, 32 query and 8 K/V heads, d = 128, bf16 / E4M3 pages, us: 4 rows 99 / 63, 16 rows
-// 101 / 73, 32 rows 106 / 93 by the first (with the second's empty launch); any up to 256 by the second, 115 / 154.
+// Measured through the public call, 32 requests over 4096 keys, 32 query and 8 K/V heads, d = 128, bf16 / E4M3 pages, us: 4 rows
+// 89 / 54, 16 rows 91 / 65, 32 rows 96 / 86 by the first (with the second's empty launch); 80 rows by the second 109 / 142, as
+// any up to 256 (by events, 115 / 154, with 99 / 63 for 4 rows by the first).
 // Over E4M3 the first takes up to 64, in two units: 33 to 64 rows of 32 requests 150 to 153 us and 149, of 8 requests over 2000
 // keys 34 and 41 (bf16: 171 and 108, 32 and 33).
 constexpr int kFewRows = 32, kFewRowsE4m3 = 64;

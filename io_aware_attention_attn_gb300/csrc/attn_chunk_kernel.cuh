@@ -13,7 +13,7 @@
 //   - Roles: a producer and two issuers, eight softmax warps (32 rows and 64 of a tile's 128 keys each: two warps share a
 //     row, its reference and its sum, and meet when one of them needs the reference moved), four that store a unit's
 //     O while the next one's tiles run, and over E4M3 pages four that turn V.  Registers go to the softmax (setmaxnreg).
-//     With one softmax warp a row, which stored O too, 2048 tokens behind 14336 took 375 us, now 311.
+//     With one softmax warp a row, which stored O too, 2048 tokens behind 14336 took 375 us, now 310 (events).
 //   - The producer walks the units and tells the others what comes next through a ring in shared memory.
 //   - K and V come page by page: a tile is up to 8 + 8 boxes a CTA (one each from pages of 64 rows up), a
 //     lane each; a part of a tile past the request's rows is asked for outside the map, which gives

@@ -45,8 +45,8 @@
 //
 // MULTI: a unit's rows are (token, query head) of a request's new tokens, in groups of up to 32, as many groups as
 // the request has rows for, each over all of the request's keys; causal from the end, row by row (token i
-// of n sees keys below length - n + i + 1).  attn_chunk_kernel takes many rows; 32 rows over 4096 keys take it
-// 115 us (bf16, 32 requests) and 154 (E4M3), for the time of its products, whatever the rows.
+// of n sees keys below length - n + i + 1).  attn_chunk_kernel takes many rows; 80 rows over 4096 keys take it
+// 109 us (bf16, 32 requests) and 142 (E4M3), for the time of its products, whatever the rows up to 256.
 #pragma once
 
 #include "attn_gen.cuh"
@@ -431,9 +431,10 @@ __device__ __forceinline__ void store_row(const PagedParams& p, bool own, int h,
 // of warps turn it twice; and a unit's end adds nothing up between warps.  The query rows lie in shared memory as the
 // products take them.  The warps agree on the reference of a row: one barrier a tile (P is there; does any warp need a
 // reference moved?), and two more where one does.
-// Measured, 32 requests over 4096 keys, 32 query and 8 K/V heads: 32 rows, E4M3, d = 128: 93 us (16-row units: 136), d = 64:
-// 69 (91), bf16 106 and 65 (113 and 73); 16 rows, d = 128: E4M3 73 (81), bf16 101 (103).  At 32 rows over E4M3 a tile's 620
-// instructions a warp bound it (two CTAs an SM: 43 % of the issue slots, half the waits for a fixed latency).
+// Measured, 32 requests over 4096 keys, 32 query and 8 K/V heads, by events when it came in, 16-row units before: 32 rows, E4M3,
+// d = 128: 136 -> 99 us, d = 64: 91 -> 77, bf16 113 -> 106 and 73 -> 69; 16 rows, d = 128: E4M3 81 -> 79.  Now, through the
+// public call: 86, 62, 96 and 57; 65, bf16 91.  At 32 rows over E4M3 a tile's 620 instructions a warp bound it (three CTAs an
+// SM: 47 % of the issue slots, the longest waits for a fixed latency).
 template <int D, bool E4M3, int NT>
 __device__ __forceinline__ void consume_columns(const PagedParams& p, uint8_t* sm, uint32_t base, Walk& w, int left,
                                                 const WaitCtx& ctx) {
