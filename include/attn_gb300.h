@@ -403,7 +403,7 @@ ATTN_API size_t attn_fwd_paged_workspace_bytes(int B, int H, int H_kv, int d);
  * depends on lengths is decided on the GPU: a captured call can be replayed with other lengths, tables and contents.
  * Equal inputs give equal bits.  A table entry that is needed and names no page of the cache is read as a page of
  * zeros, and the status word reports kind 5.
- * H_kv must divide H; B, max_pages * page_size and T are below 2^31 - 1024, and so is the number of places
+ * H_kv must divide H; B, max_pages * page_size and T are below 2^31 - 1024, T * H below 2^31, and so is the number of places
  * (128-row key tiles, and two more, of every run of new tokens that shares a product: 256 query rows of a
  * K/V head) that the table's shape allows (ATTN_ERR_SHAPE).  Returns an attn_status.
  */
